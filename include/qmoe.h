@@ -323,8 +323,9 @@ moe_status moe_plan_set_tp_exchange(moe_plan* plan, const moe_tp_exchange* x);
  * the intermediates of moe_plan_layout are then in that scratch). Allocates
  * nothing and calls no allocating routine. The caller still passes inputs
  * and outputs as for moe_forward, with the same checks.
- * MOE_ERR_UNSUPPORTED when the plan's workspace (moe_plan_workspace_bytes,
- * set by its shape's maximum M) exceeds MOE_NOALLOC_SCRATCH_BYTES, before
+ * MOE_ERR_UNSUPPORTED when moe_forward's part of the plan's workspace
+ * (moe_plan_workspace_bytes, set by its shape's maximum M, without the regions
+ * of moe_layer_forward) exceeds MOE_NOALLOC_SCRATCH_BYTES, before
  * anything is enqueued; MOE_ERR_HIP when the scratch's address cannot be
  * found or a launch fails. Every call on a device shares that device's
  * scratch, which keeps the last call's contents: calls that may overlap on
@@ -333,6 +334,87 @@ moe_status moe_plan_set_tp_exchange(moe_plan* plan, const moe_tp_exchange* x);
 moe_status moe_forward_noalloc(moe_plan* plan, int64_t M, const void* x, const float* logits,
                                const void* w13, const void* s13, const void* w2, const void* s2,
                                void* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators beside the routed-MoE call. They share its conventions (caller's
+ * buffers, validation before anything is enqueued, no allocation, no
+ * synchronization, one stream in order, capturable).
+ *
+ * Element types of activations, router weights and outputs. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
+
+/* Router projection: the fp32 logits that moe_forward takes, from the hidden
+ * states:  logits[m][e] = sum_h x[m][h] * w[e][h],  summed exactly enough
+ * (float64 up to 16 tokens) and rounded to fp32.
+ *   w  [E, H]  bf16 or fp32 (w_type), kept by the handle, not copied: it must
+ *              stay valid while the handle is used
+ *   x  [M, H]  bf16 or fp16 (x_type), rows ldx elements apart (ldx >= H, a
+ *              multiple of 8)
+ *   logits  fp32 [M, E], dense
+ * max_M bounds a call's M. MOE_ERR_INVALID_ARG for null or misaligned
+ * pointers (16 bytes), non-positive sizes, unknown types, M > max_M, a bad
+ * ldx, or logits overlapping an input; MOE_ERR_UNSUPPORTED for E > 1024, H not
+ * a multiple of 8 or above 65536, max_M > 2^20; MOE_ERR_DEVICE for pointers
+ * not on one gfx950 device. M = 0 enqueues nothing. A handle holds no mutable
+ * state: calls on several streams may overlap. */
+typedef struct moe_router moe_router;
+moe_status moe_router_create(int64_t E, int64_t H, int x_type, const void* w, int w_type, int64_t max_M,
+                             moe_router** out);
+void moe_router_destroy(moe_router* router);
+moe_status moe_router_forward(const moe_router* router, int64_t M, const void* x, int64_t ldx, float* logits,
+                              void* stream);
+
+/* Linear layer on MXFP4 weights (the dense layers around the experts, in the
+ * experts' format), activations in 16 bits, for one row or many:
+ *   y[m][n] = sum_k x[m][k] * E2M1(w[n][k]) * 2^(s[n][k/32] - 127)
+ *             (+ bias[n]) (+ residual[m][n])
+ * The products are exact, summed in fp32, y rounded once.
+ *
+ * moe_pack_linear rewrites row-major weights once, at load time: w u8 [N, K/2]
+ * (element 2i in the low nibble) and s u8 [N, K/32] into w_packed and s_packed
+ * of moe_linear_pack_bytes bytes:
+ *   w_packed [ceil(N/16)][ceil(K/128)][4 g][16 r][4 j] dwords: the 8 codes of
+ *     K elements 128 ks + 32 j + 8 g .. + 7 of row 16 rb + r, zero past N or K
+ *   s_packed [ceil(N/16)][ceil(K/128)][16 r][4 j]: the scale of MX block
+ *     4 ks + j of row 16 rb + r, 127 past N or K
+ * A scale byte of 255 (NaN) makes its row's results NaN.
+ * Errors as moe_pack_w13; shapes: N 1 .. 2^24, K a multiple of 32 up to 65536,
+ * else MOE_ERR_UNSUPPORTED.
+ *
+ * moe_linear_create keeps (does not copy) w_packed, s_packed and bias ([N] of
+ * x's type, or NULL); x_type is MOE_BF16 or MOE_FP16, max_M <= 2^20 bounds a
+ * call's rows. moe_linear_forward: x [M, K], rows ldx elements apart (ldx >=
+ * K, a multiple of 8; x 16-byte aligned); y [M, N], rows ldy >= N apart, of
+ * x's type or MOE_FP32 (y_type); residual [M, N] of y's type, rows ldr >= N
+ * apart, or NULL. residual may be y itself (same pointer and stride: added in
+ * place); any other overlap of y with an input is MOE_ERR_INVALID_ARG.
+ * M = 0 enqueues nothing. Calls on several streams may overlap. */
+typedef struct moe_linear moe_linear;
+moe_status moe_linear_pack_bytes(int64_t N, int64_t K, size_t* w_bytes, size_t* s_bytes);
+moe_status moe_pack_linear(const void* w, const void* s, int64_t N, int64_t K, void* w_packed, void* s_packed,
+                           void* stream);
+moe_status moe_linear_create(int64_t N, int64_t K, int x_type, const void* w_packed, const void* s_packed,
+                             const void* bias, int64_t max_M, moe_linear** out);
+void moe_linear_destroy(moe_linear* linear);
+moe_status moe_linear_forward(const moe_linear* linear, int64_t M, const void* x, int64_t ldx, const void* residual,
+                              int64_t ldr, void* y, int64_t ldy, int y_type, void* stream);
+
+/* The whole MoE layer of up to 16 tokens from their hidden states, with the
+ * activations kept in 16 bits (moe_forward takes logits and quantizes x and
+ * mid). On the weights moe_forward reads (w13/s13 packed by moe_pack_w13,
+ * w2/s2 row-major), so a decode step and a prefill share one copy:
+ *   logits = fl32(x router^T), routed as in moe_forward (steps 1 of the call)
+ *   h      = SiLU(x Wg^T) * (x Wu^T)  in fp32 per (token, slot)
+ *   out    = bf16(sum over slots of weight * h W2^T)
+ * `router` has the plan's E and H, bf16 x and the plan's device. x bf16
+ * [M, H], out bf16 [M, H] fully overwritten, no overlap with an input or the
+ * workspace. Leaves topk_ids and topk_w of moe_plan_layout; the other regions
+ * are not written. MOE_ERR_UNSUPPORTED for M > 16, H > 8192, a plan with a
+ * shared expert or shared slot, the tensor-parallel exchange, the MXFP4 mid or
+ * a declared layout other than MOE_LAYOUT_W13_PACKED; other errors as
+ * moe_forward. Weights must be finite (scale bytes up to 252). */
+moe_status moe_layer_forward(moe_plan* plan, const moe_router* router, int64_t M, const void* x, const void* w13,
+                             const void* s13, const void* w2, const void* s2, void* out, void* stream);
 
 /* Profiling aid: when `events` is non-NULL, moe_forward brackets stage i
  * with events[2i] (start of its first kernel) and events[2i+1] (end of its

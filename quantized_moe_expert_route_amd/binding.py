@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "lib
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE, MOE_ERR_HIP = range(6)
 MID_E4M3, MID_MXFP4 = 0, 1  # moe_mid_format
+BF16, FP16, FP32 = range(3)  # moe_dtype
 LAYOUT_W13_PACKED, LAYOUT_W2_PACKED = 1, 2  # moe_weight_layout flags
 
 
@@ -109,6 +110,24 @@ def lib() -> ctypes.CDLL:
     L.moe_plan_set_mid_format.argtypes = [vp, ctypes.c_int]
     L.moe_plan_set_weight_layout.restype = st
     L.moe_plan_set_weight_layout.argtypes = [vp, ctypes.c_uint]
+    L.moe_router_create.restype = st
+    L.moe_router_create.argtypes = [i64, i64, ctypes.c_int, vp, ctypes.c_int, i64, ctypes.POINTER(vp)]
+    L.moe_router_destroy.restype = None
+    L.moe_router_destroy.argtypes = [vp]
+    L.moe_router_forward.restype = st
+    L.moe_router_forward.argtypes = [vp, i64, vp, i64, vp, vp]
+    L.moe_linear_pack_bytes.restype = st
+    L.moe_linear_pack_bytes.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)]
+    L.moe_pack_linear.restype = st
+    L.moe_pack_linear.argtypes = [vp, vp, i64, i64, vp, vp, vp]
+    L.moe_linear_create.restype = st
+    L.moe_linear_create.argtypes = [i64, i64, ctypes.c_int, vp, vp, vp, i64, ctypes.POINTER(vp)]
+    L.moe_linear_destroy.restype = None
+    L.moe_linear_destroy.argtypes = [vp]
+    L.moe_linear_forward.restype = st
+    L.moe_linear_forward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, ctypes.c_int, vp]
+    L.moe_layer_forward.restype = st
+    L.moe_layer_forward.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, vp, vp]
     L.moe_plan_set_tp_exchange.restype = st
     L.moe_plan_set_tp_exchange.argtypes = [vp, ctypes.POINTER(moe_tp_exchange)]
     _lib = L
@@ -180,6 +199,167 @@ def pack_w2(w2, s2, out=None, stream=None):
     if st != MOE_OK:
         raise MoeError(st, "moe_pack_w2")
     return wp, sp
+
+
+class _Handle:
+    """A library handle on one device, destroyed with the object."""
+
+    _h = None
+    _destroy = ""
+
+    def _check(self, name, t, dtype, rows, cols, dense=False):
+        """The library sees bare pointers: a tensor on another device, of
+        another type, smaller than the call, or with strided columns is
+        refused here."""
+        import torch
+
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the weights on {self.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols:
+            raise ValueError(f"{name} is {tuple(t.shape)}, expected at least [{rows}, {cols}]")
+        if (t.stride(1) != 1 and cols != 1) or (rows > 1 and t.stride(0) < cols):
+            raise ValueError(f"{name} has strides {t.stride()}: columns must be adjacent, rows apart")
+        if dense and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+    def _rows(self, x, M):
+        M = x.shape[0] if M is None else int(M)
+        if not 0 <= M <= self.max_M:
+            raise ValueError(f"M = {M} outside [0, {self.max_M}]")
+        return M
+
+    def _stream(self, stream):
+        import torch
+
+        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+
+    def close(self):
+        if self._h:
+            getattr(lib(), self._destroy)(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _row_stride(t, rows, cols):
+    """Elements between rows; a single row's stride says nothing."""
+    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
+
+
+def _dtype_code(dtype):
+    import torch
+
+    code = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}.get(dtype)
+    if code is None:
+        raise ValueError(f"dtype {dtype} is none of bfloat16, float16, float32")
+    return code
+
+
+class Router(_Handle):
+    """Router projection on weights w [E, H] (bf16 or fp32): the fp32 logits
+    moe_forward takes, and the routing of Plan.layer."""
+
+    _destroy = "moe_router_destroy"
+
+    def __init__(self, w, x_dtype=None, max_M: int = 1 << 20):
+        import torch
+
+        if not isinstance(w, torch.Tensor) or w.dim() != 2 or not w.is_contiguous():
+            raise ValueError("w must be a contiguous [E, H] tensor")
+        self.x_dtype = torch.bfloat16 if x_dtype is None else x_dtype
+        self.device, self.max_M, self.w = w.device, int(max_M), w  # the library keeps w's pointer
+        self.E, self.H = w.shape
+        h = ctypes.c_void_p()
+        st = lib().moe_router_create(self.E, self.H, _dtype_code(self.x_dtype), _ptr(w), _dtype_code(w.dtype),
+                                     self.max_M, ctypes.byref(h))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_router_create")
+        self._h = h
+
+    def forward(self, x, logits, M: Optional[int] = None, stream=None):
+        """logits[:M] = x[:M] w^T, enqueued on `stream` (default: the current
+        stream of the weights' device)."""
+        import torch
+
+        M = self._rows(x, M)
+        self._check("x", x, self.x_dtype, M, self.H)
+        self._check("logits", logits, torch.float32, M, self.E, dense=True)
+        st = lib().moe_router_forward(self._h, M, _ptr(x), _row_stride(x, M, self.H), _ptr(logits),
+                                      self._stream(stream))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_router_forward")
+        return logits
+
+
+class Linear(_Handle):
+    """Linear layer on MXFP4 weights: row-major codes w [N, K/2] and E8M0
+    scales s [N, K/32] (uint8), packed here into buffers this object keeps (w
+    and s are free afterwards), with an optional bias [N] of x's type."""
+
+    _destroy = "moe_linear_destroy"
+
+    def __init__(self, w, s, bias=None, x_dtype=None, max_M: int = 1 << 20):
+        import torch
+
+        u8 = torch.uint8
+        if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.dtype != u8 or not w.is_contiguous():
+            raise ValueError("w must be a contiguous uint8 [N, K/2] tensor")
+        self.N, self.K = w.shape[0], 2 * w.shape[1]
+        if (not isinstance(s, torch.Tensor) or s.dtype != u8 or not s.is_contiguous() or s.device != w.device
+                or tuple(s.shape) != (self.N, w.shape[1] // 16) or w.shape[1] % 16):
+            raise ValueError("s must be a contiguous uint8 [N, K/32] tensor beside w")
+        self.x_dtype = torch.bfloat16 if x_dtype is None else x_dtype
+        self.device, self.max_M = w.device, int(max_M)
+        if bias is not None and (bias.dtype != self.x_dtype or tuple(bias.shape) != (self.N,)
+                                 or bias.device != w.device or not bias.is_contiguous()):
+            raise ValueError("bias must be a contiguous [N] tensor of x's type beside w")
+        nw, ns = ctypes.c_size_t(0), ctypes.c_size_t(0)
+        st = lib().moe_linear_pack_bytes(self.N, self.K, ctypes.byref(nw), ctypes.byref(ns))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_linear_pack_bytes")
+        self.w_packed = torch.empty(nw.value, dtype=u8, device=w.device)
+        self.s_packed = torch.empty(ns.value, dtype=u8, device=w.device)
+        self.bias = bias
+        here = torch.cuda.current_stream(self.device)
+        st = lib().moe_pack_linear(_ptr(w), _ptr(s), self.N, self.K, _ptr(self.w_packed), _ptr(self.s_packed),
+                                   here.cuda_stream)
+        if st != MOE_OK:
+            raise MoeError(st, "moe_pack_linear")
+        here.synchronize()  # load time: calls on any stream find the weights packed
+        h = ctypes.c_void_p()
+        st = lib().moe_linear_create(self.N, self.K, _dtype_code(self.x_dtype), _ptr(self.w_packed),
+                                     _ptr(self.s_packed), None if bias is None else _ptr(bias), self.max_M,
+                                     ctypes.byref(h))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_linear_create")
+        self._h = h
+
+    def forward(self, x, out, residual=None, M: Optional[int] = None, stream=None):
+        """out[:M] = x[:M] w^T (+ bias) (+ residual[:M]); out is of x's type or
+        float32, residual of out's; residual may be out itself."""
+        import torch
+
+        M = self._rows(x, M)
+        self._check("x", x, self.x_dtype, M, self.K)
+        y_dtype = torch.float32 if isinstance(out, torch.Tensor) and out.dtype == torch.float32 else self.x_dtype
+        self._check("out", out, y_dtype, M, self.N)
+        if residual is not None:
+            self._check("residual", residual, y_dtype, M, self.N)
+        st = lib().moe_linear_forward(
+            self._h, M, _ptr(x), _row_stride(x, M, self.K), None if residual is None else _ptr(residual),
+            0 if residual is None else max(residual.stride(0), self.N), _ptr(out), max(out.stride(0), self.N),
+            _dtype_code(y_dtype), self._stream(stream))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_linear_forward")
+        return out
 
 
 class Plan:
@@ -368,6 +548,31 @@ class Plan:
                                        _ptr(s2), _ptr(out), _stream(stream))
         if st != MOE_OK:
             raise MoeError(st, "moe_forward_noalloc")
+        return out
+
+    def layer(self, x, router, w13, s13, w2, s2, out, M: Optional[int] = None, stream=None):
+        """The whole layer of up to 16 tokens from their hidden states x
+        (moe_layer_forward): `router` is a Router on [E, H] weights, the expert
+        weights are those of forward (E4M3 mid). Leaves topk_ids and topk_w."""
+        import torch
+
+        if not isinstance(router, Router):
+            raise TypeError("router must be a Router")
+        M = x.shape[0] if M is None else int(M)
+        s = self.shape
+        if not 0 <= M <= s.M:
+            raise ValueError(f"M = {M} outside [0, {s.M}] (the plan's shape)")
+        bf16, u8 = (torch.int16, torch.bfloat16), (torch.uint8,)
+        self._tensor("x", x, bf16, rows=M, cols=s.H)
+        self._tensor("out", out, bf16, rows=M, cols=s.H)
+        self._tensor("w13", w13, u8, numel=s.E * s.I * s.H)
+        self._tensor("s13", s13, u8, numel=s.E * s.I * s.H // 16)
+        self._tensor("w2", w2, u8, numel=s.E * s.H * s.I // 2)
+        self._tensor("s2", s2, u8, numel=s.E * s.H * s.I // 32)
+        st = lib().moe_layer_forward(self._h, router._h, M, _ptr(x), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2),
+                                     _ptr(out), router._stream(stream))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_layer_forward")
         return out
 
     def stage_launches(self, M: int):

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <new>
 
+#include "api_util.h"
 #include "internal.h"
 
 #include <climits>
@@ -16,8 +17,6 @@ namespace {
 
 const char* kStageNames[] = {"route", "align", "gate_up", "act_quant", "shared", "down", "combine"};
 constexpr int kStages = 7;
-
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 moe_status check_shape(const moe_shape* s) {
   if (!s) return MOE_ERR_INVALID_ARG;
@@ -37,6 +36,7 @@ struct Layout {
   moe_ws_layout L;
   Internal X;
   int64_t t16, tb, tg, words;
+  size_t call_bytes;
 };
 
 Layout make_layout(const moe_shape& s) {
@@ -89,40 +89,13 @@ Layout make_layout(const moe_shape& s) {
     r.L.sh_y = take(4 * M * H);
     r.X.sh_part = take(8 * std::min<size_t>(M, kSmallM) * (H / 128) * 2 * Is);
   }
+  r.call_bytes = align256(off);
+  const size_t Ml = std::min<size_t>(M, kSmallM);
+  r.X.layer_logits = take(4 * Ml * E);
+  r.X.layer_g = take(4 * Ml * k * I);
   r.L.total_bytes = align256(off);
   return r;
 }
-
-// Device that owns a device pointer, or -1.
-int ptr_device(const void* p) {
-  hipPointerAttribute_t a;
-  if (hipPointerGetAttributes(&a, p) != hipSuccess) {
-    (void)hipGetLastError();
-    return -1;
-  }
-  if (a.type != hipMemoryTypeDevice && a.type != hipMemoryTypeManaged) return -1;
-  return a.device;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) { ok = false; return; }
-    if (prev != dev && hipSetDevice(dev) != hipSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
 
 // Checks of a call shared by moe_forward and moe_forward_noalloc (the
 // workspace, `ws` of `ws_bytes` or none, is the caller's concern).
@@ -316,6 +289,7 @@ moe_status moe_plan_create(const moe_shape* shape, moe_plan** out) {
   Layout lay = make_layout(*shape);
   p->L = lay.L;
   p->X = lay.X;
+  p->call_bytes = lay.call_bytes;
   p->t16_max = lay.t16;
   p->words = lay.words;
   p->tb_max = lay.tb;
@@ -523,7 +497,7 @@ moe_status moe_forward_noalloc(moe_plan* plan, int64_t M, const void* x, const f
                                const void* s13, const void* w2, const void* s2, void* out, void* stream) {
   if (!plan) return MOE_ERR_INVALID_ARG;
   if (M < 0 || M > plan->s.M) return MOE_ERR_INVALID_ARG;
-  if (plan->L.total_bytes > (size_t)MOE_NOALLOC_SCRATCH_BYTES) return MOE_ERR_UNSUPPORTED;
+  if (plan->call_bytes > (size_t)MOE_NOALLOC_SCRATCH_BYTES) return MOE_ERR_UNSUPPORTED;
   const void* ptrs[7] = {x, logits, w13, s13, w2, s2, out};
   moe_status st = check_call(plan, M, ptrs, nullptr, 0);
   if (st != MOE_OK || M == 0) return st;

@@ -30,6 +30,9 @@ struct Internal {
   size_t sh_h;     // fp32 [M, Is]
   size_t sh_part;  // float64 [min(M, kSmallM), H/128, 2 Is]: block partials of the fused shared gate/up
   size_t sync_begin, sync_bytes;  // region zeroed once when the workspace is bound
+  // of moe_layer_forward, behind moe_forward's regions
+  size_t layer_logits;  // fp32 [min(M, kSmallM), E]
+  size_t layer_g;       // bf16 [2, n, I]: weighted h of its up to kSmallM tokens, value and remainder
 };
 
 }  // namespace qmoe
@@ -44,6 +47,7 @@ struct moe_plan {
   int64_t tb_max;  // upper bound on tiles of kBigRows sorted rows
   moe_ws_layout L;
   qmoe::Internal X;
+  size_t call_bytes; // workspace of moe_forward alone (the regions of moe_layer_forward follow)
   uint8_t* ws;
   size_t ws_bytes;
   const void* ws13;   // the shared expert's gate/up and down weights as digit rows (moe_plan_set_shared)

@@ -1,0 +1,185 @@
+// Linear layer on MXFP4 weights with 16-bit activations:
+//   y[m][n] = sum_k x[m][k] E2M1(w[n][k]) 2^(s[n][k/32] - 127) (+ bias[n]) (+ residual[m][n])
+// products exact, sums in binary32, one rounding to y's type.
+//
+// Weights are packed once (moe_pack_linear): a K-step of 128 of a block of 16
+// rows is 1 KB contiguous, lane 16 g + r holding row r, dword j the 8 codes
+// of K 32 j + 8 g .. + 7, so that one MFMA (K = 32) covers exactly the MX
+// block j of every row and the activations' operand of a lane is 16
+// contiguous bytes, 64 over the four lane groups:
+//   wp [ceil(N/16)][ceil(K/128)][4 g][16 r][4 j] dwords, codes past N or K zero
+//   sp [ceil(N/16)][ceil(K/128)][16 r][4 j] bytes, past N or K 127 (2^0)
+#include <algorithm>
+
+#include "internal.h"
+#include "mxfp4.h"
+#include "ops.h"
+
+namespace qmoe {
+
+// ----------------------------------------------------------------- packing
+__global__ __launch_bounds__(256) void pack_linear_kernel(const uint8_t* __restrict__ w, uint32_t* __restrict__ wp,
+                                                          int64_t dwords, int nks, int64_t N, int64_t K) {
+  for (int64_t o = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; o < dwords; o += (int64_t)gridDim.x * blockDim.x) {
+    const int j = (int)(o & 3), r = (int)((o >> 2) & 15), g = (int)((o >> 6) & 3);
+    const int64_t rest = o >> 8;
+    const int64_t n = rest / nks * 16 + r, k = rest % nks * 128 + 32 * j + 8 * g;
+    wp[o] = n < N && k < K ? *reinterpret_cast<const uint32_t*>(w + n * (K / 2) + k / 2) : 0u;
+  }
+}
+
+__global__ __launch_bounds__(256) void pack_linear_scale_kernel(const uint8_t* __restrict__ s,
+                                                                uint8_t* __restrict__ sp, int64_t bytes, int nks,
+                                                                int64_t N, int64_t K) {
+  for (int64_t o = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; o < bytes; o += (int64_t)gridDim.x * blockDim.x) {
+    const int j = (int)(o & 3), r = (int)((o >> 2) & 15);
+    const int64_t rest = o >> 6;
+    const int64_t n = rest / nks * 16 + r, b = rest % nks * 4 + j;
+    sp[o] = n < N && b < K / 32 ? s[n * (K / 32) + b] : (uint8_t)127;
+  }
+}
+
+hipError_t launch_pack_linear(const void* w, const void* s, int64_t N, int64_t K, void* wp, void* sp,
+                              hipStream_t stream) {
+  const int64_t nrb = (N + 15) / 16, nks = (K + 127) / 128;
+  const int64_t dwords = nrb * nks * 256, bytes = nrb * nks * 64;
+  hipError_t e = launch_k(pack_linear_kernel, dim3((unsigned)std::min<int64_t>((dwords + 255) / 256, 1 << 16)),
+                          dim3(256), 0, stream, Ev{}, (const uint8_t*)w, (uint32_t*)wp, dwords, (int)nks, N, K);
+  if (e == hipSuccess)
+    e = launch_k(pack_linear_scale_kernel, dim3((unsigned)std::min<int64_t>((bytes + 255) / 256, 1 << 16)), dim3(256),
+                 0, stream, Ev{}, (const uint8_t*)s, (uint8_t*)sp, bytes, (int)nks, N, K);
+  return e;
+}
+
+// ----------------------------------------------------------------- epilogue
+// Four consecutive columns n .. n + 3 of row m.
+__device__ __forceinline__ void store4(const LinearArgs& a, int64_t m, int64_t n, v4f v) {
+  const bool f16 = a.x_type == MOE_FP16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n + i >= a.N) break;
+    float t = v[i];
+    if (a.bias) {
+      const uint16_t b = reinterpret_cast<const uint16_t*>(a.bias)[n + i];
+      t += f16 ? fp16_value(b) : bf16_value(b);
+    }
+    if (a.y_type == MOE_FP32) {
+      if (a.residual) t += reinterpret_cast<const float*>(a.residual)[m * a.ldr + n + i];
+      reinterpret_cast<float*>(a.y)[m * a.ldy + n + i] = t;
+    } else {
+      if (a.residual) {
+        const uint16_t b = reinterpret_cast<const uint16_t*>(a.residual)[m * a.ldr + n + i];
+        t += f16 ? fp16_value(b) : bf16_value(b);
+      }
+      reinterpret_cast<uint16_t*>(a.y)[m * a.ldy + n + i] = f16 ? fp16_bits(t) : bf16_bits(t);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- few rows
+// A workgroup of W waves computes 16 columns of y for up to 16 rows of x at a
+// time. The waves split K: wave w owns S K-steps of 128 in every segment of
+// W S steps, and keeps its fragments of x in registers over all the tiles of
+// the workgroup while one segment covers K. The W partial sums are added in
+// wave order through LDS.
+template <bool F16, int W, int S>
+__global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a) {
+  __shared__ v4f red[2][W][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+  const int K = (int)a.K, nks = (K + 127) / 128, nseg = (nks + W * S - 1) / (W * S);
+  const int64_t m0 = (int64_t)blockIdx.y * 16;
+  const bool row = m0 + r < a.M;
+  const uint16_t* xr = reinterpret_cast<const uint16_t*>(a.x) + (row ? m0 + r : 0) * a.ldx;
+  const int ntiles = (int)((a.N + 15) / 16);
+
+  uint4 xf[S][4], q[S], nq[S];
+  uint4 sc[S], nsc[S];  // bf16: .x is the row's four scales; fp16: rows 4g..4g+3
+  auto load_x = [&](int seg) {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = 128 * ((seg * W + wave) * S + s) + 32 * j + 8 * g;
+        xf[s][j] = row && k < K ? ld16(xr + k) : make_uint4(0, 0, 0, 0);
+      }
+  };
+  auto load_w = [&](int tile, int seg, uint4(&qq)[S], uint4(&ss)[S]) {
+    const size_t base = (size_t)tile * nks;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      // past the last step: that step again, with x zero
+      const size_t p = base + min((seg * W + wave) * S + s, nks - 1);
+      qq[s] = ld16(a.wp + p * 1024 + 16 * lane);
+      if (F16) ss[s] = ld16(a.sp + p * 64 + 16 * g);
+      else ss[s].x = ld4(a.sp + p * 64 + 4 * r);
+    }
+  };
+
+  int tile = blockIdx.x, seg = 0, buf = 0;
+  if (tile >= ntiles) return;
+  load_w(tile, 0, nq, nsc);
+  load_x(0);
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  while (tile < ntiles) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) { q[s] = nq[s]; sc[s] = nsc[s]; }
+    int ntile = tile, nsg = seg + 1;
+    if (nsg == nseg) { nsg = 0; ntile += gridDim.x; }
+    if (ntile < ntiles) load_w(ntile, nsg, nq, nsc);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      // a step past the last one takes no part (its codes could meet a scale
+      // that overflows, and zero times that is not zero)
+      const bool in = (seg * W + wave) * S + s < nks;
+      const uint32_t d[4] = {in ? q[s].x : 0u, in ? q[s].y : 0u, in ? q[s].z : 0u, in ? q[s].w : 0u};
+      const uint32_t rs[4] = {sc[s].x, sc[s].y, sc[s].z, sc[s].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (F16) {
+          const v4f z = {0.f, 0.f, 0.f, 0.f};
+          const v4f p = mfma_f16(fp4x8_f16(d[j]), __builtin_bit_cast(v8h, xf[s][j]), z);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] += p[i] * e8m0_value((rs[i] >> (8 * j)) & 255u);
+        } else {
+          acc = mfma_bf16(fp4x8_bf16(d[j], e8m0_value((sc[s].x >> (8 * j)) & 255u)),
+                          __builtin_bit_cast(v8s, xf[s][j]), acc);
+        }
+      }
+    }
+    if (nsg == 0) {
+      red[buf][wave][lane] = acc;
+      acc = v4f{0.f, 0.f, 0.f, 0.f};
+      barrier_lds();
+      // lane holds rows 4 g .. 4 g + 3 (columns of y) of column r (row of x)
+      if (wave == buf && row) {
+        v4f v = red[buf][0][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += red[buf][w][lane];
+        store4(a, m0 + r, (int64_t)tile * 16 + 4 * g, v);
+      }
+      buf ^= 1;
+    }
+    if (nseg > 1 && ntile < ntiles) load_x(nsg);
+    tile = ntile;
+    seg = nsg;
+  }
+}
+
+template <bool F16, int S>
+static hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t stream) {
+  const int64_t tiles = (a.N + 15) / 16;
+  const dim3 grid((unsigned)std::min<int64_t>(tiles, 2 * cus), (unsigned)((a.M + 15) / 16));
+  return launch_k(linear_rows_kernel<F16, 8, S>, grid, dim3(512), 0, stream, Ev{}, a);
+}
+
+hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream) {
+  const int64_t nks = (a.K + 127) / 128;
+  const bool f16 = a.x_type == MOE_FP16;
+  if (nks <= 8) return f16 ? launch_rows<true, 1>(a, cus, stream) : launch_rows<false, 1>(a, cus, stream);
+  if (nks <= 16) return f16 ? launch_rows<true, 2>(a, cus, stream) : launch_rows<false, 2>(a, cus, stream);
+  if (nks <= 32) return f16 ? launch_rows<true, 4>(a, cus, stream) : launch_rows<false, 4>(a, cus, stream);
+  return f16 ? launch_rows<true, 6>(a, cus, stream) : launch_rows<false, 6>(a, cus, stream);
+}
+
+}  // namespace qmoe

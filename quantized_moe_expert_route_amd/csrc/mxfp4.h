@@ -1,0 +1,52 @@
+// Fragments of 16-bit activations x MXFP4 weights on the 16x16x32 MFMA,
+// shared by the linear layer and the few-token MoE layer.
+//
+// A wave's weight piece is 16 rows x 128 K: lane 16 g + r holds 16 bytes (32
+// E2M1 codes) of row r, four dwords of 8 codes, each one MFMA's A operand.
+// bf16 activations take the weights as bf16 with the block's scale folded in
+// by the conversion (E2M1 x 2^e has two significant bits: exact). fp16
+// activations take the bare E2M1 values (exact in fp16, where E8M0's range
+// does not fit) and the scale goes to the MFMA's sums. Products of a bf16
+// (8 significant bits) or fp16 (11) with E2M1 are exact; sums are binary32.
+#pragma once
+
+#include "common.h"
+
+namespace qmoe {
+
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// 8 E2M1 codes (a dword, first code in the low nibble) x 2^e -> 8 bf16.
+__device__ __forceinline__ v8s fp4x8_bf16(uint32_t q, float scale) {
+  return as_v8s(cvt_fp4x2_bf16<0>(q, scale), cvt_fp4x2_bf16<1>(q, scale), cvt_fp4x2_bf16<2>(q, scale),
+                cvt_fp4x2_bf16<3>(q, scale));
+}
+
+template <int SEL>
+__device__ __forceinline__ uint32_t cvt_fp4x2_f16(uint32_t src) {
+  const f16x2 r = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(src, 1.0f, SEL);
+  return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ v8h fp4x8_f16(uint32_t q) {
+  const uint4 v = make_uint4(cvt_fp4x2_f16<0>(q), cvt_fp4x2_f16<1>(q), cvt_fp4x2_f16<2>(q), cvt_fp4x2_f16<3>(q));
+  return __builtin_bit_cast(v8h, v);
+}
+
+__device__ __forceinline__ v4f mfma_f16(v8h a, v8h b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// E8M0 scale byte -> binary32: 2^(s - 127), NaN for 255 (the format's NaN).
+__device__ __forceinline__ float e8m0_value(uint32_t s) {
+  const uint32_t u = s << 23;
+  return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : u);
+}
+
+// binary32 -> bf16 / fp16 bits, nearest even.
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ uint16_t fp16_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+__device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ float fp16_value(uint16_t b) { return (float)__builtin_bit_cast(_Float16, b); }
+
+}  // namespace qmoe

@@ -1,0 +1,259 @@
+"""MXFP4 linear layer on the GPU against its 64-bit definition: bitwise on
+inputs whose sums are representable, within the arithmetic's bound on random
+ones."""
+
+import numpy as np
+import pytest
+
+import ops_ref as R
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": "bfloat16", "fp16": "float16", "fp32": "float32"}
+
+
+def _dt(name):
+    import torch
+
+    return getattr(torch, DT[name])
+
+
+def _case(rng, M, N, K, xt, yt, bias=False, residual=False, integers=False):
+    import torch
+
+    if integers:
+        # multiples of 1/2 of magnitude <= 3 * 6 * K: binary32 sums are exact in any order
+        x = torch.from_numpy(rng.integers(-3, 4, (M, K)).astype(np.float32))
+        codes = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+        scales = rng.integers(126, 129, (N, K // 32), dtype=np.uint8)
+        extra = lambda *s: torch.from_numpy(rng.integers(-9, 10, s).astype(np.float32))
+    else:
+        x = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32))
+        codes, scales = R.random_weights(rng, N, K)
+        extra = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32))
+    return dict(x=x.to(_dt(xt)), codes=codes, scales=scales, bias=extra(N).to(_dt(xt)) if bias else None,
+                residual=extra(M, N).to(_dt(yt)) if residual else None, xt=xt, yt=yt)
+
+
+def _f64(t):
+    return None if t is None else t.double().numpy()
+
+
+def _linear(d, max_M=1 << 20):
+    import torch
+    from quantized_moe_expert_route_amd.binding import Linear
+
+    cu = lambda a: None if a is None else (torch.from_numpy(a) if isinstance(a, np.ndarray) else a).cuda()
+    return Linear(cu(d["codes"]), cu(d["scales"]), bias=cu(d["bias"]), x_dtype=_dt(d["xt"]), max_M=max_M)
+
+
+def _run(d, lin=None):
+    import torch
+
+    lin = lin or _linear(d)
+    out = torch.full((d["x"].shape[0], lin.N), float("nan"), dtype=_dt(d["yt"]), device="cuda")
+    res = None if d["residual"] is None else d["residual"].cuda()
+    lin.forward(d["x"].cuda(), out, residual=res)
+    torch.cuda.synchronize()
+    return out.cpu()
+
+
+def _expect(d):
+    return R.linear(_f64(d["x"]), d["codes"], d["scales"], _f64(d["bias"]), _f64(d["residual"]))
+
+
+def _check(got, d):
+    y, mag = _expect(d)
+    err = np.abs(_f64(got) - y)
+    tol = (R.sum_error(d["x"].shape[1]) * mag) * (1 + R.half_step(d["yt"])) + R.half_step(d["yt"]) * np.abs(y)
+    tol += 2.0 ** -25 if d["yt"] == "fp16" else 0.0  # half a subnormal step
+    assert not np.isnan(_f64(got)).any()
+    bad = np.argwhere(err > tol)
+    assert len(bad) == 0, (len(bad), bad[:4].tolist(), float((err / tol).max()))
+
+
+SIZES = [(1, 16, 32), (1, 1, 32), (2, 17, 160), (3, 5, 1024), (16, 64, 2048), (15, 33, 1056), (7, 130, 6144),
+         (16, 40, 8192), (1, 24, 8224), (5, 48, 16384), (16, 16, 65536), (17, 50, 512), (31, 96, 4128),
+         (33, 257, 1440), (64, 48, 2048), (65, 300, 672), (130, 70, 96), (257, 520, 1280), (300, 1543, 480)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp16", "fp32")])
+def test_exact_sums_are_bitwise(M, N, K, xt, yt):
+    rng = np.random.default_rng([M, N, K])
+    d = _case(rng, M, N, K, xt, yt, bias=(M + N) % 2 == 0, residual=(N + K // 32) % 2 == 0, integers=True)
+    if yt == "fp16":  # keep the sums inside fp16's range
+        d["scales"] -= np.uint8(6)
+    y, mag = _expect(d)
+    assert mag.max() < 2.0 ** 22
+    import torch
+
+    want = torch.from_numpy(y).float().to(_dt(yt))  # y is exact in binary32: one rounding
+    assert torch.equal(_run(d), want)
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("xt,yt,bias,residual", [("bf16", "bf16", True, True), ("fp16", "fp32", False, True),
+                                                ("bf16", "fp32", True, False), ("fp16", "fp16", False, False)])
+def test_random_within_the_bound(M, N, K, xt, yt, bias, residual):
+    rng = np.random.default_rng([M, N, K, 1])
+    d = _case(rng, M, N, K, xt, yt, bias, residual)
+    _check(_run(d), d)
+
+
+def test_large_weights_and_many_tiles():
+    """More tiles than workgroups, at the widths the repository's workloads have."""
+    rng = np.random.default_rng(5)
+    for M, N in ((4, 20000), (16, 9000), (100, 12300)):
+        d = _case(rng, M, N, 6144 if M < 100 else 512, "bf16", "bf16")
+        _check(_run(d), d)
+
+
+def test_one_handle_many_row_counts():
+    """One handle serves every row count up to its bound; rows past M are left as they were."""
+    import torch
+
+    rng = np.random.default_rng(7)
+    d = _case(rng, 300, 200, 1440, "bf16", "bf16")
+    lin = _linear(d, max_M=300)
+    y, mag = _expect(d)
+    x = d["x"].cuda()
+    for M in (0, 1, 2, 16, 17, 32, 33, 48, 64, 65, 127, 128, 129, 255, 300):
+        out = torch.full((300, 200), 7.0, dtype=torch.bfloat16, device="cuda")
+        lin.forward(x, out, M=M)
+        got = _f64(out.cpu())
+        assert np.all(got[M:] == 7.0)
+        tol = R.sum_error(1440) * mag[:M] * 1.01 + R.half_step("bf16") * np.abs(y[:M])
+        assert np.all(np.abs(got[:M] - y[:M]) <= tol)
+    with pytest.raises(ValueError):
+        lin.forward(torch.zeros(301, 1440, dtype=torch.bfloat16, device="cuda"), out)
+
+
+@pytest.mark.parametrize("M", [1, 5, 40, 200])
+def test_strided_rows_and_in_place_residual(M):
+    import torch
+
+    rng = np.random.default_rng(M)
+    N, K = 83, 352
+    for xt, yt in (("bf16", "bf16"), ("fp16", "fp32")):
+        d = _case(rng, M, N, K, xt, yt, residual=True)
+        y, mag = _expect(d)
+        xw = torch.full((M, K + 40), float("nan"), dtype=_dt(xt), device="cuda")
+        xw[:, 8:K + 8] = d["x"].cuda()
+        yw = torch.full((M, N + 13), 3.0, dtype=_dt(yt), device="cuda")
+        yw[:, 5:N + 5] = d["residual"].cuda()
+        view = yw[:, 5:N + 5]
+        _linear(d).forward(xw[:, 8:K + 8], view, residual=view)
+        got = yw.cpu()
+        assert torch.all(got[:, :5] == 3.0) and torch.all(got[:, N + 5:] == 3.0)
+        tol = R.sum_error(K) * mag * 1.01 + R.half_step(yt) * np.abs(y)
+        assert np.all(np.abs(_f64(got[:, 5:N + 5]) - y) <= tol)
+
+
+@pytest.mark.parametrize("M", [3, 50, 140])
+@pytest.mark.parametrize("xt", ["bf16", "fp16"])
+def test_extreme_scales(M, xt):
+    """Scales from 2^-127 to 2^125 (x small and large to match), and rows
+    whose blocks lie 2^40 apart."""
+    import torch
+
+    rng = np.random.default_rng(9)
+    N, K = 48, 256
+    d = _case(rng, M, N, K, xt, "fp32", integers=True)
+    d["scales"][:16] = 252
+    d["scales"][16:32] = rng.choice([90, 130], (16, K // 32))
+    d["scales"][32:40] = 20
+    d["x"] = (d["x"].float() * 2.0 ** -12).to(_dt(xt))
+    y, mag = _expect(d)
+    got = _f64(_run(d))
+    with np.errstate(over="ignore"):
+        want = y.astype(np.float32).astype(np.float64)
+    assert np.array_equal(np.isfinite(got), np.isfinite(want))
+    assert np.all(np.abs(got - y) <= R.sum_error(K) * mag)
+    d["scales"][:] = 1  # 2^-126: the sums are binary32 subnormals
+    d["scales"][::2] = 0
+    y, _ = _expect(d)
+    assert np.all(np.abs(_f64(_run(d)) - y) <= 2.0 ** -140)
+
+
+@pytest.mark.parametrize("M", [2, 40, 140])
+@pytest.mark.parametrize("xt", ["bf16", "fp16"])
+def test_non_finite_values_stay_in_their_row_and_column(M, xt):
+    """A NaN or infinity in one row of x, and a NaN scale in one row of w,
+    reach only that row and column of y."""
+    import torch
+
+    rng = np.random.default_rng(11)
+    N, K = 40, 320
+    d = _case(rng, M, N, K, xt, "fp32")
+    y, mag = _expect(d)
+    base = _f64(_run(d))
+    for v in (float("nan"), float("inf")):
+        e = dict(d, x=d["x"].clone())
+        e["x"][1, 77] = v
+        got = _f64(_run(e))
+        rest = np.arange(M) != 1
+        assert np.array_equal(got[rest], base[rest])
+        w = R.weights(d["codes"], d["scales"])[:, 77]
+        assert np.all(~np.isfinite(got[1][w != 0]))
+    e = dict(d, scales=d["scales"].copy())
+    e["scales"][13, 4] = 255
+    got = _f64(_run(e))
+    assert np.all(np.isnan(got[:, 13]))
+    rest = np.arange(N) != 13
+    assert np.array_equal(got[:, rest], base[:, rest])
+
+
+@pytest.mark.parametrize("M,N,K", [(4, 300, 1024), (40, 300, 1024), (300, 520, 1280)])
+def test_graph_replays_streams_and_repeats_are_bitwise(M, N, K):
+    import torch
+
+    rng = np.random.default_rng(13)
+    d = _case(rng, M, N, K, "bf16", "bf16", residual=True)
+    lin = _linear(d)
+    x, res = d["x"].cuda(), d["residual"].cuda()
+    want = _run(d, lin)
+    out, eager = torch.empty_like(res), torch.empty_like(res)
+    lin.forward(x, out, residual=res)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lin.forward(x, out, residual=res)
+    for i in range(4):
+        out.zero_()
+        graph.replay()
+        lin.forward(x, eager, residual=res)
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), want) and torch.equal(eager.cpu(), want)
+    # two streams at once on one handle
+    outs = [torch.empty_like(res) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, o in zip(streams, outs):
+            lin.forward(x, o, residual=res, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o.cpu(), want) for o in outs)
+
+
+def test_refusals_on_the_device():
+    import torch
+    from quantized_moe_expert_route_amd import binding as B
+
+    rng = np.random.default_rng(15)
+    d = _case(rng, 4, 32, 64, "bf16", "bf16")
+    lin = _linear(d, max_M=4)
+    buf = torch.zeros(4 * 64 + 4 * 32, dtype=torch.bfloat16, device="cuda")
+    x, y = buf[:256].view(4, 64), buf[256:].view(4, 32)
+    lin.forward(x, y)
+    for xx, yy, rr in ((x, buf[128:256].view(4, 32), None),           # y over x
+                       (buf[4:260].view(4, 64), torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda"), None),  # misaligned x
+                       (x, y, buf[240:368].view(4, 32))):             # residual over part of y
+        with pytest.raises(B.MoeError) as e:
+            lin.forward(xx, yy, residual=rr)
+        assert e.value.status == B.MOE_ERR_INVALID_ARG
+    strided = torch.zeros(4, 68, dtype=torch.bfloat16, device="cuda")[:, :64]
+    with pytest.raises(B.MoeError):
+        lin.forward(strided, y)  # rows not 16-byte aligned
+    with pytest.raises(ValueError):
+        lin.forward(x.cpu(), y)

@@ -1,0 +1,126 @@
+"""Router projection on the GPU against 64-bit sums."""
+
+import numpy as np
+import pytest
+
+import ops_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(M, E, H, xt, wt, seed=0):
+    import torch
+
+    g = torch.Generator().manual_seed(seed + 7 * M + 11 * E + H)
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+    return torch.randn(M, H, generator=g).to(dt[xt]), (torch.randn(E, H, generator=g) / H ** 0.5).to(dt[wt])
+
+
+def _run(x, w, **kw):
+    import torch
+    from quantized_moe_expert_route_amd.binding import Router
+
+    r = Router(w.cuda(), x_dtype=x.dtype)
+    out = torch.full((x.shape[0], w.shape[0]), float("nan"), device="cuda")
+    r.forward(x.cuda(), out, **kw)
+    return out.cpu().double().numpy()
+
+
+def _check(got, x, w):
+    xd, wd = x.double().numpy(), w.double().numpy()
+    y, mag = xd @ wd.T, np.abs(xd) @ np.abs(wd).T
+    H = x.shape[1]
+    # up to 16 tokens the sums are float64 (H roundings of at most the magnitudes' sum), one rounding at the end
+    err = H * 2.0 ** -52 * mag if x.shape[0] <= 16 else R.sum_error(H) * mag
+    tol = R.U32 * np.abs(y) * (1 + 1e-6) + err
+    assert not np.isnan(got).any()
+    assert np.all(np.abs(got - y) <= tol), float((np.abs(got - y) / tol).max())
+
+
+@pytest.mark.parametrize("M,E,H", [(1, 1, 8), (1, 256, 6144), (2, 3, 40), (4, 256, 6144), (5, 161, 2056),
+                                   (13, 60, 2560), (16, 384, 7168), (16, 1024, 512), (17, 64, 1024), (31, 7, 264),
+                                   (64, 256, 6144), (65, 129, 2056), (200, 40, 1000), (257, 300, 512),
+                                   (1000, 161, 264)])
+@pytest.mark.parametrize("xt,wt", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "bf16"), ("fp16", "fp32")])
+def test_logits(M, E, H, xt, wt):
+    x, w = _case(M, E, H, xt, wt)
+    _check(_run(x, w), x, w)
+
+
+def test_strided_rows_and_rows_past_M():
+    import torch
+    from quantized_moe_expert_route_amd.binding import Router
+
+    for M in (3, 40, 150):
+        x, w = _case(M, 33, 520, "bf16", "fp32")
+        wide = torch.full((M, 600), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:, 16:536] = x.cuda()
+        out = torch.full((M + 2, 33), 5.0, device="cuda")
+        Router(w.cuda()).forward(wide[:, 16:536], out, M=M)
+        got = out.cpu().double().numpy()
+        assert np.all(got[M:] == 5.0)
+        _check(got[:M], x, w)
+
+
+def test_values_across_the_range():
+    """Large and tiny weights beside each other (fp32 holds more than 16 bits
+    can), infinities and NaN in one token only."""
+    import torch
+
+    for M in (4, 40):
+        x, w = _case(M, 24, 256, "bf16", "fp32")
+        w[:, ::3] *= 2.0 ** 60
+        w[:, 1::3] *= 2.0 ** -60
+        _check(_run(x, w), x, w)
+        base = _run(x, w)
+        x[2, 9] = float("nan")
+        got = _run(x, w)
+        rest = np.arange(M) != 2
+        assert np.all(np.isnan(got[2])) and np.array_equal(got[rest], base[rest])
+
+
+@pytest.mark.parametrize("M", [4, 16, 40, 300])
+def test_graph_replay_and_repeats(M):
+    import torch
+    from quantized_moe_expert_route_amd.binding import Router
+
+    x, w = _case(M, 160, 1024, "bf16", "bf16")
+    want = _run(x, w)
+    r, xg = Router(w.cuda()), x.cuda()
+    out, eager = torch.empty(M, 160, device="cuda"), torch.empty(M, 160, device="cuda")
+    r.forward(xg, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r.forward(xg, out)
+    for _ in range(4):
+        out.zero_()
+        graph.replay()
+        r.forward(xg, eager)
+        torch.cuda.synchronize()
+        assert np.array_equal(out.cpu().double().numpy(), want)
+        assert np.array_equal(eager.cpu().double().numpy(), want)
+
+
+def test_feeds_the_routed_call():
+    """x -> logits -> moe_forward: the call picks the experts of the 64-bit logits."""
+    import torch
+    from quantized_moe_expert_route_amd import binding as B
+
+    rng = np.random.default_rng(3)
+    for M in (4, 40):
+        H, E, I, k = 512, 24, 128, 3
+        x, rw = _case(M, E, H, "bf16", "fp32", seed=5)
+        w13, s13 = R.random_weights(rng, E, 2 * I, H)
+        w2, s2 = R.random_weights(rng, E, H, I)
+        cu = lambda a: torch.from_numpy(a).cuda()
+        plan = B.Plan(M, H, E, I, k)
+        wp, sp = B.pack_w13(cu(w13), cu(s13))
+        logits = torch.empty(M, E, device="cuda")
+        out = torch.empty(M, H, dtype=torch.bfloat16, device="cuda")
+        router = B.Router(rw.cuda())
+        plan.forward(x.cuda(), router.forward(x.cuda(), logits), wp, sp, cu(w2), cu(s2), out)
+        ids = plan.view("topk_ids", torch.int32, (M, k)).cpu().numpy()
+        want, _ = R.route((x.double().numpy() @ rw.double().numpy().T).astype(np.float32), k, 2.5)
+        assert np.array_equal(ids, want)
+        assert torch.isfinite(out.float()).all()
