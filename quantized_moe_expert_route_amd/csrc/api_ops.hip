@@ -164,7 +164,9 @@ moe_status moe_linear_forward(const moe_linear* l, int64_t M, const void* x, int
     return MOE_ERR_INVALID_ARG;
   DeviceGuard guard(l->device);
   if (!guard.ok) return MOE_ERR_DEVICE;
-  const LinearArgs a{M, l->N, l->K, ldx, ldr, ldy, x, l->wp, l->sp, l->bias, residual, y, l->x_type, y_type};
+  const int vec = l->N % 4 == 0 && ldy % 4 == 0 && ((uintptr_t)y & (4 * es - 1)) == 0 &&
+                  (!residual || (ldr % 4 == 0 && ((uintptr_t)residual & (4 * es - 1)) == 0));
+  const LinearArgs a{M, l->N, l->K, ldx, ldr, ldy, x, l->wp, l->sp, l->bias, residual, y, l->x_type, y_type, vec};
   return launch_linear(a, l->num_cus, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

@@ -52,27 +52,54 @@ hipError_t launch_pack_linear(const void* w, const void* s, int64_t N, int64_t K
 }
 
 // ----------------------------------------------------------------- epilogue
-// Four consecutive columns n .. n + 3 of row m.
+// Four consecutive columns n .. n + 3 of row m (n a multiple of 4). `a.vec`: all
+// of a row's groups of four lie inside N and are aligned (uniform over the
+// call), so that they move as one piece.
 __device__ __forceinline__ void store4(const LinearArgs& a, int64_t m, int64_t n, v4f v) {
   const bool f16 = a.x_type == MOE_FP16;
+  if (n >= a.N) return;
+  const int left = (int)min((int64_t)4, a.N - n);
+  if (a.bias) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n + i >= a.N) break;
-    float t = v[i];
-    if (a.bias) {
-      const uint16_t b = reinterpret_cast<const uint16_t*>(a.bias)[n + i];
-      t += f16 ? fp16_value(b) : bf16_value(b);
-    }
-    if (a.y_type == MOE_FP32) {
-      if (a.residual) t += reinterpret_cast<const float*>(a.residual)[m * a.ldr + n + i];
-      reinterpret_cast<float*>(a.y)[m * a.ldy + n + i] = t;
-    } else {
-      if (a.residual) {
-        const uint16_t b = reinterpret_cast<const uint16_t*>(a.residual)[m * a.ldr + n + i];
-        t += f16 ? fp16_value(b) : bf16_value(b);
+    for (int i = 0; i < 4; ++i)
+      if (i < left) {
+        const uint16_t b = reinterpret_cast<const uint16_t*>(a.bias)[n + i];
+        v[i] += f16 ? fp16_value(b) : bf16_value(b);
       }
-      reinterpret_cast<uint16_t*>(a.y)[m * a.ldy + n + i] = f16 ? fp16_bits(t) : bf16_bits(t);
+  }
+  if (a.y_type == MOE_FP32) {
+    float* y = reinterpret_cast<float*>(a.y) + m * a.ldy + n;
+    const float* res = reinterpret_cast<const float*>(a.residual) + m * a.ldr + n;
+    if (a.vec) {
+      if (a.residual) v += *reinterpret_cast<const v4f*>(res);
+      *reinterpret_cast<v4f*>(y) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) y[i] = v[i] + (a.residual ? res[i] : 0.f);
     }
+    return;
+  }
+  uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + m * a.ldy + n;
+  const uint16_t* res = reinterpret_cast<const uint16_t*>(a.residual) + m * a.ldr + n;
+  if (a.vec) {
+    if (a.residual) {
+      const uint2 p = *reinterpret_cast<const uint2*>(res);
+      const uint16_t b[4] = {(uint16_t)p.x, (uint16_t)(p.x >> 16), (uint16_t)p.y, (uint16_t)(p.y >> 16)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += f16 ? fp16_value(b[i]) : bf16_value(b[i]);
+    }
+    uint16_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = f16 ? fp16_bits(v[i]) : bf16_bits(v[i]);
+    *reinterpret_cast<uint2*>(y) = make_uint2((uint32_t)o[0] | ((uint32_t)o[1] << 16), (uint32_t)o[2] | ((uint32_t)o[3] << 16));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) {
+        if (a.residual) v[i] += f16 ? fp16_value(res[i]) : bf16_value(res[i]);
+        y[i] = f16 ? fp16_bits(v[i]) : bf16_bits(v[i]);
+      }
   }
 }
 
@@ -173,9 +200,144 @@ static hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t stream) 
   return launch_k(linear_rows_kernel<F16, 8, S>, grid, dim3(512), 0, stream, Ev{}, a);
 }
 
+// ----------------------------------------------------------------- many rows
+// A workgroup of WN x WM waves computes BN = 16 TN WN columns of y for BM =
+// 16 TM WM rows of x; a wave 16 TN x 16 TM of it. x goes through LDS in the
+// MFMA's operand order (a fragment of 16 rows x 32 K is 1 KB contiguous, read
+// back in lane order), two buffers of one K-step of 128, the next step's x in
+// registers meanwhile; weights go straight from their packed form to
+// registers, one K-step ahead, and are widened there: a wave's rows are read
+// by WM waves only.
+template <bool F16, int TN, int TM, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearArgs a, int tiles_m, int tiles_n) {
+  constexpr int W = WN * WM, BM = 16 * TM * WM, BN = 16 * TN * WN;
+  constexpr int NF = BM / 16 * 4;        // fragments of a K-step
+  constexpr int NX = (NF + W - 1) / W;   // of them staged by a wave
+  __shared__ uint4 xs[2][NF][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+  const int wn = wave % WN, wm = wave / WN;
+  const int K = (int)a.K, nks = (K + 127) / 128;
+
+  // Workgroups go to the eight XCDs in turn: XCD x takes a contiguous eighth
+  // of the tiles, walked in groups of 8 row blocks, so that the tiles it runs
+  // at a time share their x rows and weight rows in its L2.
+  const int total = tiles_m * tiles_n;
+  int id;
+  {
+    const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
+    const int per = total >> 3, rest = total & 7;
+    id = xcd * per + min(xcd, rest) + at;
+  }
+  constexpr int GM = 8;
+  const int group = id / (GM * tiles_n), first = group * GM, rows = min(GM, tiles_m - first);
+  const int in = id - group * GM * tiles_n;
+  const int64_t m0 = (int64_t)(first + in % rows) * BM;
+  const int64_t n0 = (int64_t)(in / rows) * BN;
+
+  const uint16_t* xp = reinterpret_cast<const uint16_t*>(a.x);
+  const uint16_t* xr[NX];
+#pragma unroll
+  for (int i = 0; i < NX; ++i) {
+    const int f = min(wave + i * W, NF - 1);
+    xr[i] = xp + min(m0 + 16 * (f >> 2) + r, a.M - 1) * a.ldx + 32 * (f & 3) + 8 * g;
+  }
+  uint4 xv[NX];
+  auto load_x = [&](int ks) {
+    if (128 * ks + 128 <= K) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) xv[i] = ld16(xr[i] + 128 * ks);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) {
+        const int k = 128 * ks + 32 * (min(wave + i * W, NF - 1) & 3) + 8 * g;
+        xv[i] = k < K ? ld16(xr[i] + 128 * ks) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  auto put_x = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+      if (NF % W == 0 || wave + i * W < NF) xs[buf][wave + i * W][lane] = xv[i];
+  };
+  // row blocks past N: the last one again (not stored)
+  size_t rb[TN];
+#pragma unroll
+  for (int t = 0; t < TN; ++t)
+    rb[t] = (size_t)min(n0 / 16 + wn * TN + t, (a.N + 15) / 16 - 1) * nks;
+  uint4 q[TN], nq[TN];
+  uint32_t sc[TN], nsc[TN];
+  auto load_w = [&](int ks) {
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      nq[t] = ld16(a.wp + (rb[t] + ks) * 1024 + 16 * lane);
+      nsc[t] = ld4(a.sp + (rb[t] + ks) * 64 + 4 * r);
+    }
+  };
+
+  v4f acc[TN][TM];
+#pragma unroll
+  for (int t = 0; t < TN; ++t)
+#pragma unroll
+    for (int u = 0; u < TM; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
+  load_x(0);
+  load_w(0);
+  put_x(0);
+  barrier_lds();
+  for (int ks = 0; ks < nks; ++ks) {
+#pragma unroll
+    for (int t = 0; t < TN; ++t) { q[t] = nq[t]; sc[t] = nsc[t]; }
+    if (ks + 1 < nks) {
+      load_x(ks + 1);
+      load_w(ks + 1);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v8s wf[TN];
+#pragma unroll
+      for (int t = 0; t < TN; ++t) {
+        const uint32_t d = j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w;
+        wf[t] = fp4x8_bf16(d, e8m0_value((sc[t] >> (8 * j)) & 255u));
+      }
+#pragma unroll
+      for (int u = 0; u < TM; ++u) {
+        const uint4 f = xs[ks & 1][(wm * TM + u) * 4 + j][lane];
+        if constexpr (F16) {
+          v8s hi, lo;
+          fp16x8_planes(f, hi, lo);
+#pragma unroll
+          for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], lo, mfma_bf16(wf[t], hi, acc[t][u]));
+        } else {
+#pragma unroll
+          for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], __builtin_bit_cast(v8s, f), acc[t][u]);
+        }
+      }
+    }
+    if (ks + 1 < nks) {
+      put_x((ks + 1) & 1);  // the buffer of step ks - 1: read by nobody since the last barrier
+      barrier_lds();
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < TM; ++u) {
+    const int64_t m = m0 + 16 * (wm * TM + u) + r;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int t = 0; t < TN; ++t) store4(a, m, n0 + 16 * (wn * TN + t) + 4 * g, acc[t][u]);
+  }
+}
+
+template <bool F16, int TN, int TM, int WN, int WM>
+static hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
+  const int64_t tm = (a.M + 16 * TM * WM - 1) / (16 * TM * WM), tn = (a.N + 16 * TN * WN - 1) / (16 * TN * WN);
+  return launch_k(linear_tile_kernel<F16, TN, TM, WN, WM>, dim3((unsigned)(tm * tn)), dim3(64 * WN * WM), 0, stream,
+                  Ev{}, a, (int)tm, (int)tn);
+}
+
 hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream) {
   const int64_t nks = (a.K + 127) / 128;
   const bool f16 = a.x_type == MOE_FP16;
+  if (a.M > 64) return f16 ? launch_tile<true, 4, 4, 4, 2>(a, stream) : launch_tile<false, 4, 4, 4, 2>(a, stream);
   if (nks <= 8) return f16 ? launch_rows<true, 1>(a, cus, stream) : launch_rows<false, 1>(a, cus, stream);
   if (nks <= 16) return f16 ? launch_rows<true, 2>(a, cus, stream) : launch_rows<false, 2>(a, cus, stream);
   if (nks <= 32) return f16 ? launch_rows<true, 4>(a, cus, stream) : launch_rows<false, 4>(a, cus, stream);

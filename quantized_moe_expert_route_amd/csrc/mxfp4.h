@@ -43,6 +43,27 @@ __device__ __forceinline__ float e8m0_value(uint32_t s) {
   return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : u);
 }
 
+// 8 fp16 values as two bf16 each, value = hi + lo exactly: hi keeps the upper
+// 8 of 11 significant bits, lo the rest (both in bf16's wider range, fp16
+// subnormals included). An infinity or NaN stays in hi, lo zero.
+__device__ __forceinline__ void fp16x8_planes(uint4 f, v8s& hi, v8s& lo) {
+  const uint32_t d[4] = {f.x, f.y, f.z, f.w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f16x2 p = __builtin_bit_cast(f16x2, d[i]);
+    const float a = (float)p[0], b = (float)p[1];
+    const uint32_t ha = __float_as_uint(a) & 0xFFFF0000u, hb = __float_as_uint(b) & 0xFFFF0000u;
+    const float la = a - __uint_as_float(ha), lb = b - __uint_as_float(hb);
+    h[i] = (ha >> 16) | hb;
+    const uint32_t ka = (d[i] & 0x7C00u) == 0x7C00u ? 0u : __float_as_uint(la) >> 16;
+    const uint32_t kb = (d[i] & 0x7C000000u) == 0x7C000000u ? 0u : __float_as_uint(lb) & 0xFFFF0000u;
+    l[i] = ka | kb;
+  }
+  hi = as_v8s(h[0], h[1], h[2], h[3]);
+  lo = as_v8s(l[0], l[1], l[2], l[3]);
+}
+
 // binary32 -> bf16 / fp16 bits, nearest even.
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 __device__ __forceinline__ uint16_t fp16_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
