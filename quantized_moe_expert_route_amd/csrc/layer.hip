@@ -122,7 +122,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
     for (int s = 0; s < S; ++s) {
       const int ks = wave * S + s;
       if (ks >= nks) break;
-      const float fg = e8m0_value((sg[s] >> (8 * (ks & 3))) & 255u), fu = e8m0_value((su[s] >> (8 * (ks & 3))) & 255u);
+      const float fg = scale_operand<0>(sg[s] >> (8 * (ks & 3))), fu = scale_operand<0>(su[s] >> (8 * (ks & 3)));
       const uint32_t dg[4] = {qg[s].x, qg[s].y, qg[s].z, qg[s].w}, du[4] = {qu[s].x, qu[s].y, qu[s].z, qu[s].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
       v4f d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float f = e8m0_value((sc[b] >> (8 * g)) & 255u);
+        const float f = scale_operand<0>(sc[b] >> (8 * g));
         const uint32_t w[4] = {q[b].x, q[b].y, q[b].z, q[b].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -103,6 +103,11 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int64_t m, int64_t n
   }
 }
 
+// scale_operand of a byte number known after unrolling
+__device__ __forceinline__ float scale_of(uint32_t d, int j) {
+  return j == 0 ? scale_operand<0>(d) : j == 1 ? scale_operand<1>(d) : j == 2 ? scale_operand<2>(d) : scale_operand<3>(d);
+}
+
 // ----------------------------------------------------------------- few rows
 // A workgroup of W waves computes 16 columns of y for up to 16 rows of x at a
 // time. The waves split K: wave w owns S K-steps of 128 in every segment of
@@ -169,8 +174,7 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[i] += p[i] * e8m0_value((rs[i] >> (8 * j)) & 255u);
         } else {
-          acc = mfma_bf16(fp4x8_bf16(d[j], e8m0_value((sc[s].x >> (8 * j)) & 255u)),
-                          __builtin_bit_cast(v8s, xf[s][j]), acc);
+          acc = mfma_bf16(fp4x8_bf16(d[j], scale_of(sc[s].x, j)), __builtin_bit_cast(v8s, xf[s][j]), acc);
         }
       }
     }
@@ -297,7 +301,7 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
 #pragma unroll
       for (int t = 0; t < TN; ++t) {
         const uint32_t d = j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w;
-        wf[t] = fp4x8_bf16(d, e8m0_value((sc[t] >> (8 * j)) & 255u));
+        wf[t] = fp4x8_bf16(d, scale_of(sc[t], j));
       }
 #pragma unroll
       for (int u = 0; u < TM; ++u) {

@@ -17,6 +17,14 @@ namespace qmoe {
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
+// Byte J of a dword of four E8M0 scales, as the conversions below take it:
+// they read bits 23..30 alone (any sign and fraction), as 2^(s - 127) with 0
+// meaning 2^-127 and 255 NaN, over all 256 scales and 16 codes.
+template <int J>
+__device__ __forceinline__ float scale_operand(uint32_t d) {
+  return __uint_as_float(J < 3 ? d << (23 - 8 * J) : d >> 1);
+}
+
 // 8 E2M1 codes (a dword, first code in the low nibble) x 2^e -> 8 bf16.
 __device__ __forceinline__ v8s fp4x8_bf16(uint32_t q, float scale) {
   return as_v8s(cvt_fp4x2_bf16<0>(q, scale), cvt_fp4x2_bf16<1>(q, scale), cvt_fp4x2_bf16<2>(q, scale),

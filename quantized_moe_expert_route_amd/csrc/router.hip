@@ -79,22 +79,182 @@ __global__ __launch_bounds__(256) void router_kernel(const RouterArgs a) {
   }
 }
 
+// 8 elements as P planes of bf16 whose sum they are: bf16 is one, fp16 two,
+// fp32 three (each plane keeps the upper 8 significant bits of what is left:
+// 24 = 3 x 8, exact down to bf16's smallest number). A value that is not
+// finite stays in the first.
+template <int TYPE>
+constexpr int kPlanes = TYPE == MOE_BF16 ? 1 : TYPE == MOE_FP16 ? 2 : 3;
+
+template <int TYPE>
+struct Raw8 {
+  uint4 v[TYPE == MOE_FP32 ? 2 : 1];
+};
+template <int TYPE>
+__device__ __forceinline__ void raw8(const void* p, int64_t i, Raw8<TYPE>& q) {
+  if constexpr (TYPE == MOE_FP32) {
+    q.v[0] = ld16(reinterpret_cast<const float*>(p) + i);
+    q.v[1] = ld16(reinterpret_cast<const float*>(p) + i + 4);
+  } else {
+    q.v[0] = ld16(reinterpret_cast<const uint16_t*>(p) + i);
+  }
+}
+template <int TYPE>
+__device__ __forceinline__ void planes8(const Raw8<TYPE>& q, v8s (&out)[kPlanes<TYPE>]) {
+  if constexpr (TYPE == MOE_BF16) {
+    out[0] = __builtin_bit_cast(v8s, q.v[0]);
+  } else if constexpr (TYPE == MOE_FP16) {
+    fp16x8_planes(q.v[0], out[0], out[1]);
+  } else {
+    const uint32_t d[8] = {q.v[0].x, q.v[0].y, q.v[0].z, q.v[0].w, q.v[1].x, q.v[1].y, q.v[1].z, q.v[1].w};
+    uint32_t h[4], m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t hi = d[i] & 0xFFFF0000u;
+      const bool fine = (d[i] & 0x7F800000u) != 0x7F800000u;
+      const float r1 = fine ? __uint_as_float(d[i]) - __uint_as_float(hi) : 0.f;
+      const uint32_t mi = __float_as_uint(r1) & 0xFFFF0000u;
+      const uint32_t lo = __float_as_uint(r1 - __uint_as_float(mi));
+      if (i & 1) {
+        h[i >> 1] |= hi;
+        m[i >> 1] |= mi;
+        l[i >> 1] |= lo & 0xFFFF0000u;
+      } else {
+        h[i >> 1] = hi >> 16;
+        m[i >> 1] = mi >> 16;
+        l[i >> 1] = lo >> 16;
+      }
+    }
+    out[0] = as_v8s(h[0], h[1], h[2], h[3]);
+    out[1] = as_v8s(m[0], m[1], m[2], m[3]);
+    out[2] = as_v8s(l[0], l[1], l[2], l[3]);
+  }
+}
+
+// Above 16 tokens: tiles of 16 TN experts x 16 TM tokens on the bf16 MFMA
+// (binary32 sums of exact products, planes as above). The W waves of a
+// workgroup split K in pieces of 64, so that no operand is shared between
+// them: each goes from memory to the wave's registers, without LDS or
+// barriers in the loop. The W partial tiles are added in wave order.
+template <int XT, int WT, int TN, int TM, int W>
+__global__ __launch_bounds__(64 * W) void router_tile_kernel(const RouterArgs a, int tiles_e) {
+  __shared__ v4f red[W][TN * TM > 4 ? 4 : TN * TM][64];
+  constexpr int C = TN * TM > 4 ? 4 : TN * TM;  // sub-tiles joined at a time
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+  const int e0 = (int)(blockIdx.x % tiles_e) * 16 * TN;
+  const int64_t m0 = (int64_t)(blockIdx.x / tiles_e) * 16 * TM;
+  const int H = (int)a.H;
+  int64_t wo[TN], xo[TM];
+#pragma unroll
+  for (int t = 0; t < TN; ++t) wo[t] = (int64_t)min(e0 + 16 * t + r, (int)a.E - 1) * H;
+#pragma unroll
+  for (int u = 0; u < TM; ++u) xo[u] = min(m0 + 16 * u + r, a.M - 1) * a.ldx;
+  v4f acc[TN][TM];
+#pragma unroll
+  for (int t = 0; t < TN; ++t)
+#pragma unroll
+    for (int u = 0; u < TM; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
+  // piece c: K 64 c .. + 63, lane group g its elements 16 g .. + 15 as two
+  // operands; past H they are taken as zero (H is a multiple of 8)
+  Raw8<WT> wr[2][TN];
+  Raw8<XT> xr[2][TM];
+  auto load = [&](int c) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int k = 64 * c + 16 * g + 8 * j;
+      const int kc = min(k, H - 8);
+#pragma unroll
+      for (int t = 0; t < TN; ++t) raw8<WT>(a.w, wo[t] + kc, wr[j][t]);
+#pragma unroll
+      for (int u = 0; u < TM; ++u) raw8<XT>(a.x, xo[u] + kc, xr[j][u]);
+    }
+    if (64 * c + 64 > H) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (64 * c + 16 * g + 8 * j >= H) {
+#pragma unroll
+          for (int t = 0; t < TN; ++t)
+            for (auto& v : wr[j][t].v) v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int u = 0; u < TM; ++u)
+            for (auto& v : xr[j][u].v) v = make_uint4(0, 0, 0, 0);
+        }
+    }
+  };
+  const int pieces = (H + 63) / 64;
+  for (int c = wave; c < pieces; c += W) {
+    load(c);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      v8s wf[TN][kPlanes<WT>];
+#pragma unroll
+      for (int t = 0; t < TN; ++t) planes8<WT>(wr[j][t], wf[t]);
+#pragma unroll
+      for (int u = 0; u < TM; ++u) {
+        v8s xf[kPlanes<XT>];
+        planes8<XT>(xr[j][u], xf);
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+#pragma unroll
+          for (int p = kPlanes<WT> - 1; p >= 0; --p)
+#pragma unroll
+            for (int q = kPlanes<XT> - 1; q >= 0; --q) acc[t][u] = mfma_bf16(wf[t][p], xf[q], acc[t][u]);
+      }
+    }
+  }
+  // lane (g, r): experts 4 g .. + 3 of token r of a sub-tile
+#pragma unroll
+  for (int s0 = 0; s0 < TN * TM; s0 += C) {
+    if (s0) __syncthreads();
+#pragma unroll
+    for (int s = 0; s < C; ++s) red[wave][s][lane] = acc[(s0 + s) / TM][(s0 + s) % TM];
+    __syncthreads();
+    for (int i = threadIdx.x; i < C * 64; i += 64 * W) {
+      const int s = i >> 6, l = i & 63;
+      v4f v = red[0][s][l];
+#pragma unroll
+      for (int w = 1; w < W; ++w) v += red[w][s][l];
+      const int64_t m = m0 + 16 * ((s0 + s) % TM) + (l & 15);
+      const int e = e0 + 16 * ((s0 + s) / TM) + 4 * (l >> 4);
+      if (m < a.M) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (e + q < a.E) a.logits[m * a.E + e + q] = v[q];
+      }
+    }
+  }
+}
+
+template <int XT, int WT, int TN, int TM, int W>
+static hipError_t launch_tiles(const RouterArgs& a, hipStream_t stream) {
+  const int64_t te = (a.E + 16 * TN - 1) / (16 * TN), tm = (a.M + 16 * TM - 1) / (16 * TM);
+  return launch_k(router_tile_kernel<XT, WT, TN, TM, W>, dim3((unsigned)(te * tm)), dim3(64 * W), 0, stream, Ev{}, a,
+                  (int)te);
+}
+
 template <int XT, int WT>
-static hipError_t launch_types(const RouterArgs& a, hipStream_t stream) {
+static hipError_t launch_types(const RouterArgs& a, int cus, hipStream_t stream) {
   if (a.M <= 1)
     return launch_k(router_kernel<XT, WT, 1>, dim3((unsigned)a.E, 1), dim3(256), 0, stream, Ev{}, a);
   if (a.M <= 4)
     return launch_k(router_kernel<XT, WT, 4>, dim3((unsigned)a.E, 1), dim3(256), 0, stream, Ev{}, a);
-  return launch_k(router_kernel<XT, WT, 8>, dim3((unsigned)a.E, (unsigned)((a.M + 7) / 8)), dim3(256), 0, stream, Ev{},
-                  a);
+  if (a.M <= 16)
+    return launch_k(router_kernel<XT, WT, 8>, dim3((unsigned)a.E, (unsigned)((a.M + 7) / 8)), dim3(256), 0, stream,
+                    Ev{}, a);
+  // the largest tile that still gives every CU a workgroup
+  auto groups = [&](int t) { return ((a.E + 16 * t - 1) / (16 * t)) * ((a.M + 16 * t - 1) / (16 * t)); };
+  if (groups(4) >= cus) return launch_tiles<XT, WT, 4, 4, 8>(a, stream);
+  if (groups(2) >= cus) return launch_tiles<XT, WT, 2, 2, 8>(a, stream);
+  return launch_tiles<XT, WT, 1, 1, 16>(a, stream);
 }
 
 hipError_t launch_router(const RouterArgs& a, int cus, hipStream_t stream) {
   if (a.x_type == MOE_BF16)
-    return a.w_type == MOE_BF16 ? launch_types<MOE_BF16, MOE_BF16>(a, stream)
-                                : launch_types<MOE_BF16, MOE_FP32>(a, stream);
-  return a.w_type == MOE_BF16 ? launch_types<MOE_FP16, MOE_BF16>(a, stream)
-                              : launch_types<MOE_FP16, MOE_FP32>(a, stream);
+    return a.w_type == MOE_BF16 ? launch_types<MOE_BF16, MOE_BF16>(a, cus, stream)
+                                : launch_types<MOE_BF16, MOE_FP32>(a, cus, stream);
+  return a.w_type == MOE_BF16 ? launch_types<MOE_FP16, MOE_BF16>(a, cus, stream)
+                              : launch_types<MOE_FP16, MOE_FP32>(a, cus, stream);
 }
 
 }  // namespace qmoe
