@@ -210,7 +210,13 @@ class _Handle:
     def _check(self, name, t, dtype, rows, cols, dense=False):
         """The library sees bare pointers: a tensor on another device, of
         another type, smaller than the call, or with strided columns is
-        refused here."""
+        refused here. Returns the elements between its rows."""
+        try:
+            n, c = t.shape
+            if t.dtype is dtype and c == cols and n >= rows and t.is_contiguous() and t.device == self.device:
+                return cols  # one expression for the common case: a small call's time is host time
+        except (AttributeError, ValueError):
+            pass
         import torch
 
         if not isinstance(t, torch.Tensor):
@@ -225,6 +231,7 @@ class _Handle:
             raise ValueError(f"{name} has strides {t.stride()}: columns must be adjacent, rows apart")
         if dense and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+        return t.stride(0) if rows > 1 else cols  # a single row's stride says nothing
 
     def _rows(self, x, M):
         M = x.shape[0] if M is None else int(M)
@@ -233,9 +240,7 @@ class _Handle:
         return M
 
     def _stream(self, stream):
-        import torch
-
-        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+        return _raw_stream(self.device) if stream is None else stream.cuda_stream
 
     def close(self):
         if self._h:
@@ -249,9 +254,15 @@ class _Handle:
             pass
 
 
-def _row_stride(t, rows, cols):
-    """Elements between rows; a single row's stride says nothing."""
-    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
+def _raw_stream(device):
+    """The hipStream_t of torch's current stream on `device` (without the
+    Python stream object where torch has that: 0.1 against 2 us)."""
+    import torch
+
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if get is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return get(device.index)
 
 
 def _dtype_code(dtype):
@@ -276,6 +287,7 @@ class Router(_Handle):
             raise ValueError("w must be a contiguous [E, H] tensor")
         self.x_dtype = torch.bfloat16 if x_dtype is None else x_dtype
         self.device, self.max_M, self.w = w.device, int(max_M), w  # the library keeps w's pointer
+        self._fp32 = torch.float32
         self.E, self.H = w.shape
         h = ctypes.c_void_p()
         st = lib().moe_router_create(self.E, self.H, _dtype_code(self.x_dtype), _ptr(w), _dtype_code(w.dtype),
@@ -287,13 +299,10 @@ class Router(_Handle):
     def forward(self, x, logits, M: Optional[int] = None, stream=None):
         """logits[:M] = x[:M] w^T, enqueued on `stream` (default: the current
         stream of the weights' device)."""
-        import torch
-
         M = self._rows(x, M)
-        self._check("x", x, self.x_dtype, M, self.H)
-        self._check("logits", logits, torch.float32, M, self.E, dense=True)
-        st = lib().moe_router_forward(self._h, M, _ptr(x), _row_stride(x, M, self.H), _ptr(logits),
-                                      self._stream(stream))
+        ldx = self._check("x", x, self.x_dtype, M, self.H)
+        self._check("logits", logits, self._fp32, M, self.E, dense=True)
+        st = lib().moe_router_forward(self._h, M, x.data_ptr(), ldx, logits.data_ptr(), self._stream(stream))
         if st != MOE_OK:
             raise MoeError(st, "moe_router_forward")
         return logits
@@ -317,6 +326,7 @@ class Linear(_Handle):
                 or tuple(s.shape) != (self.N, w.shape[1] // 16) or w.shape[1] % 16):
             raise ValueError("s must be a contiguous uint8 [N, K/32] tensor beside w")
         self.x_dtype = torch.bfloat16 if x_dtype is None else x_dtype
+        self._x_code, self._fp32 = _dtype_code(self.x_dtype), torch.float32
         self.device, self.max_M = w.device, int(max_M)
         if bias is not None and (bias.dtype != self.x_dtype or tuple(bias.shape) != (self.N,)
                                  or bias.device != w.device or not bias.is_contiguous()):
@@ -335,7 +345,7 @@ class Linear(_Handle):
             raise MoeError(st, "moe_pack_linear")
         here.synchronize()  # load time: calls on any stream find the weights packed
         h = ctypes.c_void_p()
-        st = lib().moe_linear_create(self.N, self.K, _dtype_code(self.x_dtype), _ptr(self.w_packed),
+        st = lib().moe_linear_create(self.N, self.K, self._x_code, _ptr(self.w_packed),
                                      _ptr(self.s_packed), None if bias is None else _ptr(bias), self.max_M,
                                      ctypes.byref(h))
         if st != MOE_OK:
@@ -345,18 +355,15 @@ class Linear(_Handle):
     def forward(self, x, out, residual=None, M: Optional[int] = None, stream=None):
         """out[:M] = x[:M] w^T (+ bias) (+ residual[:M]); out is of x's type or
         float32, residual of out's; residual may be out itself."""
-        import torch
-
         M = self._rows(x, M)
-        self._check("x", x, self.x_dtype, M, self.K)
-        y_dtype = torch.float32 if isinstance(out, torch.Tensor) and out.dtype == torch.float32 else self.x_dtype
-        self._check("out", out, y_dtype, M, self.N)
-        if residual is not None:
-            self._check("residual", residual, y_dtype, M, self.N)
+        ldx = self._check("x", x, self.x_dtype, M, self.K)
+        wide = getattr(out, "dtype", None) is self._fp32
+        y_dtype = self._fp32 if wide else self.x_dtype
+        ldy = self._check("out", out, y_dtype, M, self.N)
+        ldr = 0 if residual is None else self._check("residual", residual, y_dtype, M, self.N)
         st = lib().moe_linear_forward(
-            self._h, M, _ptr(x), _row_stride(x, M, self.K), None if residual is None else _ptr(residual),
-            0 if residual is None else max(residual.stride(0), self.N), _ptr(out), max(out.stride(0), self.N),
-            _dtype_code(y_dtype), self._stream(stream))
+            self._h, M, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy,
+            FP32 if wide else self._x_code, self._stream(stream))
         if st != MOE_OK:
             raise MoeError(st, "moe_linear_forward")
         return out
@@ -562,13 +569,13 @@ class Plan:
         s = self.shape
         if not 0 <= M <= s.M:
             raise ValueError(f"M = {M} outside [0, {s.M}] (the plan's shape)")
+        H, codes = s.H, s.E * s.I * s.H
         bf16, u8 = (torch.int16, torch.bfloat16), (torch.uint8,)
-        self._tensor("x", x, bf16, rows=M, cols=s.H)
-        self._tensor("out", out, bf16, rows=M, cols=s.H)
-        self._tensor("w13", w13, u8, numel=s.E * s.I * s.H)
-        self._tensor("s13", s13, u8, numel=s.E * s.I * s.H // 16)
-        self._tensor("w2", w2, u8, numel=s.E * s.H * s.I // 2)
-        self._tensor("s2", s2, u8, numel=s.E * s.H * s.I // 32)
+        for name, t in (("x", x), ("out", out)):
+            self._tensor(name, t, bf16, rows=M, cols=H)
+        for name, t, n in (("w13", w13, codes), ("s13", s13, codes // 16), ("w2", w2, codes // 2),
+                           ("s2", s2, codes // 32)):
+            self._tensor(name, t, u8, numel=n)
         st = lib().moe_layer_forward(self._h, router._h, M, _ptr(x), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2),
                                      _ptr(out), router._stream(stream))
         if st != MOE_OK:

@@ -113,7 +113,7 @@ def test_binding_refuses_bad_tensors():
     """The binding checks every tensor before the library sees its pointer
     (objects without a device handle: the checks come first)."""
     cpu = torch.device("cpu")
-    lin = _bare(B.Linear, device=cpu, max_M=4, N=24, K=64, x_dtype=torch.bfloat16, bias=None)
+    lin = _bare(B.Linear, device=cpu, max_M=4, N=24, K=64, x_dtype=torch.bfloat16, bias=None, _fp32=torch.float32)
     x, y = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 24, dtype=torch.bfloat16)
     for bad in (dict(x=x.float()), dict(x=x[:, :32]), dict(x=torch.zeros(64, 4, dtype=torch.bfloat16).t()),
                 dict(x=torch.zeros(5, 64, dtype=torch.bfloat16)), dict(out=y.half()), dict(out=y[:2]),
@@ -123,7 +123,7 @@ def test_binding_refuses_bad_tensors():
             lin.forward(**dict(dict(x=x, out=y), **bad))
     with pytest.raises(TypeError):
         lin.forward(x, None)
-    rt = _bare(B.Router, device=cpu, max_M=4, E=8, H=64, x_dtype=torch.bfloat16)
+    rt = _bare(B.Router, device=cpu, max_M=4, E=8, H=64, x_dtype=torch.bfloat16, _fp32=torch.float32)
     lg = torch.zeros(4, 8)
     for bad in (dict(x=x.half()), dict(logits=lg.double()), dict(logits=torch.zeros(4, 16)[:, :8]),
                 dict(logits=lg[:3]), dict(x=x[:, ::2]), dict(M=-1)):
