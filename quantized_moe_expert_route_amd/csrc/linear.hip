@@ -10,6 +10,7 @@
 //   wp [ceil(N/16)][ceil(K/128)][4 g][16 r][4 j] dwords, codes past N or K zero
 //   sp [ceil(N/16)][ceil(K/128)][16 r][4 j] bytes, past N or K 127 (2^0)
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "mxfp4.h"
@@ -109,99 +110,165 @@ __device__ __forceinline__ float scale_of(uint32_t d, int j) {
 }
 
 // ----------------------------------------------------------------- few rows
-// A workgroup of W waves computes 16 columns of y for up to 16 rows of x at a
-// time. The waves split K: wave w owns S K-steps of 128 in every segment of
-// W S steps, and keeps its fragments of x in registers over all the tiles of
-// the workgroup while one segment covers K. The W partial sums are added in
-// wave order through LDS.
-template <bool F16, int W, int S>
+// A workgroup of W waves computes 16 columns of y at a time for up to 16 rows
+// of x; the waves split K. Wave w owns K-steps w S .. w S + S - 1 of 128 and
+// keeps its fragments of x as MFMA operands in registers over all the tiles
+// of the workgroup. Its weights stream through a ring of D tiles' registers:
+// the piece of a tile D ahead is requested as soon as a slot's products are
+// issued, so a wave has about S D KB under way at any time. The W partial
+// sums of a tile are added in wave order through LDS.
+template <bool F16>
+struct WeightStep {  // one K-step of 16 weight rows: a lane's codes and scales
+  uint4 q;
+  uint4 sc;  // bf16: .x is the lane's row's four scales; fp16: rows 4 g .. 4 g + 3
+  __device__ __forceinline__ void load(const LinearArgs& a, size_t piece, int lane) {
+    q = ld16(a.wp + piece * 1024 + 16 * lane);
+    if constexpr (F16) sc = ld16(a.sp + piece * 64 + 16 * (lane >> 4));
+    else sc.x = ld4(a.sp + piece * 64 + 4 * (lane & 15));
+  }
+  __device__ __forceinline__ void clear() { q = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void mul(const uint4 (&x)[4], v4f& acc) const {
+    const uint32_t d[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (F16) {
+      const uint32_t rs[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const v4f p = mfma_f16(fp4x8_f16(d[j]), __builtin_bit_cast(v8h, x[j]), v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += p[i] * e8m0_value((rs[i] >> (8 * j)) & 255u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc = mfma_bf16(fp4x8_bf16(d[j], scale_of(sc.x, j)), __builtin_bit_cast(v8s, x[j]), acc);
+    }
+  }
+};
+
+template <bool F16, int W, int S, int D>
 __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a) {
   __shared__ v4f red[2][W][64];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
-  const int K = (int)a.K, nks = (K + 127) / 128, nseg = (nks + W * S - 1) / (W * S);
-  const int64_t m0 = (int64_t)blockIdx.y * 16;
-  const bool row = m0 + r < a.M;
-  const uint16_t* xr = reinterpret_cast<const uint16_t*>(a.x) + (row ? m0 + r : 0) * a.ldx;
-  const int ntiles = (int)((a.N + 15) / 16);
+  const int K = (int)a.K, nks = (K + 127) / 128;
+  const bool row = r < a.M;
+  const int ntiles = (int)((a.N + 15) / 16), step = gridDim.x;
+  const int own = (ntiles - (int)blockIdx.x + step - 1) / step;  // this workgroup's tiles (grid <= ntiles)
 
-  uint4 xf[S][4], q[S], nq[S];
-  uint4 sc[S], nsc[S];  // bf16: .x is the row's four scales; fp16: rows 4g..4g+3
-  auto load_x = [&](int seg) {
+  WeightStep<F16> ring[D][S];
+  auto load = [&](int d, int s, int i) {
+    // past the last step of K or the last tile: that one again, not used
+    const int tile = blockIdx.x + min(i, own - 1) * step;
+    ring[d][s].load(a, (size_t)tile * nks + min(wave * S + s, nks - 1), lane);
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+#pragma unroll
+    for (int s = 0; s < S; ++s) load(d, s, d);
+  uint4 xf[S][4];
+  const uint16_t* xr = reinterpret_cast<const uint16_t*>(a.x) + (row ? r : 0) * a.ldx;
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = 128 * (wave * S + s) + 32 * j + 8 * g;
+      xf[s][j] = row && k < K ? ld16(xr + k) : make_uint4(0, 0, 0, 0);
+    }
+
+  auto tile_done = [&](int i, const v4f& acc) {
+    const int buf = i & 1;
+    red[buf][wave][lane] = acc;
+    barrier_lds();
+    // lane holds rows 4 g .. 4 g + 3 (columns of y) of column r (row of x)
+    if (wave == i % W && row) {
+      v4f v = red[buf][0][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) v += red[buf][w][lane];
+      store4(a, r, (int64_t)(blockIdx.x + i * step) * 16 + 4 * g, v);
+    }
+  };
+  auto compute = [&](int d, int i, auto reload) {
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      // a step past the last takes no part (its codes could meet a scale that
+      // overflows, and zero times that is not zero)
+      if (wave * S + s >= nks) ring[d][s].clear();
+      ring[d][s].mul(xf[s], acc);
+      if constexpr (reload) load(d, s, i + D);
+    }
+    tile_done(i, acc);
+  };
+  int i = 0;
+  for (; i + D < own; i += D)
+#pragma unroll
+    for (int d = 0; d < D; ++d) compute(d, i + d, std::true_type{});
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (i + d < own) compute(d, i + d, std::false_type{});
+}
+
+// K beyond the W S steps that the waves hold: segment after segment, x loaded
+// again for each (from the cache), the next segment's weights under way.
+template <bool F16, int W, int S>
+__global__ __launch_bounds__(64 * W) void linear_rows_long_kernel(const LinearArgs a) {
+  __shared__ v4f red[2][W][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+  const int K = (int)a.K, nks = (K + 127) / 128, nseg = (nks + W * S - 1) / (W * S);
+  const bool row = r < a.M;
+  const uint16_t* xr = reinterpret_cast<const uint16_t*>(a.x) + (row ? r : 0) * a.ldx;
+  const int ntiles = (int)((a.N + 15) / 16);
+  uint4 xf[S][4];
+  WeightStep<F16> cur[S], next[S];
+  auto load_w = [&](int tile, int seg) {
 #pragma unroll
     for (int s = 0; s < S; ++s)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = 128 * ((seg * W + wave) * S + s) + 32 * j + 8 * g;
-        xf[s][j] = row && k < K ? ld16(xr + k) : make_uint4(0, 0, 0, 0);
-      }
+      next[s].load(a, (size_t)tile * nks + min((seg * W + wave) * S + s, nks - 1), lane);
   };
-  auto load_w = [&](int tile, int seg, uint4(&qq)[S], uint4(&ss)[S]) {
-    const size_t base = (size_t)tile * nks;
+  int buf = 0;
+  load_w(blockIdx.x, 0);
+  for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    for (int seg = 0; seg < nseg; ++seg) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      // past the last step: that step again, with x zero
-      const size_t p = base + min((seg * W + wave) * S + s, nks - 1);
-      qq[s] = ld16(a.wp + p * 1024 + 16 * lane);
-      if (F16) ss[s] = ld16(a.sp + p * 64 + 16 * g);
-      else ss[s].x = ld4(a.sp + p * 64 + 4 * r);
-    }
-  };
-
-  int tile = blockIdx.x, seg = 0, buf = 0;
-  if (tile >= ntiles) return;
-  load_w(tile, 0, nq, nsc);
-  load_x(0);
-  v4f acc = {0.f, 0.f, 0.f, 0.f};
-  while (tile < ntiles) {
+      for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int s = 0; s < S; ++s) { q[s] = nq[s]; sc[s] = nsc[s]; }
-    int ntile = tile, nsg = seg + 1;
-    if (nsg == nseg) { nsg = 0; ntile += gridDim.x; }
-    if (ntile < ntiles) load_w(ntile, nsg, nq, nsc);
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      // a step past the last one takes no part (its codes could meet a scale
-      // that overflows, and zero times that is not zero)
-      const bool in = (seg * W + wave) * S + s < nks;
-      const uint32_t d[4] = {in ? q[s].x : 0u, in ? q[s].y : 0u, in ? q[s].z : 0u, in ? q[s].w : 0u};
-      const uint32_t rs[4] = {sc[s].x, sc[s].y, sc[s].z, sc[s].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (F16) {
-          const v4f z = {0.f, 0.f, 0.f, 0.f};
-          const v4f p = mfma_f16(fp4x8_f16(d[j]), __builtin_bit_cast(v8h, xf[s][j]), z);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] += p[i] * e8m0_value((rs[i] >> (8 * j)) & 255u);
-        } else {
-          acc = mfma_bf16(fp4x8_bf16(d[j], scale_of(sc[s].x, j)), __builtin_bit_cast(v8s, xf[s][j]), acc);
+        for (int j = 0; j < 4; ++j) {
+          const int k = 128 * ((seg * W + wave) * S + s) + 32 * j + 8 * g;
+          xf[s][j] = row && k < K ? ld16(xr + k) : make_uint4(0, 0, 0, 0);
         }
-      }
-    }
-    if (nsg == 0) {
-      red[buf][wave][lane] = acc;
-      acc = v4f{0.f, 0.f, 0.f, 0.f};
-      barrier_lds();
-      // lane holds rows 4 g .. 4 g + 3 (columns of y) of column r (row of x)
-      if (wave == buf && row) {
-        v4f v = red[buf][0][lane];
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += red[buf][w][lane];
-        store4(a, m0 + r, (int64_t)tile * 16 + 4 * g, v);
+      for (int s = 0; s < S; ++s) cur[s] = next[s];
+      if (seg + 1 < nseg) load_w(tile, seg + 1);
+      else load_w(min(tile + (int)gridDim.x, ntiles - 1), 0);
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        if ((seg * W + wave) * S + s >= nks) cur[s].clear();
+        cur[s].mul(xf[s], acc);
       }
-      buf ^= 1;
     }
-    if (nseg > 1 && ntile < ntiles) load_x(nsg);
-    tile = ntile;
-    seg = nsg;
+    red[buf][wave][lane] = acc;
+    barrier_lds();
+    if (wave == buf && row) {
+      v4f v = red[buf][0][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) v += red[buf][w][lane];
+      store4(a, r, (int64_t)tile * 16 + 4 * g, v);
+    }
+    buf ^= 1;
   }
 }
 
-template <bool F16, int S>
+// OCC workgroups fit a CU's registers: one a tile while they all fit at once,
+// else OCC a CU, each over several tiles.
+template <bool F16, int W, int S, int OCC>
 static hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t stream) {
   const int64_t tiles = (a.N + 15) / 16;
-  const dim3 grid((unsigned)std::min<int64_t>(tiles, 2 * cus), (unsigned)((a.M + 15) / 16));
-  return launch_k(linear_rows_kernel<F16, 8, S>, grid, dim3(512), 0, stream, Ev{}, a);
+  if (tiles <= OCC * cus)
+    return launch_k(linear_rows_kernel<F16, W, S, 1>, dim3((unsigned)tiles), dim3(64 * W), 0, stream, Ev{}, a);
+  return launch_k(linear_rows_kernel<F16, W, S, S == 1 ? 4 : 2>, dim3((unsigned)(OCC * cus)), dim3(64 * W), 0, stream,
+                  Ev{}, a);
 }
 
 // ----------------------------------------------------------------- many rows
@@ -338,14 +405,35 @@ static hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
                   Ev{}, a, (int)tm, (int)tn);
 }
 
-hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream) {
+template <bool F16>
+static hipError_t launch_16_rows(const LinearArgs& a, int cus, hipStream_t stream) {
   const int64_t nks = (a.K + 127) / 128;
+  if (nks <= 8) return launch_rows<F16, 8, 1, 3>(a, cus, stream);
+  if (nks <= 16) return launch_rows<F16, 8, 2, 2>(a, cus, stream);
+  if (nks <= 24) return launch_rows<F16, 8, 3, 1>(a, cus, stream);
+  if (nks <= 32) return launch_rows<F16, 8, 4, 1>(a, cus, stream);
+  // (fp16 carries four scale dwords a step: 6 steps do not fit the registers)
+  if constexpr (!F16)
+    if (nks <= 48) return launch_rows<F16, 8, 6, 1>(a, cus, stream);
+  const dim3 grid((unsigned)std::min<int64_t>((a.N + 15) / 16, cus));
+  return launch_k(linear_rows_long_kernel<F16, 8, 4>, grid, dim3(512), 0, stream, Ev{}, a);
+}
+
+hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream) {
   const bool f16 = a.x_type == MOE_FP16;
   if (a.M > 64) return f16 ? launch_tile<true, 4, 4, 4, 2>(a, stream) : launch_tile<false, 4, 4, 4, 2>(a, stream);
-  if (nks <= 8) return f16 ? launch_rows<true, 1>(a, cus, stream) : launch_rows<false, 1>(a, cus, stream);
-  if (nks <= 16) return f16 ? launch_rows<true, 2>(a, cus, stream) : launch_rows<false, 2>(a, cus, stream);
-  if (nks <= 32) return f16 ? launch_rows<true, 4>(a, cus, stream) : launch_rows<false, 4>(a, cus, stream);
-  return f16 ? launch_rows<true, 6>(a, cus, stream) : launch_rows<false, 6>(a, cus, stream);
+  // up to 64 rows: 16 at a time
+  hipError_t e = hipSuccess;
+  for (int64_t m = 0; m < a.M && e == hipSuccess; m += 16) {
+    LinearArgs b = a;
+    const size_t es = a.y_type == MOE_FP32 ? 4 : 2;
+    b.M = std::min<int64_t>(16, a.M - m);
+    b.x = reinterpret_cast<const uint16_t*>(a.x) + m * a.ldx;
+    b.y = reinterpret_cast<uint8_t*>(a.y) + m * a.ldy * es;
+    if (a.residual) b.residual = reinterpret_cast<const uint8_t*>(a.residual) + m * a.ldr * es;
+    e = f16 ? launch_16_rows<true>(b, cus, stream) : launch_16_rows<false>(b, cus, stream);
+  }
+  return e;
 }
 
 }  // namespace qmoe
