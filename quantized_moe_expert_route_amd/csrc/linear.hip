@@ -127,20 +127,28 @@ struct WeightStep {  // one K-step of 16 weight rows: a lane's codes and scales
     else sc.x = ld4(a.sp + piece * 64 + 4 * (lane & 15));
   }
   __device__ __forceinline__ void clear() { q = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void mul(const uint4 (&x)[4], v4f& acc) const {
-    const uint32_t d[4] = {q.x, q.y, q.z, q.w};
-    if constexpr (F16) {
-      const uint32_t rs[4] = {sc.x, sc.y, sc.z, sc.w};
+  // against CT column tiles of x: acc[u] += w x[u]
+  template <int CT>
+  __device__ __forceinline__ void mul_columns(const uint4 (&x)[CT][4], v4f (&acc)[CT]) const {
+    const uint32_t d[4] = {q.x, q.y, q.z, q.w}, rs[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const v4f p = mfma_f16(fp4x8_f16(d[j]), __builtin_bit_cast(v8h, x[j]), v4f{0.f, 0.f, 0.f, 0.f});
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (F16) {
+        const v8h wf = fp4x8_f16(d[j]);
+        float f[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += p[i] * e8m0_value((rs[i] >> (8 * j)) & 255u);
+        for (int i = 0; i < 4; ++i) f[i] = e8m0_value((rs[i] >> (8 * j)) & 255u);
+#pragma unroll
+        for (int u = 0; u < CT; ++u) {
+          const v4f p = mfma_f16(wf, __builtin_bit_cast(v8h, x[u][j]), v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[u][i] += p[i] * f[i];
+        }
+      } else {
+        const v8s wf = fp4x8_bf16(d[j], scale_of(sc.x, j));
+#pragma unroll
+        for (int u = 0; u < CT; ++u) acc[u] = mfma_bf16(wf, __builtin_bit_cast(v8s, x[u][j]), acc[u]);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc = mfma_bf16(fp4x8_bf16(d[j], scale_of(sc.x, j)), __builtin_bit_cast(v8s, x[j]), acc);
     }
   }
 };
@@ -165,14 +173,14 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a)
   for (int d = 0; d < D; ++d)
 #pragma unroll
     for (int s = 0; s < S; ++s) load(d, s, d);
-  uint4 xf[S][4];
+  uint4 xf[S][1][4];
   const uint16_t* xr = reinterpret_cast<const uint16_t*>(a.x) + (row ? r : 0) * a.ldx;
 #pragma unroll
   for (int s = 0; s < S; ++s)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int k = 128 * (wave * S + s) + 32 * j + 8 * g;
-      xf[s][j] = row && k < K ? ld16(xr + k) : make_uint4(0, 0, 0, 0);
+      xf[s][0][j] = row && k < K ? ld16(xr + k) : make_uint4(0, 0, 0, 0);
     }
 
   auto tile_done = [&](int i, const v4f& acc) {
@@ -188,16 +196,16 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a)
     }
   };
   auto compute = [&](int d, int i, auto reload) {
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    v4f acc[1] = {{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       // a step past the last takes no part (its codes could meet a scale that
       // overflows, and zero times that is not zero)
       if (wave * S + s >= nks) ring[d][s].clear();
-      ring[d][s].mul(xf[s], acc);
+      ring[d][s].template mul_columns<1>(xf[s], acc);
       if constexpr (reload) load(d, s, i + D);
     }
-    tile_done(i, acc);
+    tile_done(i, acc[0]);
   };
   int i = 0;
   for (; i + D < own; i += D)
@@ -219,7 +227,7 @@ __global__ __launch_bounds__(64 * W) void linear_rows_long_kernel(const LinearAr
   const bool row = r < a.M;
   const uint16_t* xr = reinterpret_cast<const uint16_t*>(a.x) + (row ? r : 0) * a.ldx;
   const int ntiles = (int)((a.N + 15) / 16);
-  uint4 xf[S][4];
+  uint4 xf[S][1][4];
   WeightStep<F16> cur[S], next[S];
   auto load_w = [&](int tile, int seg) {
 #pragma unroll
@@ -229,14 +237,14 @@ __global__ __launch_bounds__(64 * W) void linear_rows_long_kernel(const LinearAr
   int buf = 0;
   load_w(blockIdx.x, 0);
   for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    v4f acc[1] = {{0.f, 0.f, 0.f, 0.f}};
     for (int seg = 0; seg < nseg; ++seg) {
 #pragma unroll
       for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int k = 128 * ((seg * W + wave) * S + s) + 32 * j + 8 * g;
-          xf[s][j] = row && k < K ? ld16(xr + k) : make_uint4(0, 0, 0, 0);
+          xf[s][0][j] = row && k < K ? ld16(xr + k) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
       for (int s = 0; s < S; ++s) cur[s] = next[s];
@@ -245,10 +253,10 @@ __global__ __launch_bounds__(64 * W) void linear_rows_long_kernel(const LinearAr
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         if ((seg * W + wave) * S + s >= nks) cur[s].clear();
-        cur[s].mul(xf[s], acc);
+        cur[s].template mul_columns<1>(xf[s], acc);
       }
     }
-    red[buf][wave][lane] = acc;
+    red[buf][wave][lane] = acc[0];
     barrier_lds();
     if (wave == buf && row) {
       v4f v = red[buf][0][lane];
@@ -271,20 +279,98 @@ static hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t stream) 
                   Ev{}, a);
 }
 
+// ----------------------------------------------------------------- tens of rows
+// 16 R columns of y for 16 CT rows of x a workgroup. The 8 waves take K-steps
+// in turn, weights and x both straight from memory to registers, one K-step
+// ahead: no operand is shared between waves, so the loop has no barrier. The
+// partial sums are joined through LDS at the end, R sub-tiles' columns at a
+// time. x is read once per 16 R columns (from the L2): R = 2 where there are
+// tiles enough.
+template <bool F16, int CT, int R>
+__global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int tiles_n) {
+  constexpr int W = 8;
+  __shared__ v4f red[W][CT][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+  const int K = (int)a.K, nks = (K + 127) / 128;
+  const int tile = (int)(blockIdx.x % tiles_n) * R;
+  const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * (16 * CT);
+  const int last = (int)((a.N + 15) / 16) - 1;
+  const uint16_t* xr[CT];
+#pragma unroll
+  for (int u = 0; u < CT; ++u)
+    xr[u] = reinterpret_cast<const uint16_t*>(a.x) + min(m0 + 16 * u + r, a.M - 1) * a.ldx + 8 * g;
+  WeightStep<F16> w[R], nw[R];
+  uint4 x[CT][4], nx[CT][4];
+  auto load = [&](int ks) {
+    const int kc = min(ks, nks - 1);
+#pragma unroll
+    for (int t = 0; t < R; ++t) nw[t].load(a, (size_t)min(tile + t, last) * nks + kc, lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = 128 * kc + 32 * j;
+      const bool in = k < K;  // K is a multiple of 32: whole operands
+#pragma unroll
+      for (int u = 0; u < CT; ++u) nx[u][j] = in ? ld16(xr[u] + k) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  v4f acc[R][CT];
+#pragma unroll
+  for (int t = 0; t < R; ++t)
+#pragma unroll
+    for (int u = 0; u < CT; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
+  load(wave);
+  for (int ks = wave; ks < nks; ks += W) {
+#pragma unroll
+    for (int t = 0; t < R; ++t) w[t] = nw[t];
+#pragma unroll
+    for (int u = 0; u < CT; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[u][j] = nx[u][j];
+    load(ks + W);
+#pragma unroll
+    for (int t = 0; t < R; ++t) w[t].template mul_columns<CT>(x, acc[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    if (t) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < CT; ++u) red[wave][u][lane] = acc[t][u];
+    __syncthreads();
+    if (wave < CT) {
+      v4f v = red[0][wave][lane];
+#pragma unroll
+      for (int q = 1; q < W; ++q) v += red[q][wave][lane];
+      const int64_t m = m0 + 16 * wave + r;
+      if (m < a.M && tile + t <= last) store4(a, m, (int64_t)(tile + t) * 16 + 4 * g, v);
+    }
+  }
+}
+
 // ----------------------------------------------------------------- many rows
+// Where x's 16-byte chunk c (of a row's 16 in a K-step) of row m of a 16-row
+// block lies in LDS, in chunks: operand j = c / 4 of the block is 64
+// consecutive chunks, lane 16 g + r reading row r, g = c % 4. The rows of a
+// group are exchanged by r ^ c, so that the 16 lanes that write a row's
+// chunks, like the 16 that read a group, meet all banks.
+__device__ __forceinline__ int x_slot(int block, int c, int m) {
+  return (block * 4 + (c >> 2)) * 64 + 16 * (c & 3) + (m ^ c);
+}
+
 // A workgroup of WN x WM waves computes BN = 16 TN WN columns of y for BM =
-// 16 TM WM rows of x; a wave 16 TN x 16 TM of it. x goes through LDS in the
-// MFMA's operand order (a fragment of 16 rows x 32 K is 1 KB contiguous, read
-// back in lane order), two buffers of one K-step of 128, the next step's x in
-// registers meanwhile; weights go straight from their packed form to
-// registers, one K-step ahead, and are widened there: a wave's rows are read
-// by WM waves only.
+// 16 TM WM rows of x; a wave 16 TN x 16 TM of it. x goes through LDS (two
+// buffers of one K-step of 128; whole 256-byte row pieces are read, and kept
+// in registers for two steps until their buffer is free); weights go straight
+// from their packed form to registers, PW steps ahead, and are widened there:
+// a wave's rows are read by WM waves only. With one step ahead a step took
+// 2.2 us, the weights' latency, where its products take 0.85.
 template <bool F16, int TN, int TM, int WN, int WM>
 __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearArgs a, int tiles_m, int tiles_n) {
   constexpr int W = WN * WM, BM = 16 * TM * WM, BN = 16 * TN * WN;
-  constexpr int NF = BM / 16 * 4;        // fragments of a K-step
-  constexpr int NX = (NF + W - 1) / W;   // of them staged by a wave
-  __shared__ uint4 xs[2][NF][64];
+  constexpr int NX = BM / 4 / W;  // pieces of 4 rows x 128 K staged by a wave
+  constexpr int PW = 4;           // weight steps in registers
+  static_assert(BM % (4 * W) == 0, "whole pieces");
+  __shared__ uint4 xs[2][BM * 16];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int wn = wave % WN, wm = wave / WN;
@@ -306,43 +392,43 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
   const int64_t m0 = (int64_t)(first + in % rows) * BM;
   const int64_t n0 = (int64_t)(in / rows) * BN;
 
-  const uint16_t* xp = reinterpret_cast<const uint16_t*>(a.x);
   const uint16_t* xr[NX];
 #pragma unroll
-  for (int i = 0; i < NX; ++i) {
-    const int f = min(wave + i * W, NF - 1);
-    xr[i] = xp + min(m0 + 16 * (f >> 2) + r, a.M - 1) * a.ldx + 32 * (f & 3) + 8 * g;
-  }
-  uint4 xv[NX];
-  auto load_x = [&](int ks) {
-    if (128 * ks + 128 <= K) {
+  for (int i = 0; i < NX; ++i)
+    xr[i] = reinterpret_cast<const uint16_t*>(a.x) + min(m0 + 4 * (wave * NX + i) + g, a.M - 1) * a.ldx;
+  uint4 xv[2][NX];
+  auto load_x = [&](uint4(&v)[NX], int ks) {
+    const int k = 128 * min(ks, nks - 1);
+    // K's last step may end inside a row piece: zero there (as the codes are)
+    const bool in_k = k + 8 * r < K;
+    const int at = in_k ? k + 8 * r : 0;
 #pragma unroll
-      for (int i = 0; i < NX; ++i) xv[i] = ld16(xr[i] + 128 * ks);
-    } else {
+    for (int i = 0; i < NX; ++i) v[i] = ld16(xr[i] + at);
+    if (k + 128 > K) {
 #pragma unroll
-      for (int i = 0; i < NX; ++i) {
-        const int k = 128 * ks + 32 * (min(wave + i * W, NF - 1) & 3) + 8 * g;
-        xv[i] = k < K ? ld16(xr[i] + 128 * ks) : make_uint4(0, 0, 0, 0);
-      }
+      for (int i = 0; i < NX; ++i) v[i] = in_k ? v[i] : make_uint4(0, 0, 0, 0);
     }
   };
-  auto put_x = [&](int buf) {
+  auto put_x = [&](const uint4(&v)[NX], int buf) {
 #pragma unroll
-    for (int i = 0; i < NX; ++i)
-      if (NF % W == 0 || wave + i * W < NF) xs[buf][wave + i * W][lane] = xv[i];
+    for (int i = 0; i < NX; ++i) {
+      const int piece = wave * NX + i;
+      xs[buf][x_slot(piece >> 2, r, 4 * (piece & 3) + g)] = v[i];
+    }
   };
   // row blocks past N: the last one again (not stored)
   size_t rb[TN];
 #pragma unroll
   for (int t = 0; t < TN; ++t)
     rb[t] = (size_t)min(n0 / 16 + wn * TN + t, (a.N + 15) / 16 - 1) * nks;
-  uint4 q[TN], nq[TN];
-  uint32_t sc[TN], nsc[TN];
-  auto load_w = [&](int ks) {
+  uint4 q[PW][TN];
+  uint32_t sc[PW][TN];
+  auto load_w = [&](int p, int ks) {
+    const int kc = min(ks, nks - 1);
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
-      nq[t] = ld16(a.wp + (rb[t] + ks) * 1024 + 16 * lane);
-      nsc[t] = ld4(a.sp + (rb[t] + ks) * 64 + 4 * r);
+      q[p][t] = ld16(a.wp + (rb[t] + kc) * 1024 + 16 * lane);
+      sc[p][t] = ld4(a.sp + (rb[t] + kc) * 64 + 4 * r);
     }
   };
 
@@ -351,41 +437,44 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
   for (int t = 0; t < TN; ++t)
 #pragma unroll
     for (int u = 0; u < TM; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
-  load_x(0);
-  load_w(0);
-  put_x(0);
+  load_x(xv[0], 0);
+  load_x(xv[1], 1);
+#pragma unroll
+  for (int p = 0; p < PW; ++p) load_w(p, p);
+  put_x(xv[0], 0);
+  load_x(xv[0], 2);
   barrier_lds();
-  for (int ks = 0; ks < nks; ++ks) {
+  for (int k0 = 0; k0 < nks; k0 += PW) {
 #pragma unroll
-    for (int t = 0; t < TN; ++t) { q[t] = nq[t]; sc[t] = nsc[t]; }
-    if (ks + 1 < nks) {
-      load_x(ks + 1);
-      load_w(ks + 1);
-    }
+    for (int p = 0; p < PW; ++p) {
+      const int ks = k0 + p;
+      if (ks >= nks) break;
+      // step ks + 1's x into the buffer that step ks - 1 was read from
+      put_x(xv[(p + 1) & 1], (p + 1) & 1);
+      load_x(xv[(p + 1) & 1], ks + 3);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v8s wf[TN];
+      for (int j = 0; j < 4; ++j) {
+        v8s wf[TN];
 #pragma unroll
-      for (int t = 0; t < TN; ++t) {
-        const uint32_t d = j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w;
-        wf[t] = fp4x8_bf16(d, scale_of(sc[t], j));
-      }
+        for (int t = 0; t < TN; ++t) {
+          const uint32_t d = j == 0 ? q[p][t].x : j == 1 ? q[p][t].y : j == 2 ? q[p][t].z : q[p][t].w;
+          wf[t] = fp4x8_bf16(d, scale_of(sc[p][t], j));
+        }
 #pragma unroll
-      for (int u = 0; u < TM; ++u) {
-        const uint4 f = xs[ks & 1][(wm * TM + u) * 4 + j][lane];
-        if constexpr (F16) {
-          v8s hi, lo;
-          fp16x8_planes(f, hi, lo);
+        for (int u = 0; u < TM; ++u) {
+          const uint4 f = xs[p & 1][x_slot(wm * TM + u, 4 * j + g, r)];
+          if constexpr (F16) {
+            v8s hi, lo;
+            fp16x8_planes(f, hi, lo);
 #pragma unroll
-          for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], lo, mfma_bf16(wf[t], hi, acc[t][u]));
-        } else {
+            for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], lo, mfma_bf16(wf[t], hi, acc[t][u]));
+          } else {
 #pragma unroll
-          for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], __builtin_bit_cast(v8s, f), acc[t][u]);
+            for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], __builtin_bit_cast(v8s, f), acc[t][u]);
+          }
         }
       }
-    }
-    if (ks + 1 < nks) {
-      put_x((ks + 1) & 1);  // the buffer of step ks - 1: read by nobody since the last barrier
+      load_w(p, ks + PW);
       barrier_lds();
     }
   }
@@ -419,21 +508,28 @@ static hipError_t launch_16_rows(const LinearArgs& a, int cus, hipStream_t strea
   return launch_k(linear_rows_long_kernel<F16, 8, 4>, grid, dim3(512), 0, stream, Ev{}, a);
 }
 
+template <bool F16, int CT>
+static hipError_t launch_mid(const LinearArgs& a, int cus, hipStream_t stream) {
+  const int64_t tiles = (a.N + 15) / 16, rows = (a.M + 16 * CT - 1) / (16 * CT);
+  if (tiles * rows <= cus)
+    return launch_k(linear_mid_kernel<F16, CT, 1>, dim3((unsigned)(tiles * rows)), dim3(512), 0, stream, Ev{}, a,
+                    (int)tiles);
+  const int64_t pairs = (tiles + 1) / 2;
+  return launch_k(linear_mid_kernel<F16, CT, 2>, dim3((unsigned)(pairs * rows)), dim3(512), 0, stream, Ev{}, a,
+                  (int)pairs);
+}
+
+template <bool F16>
+static hipError_t launch_type(const LinearArgs& a, int cus, hipStream_t stream) {
+  if (a.M <= 16) return launch_16_rows<F16>(a, cus, stream);
+  if (a.M <= 32) return launch_mid<F16, 2>(a, cus, stream);
+  if (a.M <= 64 || getenv("LMID")) return launch_mid<F16, 4>(a, cus, stream);
+  if (getenv("LT2")) return launch_tile<F16, 2, 4, 4, 2>(a, stream);
+  return launch_tile<F16, 4, 4, 4, 2>(a, stream);
+}
+
 hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream) {
-  const bool f16 = a.x_type == MOE_FP16;
-  if (a.M > 64) return f16 ? launch_tile<true, 4, 4, 4, 2>(a, stream) : launch_tile<false, 4, 4, 4, 2>(a, stream);
-  // up to 64 rows: 16 at a time
-  hipError_t e = hipSuccess;
-  for (int64_t m = 0; m < a.M && e == hipSuccess; m += 16) {
-    LinearArgs b = a;
-    const size_t es = a.y_type == MOE_FP32 ? 4 : 2;
-    b.M = std::min<int64_t>(16, a.M - m);
-    b.x = reinterpret_cast<const uint16_t*>(a.x) + m * a.ldx;
-    b.y = reinterpret_cast<uint8_t*>(a.y) + m * a.ldy * es;
-    if (a.residual) b.residual = reinterpret_cast<const uint8_t*>(a.residual) + m * a.ldr * es;
-    e = f16 ? launch_16_rows<true>(b, cus, stream) : launch_16_rows<false>(b, cus, stream);
-  }
-  return e;
+  return a.x_type == MOE_FP16 ? launch_type<true>(a, cus, stream) : launch_type<false>(a, cus, stream);
 }
 
 }  // namespace qmoe
