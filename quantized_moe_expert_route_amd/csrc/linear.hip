@@ -109,6 +109,19 @@ __device__ __forceinline__ float scale_of(uint32_t d, int j) {
   return j == 0 ? scale_operand<0>(d) : j == 1 ? scale_operand<1>(d) : j == 2 ? scale_operand<2>(d) : scale_operand<3>(d);
 }
 
+__device__ __forceinline__ float scale_value(uint32_t d, int j) {
+  return j == 0 ? e8m0_value<0>(d) : j == 1 ? e8m0_value<1>(d) : j == 2 ? e8m0_value<2>(d) : e8m0_value<3>(d);
+}
+
+// Where x's 16-byte chunk c (of a row's 16 in a K-step) of row m of a 16-row
+// block lies in LDS, in chunks: operand j = c / 4 of the block is 64
+// consecutive chunks, lane 16 g + r reading row r, g = c % 4. The rows of a
+// group are exchanged by r ^ c, so that the 16 lanes that write a row's
+// chunks, like the 16 that read a group, meet all banks.
+__device__ __forceinline__ int x_slot(int block, int c, int m) {
+  return (block * 4 + (c >> 2)) * 64 + 16 * (c & 3) + (m ^ c);
+}
+
 // ----------------------------------------------------------------- few rows
 // A workgroup of W waves computes 16 columns of y at a time for up to 16 rows
 // of x; the waves split K. Wave w owns K-steps w S .. w S + S - 1 of 128 and
@@ -127,28 +140,26 @@ struct WeightStep {  // one K-step of 16 weight rows: a lane's codes and scales
     else sc.x = ld4(a.sp + piece * 64 + 4 * (lane & 15));
   }
   __device__ __forceinline__ void clear() { q = make_uint4(0, 0, 0, 0); }
-  // against CT column tiles of x: acc[u] += w x[u]
+  // MFMA j (K 32 j .. + 31) against CT column tiles: acc[u] += w x[u]
   template <int CT>
-  __device__ __forceinline__ void mul_columns(const uint4 (&x)[CT][4], v4f (&acc)[CT]) const {
-    const uint32_t d[4] = {q.x, q.y, q.z, q.w}, rs[4] = {sc.x, sc.y, sc.z, sc.w};
+  __device__ __forceinline__ void mul(int j, const uint4 (&x)[CT], v4f (&acc)[CT]) const {
+    const uint32_t d = j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w;
+    if constexpr (F16) {
+      const uint32_t rs[4] = {sc.x, sc.y, sc.z, sc.w};
+      const v8h wf = fp4x8_f16(d);
+      float f[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (F16) {
-        const v8h wf = fp4x8_f16(d[j]);
-        float f[4];
+      for (int i = 0; i < 4; ++i) f[i] = scale_value(rs[i], j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = e8m0_value((rs[i] >> (8 * j)) & 255u);
+      for (int u = 0; u < CT; ++u) {
+        const v4f p = mfma_f16(wf, __builtin_bit_cast(v8h, x[u]), v4f{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-        for (int u = 0; u < CT; ++u) {
-          const v4f p = mfma_f16(wf, __builtin_bit_cast(v8h, x[u][j]), v4f{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[u][i] += p[i] * f[i];
-        }
-      } else {
-        const v8s wf = fp4x8_bf16(d[j], scale_of(sc.x, j));
-#pragma unroll
-        for (int u = 0; u < CT; ++u) acc[u] = mfma_bf16(wf, __builtin_bit_cast(v8s, x[u][j]), acc[u]);
+        for (int i = 0; i < 4; ++i) acc[u][i] += p[i] * f[i];
       }
+    } else {
+      const v8s wf = fp4x8_bf16(d, scale_of(sc.x, j));
+#pragma unroll
+      for (int u = 0; u < CT; ++u) acc[u] = mfma_bf16(wf, __builtin_bit_cast(v8s, x[u]), acc[u]);
     }
   }
 };
@@ -156,6 +167,7 @@ struct WeightStep {  // one K-step of 16 weight rows: a lane's codes and scales
 template <bool F16, int W, int S, int D>
 __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a) {
   __shared__ v4f red[2][W][64];
+  __shared__ uint4 xs[W][256];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int K = (int)a.K, nks = (K + 127) / 128;
@@ -169,19 +181,34 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a)
     const int tile = blockIdx.x + min(i, own - 1) * step;
     ring[d][s].load(a, (size_t)tile * nks + min(wave * S + s, nks - 1), lane);
   };
+  // x: whole 256-byte row pieces, four rows a load, turned into operands
+  // through 4 KB of LDS of the wave's own as the first tile's steps come to
+  // them. (Every CU reads all of x: 16 x 6144 is 50 MB from the L2s, 2.6 us of
+  // their bandwidth, so the first products do not wait for all of it.)
+  uint4 xf[S][4][1], xv[S][4];
+  const uint16_t* xp = reinterpret_cast<const uint16_t*>(a.x);
 #pragma unroll
-  for (int d = 0; d < D; ++d)
+  for (int s = 0; s < S; ++s) {
+    load(0, s, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = 128 * (wave * S + s) + 8 * r, m = 4 * i + g;
+      xv[s][i] = m < a.M && k < K ? ld16(xp + m * a.ldx + k) : make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < D; ++d)
 #pragma unroll
     for (int s = 0; s < S; ++s) load(d, s, d);
-  uint4 xf[S][1][4];
-  const uint16_t* xr = reinterpret_cast<const uint16_t*>(a.x) + (row ? r : 0) * a.ldx;
+  auto operands = [&](int s) {
+    uint4* mine = &xs[wave][0];
 #pragma unroll
-  for (int s = 0; s < S; ++s)
+    for (int i = 0; i < 4; ++i) mine[x_slot(0, r, 4 * i + g)] = xv[s][i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = 128 * (wave * S + s) + 32 * j + 8 * g;
-      xf[s][0][j] = row && k < K ? ld16(xr + k) : make_uint4(0, 0, 0, 0);
-    }
+    for (int j = 0; j < 4; ++j) xf[s][j][0] = mine[x_slot(0, 4 * j + g, r)];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
 
   auto tile_done = [&](int i, const v4f& acc) {
     const int buf = i & 1;
@@ -195,76 +222,36 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a)
       store4(a, r, (int64_t)(blockIdx.x + i * step) * 16 + 4 * g, v);
     }
   };
-  auto compute = [&](int d, int i, auto reload) {
+  auto compute = [&](int d, int i, auto reload, auto first) {
     v4f acc[1] = {{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
+      if constexpr (first) operands(s);
       // a step past the last takes no part (its codes could meet a scale that
       // overflows, and zero times that is not zero)
       if (wave * S + s >= nks) ring[d][s].clear();
-      ring[d][s].template mul_columns<1>(xf[s], acc);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ring[d][s].template mul<1>(j, xf[s][j], acc);
       if constexpr (reload) load(d, s, i + D);
     }
     tile_done(i, acc[0]);
   };
-  int i = 0;
-  for (; i + D < own; i += D)
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  if constexpr (D == 1) {  // one tile
+    compute(0, 0, no, yes);
+  } else {
+    compute(0, 0, yes, yes);
 #pragma unroll
-    for (int d = 0; d < D; ++d) compute(d, i + d, std::true_type{});
+    for (int d = 1; d < D; ++d)
+      if (d < own) compute(d, d, yes, no);
+    int i = D;
+    for (; i + D < own; i += D)
 #pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (i + d < own) compute(d, i + d, std::false_type{});
-}
-
-// K beyond the W S steps that the waves hold: segment after segment, x loaded
-// again for each (from the cache), the next segment's weights under way.
-template <bool F16, int W, int S>
-__global__ __launch_bounds__(64 * W) void linear_rows_long_kernel(const LinearArgs a) {
-  __shared__ v4f red[2][W][64];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int r = lane & 15, g = lane >> 4;
-  const int K = (int)a.K, nks = (K + 127) / 128, nseg = (nks + W * S - 1) / (W * S);
-  const bool row = r < a.M;
-  const uint16_t* xr = reinterpret_cast<const uint16_t*>(a.x) + (row ? r : 0) * a.ldx;
-  const int ntiles = (int)((a.N + 15) / 16);
-  uint4 xf[S][1][4];
-  WeightStep<F16> cur[S], next[S];
-  auto load_w = [&](int tile, int seg) {
+      for (int d = 0; d < D; ++d) compute(d, i + d, yes, no);
 #pragma unroll
-    for (int s = 0; s < S; ++s)
-      next[s].load(a, (size_t)tile * nks + min((seg * W + wave) * S + s, nks - 1), lane);
-  };
-  int buf = 0;
-  load_w(blockIdx.x, 0);
-  for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-    v4f acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-    for (int seg = 0; seg < nseg; ++seg) {
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = 128 * ((seg * W + wave) * S + s) + 32 * j + 8 * g;
-          xf[s][0][j] = row && k < K ? ld16(xr + k) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-      for (int s = 0; s < S; ++s) cur[s] = next[s];
-      if (seg + 1 < nseg) load_w(tile, seg + 1);
-      else load_w(min(tile + (int)gridDim.x, ntiles - 1), 0);
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        if ((seg * W + wave) * S + s >= nks) cur[s].clear();
-        cur[s].template mul_columns<1>(xf[s], acc);
-      }
-    }
-    red[buf][wave][lane] = acc[0];
-    barrier_lds();
-    if (wave == buf && row) {
-      v4f v = red[buf][0][lane];
-#pragma unroll
-      for (int w = 1; w < W; ++w) v += red[buf][w][lane];
-      store4(a, r, (int64_t)tile * 16 + 4 * g, v);
-    }
-    buf ^= 1;
+    for (int d = 0; d < D; ++d)
+      if (i + d < own) compute(d, i + d, no, no);
   }
 }
 
@@ -281,37 +268,41 @@ static hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t stream) 
 
 // ----------------------------------------------------------------- tens of rows
 // 16 R columns of y for 16 CT rows of x a workgroup. The 8 waves take K-steps
-// in turn, weights and x both straight from memory to registers, one K-step
-// ahead: no operand is shared between waves, so the loop has no barrier. The
-// partial sums are joined through LDS at the end, R sub-tiles' columns at a
-// time. x is read once per 16 R columns (from the L2): R = 2 where there are
-// tiles enough.
+// in turn and share no operand, so the loop has no barrier: weights go from
+// memory to registers, x through a piece of LDS of the wave's own (whole
+// 256-byte row pieces are read: operand-shaped loads, 64 bytes of 16 rows
+// each, took three times as long), both P of the wave's steps ahead. The
+// partial sums are joined through LDS at the end. x is read once per 16 R
+// columns (from the L2): R = 2 where there are tiles enough.
 template <bool F16, int CT, int R>
 __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int tiles_n) {
-  constexpr int W = 8;
-  __shared__ v4f red[W][CT][64];
+  constexpr int W = 8, P = CT == 1 ? 4 : 2;
+  __shared__ uint4 xs[W][CT * 256];  // and the partial sums [W][CT][64]
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int K = (int)a.K, nks = (K + 127) / 128;
   const int tile = (int)(blockIdx.x % tiles_n) * R;
   const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * (16 * CT);
   const int last = (int)((a.N + 15) / 16) - 1;
-  const uint16_t* xr[CT];
+  const uint16_t* xr[CT * 4];
 #pragma unroll
-  for (int u = 0; u < CT; ++u)
-    xr[u] = reinterpret_cast<const uint16_t*>(a.x) + min(m0 + 16 * u + r, a.M - 1) * a.ldx + 8 * g;
-  WeightStep<F16> w[R], nw[R];
-  uint4 x[CT][4], nx[CT][4];
-  auto load = [&](int ks) {
-    const int kc = min(ks, nks - 1);
+  for (int i = 0; i < CT * 4; ++i)
+    xr[i] = reinterpret_cast<const uint16_t*>(a.x) + min(m0 + 4 * i + g, a.M - 1) * a.ldx;
+  WeightStep<F16> w[P][R];
+  uint4 xv[P][CT * 4];
+  auto load_w = [&](int p, int ks) {
 #pragma unroll
-    for (int t = 0; t < R; ++t) nw[t].load(a, (size_t)min(tile + t, last) * nks + kc, lane);
+    for (int t = 0; t < R; ++t) w[p][t].load(a, (size_t)min(tile + t, last) * nks + min(ks, nks - 1), lane);
+  };
+  auto load_x = [&](int p, int ks) {
+    const int k = 128 * min(ks, nks - 1);
+    const bool in_k = k + 8 * r < K;
+    const int at = in_k ? k + 8 * r : 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = 128 * kc + 32 * j;
-      const bool in = k < K;  // K is a multiple of 32: whole operands
+    for (int i = 0; i < CT * 4; ++i) xv[p][i] = ld16(xr[i] + at);
+    if (k + 128 > K) {
 #pragma unroll
-      for (int u = 0; u < CT; ++u) nx[u][j] = in ? ld16(xr[u] + k) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < CT * 4; ++i) xv[p][i] = in_k ? xv[p][i] : make_uint4(0, 0, 0, 0);
     }
   };
   v4f acc[R][CT];
@@ -319,21 +310,36 @@ __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int
   for (int t = 0; t < R; ++t)
 #pragma unroll
     for (int u = 0; u < CT; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
-  load(wave);
-  for (int ks = wave; ks < nks; ks += W) {
 #pragma unroll
-    for (int t = 0; t < R; ++t) w[t] = nw[t];
+  for (int p = 0; p < P; ++p) load_w(p, wave + p * W);
 #pragma unroll
-    for (int u = 0; u < CT; ++u)
+  for (int p = 0; p < P; ++p) load_x(p, wave + p * W);
+  for (int k0 = wave; k0 < nks; k0 += P * W) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[u][j] = nx[u][j];
-    load(ks + W);
+    for (int p = 0; p < P; ++p) {
+      const int ks = k0 + p * W;
+      if (ks >= nks) break;
 #pragma unroll
-    for (int t = 0; t < R; ++t) w[t].template mul_columns<CT>(x, acc[t]);
+      for (int i = 0; i < CT * 4; ++i) xs[wave][x_slot(i >> 2, r, 4 * (i & 3) + g)] = xv[p][i];
+      // the wave's lanes read what its other lanes wrote: LDS keeps a wave's order
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      load_x(p, ks + P * W);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4 x[CT];
+#pragma unroll
+        for (int u = 0; u < CT; ++u) x[u] = xs[wave][x_slot(u, 4 * j + g, r)];
+#pragma unroll
+        for (int t = 0; t < R; ++t) w[p][t].template mul<CT>(j, x, acc[t]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      load_w(p, ks + P * W);
+    }
   }
+  v4f(*red)[CT][64] = reinterpret_cast<v4f(*)[CT][64]>(&xs[0][0]);
 #pragma unroll
   for (int t = 0; t < R; ++t) {
-    if (t) __syncthreads();
+    __syncthreads();
 #pragma unroll
     for (int u = 0; u < CT; ++u) red[wave][u][lane] = acc[t][u];
     __syncthreads();
@@ -348,21 +354,13 @@ __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int
 }
 
 // ----------------------------------------------------------------- many rows
-// Where x's 16-byte chunk c (of a row's 16 in a K-step) of row m of a 16-row
-// block lies in LDS, in chunks: operand j = c / 4 of the block is 64
-// consecutive chunks, lane 16 g + r reading row r, g = c % 4. The rows of a
-// group are exchanged by r ^ c, so that the 16 lanes that write a row's
-// chunks, like the 16 that read a group, meet all banks.
-__device__ __forceinline__ int x_slot(int block, int c, int m) {
-  return (block * 4 + (c >> 2)) * 64 + 16 * (c & 3) + (m ^ c);
-}
-
 // A workgroup of WN x WM waves computes BN = 16 TN WN columns of y for BM =
 // 16 TM WM rows of x; a wave 16 TN x 16 TM of it. x goes through LDS (two
 // buffers of one K-step of 128; whole 256-byte row pieces are read, and kept
 // in registers for two steps until their buffer is free); weights go straight
 // from their packed form to registers, PW steps ahead, and are widened there:
-// a wave's rows are read by WM waves only. With one step ahead a step took
+// a wave's rows are read by WM waves only. fp16 x is split into two bf16 on its
+// way into LDS (exact; the same products, twice the MFMAs). With one step ahead a step took
 // 2.2 us, the weights' latency, where its products take 0.85.
 template <bool F16, int TN, int TM, int WN, int WM>
 __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearArgs a, int tiles_m, int tiles_n) {
@@ -370,7 +368,8 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
   constexpr int NX = BM / 4 / W;  // pieces of 4 rows x 128 K staged by a wave
   constexpr int PW = 4;           // weight steps in registers
   static_assert(BM % (4 * W) == 0, "whole pieces");
-  __shared__ uint4 xs[2][BM * 16];
+  constexpr int P = F16 ? 2 : 1;  // bf16 planes of x
+  __shared__ uint4 xs[2][P][BM * 16];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int wn = wave % WN, wm = wave / WN;
@@ -413,7 +412,15 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const int piece = wave * NX + i;
-      xs[buf][x_slot(piece >> 2, r, 4 * (piece & 3) + g)] = v[i];
+      const int at = x_slot(piece >> 2, r, 4 * (piece & 3) + g);
+      if constexpr (F16) {
+        v8s hi, lo;
+        fp16x8_planes(v[i], hi, lo);
+        xs[buf][0][at] = __builtin_bit_cast(uint4, hi);
+        xs[buf][P - 1][at] = __builtin_bit_cast(uint4, lo);
+      } else {
+        xs[buf][0][at] = v[i];
+      }
     }
   };
   // row blocks past N: the last one again (not stored)
@@ -462,15 +469,12 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
         }
 #pragma unroll
         for (int u = 0; u < TM; ++u) {
-          const uint4 f = xs[p & 1][x_slot(wm * TM + u, 4 * j + g, r)];
-          if constexpr (F16) {
-            v8s hi, lo;
-            fp16x8_planes(f, hi, lo);
+          const int at = x_slot(wm * TM + u, 4 * j + g, r);
 #pragma unroll
-            for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], lo, mfma_bf16(wf[t], hi, acc[t][u]));
-          } else {
+          for (int pl = P - 1; pl >= 0; --pl) {
+            const v8s f = __builtin_bit_cast(v8s, xs[p & 1][pl][at]);
 #pragma unroll
-            for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], __builtin_bit_cast(v8s, f), acc[t][u]);
+            for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], f, acc[t][u]);
           }
         }
       }
@@ -494,38 +498,48 @@ static hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
                   Ev{}, a, (int)tm, (int)tn);
 }
 
+template <bool F16, int CT, int R>
+static hipError_t launch_mid(const LinearArgs& a, hipStream_t stream) {
+  const int64_t tiles = (a.N + 16 * R - 1) / (16 * R), rows = (a.M + 16 * CT - 1) / (16 * CT);
+  return launch_k(linear_mid_kernel<F16, CT, R>, dim3((unsigned)(tiles * rows)), dim3(512), 0, stream, Ev{}, a,
+                  (int)tiles);
+}
+
 template <bool F16>
 static hipError_t launch_16_rows(const LinearArgs& a, int cus, hipStream_t stream) {
   const int64_t nks = (a.K + 127) / 128;
   if (nks <= 8) return launch_rows<F16, 8, 1, 3>(a, cus, stream);
   if (nks <= 16) return launch_rows<F16, 8, 2, 2>(a, cus, stream);
   if (nks <= 24) return launch_rows<F16, 8, 3, 1>(a, cus, stream);
-  if (nks <= 32) return launch_rows<F16, 8, 4, 1>(a, cus, stream);
-  // (fp16 carries four scale dwords a step: 6 steps do not fit the registers)
-  if constexpr (!F16)
+  // (fp16 carries four scale dwords a step: more steps do not fit the registers)
+  if constexpr (!F16) {
+    if (nks <= 32) return launch_rows<F16, 8, 4, 1>(a, cus, stream);
     if (nks <= 48) return launch_rows<F16, 8, 6, 1>(a, cus, stream);
-  const dim3 grid((unsigned)std::min<int64_t>((a.N + 15) / 16, cus));
-  return launch_k(linear_rows_long_kernel<F16, 8, 4>, grid, dim3(512), 0, stream, Ev{}, a);
-}
-
-template <bool F16, int CT>
-static hipError_t launch_mid(const LinearArgs& a, int cus, hipStream_t stream) {
-  const int64_t tiles = (a.N + 15) / 16, rows = (a.M + 16 * CT - 1) / (16 * CT);
-  if (tiles * rows <= cus)
-    return launch_k(linear_mid_kernel<F16, CT, 1>, dim3((unsigned)(tiles * rows)), dim3(512), 0, stream, Ev{}, a,
-                    (int)tiles);
-  const int64_t pairs = (tiles + 1) / 2;
-  return launch_k(linear_mid_kernel<F16, CT, 2>, dim3((unsigned)(pairs * rows)), dim3(512), 0, stream, Ev{}, a,
-                  (int)pairs);
+  }
+  // a longer K: x from the L2 for every 16 or 32 columns
+  return (a.N + 15) / 16 <= cus ? launch_mid<F16, 1, 1>(a, stream) : launch_mid<F16, 1, 2>(a, stream);
 }
 
 template <bool F16>
 static hipError_t launch_type(const LinearArgs& a, int cus, hipStream_t stream) {
   if (a.M <= 16) return launch_16_rows<F16>(a, cus, stream);
-  if (a.M <= 32) return launch_mid<F16, 2>(a, cus, stream);
-  if (a.M <= 64 || getenv("LMID")) return launch_mid<F16, 4>(a, cus, stream);
-  if (getenv("LT2")) return launch_tile<F16, 2, 4, 4, 2>(a, stream);
-  return launch_tile<F16, 4, 4, 4, 2>(a, stream);
+  // Rounds of workgroups over the CUs times a round's time per K-step, in
+  // units of 10 ns (one workgroup a CU, K 6144; e.g. M 64, N 6144: 17.9 us by
+  // the second against 28.1 by the third; M 256: 50.5, 31.1 and 45.1 by the
+  // second to fourth; M 4096: 304, 298 and 248 by the last three).
+  auto cost = [&](int64_t bm, int64_t bn, int per) {
+    const int64_t groups = ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);
+    return ((groups + cus - 1) / cus) * per;
+  };
+  const int64_t c[5] = {cost(32, 16, F16 ? 15 : 11), cost(32, 32, F16 ? 22 : 17), cost(64, 128, F16 ? 110 : 50),
+                        cost(128, 128, F16 ? 195 : 82), cost(128, 256, F16 ? 280 : 140)};
+  switch (std::min_element(c, c + 5) - c) {
+    case 0: return launch_mid<F16, 2, 1>(a, stream);
+    case 1: return launch_mid<F16, 2, 2>(a, stream);
+    case 2: return launch_tile<F16, 2, 2, 4, 2>(a, stream);
+    case 3: return launch_tile<F16, 2, 4, 4, 2>(a, stream);
+    default: return launch_tile<F16, 4, 4, 4, 2>(a, stream);
+  }
 }
 
 hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream) {

@@ -45,10 +45,13 @@ __device__ __forceinline__ v4f mfma_f16(v8h a, v8h b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// E8M0 scale byte -> binary32: 2^(s - 127), NaN for 255 (the format's NaN).
-__device__ __forceinline__ float e8m0_value(uint32_t s) {
-  const uint32_t u = s << 23;
-  return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : u);
+// Byte J of a dword of E8M0 scales -> binary32 2^(s - 127), 2^-127 for 0 and
+// NaN for 255: E2M1's 1.0 (code 2) under that scale.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+template <int J>
+__device__ __forceinline__ float e8m0_value(uint32_t d) {
+  const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(0x22u, scale_operand<J>(d), 0);
+  return v[0];
 }
 
 // 8 fp16 values as two bf16 each, value = hi + lo exactly: hi keeps the upper
