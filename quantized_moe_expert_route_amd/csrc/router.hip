@@ -12,80 +12,7 @@
 
 namespace qmoe {
 
-// 8 consecutive elements of a row as float.
-template <int TYPE>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
-  if constexpr (TYPE == MOE_FP32) {
-    const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
-    const float4 b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 q = ld16(reinterpret_cast<const uint16_t*>(p) + i);
-    const uint32_t d[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (TYPE == MOE_BF16) {
-        v[2 * j] = __uint_as_float(d[j] << 16);
-        v[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
-      } else {
-        v[2 * j] = fp16_value((uint16_t)(d[j] & 0xFFFFu));
-        v[2 * j + 1] = fp16_value((uint16_t)(d[j] >> 16));
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ double shfl_xor_f64(double v, int o) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __shfl_xor((uint32_t)u, o, kWave), hi = __shfl_xor((uint32_t)(u >> 32), o, kWave);
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-
-// One expert and up to T tokens a workgroup: 256 threads over chunks of 8
-// elements, one float64 sum per token and thread, added over lanes, then
-// waves.
-template <int XT, int WT, int T>
-__global__ __launch_bounds__(256) void router_kernel(const RouterArgs a) {
-  __shared__ double red[4][T];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t e = blockIdx.x, m0 = (int64_t)blockIdx.y * T;
-  const int mt = (int)min((int64_t)T, a.M - m0);
-  const int H = (int)a.H;
-  double acc[T];
-#pragma unroll
-  for (int t = 0; t < T; ++t) acc[t] = 0.0;
-  for (int c = threadIdx.x * 8; c < H; c += 256 * 8) {
-    float w[8];
-    load8<WT>(a.w, e * a.H + c, w);
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      float x[8];
-      load8<XT>(a.x, (m0 + min(t, mt - 1)) * a.ldx + c, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[t] = fma((double)x[i], (double)w[i], acc[t]);
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < T; ++t) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) acc[t] += shfl_xor_f64(acc[t], o);
-    if (lane == 0) red[wave][t] = acc[t];
-  }
-  __syncthreads();
-  if ((int)threadIdx.x < mt) {
-    const int t = threadIdx.x;
-    a.logits[(m0 + t) * a.E + e] = (float)(red[0][t] + red[1][t] + red[2][t] + red[3][t]);
-  }
-}
-
-// 8 elements as P planes of bf16 whose sum they are: bf16 is one, fp16 two,
-// fp32 three (each plane keeps the upper 8 significant bits of what is left:
-// 24 = 3 x 8, exact down to bf16's smallest number). A value that is not
-// finite stays in the first.
-template <int TYPE>
-constexpr int kPlanes = TYPE == MOE_BF16 ? 1 : TYPE == MOE_FP16 ? 2 : 3;
-
+// 8 consecutive elements of a row, as loaded and as float.
 template <int TYPE>
 struct Raw8 {
   uint4 v[TYPE == MOE_FP32 ? 2 : 1];
@@ -99,6 +26,91 @@ __device__ __forceinline__ void raw8(const void* p, int64_t i, Raw8<TYPE>& q) {
     q.v[0] = ld16(reinterpret_cast<const uint16_t*>(p) + i);
   }
 }
+template <int TYPE>
+__device__ __forceinline__ void values8(const Raw8<TYPE>& q, float (&v)[8]) {
+  const uint32_t d[4] = {q.v[0].x, q.v[0].y, q.v[0].z, q.v[0].w};
+  if constexpr (TYPE == MOE_FP32) {
+    const uint32_t u[4] = {q.v[1].x, q.v[1].y, q.v[1].z, q.v[1].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(d[i]);
+      v[4 + i] = __uint_as_float(u[i]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = TYPE == MOE_BF16 ? __uint_as_float(d[j] << 16) : fp16_value((uint16_t)(d[j] & 0xFFFFu));
+      v[2 * j + 1] = TYPE == MOE_BF16 ? __uint_as_float(d[j] & 0xFFFF0000u) : fp16_value((uint16_t)(d[j] >> 16));
+    }
+  }
+}
+
+__device__ __forceinline__ double shfl_xor_f64(double v, int o) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __shfl_xor((uint32_t)u, o, kWave), hi = __shfl_xor((uint32_t)(u >> 32), o, kWave);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Up to 16 tokens: one expert and T tokens a workgroup. A wave takes 512
+// elements of H at a time, 8 a lane, all T tokens' pieces under way at once;
+// the lanes' float64 sums are added by exchanging halves (T values shrink to
+// one a lane), then the waves'. Every workgroup reads all of x: 16 x 6144 is
+// 50 MB from the L2s, 2.6 us, about the time of the float64 products.
+template <int XT, int WT, int T>
+__global__ __launch_bounds__(1024) void router_kernel(const RouterArgs a) {
+  __shared__ double red[16][T];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int64_t e = blockIdx.x;
+  const int mt = (int)a.M, H = (int)a.H;
+  double acc[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) acc[t] = 0.0;
+  for (int c = (wave * 64 + lane) * 8; c < H; c += waves * 512) {
+    Raw8<WT> wr;
+    Raw8<XT> xr[T];
+    raw8<WT>(a.w, e * a.H + c, wr);
+#pragma unroll
+    for (int t = 0; t < T; ++t) raw8<XT>(a.x, min(t, mt - 1) * a.ldx + c, xr[t]);
+    double w[8];
+    float f[8];
+    values8<WT>(wr, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = (double)f[i];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      values8<XT>(xr[t], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[t] = fma((double)f[i], w[i], acc[t]);
+    }
+  }
+  int bit = 32;
+#pragma unroll
+  for (int n = T / 2; n >= 1; n >>= 1, bit >>= 1) {
+    const bool up = lane & bit;  // keeps the upper half of the tokens
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const double give = up ? acc[i] : acc[i + n];
+      acc[i] = (up ? acc[i + n] : acc[i]) + shfl_xor_f64(give, bit);
+    }
+  }
+  for (; bit >= 1; bit >>= 1) acc[0] += shfl_xor_f64(acc[0], bit);
+  constexpr int kLanes = 64 / T;
+  if (lane % kLanes == 0) red[wave][lane / kLanes] = acc[0];
+  __syncthreads();
+  if ((int)threadIdx.x < mt) {
+    double v = 0.0;
+    for (int w = 0; w < waves; ++w) v += red[w][threadIdx.x];
+    a.logits[threadIdx.x * a.E + e] = (float)v;
+  }
+}
+
+// 8 elements as P planes of bf16 whose sum they are: bf16 is one, fp16 two,
+// fp32 three (each plane keeps the upper 8 significant bits of what is left:
+// 24 = 3 x 8, exact down to bf16's smallest number). A value that is not
+// finite stays in the first.
+template <int TYPE>
+constexpr int kPlanes = TYPE == MOE_BF16 ? 1 : TYPE == MOE_FP16 ? 2 : 3;
+
 template <int TYPE>
 __device__ __forceinline__ void planes8(const Raw8<TYPE>& q, v8s (&out)[kPlanes<TYPE>]) {
   if constexpr (TYPE == MOE_BF16) {
@@ -235,13 +247,13 @@ static hipError_t launch_tiles(const RouterArgs& a, hipStream_t stream) {
 
 template <int XT, int WT>
 static hipError_t launch_types(const RouterArgs& a, int cus, hipStream_t stream) {
-  if (a.M <= 1)
-    return launch_k(router_kernel<XT, WT, 1>, dim3((unsigned)a.E, 1), dim3(256), 0, stream, Ev{}, a);
-  if (a.M <= 4)
-    return launch_k(router_kernel<XT, WT, 4>, dim3((unsigned)a.E, 1), dim3(256), 0, stream, Ev{}, a);
-  if (a.M <= 16)
-    return launch_k(router_kernel<XT, WT, 8>, dim3((unsigned)a.E, (unsigned)((a.M + 7) / 8)), dim3(256), 0, stream,
-                    Ev{}, a);
+  if (a.M <= 16) {
+    const dim3 grid((unsigned)a.E), block(64 * (unsigned)std::min<int64_t>(16, (a.H + 511) / 512));
+    if (a.M <= 1) return launch_k(router_kernel<XT, WT, 1>, grid, block, 0, stream, Ev{}, a);
+    if (a.M <= 4) return launch_k(router_kernel<XT, WT, 4>, grid, block, 0, stream, Ev{}, a);
+    if (a.M <= 8) return launch_k(router_kernel<XT, WT, 8>, grid, block, 0, stream, Ev{}, a);
+    return launch_k(router_kernel<XT, WT, 16>, grid, block, 0, stream, Ev{}, a);
+  }
   // the largest tile that still gives every CU a workgroup
   auto groups = [&](int t) { return ((a.E + 16 * t - 1) / (16 * t)) * ((a.M + 16 * t - 1) / (16 * t)); };
   if (groups(4) >= cus) return launch_tiles<XT, WT, 4, 4, 8>(a, stream);
