@@ -7,6 +7,7 @@
 
 #include "api_util.h"
 #include "internal.h"
+#include "ops.h"
 
 #include <climits>
 #include <mutex>
@@ -93,6 +94,7 @@ Layout make_layout(const moe_shape& s) {
   const size_t Ml = std::min<size_t>(M, kSmallM);
   r.X.layer_logits = take(4 * Ml * E);
   r.X.layer_g = take(4 * Ml * k * I);
+  r.X.layer_list = take(kLayerListBytes);
   r.L.total_bytes = align256(off);
   return r;
 }

@@ -27,38 +27,51 @@ constexpr int kLayerWaves = 8;
 // Which experts the batch picked, and which slot of a token an expert is.
 struct ActiveList {
   int n;
-  uint16_t expert[kLayerMaxEntries];       // active experts, ascending
-  uint8_t slot[kLayerMaxEntries][kSmallM]; // [active][token]: the token's slot, 255: none
+  int pad[3];
+  uint16_t expert[kLayerMaxEntries];        // active experts, ascending
+  uint8_t slot[kLayerMaxEntries][kSmallM];  // [active][token]: the token's slot, 255: none
 };
+static_assert(sizeof(ActiveList) == kLayerListBytes && sizeof(ActiveList) % 16 == 0, "copied in 16-byte pieces");
 
-// From ids[t * k + j] in LDS (every thread of a 512-thread workgroup).
-__device__ __forceinline__ void build_active(const uint16_t* ids, int M, int k, int E, uint16_t* index,
-                                             ActiveList& list) {
-  const int n = M * k;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) index[e] = 0;
-  for (int i = threadIdx.x; i < kLayerMaxEntries * kSmallM / 4; i += blockDim.x)
-    reinterpret_cast<uint32_t*>(list.slot)[i] = 0xFFFFFFFFu;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) index[ids[i]] = 1;
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    int base = 0;
-    for (int c = 0; c < E; c += 64) {
-      const int e = c + (int)threadIdx.x;
-      const bool on = e < E && index[e] != 0;
-      const unsigned long long hits = __ballot(on);
-      if (on) {
-        const int at = base + __popcll(hits & ((1ull << threadIdx.x) - 1));
-        list.expert[at] = (uint16_t)e;
-        index[e] = (uint16_t)at;
-      }
-      base += __popcll(hits);
+// Top-k of two tokens' keys by one wave (the second may be all zero: unused),
+// their rounds side by side so that one's lane exchanges hide the other's. A
+// round takes the wave's largest key; of several equal ones the lowest expert
+// id 64 c + lane. Lane j < k gets slot j's expert and logit.
+template <int EC>
+__device__ __forceinline__ void topk_pair(uint32_t (&key)[2][EC], bool second, int k, int lane, uint32_t (&sel_e)[2],
+                                          float (&sel_l)[2]) {
+  for (int j = 0; j < k; ++j) {
+    uint32_t top[2], id[2];
+    unsigned long long hits[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int c = 0; c < EC; ++c) m = max(m, key[t][c]);
+      top[t] = wave_max_u32(m);
+      int at = 0;  // this lane's first key that is the largest
+#pragma unroll
+      for (int c = EC - 1; c >= 0; --c) at = key[t][c] == top[t] ? c : at;
+      id[t] = 64 * at + lane;
+      hits[t] = __ballot(m == top[t]);
     }
-    if (threadIdx.x == 0) list.n = base;
+    uint32_t win[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) win[t] = __builtin_amdgcn_readlane(id[t], __builtin_ctzll(hits[t]));
+    if ((hits[0] & (hits[0] - 1)) || (second && (hits[1] & (hits[1] - 1)))) {  // equal logits
+#pragma unroll
+      for (int t = 0; t < 2; ++t) win[t] = wave_min_u32((hits[t] >> lane) & 1 ? id[t] : 0xFFFFFFFFu);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int c = 0; c < EC; ++c) key[t][c] = win[t] == (uint32_t)(64 * c + lane) ? 0u : key[t][c];
+      if (lane == j) {
+        sel_e[t] = win[t];
+        sel_l[t] = key_to_float(top[t]);
+      }
+    }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) list.slot[index[ids[i]]][i / k] = (uint8_t)(i % k);
-  __syncthreads();
 }
 
 // Chunk c (8 elements of a K-step of 128) of token m's x in a wave's LDS: the
@@ -67,28 +80,51 @@ __device__ __forceinline__ void build_active(const uint16_t* ids, int M, int k, 
 // conflicts (writes: one row's 16 chunks; reads: one group's 16 rows).
 __device__ __forceinline__ int x13_slot(int c, int m) { return (c & 3) * 64 + 16 * (c >> 2) + (m ^ c); }
 
+// Weighted h of the batch, as the down launch reads it: per entry t * k + j and
+// K-step b of 128, a plane of 128 bf16 values, then a plane of remainders.
+__device__ __forceinline__ size_t h_at(int entry, int nb, int col, int plane) {
+  return (((size_t)entry * nb + (col >> 7)) * 2 + plane) * 128 + (col & 127);
+}
+
+constexpr int kHoldItems = 16;  // finished items a gate/up workgroup holds before it stores them
+
 // Gate/up of every active expert. Work item: 8 columns of I of one active
 // expert: one MFMA row tile of its 8 gate rows and its 8 up rows (half of a
-// packed 16-row block each, in 128-byte runs). Wave w holds K-steps w S ..
-// w S + S - 1 of x as MFMA operands in registers over all items of the
-// workgroup; the items' weights stream through a ring of two items' registers
-// (one where x takes more), each slot requested again as soon as its products
-// are issued.
+// packed 16-row block each, in 128-byte runs; the other half goes to a
+// workgroup of the same XCD). Wave w holds K-steps w S .. w S + S - 1 of x as
+// MFMA operands in registers over all items of the workgroup; the items'
+// weights stream through a ring of two items' registers (one where x takes
+// more), each slot requested again as soon as its products are issued.
+// Results wait in LDS and are stored 16 items at a time: the compiler drains
+// all loads before it lets a store's counter mix with them.
 template <int S, int EC>
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
     const uint16_t* __restrict__ x, const float* __restrict__ logits, const uint8_t* __restrict__ w13p,
     const uint8_t* __restrict__ s13p, int* __restrict__ topk_ids, float* __restrict__ topk_w,
-    uint16_t* __restrict__ gp, int M, int H, int E, int I, int k, float scaling) {
-  __shared__ ActiveList list;
-  __shared__ uint16_t index[kRouteMaxE];
+    uint16_t* __restrict__ gp, ActiveList* __restrict__ batch, int M, int H, int E, int I, int k, float scaling) {
+  __shared__ __align__(16) ActiveList list;
+  __shared__ __align__(16) uint32_t mask[kRouteMaxE / 32];  // picked experts
   __shared__ uint16_t ids[kLayerMaxEntries];
-  __shared__ float sel[kLayerMaxEntries], wts[kLayerMaxEntries];
+  __shared__ float sel[kLayerMaxEntries], sig[kLayerMaxEntries], wts[kLayerMaxEntries];
   __shared__ float red[2][kLayerWaves][4 * 80];
   __shared__ uint4 xs[kLayerWaves][256];
+  __shared__ uint32_t hold[kHoldItems * 128];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int nks = H / 128, nkq = H / 512, nit = I / 8;
 
+  // the wave's two tokens' logits first (loads return in order), then x
+  static_assert(kSmallM == 2 * kLayerWaves, "two tokens a wave");
+  uint32_t key[2][EC];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int token = wave + kLayerWaves * t;
+    load_keys<EC>(logits + (size_t)min(token, M - 1) * E, E, lane, key[t]);
+    if (token >= M) {
+#pragma unroll
+      for (int c = 0; c < EC; ++c) key[t][c] = 0;
+    }
+  }
   uint4 xv[S][4];
 #pragma unroll
   for (int s = 0; s < S; ++s)
@@ -97,58 +133,65 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
       const int ks = wave * S + s, m = 4 * i + g;
       xv[s][i] = m < M && ks < nks ? ld16(x + (size_t)m * H + 128 * ks + 8 * r) : make_uint4(0, 0, 0, 0);
     }
-
-  for (int t = wave; t < M; t += kLayerWaves) {
-    uint32_t key[EC], sel_e = 0;
-    float sel_l = 0.f;
-    load_keys<EC>(logits + (size_t)t * E, E, lane, key);
-    topk_wave<EC>(key, k, lane, sel_e, sel_l);
-    if (lane < k) {
-      ids[t * k + lane] = (uint16_t)sel_e;
-      sel[t * k + lane] = sel_l;
-      if (blockIdx.x == 0) topk_ids[t * k + lane] = (int)sel_e;
-    }
+  if (threadIdx.x < kRouteMaxE / 32) mask[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < kLayerMaxEntries; i += 64 * kLayerWaves)
+    reinterpret_cast<uint4*>(list.slot)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+  barrier_lds();
+  if (wave < M) {
+    uint32_t sel_e[2] = {0, 0};
+    float sel_l[2] = {0.f, 0.f};
+    topk_pair<EC>(key, wave + kLayerWaves < M, k, lane, sel_e, sel_l);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (lane < k && wave + kLayerWaves * t < M) {
+        const int at = (wave + kLayerWaves * t) * k + lane;
+        ids[at] = (uint16_t)sel_e[t];
+        sel[at] = sel_l[t];
+        atomicOr(&mask[sel_e[t] >> 5], 1u << (sel_e[t] & 31));
+      }
   }
-  __syncthreads();
-  build_active(ids, M, k, E, index, list);
+  barrier_lds();
+  // an expert's place in the list: the picked ones below it
+  auto place = [&](int e) {
+    int at = 0;
+    for (int w = 0; w < (e >> 5); ++w) at += __popc(mask[w]);
+    return at + __popc(mask[e >> 5] & ((1u << (e & 31)) - 1));
+  };
+  for (int e = threadIdx.x; e < E; e += 64 * kLayerWaves)
+    if ((mask[e >> 5] >> (e & 31)) & 1) list.expert[place(e)] = (uint16_t)e;
+  if ((int)threadIdx.x < M * k) {
+    const int i = threadIdx.x;
+    list.slot[place(ids[i])][i / k] = (uint8_t)(i % k);
+  }
+  if (threadIdx.x == 511) list.n = place(E - 1) + ((mask[(E - 1) >> 5] >> ((E - 1) & 31)) & 1);
+  barrier_lds();
 
-  const int items = list.n * nit, step = gridDim.x;
-  const int own = ((int)blockIdx.x < items) ? (items - (int)blockIdx.x + step - 1) / step : 0;
+  // workgroups 16 v + x and 16 v + x + 8 (one XCD) take the halves 2 p, 2 p + 1
+  const int items = list.n * nit, step = gridDim.x, id = blockIdx.x;
+  const int first = step % 16 == 0 ? (id & ~15) + 2 * (id & 7) + ((id >> 3) & 1) : id;
+  const int own = first < items ? (items - first + step - 1) / step : 0;
   // lane r < 8: gate row r of the item, else up row r - 8
   constexpr int D = S > 6 ? 1 : 2;
   uint4 q[D][S];
   uint32_t sc[D][S];
-  auto load = [&](int d, int s, int i) {
-    const int it = blockIdx.x + min(i, own - 1) * step, a = it / nit, c = it - a * nit;
-    const uint32_t rb = (uint32_t)list.expert[a] * (I / 8) + (c >> 1) + (r >= 8 ? I / 16 : 0);
-    const uint32_t row = 8 * (c & 1) + (r & 7);
+  auto item_row = [&](int i) -> uint32_t {  // the item's (gate or up) row of this lane, in 16-row blocks' order
+    const int it = first + min(i, own - 1) * step, a = it / nit, c = it - a * nit;
+    return (uint32_t)list.expert[a] * (2 * I) + 8 * c + (r >= 8 ? I : 0) + (r & 7);
+  };
+  auto load = [&](int d, int s, uint32_t row) {
+    const size_t rb = row >> 4;
     const int ks = min(wave * S + s, nks - 1);
-    q[d][s] = ld16(w13p + ((size_t)rb * nks + ks) * 1024 + 256 * g + 16 * row);
-    sc[d][s] = ld4(s13p + ((size_t)rb * nkq + (ks >> 2)) * 256 + 64 * g + 4 * row);
+    q[d][s] = ld16(w13p + (rb * nks + ks) * 1024 + 256 * g + 16 * (row & 15));
+    sc[d][s] = ld4(s13p + (rb * nkq + (ks >> 2)) * 256 + 64 * g + 4 * (row & 15));
   };
   if (own > 0) {
 #pragma unroll
-    for (int d = 0; d < D; ++d)
+    for (int d = 0; d < D; ++d) {
+      const uint32_t row = item_row(d);
 #pragma unroll
-      for (int s = 0; s < S; ++s) load(d, s, d);
+      for (int s = 0; s < S; ++s) load(d, s, row);
+    }
   }
-  // the routing weights, while the first weights are on their way: sigmoid
-  // scores (float64, one rounding), renormalized over the token's slots
-  if ((int)threadIdx.x < M * k) wts[threadIdx.x] = (float)(1.0 / (1.0 + exp(-(double)sel[threadIdx.x])));
-  barrier_lds();
-  float weight = 0.f;
-  if ((int)threadIdx.x < M * k) {
-    const int t0 = threadIdx.x / k * k;
-    float sum = 0.f;
-    for (int j = 0; j < k; ++j) sum += wts[t0 + j];
-    weight = __fdiv_rn(wts[threadIdx.x], sum + 1e-20f) * scaling;
-  }
-  barrier_lds();
-  if ((int)threadIdx.x < M * k) {
-    wts[threadIdx.x] = weight;
-    if (blockIdx.x == 0) topk_w[threadIdx.x] = weight;
-  }
-
   uint4 xf[S][4];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
@@ -160,10 +203,32 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
     for (int j = 0; j < 4; ++j) xf[s][j] = mine[x13_slot(4 * g + j, r)];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
+  // The routing weights, while the first weights are on their way: sigmoid
+  // scores (float64, one rounding), renormalized over the token's slots. They
+  // are first read behind the first item's barrier.
+  const int n = M * k;
+  if ((int)threadIdx.x < n) sig[threadIdx.x] = (float)(1.0 / (1.0 + exp(-(double)sel[threadIdx.x])));
   barrier_lds();
+  if ((int)threadIdx.x < n) {
+    const int t0 = threadIdx.x / k * k;
+    float sum = 0.f;
+    for (int j = 0; j < k; ++j) sum += sig[t0 + j];
+    wts[threadIdx.x] = __fdiv_rn(sig[threadIdx.x], sum + 1e-20f) * scaling;
+  }
 
+  auto flush = [&](int i0, int i1) {  // store items i0 .. i1 - 1
+    for (int v = threadIdx.x; v < (i1 - i0) * 128; v += 64 * kLayerWaves) {
+      const int it = first + (i0 + (v >> 7)) * step, a = it / nit, c = it - a * nit;
+      const int t = (v & 127) >> 3, n = v & 7, slot = list.slot[a][t];
+      if (slot == 255) continue;
+      const uint32_t u = hold[v];
+      gp[h_at(t * k + slot, I / 128, 8 * c + n, 0)] = (uint16_t)u;
+      gp[h_at(t * k + slot, I / 128, 8 * c + n, 1)] = (uint16_t)(u >> 16);
+    }
+  };
   auto compute = [&](int d, int i, auto reload) {
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    const uint32_t next = reload ? item_row(i + D) : 0;
+    v4f acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const int ks = wave * S + s;
@@ -171,17 +236,18 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
       const bool in = ks < nks;  // x is zero past the last step; so are the codes, whatever their scale
       const uint32_t c[4] = {in ? q[d][s].x : 0u, in ? q[d][s].y : 0u, in ? q[d][s].z : 0u, in ? q[d][s].w : 0u};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc = mfma_bf16(fp4x8_bf16(c[j], f), __builtin_bit_cast(v8s, xf[s][j]), acc);
-      if constexpr (reload) load(d, s, i + D);
+      for (int j = 0; j < 4; ++j)
+        acc[j & 1] = mfma_bf16(fp4x8_bf16(c[j], f), __builtin_bit_cast(v8s, xf[s][j]), acc[j & 1]);
+      if constexpr (reload) load(d, s, next);
     }
     // lane (g, r): rows 4 g .. 4 g + 3 of token r (rows 0-7 gate, 8-15 up); 80
     // floats a group keep the transposed reads below off each other's banks
     const int buf = i & 1;
-    *reinterpret_cast<v4f*>(&red[buf][wave][80 * g + 4 * r]) = acc;
+    *reinterpret_cast<v4f*>(&red[buf][wave][80 * g + 4 * r]) = acc[0] + acc[1];
     barrier_lds();
     const int th = (int)threadIdx.x - 128 * (i & 3);  // two waves in turn
     if (th >= 0 && th < 128) {
-      const int it = blockIdx.x + i * step, a = it / nit, c = it - a * nit;
+      const int it = first + i * step, a = it / nit;
       const int t = th >> 3, n = th & 7;
       const int slot = list.slot[a][t];
       if (slot != 255) {
@@ -192,14 +258,17 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
           G += red[buf][w][at];
           U += red[buf][w][at + 160];
         }
-        const int entry = t * k + slot;
-        const float v = G / (1.0f + expf(-G)) * U * wts[entry];
+        const float v = G / (1.0f + expf(-G)) * U * wts[t * k + slot];
         const uint16_t hi = bf16_bits(v);
         const float rest = v - bf16_value(hi);
-        const size_t o = (size_t)entry * I + 8 * c + n;
-        gp[o] = hi;
-        gp[(size_t)M * k * I + o] = fabsf(rest) < INFINITY ? bf16_bits(rest) : (uint16_t)0;
+        hold[(i % kHoldItems) * 128 + th] =
+            hi | ((uint32_t)(fabsf(rest) < INFINITY ? bf16_bits(rest) : (uint16_t)0) << 16);
       }
+    }
+    if ((i + 1) % kHoldItems == 0) {
+      barrier_lds();
+      flush(i + 1 - kHoldItems, i + 1);
+      barrier_lds();
     }
   };
   constexpr std::true_type yes{};
@@ -211,108 +280,169 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
 #pragma unroll
   for (int d = 0; d < D; ++d)
     if (i + d < own) compute(d, i + d, no);
+  barrier_lds();
+  flush(own / kHoldItems * kHoldItems, own);
+  if (blockIdx.x == 0) {  // for the down launch and the caller
+    if ((int)threadIdx.x < n) {
+      topk_ids[threadIdx.x] = ids[threadIdx.x];
+      topk_w[threadIdx.x] = wts[threadIdx.x];
+    }
+    for (int i = threadIdx.x; i < (int)sizeof(ActiveList) / 16; i += 64 * kLayerWaves)
+      reinterpret_cast<uint4*>(batch)[i] = reinterpret_cast<const uint4*>(&list)[i];
+  }
 }
 
-// Down and combine: cw (a multiple of 8, at most 16 R) columns of out a
-// workgroup, every active expert. Wave w takes experts w, w + 8, ..., a
-// K-step of 128 at a time: R row tiles' weights PW steps ahead, and the
-// tokens' weighted h (two bf16 a value; loaded only by the lanes of tokens
-// that picked the expert) two steps ahead.
-template <int NB, int R>
+// Down and combine: 8 C8 columns of out a workgroup, over every active expert.
+// Wave w takes experts w, w + 8, ...: an expert's rows of these columns are one
+// run of 512 C8 NB bytes, read PE experts ahead in whole lines and turned
+// into MFMA operands through LDS of the wave's own (operand-shaped loads, 64
+// bytes of 16 rows, cost the memory pipeline four times as much). The batch's
+// weighted h is copied to LDS once (HL); where it does not fit, the lanes of
+// tokens that picked the expert load theirs a K-step ahead.
+template <int NB>
+struct DownRows {  // a row's 4 NB chunks of 16 bytes in LDS, exchanged against bank conflicts
+  static constexpr int kStride = NB == 3 ? 16 : 4 * NB;
+  __device__ static __forceinline__ int at(int row, int chunk) {
+    const int x = NB == 1 ? (row >> 2) & 3 : NB == 2 ? (row >> 1) & 7 : row & 15;
+    return row * kStride + (chunk ^ x);
+  }
+};
+
+template <int NB, int C8>
+struct DownLds {
+  static constexpr int kR = (C8 + 1) / 2;                                // MFMA row tiles
+  static constexpr int kRows = 8 * C8 * DownRows<NB>::kStride;           // chunks of a wave's rows
+  static constexpr int kArea = kLayerWaves * (kRows > 64 * kR ? kRows : 64 * kR);  // or the partial sums
+  static constexpr int kZero = 32 * NB;                                  // h of a token that did not pick the expert
+  static constexpr int kFixed = (int)sizeof(ActiveList) + 16 * (kArea + kZero);
+  static constexpr int kHCap = (160 * 1024 - kFixed) / (512 * NB);       // entries whose h fits beside
+};
+
+template <int NB, int C8, bool HL>
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
-    const uint16_t* __restrict__ gp, const int* __restrict__ topk_ids, const uint8_t* __restrict__ w2,
-    const uint8_t* __restrict__ s2, uint16_t* __restrict__ out, int M, int H, int E, int k, int cw) {
-  __shared__ ActiveList list;
-  __shared__ uint16_t index[kRouteMaxE];
-  __shared__ uint16_t ids[kLayerMaxEntries];
-  __shared__ v4f red[kLayerWaves][R][64];
-  constexpr int I = 128 * NB;
-  constexpr int PW = NB == 3 ? 6 : 8, PG = 2;
-  static_assert(PW % NB == 0 && PW % PG == 0, "whole experts a round");
+    const uint16_t* __restrict__ gp, const ActiveList* __restrict__ batch, const uint8_t* __restrict__ w2,
+    const uint8_t* __restrict__ s2, uint16_t* __restrict__ out, int M, int H, int k) {
+  typedef DownLds<NB, C8> Lds;
+  typedef DownRows<NB> Rows;
+  constexpr int I = 128 * NB, R = Lds::kR;
+  constexpr int kChunks = 8 * C8 * 4 * NB;                               // of an expert's rows
+  constexpr int NL = (kChunks + 63) / 64;
+  constexpr int PE = NL >= 5 ? 2 : NL >= 3 ? 4 : NL == 2 ? 6 : 8;
+  __shared__ __align__(16) ActiveList list;
+  __shared__ uint4 area[Lds::kArea + Lds::kZero];
+  __shared__ uint4 hs[HL ? Lds::kHCap * 32 * NB : 1];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
-  for (int i = threadIdx.x; i < M * k; i += blockDim.x) ids[i] = (uint16_t)topk_ids[i];
+  for (int i = threadIdx.x; i < (int)sizeof(ActiveList) / 16; i += 64 * kLayerWaves)
+    reinterpret_cast<uint4*>(&list)[i] = reinterpret_cast<const uint4*>(batch)[i];
+  if (threadIdx.x < Lds::kZero) area[Lds::kArea + threadIdx.x] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  build_active(ids, M, k, E, index, list);
-  const size_t plane = (size_t)M * k * I;
-  const int c0 = blockIdx.x * cw, cols = min(cw, H - c0);
-  const int experts = (list.n - wave + kLayerWaves - 1) / kLayerWaves;  // of this wave
-  const int units = experts > 0 ? experts * NB : 0;                     // K-steps of all of them
+  const int c0 = blockIdx.x * 8 * C8, cols = min(8 * C8, H - c0);
+  const int experts = (list.n - wave + kLayerWaves - 1) / kLayerWaves;   // of this wave
+  uint4* mine = area + wave * Lds::kRows;
 
-  uint4 q[PW][R];
-  uint32_t sc[PW][R];
-  uint4 hi[PG][4], lo[PG][4];
-  int row[R];  // rows past the workgroup's columns: the last one again (not stored)
+  typedef uint32_t scales __attribute__((ext_vector_type(NB == 1 ? 2 : NB), aligned(4)));
+  uint4 q[PE][NL];
+  uint32_t sc[PE][R][NB];
+  auto load = [&](int p, int i) {
+    const size_t row0 = (size_t)list.expert[wave + kLayerWaves * min(i, experts - 1)] * H + c0;
 #pragma unroll
-  for (int t = 0; t < R; ++t) row[t] = c0 + min(16 * t + r, cols - 1);
-  auto load_w = [&](int p, int u, int b) {
-    const int a = wave + kLayerWaves * min(u / NB, experts - 1);
-    const size_t base = (size_t)list.expert[a] * H;
+    for (int l = 0; l < NL; ++l)  // columns past H: the last chunk again
+      q[p][l] = ld16(w2 + row0 * (I / 2) + 16 * min(64 * l + lane, cols * 4 * NB - 1));
 #pragma unroll
     for (int t = 0; t < R; ++t) {
-      q[p][t] = ld16(w2 + (base + row[t]) * (I / 2) + 64 * b + 16 * g);
-      sc[p][t] = ld4(s2 + (base + row[t]) * (I / 32) + 4 * b);
-    }
-  };
-  auto slot_of = [&](int u) -> int {
-    const int a = wave + kLayerWaves * min(u / NB, experts - 1);
-    return r < M ? list.slot[a][r] : 255;
-  };
-  auto load_g = [&](int p, int u, int b) {
-    const int slot = slot_of(u);
-    const uint16_t* h = gp + (size_t)(r * k + slot) * I + 128 * b + 32 * g;
+      const uint8_t* at = s2 + (row0 + min(16 * t + r, cols - 1)) * (I / 32);
+      if constexpr (NB == 1) {
+        sc[p][t][0] = ld4(at);
+      } else {
+        const scales v = *reinterpret_cast<const scales*>(at);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      hi[p][j] = make_uint4(0, 0, 0, 0);
-      lo[p][j] = make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < NB; ++b) sc[p][t][b] = v[b];
+      }
     }
+  };
+  auto slot_of = [&](int i) -> int {
+    return r < M ? list.slot[wave + kLayerWaves * min(i, experts - 1)][r] : 255;
+  };
+  uint4 hv[HL ? 1 : 2][8];  // a K-step's h: 4 operands of values, 4 of remainders
+  auto load_h = [&](int p, int i, int b) {
+    const int slot = slot_of(i);
+    const uint16_t* h = gp + h_at(r * k + slot, NB, 128 * b + 32 * g, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) hv[p][j] = make_uint4(0, 0, 0, 0);
     if (slot != 255) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        hi[p][j] = ld16(h + 8 * j);
-        lo[p][j] = ld16(h + plane + 8 * j);
-      }
+      for (int j = 0; j < 8; ++j) hv[p][j] = ld16(h + (j >> 2) * 128 + 8 * (j & 3));
     }
   };
-  v4f acc[R], d[R];
+  if (experts > 0) {
 #pragma unroll
-  for (int t = 0; t < R; ++t) acc[t] = d[t] = v4f{0.f, 0.f, 0.f, 0.f};
-  if (units > 0) {
-#pragma unroll
-    for (int p = 0; p < PW; ++p) load_w(p, p, p % NB);
-#pragma unroll
-    for (int p = 0; p < PG; ++p) load_g(p, p, p % NB);
+    for (int p = 0; p < PE; ++p) load(p, p);
+    if constexpr (!HL) load_h(0, 0, 0);
   }
-  for (int u0 = 0; u0 < units; u0 += PW) {
+  if constexpr (HL) {
+    // chunk c of token t's K-step is kept at c ^ t: a group's 16 tokens meet all banks
+    for (int i = threadIdx.x; i < M * k * 32 * NB; i += 64 * kLayerWaves)
+      hs[(i & ~15) | ((i & 15) ^ (i / (32 * NB) / k))] = reinterpret_cast<const uint4*>(gp)[i];
+    __syncthreads();
+  }
+  v4f acc[R];
 #pragma unroll
-    for (int p = 0; p < PW; ++p) {
-      const int u = u0 + p;
-      if (u >= units) break;
+  for (int t = 0; t < R; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < experts; i0 += PE) {
 #pragma unroll
-      for (int t = 0; t < R; ++t) {
-        const float f = scale_operand<0>(sc[p][t] >> (8 * g));
-        const uint32_t w[4] = {q[p][t].x, q[p][t].y, q[p][t].z, q[p][t].w};
+    for (int p = 0; p < PE; ++p) {
+      const int i = i0 + p;
+      if (i >= experts) break;
+#pragma unroll
+      for (int l = 0; l < NL; ++l) {
+        const int n = min(64 * l + lane, cols * 4 * NB - 1);
+        mine[Rows::at(n / (4 * NB), n % (4 * NB))] = q[p][l];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
+      const int slot = slot_of(i);
+      const bool picked = slot != 255;
+      const uint4* h = HL && picked ? hs + (r * k + slot) * 32 * NB : area + Lds::kArea;
+      v4f d[R];
+#pragma unroll
+      for (int t = 0; t < R; ++t) d[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int u = p * NB + b;  // even and odd K-steps' registers in turn (PE NB is even)
+        if constexpr (!HL) load_h((u + 1) & 1, b + 1 < NB ? i : i + 1, b + 1 < NB ? b + 1 : 0);
+        uint4 w[R];
+#pragma unroll
+        for (int t = 0; t < R; ++t) w[t] = mine[Rows::at(min(16 * t + r, 8 * C8 - 1), 4 * b + g)];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const v8s wf = fp4x8_bf16(w[j], f);
-          d[t] = mfma_bf16(wf, __builtin_bit_cast(v8s, lo[p % PG][j]), d[t]);
-          d[t] = mfma_bf16(wf, __builtin_bit_cast(v8s, hi[p % PG][j]), d[t]);
-        }
-      }
-      load_w(p, u + PW, p % NB);
-      if (p % NB == NB - 1) {
-        // a token that did not pick the expert takes nothing from it, also
-        // where its weights are not finite
-        const bool mine = slot_of(u) != 255;
+          uint4 hi, lo;
+          if constexpr (HL) {
+            hi = h[32 * b + ((4 * g + j) ^ r)];
+            lo = h[32 * b + 16 + ((4 * g + j) ^ r)];
+          } else {
+            hi = hv[u & 1][j];
+            lo = hv[u & 1][4 + j];
+          }
 #pragma unroll
-        for (int t = 0; t < R; ++t) {
-          if (mine) acc[t] += d[t];
-          d[t] = v4f{0.f, 0.f, 0.f, 0.f};
+          for (int t = 0; t < R; ++t) {
+            const uint32_t c = j == 0 ? w[t].x : j == 1 ? w[t].y : j == 2 ? w[t].z : w[t].w;
+            const v8s wf = fp4x8_bf16(c, scale_operand<0>(sc[p][t][b] >> (8 * g)));
+            d[t] = mfma_bf16(wf, __builtin_bit_cast(v8s, lo), d[t]);
+            d[t] = mfma_bf16(wf, __builtin_bit_cast(v8s, hi), d[t]);
+          }
         }
       }
-      load_g(p % PG, u + PG, (p + PG) % NB);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      load(p, i + PE);
+      // a token that did not pick the expert takes nothing from it, also
+      // where its weights are not finite
+#pragma unroll
+      for (int t = 0; t < R; ++t)
+        if (picked) acc[t] += d[t];
     }
   }
+  v4f(*red)[R][64] = reinterpret_cast<v4f(*)[R][64]>(area);
+  __syncthreads();
 #pragma unroll
   for (int t = 0; t < R; ++t) red[wave][t][lane] = acc[t];
   __syncthreads();
@@ -338,9 +468,31 @@ static hipError_t launch_gate_up_s(const moe_plan* p, const LayerArgs& a, const 
   auto go = [&](auto kern) {
     return launch_k(kern, grid, dim3(64 * kLayerWaves), 0, a.stream, Ev{}, (const uint16_t*)a.x, logits,
                     (const uint8_t*)a.w13, (const uint8_t*)a.s13, wsp<int>(p, p->L.topk_ids),
-                    wsp<float>(p, p->L.topk_w), gp, (int)a.M, (int)p->s.H, E, I, k, p->s.routed_scaling);
+                    wsp<float>(p, p->L.topk_w), gp, wsp<ActiveList>(p, p->X.layer_list), (int)a.M, (int)p->s.H, E, I, k, p->s.routed_scaling);
   };
   return E <= 256 ? go(layer_gate_up_kernel<S, 4>) : go(layer_gate_up_kernel<S, 16>);
+}
+
+template <int NB, int C8>
+static hipError_t launch_down_c8(const moe_plan* p, const LayerArgs& a, const uint16_t* gp) {
+  const int H = (int)p->s.H;
+  const dim3 grid((unsigned)((H + 8 * C8 - 1) / (8 * C8)));
+  auto go = [&](auto kern) {
+    return launch_k(kern, grid, dim3(64 * kLayerWaves), 0, a.stream, Ev{}, gp, wsp<ActiveList>(p, p->X.layer_list),
+                    (const uint8_t*)a.w2, (const uint8_t*)a.s2, (uint16_t*)a.out, (int)a.M, H, (int)p->s.top_k);
+  };
+  return a.M * p->s.top_k <= DownLds<NB, C8>::kHCap ? go(layer_down_kernel<NB, C8, true>)
+                                                    : go(layer_down_kernel<NB, C8, false>);
+}
+
+template <int NB>
+static hipError_t launch_down_nb(const moe_plan* p, const LayerArgs& a, int c8, const uint16_t* gp) {
+  switch (c8) {
+    case 1: return launch_down_c8<NB, 1>(p, a, gp);
+    case 2: return launch_down_c8<NB, 2>(p, a, gp);
+    case 3: return launch_down_c8<NB, 3>(p, a, gp);
+    default: return launch_down_c8<NB, 4>(p, a, gp);
+  }
 }
 
 hipError_t launch_layer(const moe_plan* p, const moe_router* router, const LayerArgs& a) {
@@ -357,23 +509,13 @@ hipError_t launch_layer(const moe_plan* p, const moe_router* router, const Layer
                   : launch_gate_up_s<8>(p, a, logits, gp);
   if (e != hipSuccess) return e;
   // one workgroup a CU, each the same number of columns: a multiple of 8
-  // (H 6144 on 256 CUs: 24), in one or two 16-row tiles
-  const int cw = std::min(32, (H / 8 + p->num_cus - 1) / p->num_cus * 8);
-  const dim3 grid((unsigned)((H + cw - 1) / cw));
-  auto go = [&](auto kern) {
-    return launch_k(kern, grid, dim3(64 * kLayerWaves), 0, a.stream, Ev{}, (const uint16_t*)gp,
-                    wsp<int>(p, p->L.topk_ids), (const uint8_t*)a.w2, (const uint8_t*)a.s2, (uint16_t*)a.out, (int)a.M,
-                    H, (int)p->s.E, (int)p->s.top_k, cw);
-  };
-  switch (2 * (p->s.I / 128) + (cw > 16 ? 1 : 0)) {
-    case 2: return go(layer_down_kernel<1, 1>);
-    case 3: return go(layer_down_kernel<1, 2>);
-    case 4: return go(layer_down_kernel<2, 1>);
-    case 5: return go(layer_down_kernel<2, 2>);
-    case 6: return go(layer_down_kernel<3, 1>);
-    case 7: return go(layer_down_kernel<3, 2>);
-    case 8: return go(layer_down_kernel<4, 1>);
-    default: return go(layer_down_kernel<4, 2>);
+  // (H 6144 on 256 CUs: 24)
+  const int c8 = std::min(4, (H / 8 + p->num_cus - 1) / p->num_cus);
+  switch (p->s.I / 128) {
+    case 1: return launch_down_nb<1>(p, a, c8, gp);
+    case 2: return launch_down_nb<2>(p, a, c8, gp);
+    case 3: return launch_down_nb<3>(p, a, c8, gp);
+    default: return launch_down_nb<4>(p, a, c8, gp);
   }
 }
 
