@@ -33,39 +33,73 @@ struct ActiveList {
 };
 static_assert(sizeof(ActiveList) == kLayerListBytes && sizeof(ActiveList) % 16 == 0, "copied in 16-byte pieces");
 
-// Top-k of two tokens' keys by one wave (the second may be all zero: unused),
-// their rounds side by side so that one's lane exchanges hide the other's. A
-// round takes the wave's largest key; of several equal ones the lowest expert
-// id 64 c + lane. Lane j < k gets slot j's expert and logit.
-template <int EC>
-__device__ __forceinline__ void topk_pair(uint32_t (&key)[2][EC], bool second, int k, int lane, uint32_t (&sel_e)[2],
-                                          float (&sel_l)[2]) {
+// Top-k of T tokens' keys by one wave (of two the second may be all zero:
+// unused), their rounds side by side so that one's lane exchanges hide the
+// other's. A lane first sorts its own keys (EC <= 4; above, it looks for its
+// largest every round); a round takes the largest of the lanes' first keys and
+// drops it; of equal ones the lowest expert id 64 c + lane. Lane j < k gets
+// slot j's expert and logit. (Looking through all keys every round took 2.6
+// us for 8 of 256.)
+template <int EC, int T>
+__device__ __forceinline__ void topk_tokens(uint32_t (&key)[T][EC], bool second, int k, int lane,
+                                            uint32_t (&sel_e)[T], float (&sel_l)[T]) {
+  constexpr bool kSorted = EC <= 4;
+  uint32_t id[T][EC];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+#pragma unroll
+    for (int c = 0; c < EC; ++c) id[t][c] = 64 * c + lane;
+    if constexpr (kSorted) {  // stable: equal keys keep the lower id first
+#pragma unroll
+      for (int pass = 0; pass < EC - 1; ++pass)
+#pragma unroll
+        for (int c = 0; c + 1 < EC - pass; ++c) {
+          const bool swap = key[t][c + 1] > key[t][c];
+          const uint32_t k0 = key[t][c], k1 = key[t][c + 1], i0 = id[t][c], i1 = id[t][c + 1];
+          key[t][c] = swap ? k1 : k0;
+          key[t][c + 1] = swap ? k0 : k1;
+          id[t][c] = swap ? i1 : i0;
+          id[t][c + 1] = swap ? i0 : i1;
+        }
+    }
+  }
   for (int j = 0; j < k; ++j) {
-    uint32_t top[2], id[2];
-    unsigned long long hits[2];
+    uint32_t top[T], first[T], win[T];
+    unsigned long long hits[T];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      uint32_t m = 0;
+    for (int t = 0; t < T; ++t) {
+      uint32_t m = key[t][0];
+      first[t] = id[t][0];
+      if constexpr (!kSorted) {
 #pragma unroll
-      for (int c = 0; c < EC; ++c) m = max(m, key[t][c]);
+        for (int c = 1; c < EC; ++c) {
+          first[t] = key[t][c] > m ? id[t][c] : first[t];
+          m = max(m, key[t][c]);
+        }
+      }
       top[t] = wave_max_u32(m);
-      int at = 0;  // this lane's first key that is the largest
-#pragma unroll
-      for (int c = EC - 1; c >= 0; --c) at = key[t][c] == top[t] ? c : at;
-      id[t] = 64 * at + lane;
       hits[t] = __ballot(m == top[t]);
+      win[t] = __builtin_amdgcn_readlane(first[t], __builtin_ctzll(hits[t]));
     }
-    uint32_t win[2];
+    bool equal = hits[0] & (hits[0] - 1);
+    if constexpr (T == 2) equal = equal || (second && (hits[1] & (hits[1] - 1)));
+    if (equal) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) win[t] = __builtin_amdgcn_readlane(id[t], __builtin_ctzll(hits[t]));
-    if ((hits[0] & (hits[0] - 1)) || (second && (hits[1] & (hits[1] - 1)))) {  // equal logits
-#pragma unroll
-      for (int t = 0; t < 2; ++t) win[t] = wave_min_u32((hits[t] >> lane) & 1 ? id[t] : 0xFFFFFFFFu);
+      for (int t = 0; t < T; ++t) win[t] = wave_min_u32((hits[t] >> lane) & 1 ? first[t] : 0xFFFFFFFFu);
     }
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < T; ++t) {
+      if constexpr (kSorted) {
+        const bool mine = first[t] == win[t];
 #pragma unroll
-      for (int c = 0; c < EC; ++c) key[t][c] = win[t] == (uint32_t)(64 * c + lane) ? 0u : key[t][c];
+        for (int c = 0; c < EC; ++c) {
+          key[t][c] = mine ? (c + 1 < EC ? key[t][c + 1 < EC ? c + 1 : c] : 0u) : key[t][c];
+          if (c + 1 < EC) id[t][c] = mine ? id[t][c + 1] : id[t][c];
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < EC; ++c) key[t][c] = win[t] == id[t][c] ? 0u : key[t][c];
+      }
       if (lane == j) {
         sel_e[t] = win[t];
         sel_l[t] = key_to_float(top[t]);
@@ -97,7 +131,10 @@ constexpr int kHoldItems = 16;  // finished items a gate/up workgroup holds befo
 // more), each slot requested again as soon as its products are issued.
 // Results wait in LDS and are stored 16 items at a time: the compiler drains
 // all loads before it lets a store's counter mix with them.
-template <int S, int EC>
+//
+// T tokens a wave are routed, x comes operand-shaped up to 4 tokens (few
+// lines a load), else in whole row pieces turned round in LDS.
+template <int S, int EC, int T>
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
     const uint16_t* __restrict__ x, const float* __restrict__ logits, const uint8_t* __restrict__ w13p,
     const uint8_t* __restrict__ s13p, int* __restrict__ topk_ids, float* __restrict__ topk_w,
@@ -105,7 +142,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
   __shared__ __align__(16) ActiveList list;
   __shared__ __align__(16) uint32_t mask[kRouteMaxE / 32];  // picked experts
   __shared__ uint16_t ids[kLayerMaxEntries];
-  __shared__ float sel[kLayerMaxEntries], sig[kLayerMaxEntries], wts[kLayerMaxEntries];
+  __shared__ float wts[kLayerMaxEntries];
   __shared__ float red[2][kLayerWaves][4 * 80];
   __shared__ uint4 xs[kLayerWaves][256];
   __shared__ uint32_t hold[kHoldItems * 128];
@@ -113,11 +150,11 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
   const int r = lane & 15, g = lane >> 4;
   const int nks = H / 128, nkq = H / 512, nit = I / 8;
 
-  // the wave's two tokens' logits first (loads return in order), then x
-  static_assert(kSmallM == 2 * kLayerWaves, "two tokens a wave");
-  uint32_t key[2][EC];
+  // the wave's tokens' logits first (loads return in order), then x
+  static_assert(kSmallM == 2 * kLayerWaves, "at most two tokens a wave");
+  uint32_t key[T][EC];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < T; ++t) {
     const int token = wave + kLayerWaves * t;
     load_keys<EC>(logits + (size_t)min(token, M - 1) * E, E, lane, key[t]);
     if (token >= M) {
@@ -125,45 +162,60 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
       for (int c = 0; c < EC; ++c) key[t][c] = 0;
     }
   }
+  const bool few = M <= 4;
   uint4 xv[S][4];
 #pragma unroll
   for (int s = 0; s < S; ++s)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int ks = wave * S + s, m = 4 * i + g;
-      xv[s][i] = m < M && ks < nks ? ld16(x + (size_t)m * H + 128 * ks + 8 * r) : make_uint4(0, 0, 0, 0);
+      const int ks = wave * S + s, m = few ? r : 4 * i + g, c = few ? 4 * g + i : r;
+      xv[s][i] = m < M && ks < nks ? ld16(x + (size_t)m * H + 128 * ks + 8 * c) : make_uint4(0, 0, 0, 0);
     }
   if (threadIdx.x < kRouteMaxE / 32) mask[threadIdx.x] = 0;
   for (int i = threadIdx.x; i < kLayerMaxEntries; i += 64 * kLayerWaves)
     reinterpret_cast<uint4*>(list.slot)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
   barrier_lds();
-  if (wave < M) {
-    uint32_t sel_e[2] = {0, 0};
-    float sel_l[2] = {0.f, 0.f};
-    topk_pair<EC>(key, wave + kLayerWaves < M, k, lane, sel_e, sel_l);
+  uint32_t sel_e[T];
+  float sel_l[T];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+  for (int t = 0; t < T; ++t) {
+    sel_e[t] = 0;
+    sel_l[t] = 0.f;
+  }
+  if (wave < M) {
+    topk_tokens<EC, T>(key, wave + kLayerWaves < M, k, lane, sel_e, sel_l);
+#pragma unroll
+    for (int t = 0; t < T; ++t)
       if (lane < k && wave + kLayerWaves * t < M) {
-        const int at = (wave + kLayerWaves * t) * k + lane;
-        ids[at] = (uint16_t)sel_e[t];
-        sel[at] = sel_l[t];
+        ids[(wave + kLayerWaves * t) * k + lane] = (uint16_t)sel_e[t];
         atomicOr(&mask[sel_e[t] >> 5], 1u << (sel_e[t] & 31));
       }
   }
   barrier_lds();
-  // an expert's place in the list: the picked ones below it
-  auto place = [&](int e) {
-    int at = 0;
-    for (int w = 0; w < (e >> 5); ++w) at += __popc(mask[w]);
-    return at + __popc(mask[e >> 5] & ((1u << (e & 31)) - 1));
-  };
-  for (int e = threadIdx.x; e < E; e += 64 * kLayerWaves)
-    if ((mask[e >> 5] >> (e & 31)) & 1) list.expert[place(e)] = (uint16_t)e;
-  if ((int)threadIdx.x < M * k) {
-    const int i = threadIdx.x;
-    list.slot[place(ids[i])][i / k] = (uint8_t)(i % k);
+  {
+    // an expert's place in the list: the picked ones below it
+    uint32_t words[2 * EC];
+#pragma unroll
+    for (int w = 0; w < 2 * EC; ++w) words[w] = mask[w];
+    auto place = [&](int e) {
+      int at = 0;
+#pragma unroll
+      for (int w = 0; w < 2 * EC; ++w) {
+        const uint32_t below = w < (e >> 5) ? ~0u : w == (e >> 5) ? (1u << (e & 31)) - 1 : 0u;
+        at += __popc(words[w] & below);
+      }
+      return at;
+    };
+    for (int e = threadIdx.x; e < E; e += 64 * kLayerWaves)
+      if ((mask[e >> 5] >> (e & 31)) & 1) list.expert[place(e)] = (uint16_t)e;
+    if ((int)threadIdx.x < M * k) list.slot[place(ids[threadIdx.x])][threadIdx.x / k] = (uint8_t)(threadIdx.x % k);
+    if (threadIdx.x == 64 * kLayerWaves - 1) {
+      int all = 0;
+#pragma unroll
+      for (int w = 0; w < 2 * EC; ++w) all += __popc(words[w]);
+      list.n = all;
+    }
   }
-  if (threadIdx.x == 511) list.n = place(E - 1) + ((mask[(E - 1) >> 5] >> ((E - 1) & 31)) & 1);
   barrier_lds();
 
   // workgroups 16 v + x and 16 v + x + 8 (one XCD) take the halves 2 p, 2 p + 1
@@ -192,28 +244,34 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
       for (int s = 0; s < S; ++s) load(d, s, row);
     }
   }
-  uint4 xf[S][4];
+  // The routing weights, while the first weights are on their way: sigmoid
+  // scores (float64, one rounding), renormalized over the token's slots in
+  // slot order. They are first read behind the first item's barrier.
+  if (wave < M) {
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
+    for (int t = 0; t < T; ++t) {
+      const float w = route_weight(sel_l[t], k, lane, scaling);
+      if (lane < k && wave + kLayerWaves * t < M) wts[(wave + kLayerWaves * t) * k + lane] = w;
+    }
+  }
+
+  uint4 xf[S][4];
+  if (few) {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xf[s][j] = xv[s][j];
+  } else {
     uint4* mine = &xs[wave][0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mine[x13_slot(r, 4 * i + g)] = xv[s][i];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
+    for (int s = 0; s < S; ++s) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) xf[s][j] = mine[x13_slot(4 * g + j, r)];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  }
-  // The routing weights, while the first weights are on their way: sigmoid
-  // scores (float64, one rounding), renormalized over the token's slots. They
-  // are first read behind the first item's barrier.
-  const int n = M * k;
-  if ((int)threadIdx.x < n) sig[threadIdx.x] = (float)(1.0 / (1.0 + exp(-(double)sel[threadIdx.x])));
-  barrier_lds();
-  if ((int)threadIdx.x < n) {
-    const int t0 = threadIdx.x / k * k;
-    float sum = 0.f;
-    for (int j = 0; j < k; ++j) sum += sig[t0 + j];
-    wts[threadIdx.x] = __fdiv_rn(sig[threadIdx.x], sum + 1e-20f) * scaling;
+      for (int i = 0; i < 4; ++i) mine[x13_slot(r, 4 * i + g)] = xv[s][i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xf[s][j] = mine[x13_slot(4 * g + j, r)];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
   }
 
   auto flush = [&](int i0, int i1) {  // store items i0 .. i1 - 1
@@ -283,7 +341,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
   barrier_lds();
   flush(own / kHoldItems * kHoldItems, own);
   if (blockIdx.x == 0) {  // for the down launch and the caller
-    if ((int)threadIdx.x < n) {
+    if ((int)threadIdx.x < M * k) {
       topk_ids[threadIdx.x] = ids[threadIdx.x];
       topk_w[threadIdx.x] = wts[threadIdx.x];
     }
@@ -470,7 +528,8 @@ static hipError_t launch_gate_up_s(const moe_plan* p, const LayerArgs& a, const 
                     (const uint8_t*)a.w13, (const uint8_t*)a.s13, wsp<int>(p, p->L.topk_ids),
                     wsp<float>(p, p->L.topk_w), gp, wsp<ActiveList>(p, p->X.layer_list), (int)a.M, (int)p->s.H, E, I, k, p->s.routed_scaling);
   };
-  return E <= 256 ? go(layer_gate_up_kernel<S, 4>) : go(layer_gate_up_kernel<S, 16>);
+  if (E <= 256) return a.M <= kLayerWaves ? go(layer_gate_up_kernel<S, 4, 1>) : go(layer_gate_up_kernel<S, 4, 2>);
+  return a.M <= kLayerWaves ? go(layer_gate_up_kernel<S, 16, 1>) : go(layer_gate_up_kernel<S, 16, 2>);
 }
 
 template <int NB, int C8>
