@@ -146,7 +146,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
   __shared__ float red[2][kLayerWaves][4 * 80];
   __shared__ uint4 xs[kLayerWaves][256];
   __shared__ uint32_t hold[kHoldItems * 128];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int nks = H / 128, nkq = H / 512, nit = I / 8;
 
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
       gp[h_at(t * k + slot, I / 128, 8 * c + n, 1)] = (uint16_t)(u >> 16);
     }
   };
-  auto compute = [&](int d, int i, auto reload) {
+  auto compute = [&](int d, int i, auto reload) __attribute__((always_inline)) {
     const uint32_t next = reload ? item_row(i + D) : 0;
     v4f acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
@@ -356,7 +356,13 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
 // into MFMA operands through LDS of the wave's own (operand-shaped loads, 64
 // bytes of 16 rows, cost the memory pipeline four times as much). The batch's
 // weighted h is copied to LDS once (HL); where it does not fit, the lanes of
-// tokens that picked the expert load theirs a K-step ahead.
+// tokens that picked the expert load theirs as they come to it.
+// An expert is picked by few of the tokens, so the 16 MFMA columns hold both
+// parts of h at once: column c < 8 the value of token c or c + 8, whichever
+// picked the expert, column c + 8 its remainder (one MFMA, not two). Where
+// both did, tokens 8.. take a second pass over the same weights. A column's
+// result goes to the sum of tokens 0-7 or of tokens 8-15, and the two columns
+// of a token are added at the end.
 template <int NB>
 struct DownRows {  // a row's 4 NB chunks of 16 bytes in LDS, exchanged against bank conflicts
   static constexpr int kStride = NB == 3 ? 16 : 4 * NB;
@@ -389,7 +395,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
   __shared__ __align__(16) ActiveList list;
   __shared__ uint4 area[Lds::kArea + Lds::kZero];
   __shared__ uint4 hs[HL ? Lds::kHCap * 32 * NB : 1];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   for (int i = threadIdx.x; i < (int)sizeof(ActiveList) / 16; i += 64 * kLayerWaves)
     reinterpret_cast<uint4*>(&list)[i] = reinterpret_cast<const uint4*>(batch)[i];
@@ -419,90 +425,126 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
       }
     }
   };
-  auto slot_of = [&](int i) -> int {
-    return r < M ? list.slot[wave + kLayerWaves * min(i, experts - 1)][r] : 255;
+  // token and slot of this lane's column for the wave's expert i; `both`: some
+  // column's two tokens picked it (uniform), the upper ones then left for later
+  struct Column {
+    int token, slot;
+    bool both;
   };
-  uint4 hv[HL ? 1 : 2][8];  // a K-step's h: 4 operands of values, 4 of remainders
-  auto load_h = [&](int p, int i, int b) {
-    const int slot = slot_of(i);
-    const uint16_t* h = gp + h_at(r * k + slot, NB, 128 * b + 32 * g, 0);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) hv[p][j] = make_uint4(0, 0, 0, 0);
-    if (slot != 255) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) hv[p][j] = ld16(h + (j >> 2) * 128 + 8 * (j & 3));
-    }
+  const int c8 = r & 7, part = r >> 3;
+  auto column = [&](int i) -> Column {
+    const uint8_t* slots = list.slot[wave + kLayerWaves * min(i, experts - 1)];
+    const int s0 = slots[c8], s1 = slots[c8 + 8];
+    const bool both = __ballot(s0 != 255 && s1 != 255) != 0;
+    if (s0 != 255 || both) return Column{c8, s0, both};
+    return Column{c8 + 8, s1, both};
   };
   if (experts > 0) {
 #pragma unroll
     for (int p = 0; p < PE; ++p) load(p, p);
-    if constexpr (!HL) load_h(0, 0, 0);
   }
   if constexpr (HL) {
-    // chunk c of token t's K-step is kept at c ^ t: a group's 16 tokens meet all banks
-    for (int i = threadIdx.x; i < M * k * 32 * NB; i += 64 * kLayerWaves)
-      hs[(i & ~15) | ((i & 15) ^ (i / (32 * NB) / k))] = reinterpret_cast<const uint4*>(gp)[i];
+    // chunk c of token t's K-step is kept at c ^ t: a group's 16 tokens meet all
+    // banks. Four loads at a time: one by one, each waited for the one before.
+    const int total = M * k * 32 * NB, per = 64 * kLayerWaves;
+    const uint4* src = reinterpret_cast<const uint4*>(gp);
+    auto keep = [&](int i, uint4 v) __attribute__((always_inline)) {
+      if (i < total) hs[(i & ~15) | ((i & 15) ^ (i / (32 * NB) / k))] = v;
+    };
+    for (int i = threadIdx.x; i < total; i += 4 * per) {
+      const uint4 v0 = src[i], v1 = src[min(i + per, total - 1)];
+      const uint4 v2 = src[min(i + 2 * per, total - 1)], v3 = src[min(i + 3 * per, total - 1)];
+      keep(i, v0);
+      keep(i + per, v1);
+      keep(i + 2 * per, v2);
+      keep(i + 3 * per, v3);
+    }
     __syncthreads();
   }
-  v4f acc[R];
+  v4f acc[2][R];  // tokens 0-7, tokens 8-15
 #pragma unroll
-  for (int t = 0; t < R; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int i0 = 0; i0 < experts; i0 += PE) {
+  for (int t = 0; t < R; ++t) acc[0][t] = acc[1][t] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto expert = [&](int p, int i) __attribute__((always_inline)) {
 #pragma unroll
-    for (int p = 0; p < PE; ++p) {
-      const int i = i0 + p;
-      if (i >= experts) break;
+    for (int l = 0; l < NL; ++l) {
+      const int n = min(64 * l + lane, cols * 4 * NB - 1);
+      mine[Rows::at(n / (4 * NB), n % (4 * NB))] = q[p][l];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
+    Column col = column(i);
+    const bool both = col.both;
+    for (int pass = 0;; ++pass) {
+      const bool picked = col.slot != 255;
+      const uint4* h = HL && picked ? hs + ((col.token * k + col.slot) * NB * 2 + part) * 16 : area + Lds::kArea;
+      uint4 hv[2][4];
+      auto load_h = [&](int b) __attribute__((always_inline)) {
+        const uint16_t* at = gp + h_at(col.token * k + (picked ? col.slot : 0), NB, 128 * b + 32 * g, part);
 #pragma unroll
-      for (int l = 0; l < NL; ++l) {
-        const int n = min(64 * l + lane, cols * 4 * NB - 1);
-        mine[Rows::at(n / (4 * NB), n % (4 * NB))] = q[p][l];
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
-      const int slot = slot_of(i);
-      const bool picked = slot != 255;
-      const uint4* h = HL && picked ? hs + (r * k + slot) * 32 * NB : area + Lds::kArea;
+        for (int j = 0; j < 4; ++j) hv[b & 1][j] = picked ? ld16(at + 8 * j) : make_uint4(0, 0, 0, 0);
+      };
+      if constexpr (!HL) load_h(0);
       v4f d[R];
 #pragma unroll
       for (int t = 0; t < R; ++t) d[t] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int u = p * NB + b;  // even and odd K-steps' registers in turn (PE NB is even)
-        if constexpr (!HL) load_h((u + 1) & 1, b + 1 < NB ? i : i + 1, b + 1 < NB ? b + 1 : 0);
+        if constexpr (!HL)
+          if (b + 1 < NB) load_h(b + 1);
         uint4 w[R];
 #pragma unroll
         for (int t = 0; t < R; ++t) w[t] = mine[Rows::at(min(16 * t + r, 8 * C8 - 1), 4 * b + g)];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint4 hi, lo;
-          if constexpr (HL) {
-            hi = h[32 * b + ((4 * g + j) ^ r)];
-            lo = h[32 * b + 16 + ((4 * g + j) ^ r)];
-          } else {
-            hi = hv[u & 1][j];
-            lo = hv[u & 1][4 + j];
-          }
+          uint4 xw;
+          if constexpr (HL) xw = h[32 * b + ((4 * g + j) ^ col.token)];
+          else xw = hv[b & 1][j];
+          const v8s x = __builtin_bit_cast(v8s, xw);
 #pragma unroll
           for (int t = 0; t < R; ++t) {
             const uint32_t c = j == 0 ? w[t].x : j == 1 ? w[t].y : j == 2 ? w[t].z : w[t].w;
-            const v8s wf = fp4x8_bf16(c, scale_operand<0>(sc[p][t][b] >> (8 * g)));
-            d[t] = mfma_bf16(wf, __builtin_bit_cast(v8s, lo), d[t]);
-            d[t] = mfma_bf16(wf, __builtin_bit_cast(v8s, hi), d[t]);
+            d[t] = mfma_bf16(fp4x8_bf16(c, scale_operand<0>(sc[p][t][b] >> (8 * g))), x, d[t]);
           }
         }
+        if constexpr (NB * R > 4) __builtin_amdgcn_sched_barrier(0);  // one K-step's operands at a time in registers
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      load(p, i + PE);
       // a token that did not pick the expert takes nothing from it, also
       // where its weights are not finite
+      const bool low = picked && col.token < 8, high = picked && col.token >= 8;
 #pragma unroll
-      for (int t = 0; t < R; ++t)
-        if (picked) acc[t] += d[t];
+      for (int t = 0; t < R; ++t) {
+        if (low) acc[0][t] += d[t];
+        if (high) acc[1][t] += d[t];
+      }
+      if (!both || pass) break;
+      col.token = c8 + 8;
+      col.slot = list.slot[wave + kLayerWaves * i][c8 + 8];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    load(p, i + PE);
+  };
+  // out of the loop itself, not round its end: paths that met there would make
+  // the next round wait for all loads
+  for (int i0 = 0;; i0 += PE) {
+#pragma unroll
+    for (int p = 0; p < PE; ++p) {
+      if (i0 + p >= experts) goto done;
+      expert(p, i0 + p);
     }
   }
-  v4f(*red)[R][64] = reinterpret_cast<v4f(*)[R][64]>(area);
+done:
+  // value and remainder columns of a token, each in its own lane's column
+#pragma unroll
+  for (int t = 0; t < R; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float lo = acc[0][t][e] + __shfl_xor(acc[0][t][e], 8, kWave);
+      const float hi = acc[1][t][e] + __shfl_xor(acc[1][t][e], 8, kWave);
+      acc[0][t][e] = part ? hi : lo;
+    }
+  v4f(*const red)[R][64] = reinterpret_cast<v4f(*)[R][64]>(area);
   __syncthreads();
 #pragma unroll
-  for (int t = 0; t < R; ++t) red[wave][t][lane] = acc[t];
+  for (int t = 0; t < R; ++t) red[wave][t][lane] = acc[0][t];
   __syncthreads();
   if (wave < R && r < M) {
     const int n = 16 * wave + 4 * g;

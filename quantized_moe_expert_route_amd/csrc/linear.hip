@@ -168,7 +168,7 @@ template <bool F16, int W, int S, int D>
 __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a) {
   __shared__ v4f red[2][W][64];
   __shared__ uint4 xs[W][256];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int K = (int)a.K, nks = (K + 127) / 128;
   const bool row = r < a.M;
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a)
       store4(a, r, (int64_t)(blockIdx.x + i * step) * 16 + 4 * g, v);
     }
   };
-  auto compute = [&](int d, int i, auto reload, auto first) {
+  auto compute = [&](int d, int i, auto reload, auto first) __attribute__((always_inline)) {
     v4f acc[1] = {{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
@@ -278,7 +278,7 @@ template <bool F16, int CT, int R>
 __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int tiles_n) {
   constexpr int W = 8, P = CT == 1 ? 4 : 2;
   __shared__ uint4 xs[W][CT * 256];  // and the partial sums [W][CT][64]
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int K = (int)a.K, nks = (K + 127) / 128;
   const int tile = (int)(blockIdx.x % tiles_n) * R;
@@ -314,29 +314,34 @@ __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int
   for (int p = 0; p < P; ++p) load_w(p, wave + p * W);
 #pragma unroll
   for (int p = 0; p < P; ++p) load_x(p, wave + p * W);
-  for (int k0 = wave; k0 < nks; k0 += P * W) {
+  auto step = [&](int p, int ks) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < CT * 4; ++i) xs[wave][x_slot(i >> 2, r, 4 * (i & 3) + g)] = xv[p][i];
+    // the wave's lanes read what its other lanes wrote: LDS keeps a wave's order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    load_x(p, ks + P * W);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint4 x[CT];
+#pragma unroll
+      for (int u = 0; u < CT; ++u) x[u] = xs[wave][x_slot(u, 4 * j + g, r)];
+#pragma unroll
+      for (int t = 0; t < R; ++t) w[p][t].template mul<CT>(j, x, acc[t]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    load_w(p, ks + P * W);
+  };
+  // out of the loop itself, not round its end: paths that met there would make
+  // the next round wait for all loads
+  for (int k0 = wave;; k0 += P * W) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int ks = k0 + p * W;
-      if (ks >= nks) break;
-#pragma unroll
-      for (int i = 0; i < CT * 4; ++i) xs[wave][x_slot(i >> 2, r, 4 * (i & 3) + g)] = xv[p][i];
-      // the wave's lanes read what its other lanes wrote: LDS keeps a wave's order
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      load_x(p, ks + P * W);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint4 x[CT];
-#pragma unroll
-        for (int u = 0; u < CT; ++u) x[u] = xs[wave][x_slot(u, 4 * j + g, r)];
-#pragma unroll
-        for (int t = 0; t < R; ++t) w[p][t].template mul<CT>(j, x, acc[t]);
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      load_w(p, ks + P * W);
+      if (k0 + p * W >= nks) goto done;
+      step(p, k0 + p * W);
     }
   }
-  v4f(*red)[CT][64] = reinterpret_cast<v4f(*)[CT][64]>(&xs[0][0]);
+done:
+  v4f(*const red)[CT][64] = reinterpret_cast<v4f(*)[CT][64]>(&xs[0][0]);
 #pragma unroll
   for (int t = 0; t < R; ++t) {
     __syncthreads();
@@ -370,7 +375,7 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
   static_assert(BM % (4 * W) == 0, "whole pieces");
   constexpr int P = F16 ? 2 : 1;  // bf16 planes of x
   __shared__ uint4 xs[2][P][BM * 16];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int wn = wave % WN, wm = wave / WN;
   const int K = (int)a.K, nks = (K + 127) / 128;
@@ -451,37 +456,42 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
   put_x(xv[0], 0);
   load_x(xv[0], 2);
   barrier_lds();
-  for (int k0 = 0; k0 < nks; k0 += PW) {
+  auto step = [&](int p, int ks) __attribute__((always_inline)) {
+    // step ks + 1's x into the buffer that step ks - 1 was read from
+    put_x(xv[(p + 1) & 1], (p + 1) & 1);
+    load_x(xv[(p + 1) & 1], ks + 3);
 #pragma unroll
-    for (int p = 0; p < PW; ++p) {
-      const int ks = k0 + p;
-      if (ks >= nks) break;
-      // step ks + 1's x into the buffer that step ks - 1 was read from
-      put_x(xv[(p + 1) & 1], (p + 1) & 1);
-      load_x(xv[(p + 1) & 1], ks + 3);
+    for (int j = 0; j < 4; ++j) {
+      v8s wf[TN];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v8s wf[TN];
+      for (int t = 0; t < TN; ++t) {
+        const uint32_t d = j == 0 ? q[p][t].x : j == 1 ? q[p][t].y : j == 2 ? q[p][t].z : q[p][t].w;
+        wf[t] = fp4x8_bf16(d, scale_of(sc[p][t], j));
+      }
 #pragma unroll
-        for (int t = 0; t < TN; ++t) {
-          const uint32_t d = j == 0 ? q[p][t].x : j == 1 ? q[p][t].y : j == 2 ? q[p][t].z : q[p][t].w;
-          wf[t] = fp4x8_bf16(d, scale_of(sc[p][t], j));
-        }
+      for (int u = 0; u < TM; ++u) {
+        const int at = x_slot(wm * TM + u, 4 * j + g, r);
 #pragma unroll
-        for (int u = 0; u < TM; ++u) {
-          const int at = x_slot(wm * TM + u, 4 * j + g, r);
+        for (int pl = P - 1; pl >= 0; --pl) {
+          const v8s f = __builtin_bit_cast(v8s, xs[p & 1][pl][at]);
 #pragma unroll
-          for (int pl = P - 1; pl >= 0; --pl) {
-            const v8s f = __builtin_bit_cast(v8s, xs[p & 1][pl][at]);
-#pragma unroll
-            for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], f, acc[t][u]);
-          }
+          for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], f, acc[t][u]);
         }
       }
-      load_w(p, ks + PW);
-      barrier_lds();
+    }
+    load_w(p, ks + PW);
+    barrier_lds();
+  };
+  // out of the loop itself, not round its end: paths that met there would make
+  // the next round wait for all loads
+  for (int k0 = 0;; k0 += PW) {
+#pragma unroll
+    for (int p = 0; p < PW; ++p) {
+      if (k0 + p >= nks) goto done;
+      step(p, k0 + p);
     }
   }
+done:
 #pragma unroll
   for (int u = 0; u < TM; ++u) {
     const int64_t m = m0 + 16 * (wm * TM + u) + r;

@@ -54,6 +54,10 @@ __device__ __forceinline__ float e8m0_value(uint32_t d) {
   return v[0];
 }
 
+// This thread's wave, as a scalar: loops and addresses that depend on it stay
+// uniform for the compiler.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // 8 fp16 values as two bf16 each, value = hi + lo exactly: hi keeps the upper
 // 8 of 11 significant bits, lo the rest (both in bf16's wider range, fp16
 // subnormals included). An infinity or NaN stays in hi, lo zero.

@@ -51,20 +51,23 @@ __device__ __forceinline__ double shfl_xor_f64(double v, int o) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+constexpr int kRouterWaves = 12;  // 3 a SIMD: 168 registers a lane
+
 // Up to 16 tokens: one expert and T tokens a workgroup. A wave takes 512
 // elements of H at a time, 8 a lane, all T tokens' pieces under way at once;
 // the lanes' float64 sums are added by exchanging halves (T values shrink to
 // one a lane), then the waves'. Every workgroup reads all of x: 16 x 6144 is
 // 50 MB from the L2s, 2.6 us, about the time of the float64 products.
 template <int XT, int WT, int T>
-__global__ __launch_bounds__(1024) void router_kernel(const RouterArgs a) {
-  __shared__ double red[16][T];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+__global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(const RouterArgs a) {
+  __shared__ double red[kRouterWaves][T];
+  const int wave = wave_id(), lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int64_t e = blockIdx.x;
   const int mt = (int)a.M, H = (int)a.H;
   double acc[T];
 #pragma unroll
   for (int t = 0; t < T; ++t) acc[t] = 0.0;
+#pragma unroll 1
   for (int c = (wave * 64 + lane) * 8; c < H; c += waves * 512) {
     Raw8<WT> wr;
     Raw8<XT> xr[T];
@@ -152,7 +155,7 @@ template <int XT, int WT, int TN, int TM, int W>
 __global__ __launch_bounds__(64 * W) void router_tile_kernel(const RouterArgs a, int tiles_e) {
   __shared__ v4f red[W][TN * TM > 4 ? 4 : TN * TM][64];
   constexpr int C = TN * TM > 4 ? 4 : TN * TM;  // sub-tiles joined at a time
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int e0 = (int)(blockIdx.x % tiles_e) * 16 * TN;
   const int64_t m0 = (int64_t)(blockIdx.x / tiles_e) * 16 * TM;
@@ -248,7 +251,7 @@ static hipError_t launch_tiles(const RouterArgs& a, hipStream_t stream) {
 template <int XT, int WT>
 static hipError_t launch_types(const RouterArgs& a, int cus, hipStream_t stream) {
   if (a.M <= 16) {
-    const dim3 grid((unsigned)a.E), block(64 * (unsigned)std::min<int64_t>(16, (a.H + 511) / 512));
+    const dim3 grid((unsigned)a.E), block(64 * (unsigned)std::min<int64_t>(kRouterWaves, (a.H + 511) / 512));
     if (a.M <= 1) return launch_k(router_kernel<XT, WT, 1>, grid, block, 0, stream, Ev{}, a);
     if (a.M <= 4) return launch_k(router_kernel<XT, WT, 4>, grid, block, 0, stream, Ev{}, a);
     if (a.M <= 8) return launch_k(router_kernel<XT, WT, 8>, grid, block, 0, stream, Ev{}, a);
