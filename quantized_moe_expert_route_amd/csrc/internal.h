@@ -32,7 +32,7 @@ struct Internal {
   size_t sync_begin, sync_bytes;  // region zeroed once when the workspace is bound
   // of moe_layer_forward, behind moe_forward's regions
   size_t layer_logits;  // fp32 [min(M, kSmallM), E]
-  size_t layer_g;       // bf16 [n, I/128, 2, 128]: weighted h of its up to kSmallM tokens, values and remainders
+  size_t layer_g;       // bf16 [n, I/128, 256]: weighted h of its up to kSmallM tokens, values and remainders (h_at of layer.hip)
   size_t layer_list;    // the picked experts and the tokens' slots (layer.hip)
 };
 

@@ -12,6 +12,8 @@
 // tokens' x, and the columns of tokens that did not pick it are dropped; the
 // down product of 16 output columns runs over every active expert, a token's
 // column being zero where it did not pick the expert, which also combines.
+#include <stddef.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -30,6 +32,7 @@ struct ActiveList {
   int pad[3];
   uint16_t expert[kLayerMaxEntries];        // active experts, ascending
   uint8_t slot[kLayerMaxEntries][kSmallM];  // [active][token]: the token's slot, 255: none
+  uint16_t zero[256];                       // h of a token that did not pick an expert
 };
 static_assert(sizeof(ActiveList) == kLayerListBytes && sizeof(ActiveList) % 16 == 0, "copied in 16-byte pieces");
 
@@ -114,10 +117,12 @@ __device__ __forceinline__ void topk_tokens(uint32_t (&key)[T][EC], bool second,
 // conflicts (writes: one row's 16 chunks; reads: one group's 16 rows).
 __device__ __forceinline__ int x13_slot(int c, int m) { return (c & 3) * 64 + 16 * (c >> 2) + (m ^ c); }
 
-// Weighted h of the batch, as the down launch reads it: per entry t * k + j and
-// K-step b of 128, a plane of 128 bf16 values, then a plane of remainders.
-__device__ __forceinline__ size_t h_at(int entry, int nb, int col, int plane) {
-  return (((size_t)entry * nb + (col >> 7)) * 2 + plane) * 128 + (col & 127);
+// Weighted h of the batch, as the down launch's lanes read it: per entry
+// t * k + j and K-step of 128, operand j (K 32 g + 8 j .. + 7 of lane group g)
+// is one line: the four groups' values, then their remainders.
+__device__ __forceinline__ size_t h_at(int entry, int nb, int col, int part) {
+  const int e = col & 127;
+  return ((size_t)entry * nb + (col >> 7)) * 256 + (((e >> 3) & 3) * 8 + part * 4 + (e >> 5)) * 8 + (e & 7);
 }
 
 constexpr int kHoldItems = 16;  // finished items a gate/up workgroup holds before it stores them
@@ -164,14 +169,30 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
   }
   const bool few = M <= 4;
   uint4 xv[S][4];
+  int now = 1;
+  asm volatile("" : "+s"(now));  // (a branch the compiler must keep, or it asks for x only where it is used)
+  if (now) {
 #pragma unroll
-  for (int s = 0; s < S; ++s)
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ks = wave * S + s, m = few ? r : 4 * i + g, c = few ? 4 * g + i : r;
-      xv[s][i] = m < M && ks < nks ? ld16(x + (size_t)m * H + 128 * ks + 8 * c) : make_uint4(0, 0, 0, 0);
-    }
-  if (threadIdx.x < kRouteMaxE / 32) mask[threadIdx.x] = 0;
+      for (int i = 0; i < 4; ++i) {
+        // rows past M and steps past the last: the last ones again (no branch:
+        // the compiler counts the loads under way). Columns of tokens past M
+        // are dropped, steps past the last become zero below.
+        const int ks = min(wave * S + s, nks - 1), m = min(few ? r : 4 * i + g, M - 1), c = few ? 4 * g + i : r;
+        xv[s][i] = ld16(x + (size_t)m * H + 128 * ks + 8 * c);
+      }
+  } else {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xv[s][i] = make_uint4(0, 0, 0, 0);
+  }
+  if (threadIdx.x < kRouteMaxE / 32) {
+    mask[threadIdx.x] = 0;
+    reinterpret_cast<uint4*>(list.zero)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+  }
+  static_assert(kRouteMaxE / 32 == sizeof(list.zero) / 16, "cleared together");
   for (int i = threadIdx.x; i < kLayerMaxEntries; i += 64 * kLayerWaves)
     reinterpret_cast<uint4*>(list.slot)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
   barrier_lds();
@@ -273,6 +294,15 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
   }
+  // x is waited for here, once: left to its first use, inside the loop, the
+  // wait would be for all loads, every round
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (wave * S + s >= nks) xf[s][j] = make_uint4(0, 0, 0, 0);
+      asm volatile("" : "+v"(xf[s][j].x), "+v"(xf[s][j].y), "+v"(xf[s][j].z), "+v"(xf[s][j].w));
+    }
 
   auto flush = [&](int i0, int i1) {  // store items i0 .. i1 - 1
     for (int v = threadIdx.x; v < (i1 - i0) * 128; v += 64 * kLayerWaves) {
@@ -354,9 +384,11 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
 // Wave w takes experts w, w + 8, ...: an expert's rows of these columns are one
 // run of 512 C8 NB bytes, read PE experts ahead in whole lines and turned
 // into MFMA operands through LDS of the wave's own (operand-shaped loads, 64
-// bytes of 16 rows, cost the memory pipeline four times as much). The batch's
-// weighted h is copied to LDS once (HL); where it does not fit, the lanes of
-// tokens that picked the expert load theirs as they come to it.
+// bytes of 16 rows, cost the memory pipeline four times as much). The tokens'
+// weighted h is loaded UH K-steps ahead by the lanes of tokens that picked the
+// expert: loads return in order, so h asked for when it is needed would wait
+// for all weights under way (and copied to LDS beforehand, it cost 3 to 6 us
+// with nothing else moving).
 // An expert is picked by few of the tokens, so the 16 MFMA columns hold both
 // parts of h at once: column c < 8 the value of token c or c + 8, whichever
 // picked the expert, column c + 8 its remainder (one MFMA, not two). Where
@@ -373,42 +405,32 @@ struct DownRows {  // a row's 4 NB chunks of 16 bytes in LDS, exchanged against 
 };
 
 template <int NB, int C8>
-struct DownLds {
-  static constexpr int kR = (C8 + 1) / 2;                                // MFMA row tiles
-  static constexpr int kRows = 8 * C8 * DownRows<NB>::kStride;           // chunks of a wave's rows
-  static constexpr int kArea = kLayerWaves * (kRows > 64 * kR ? kRows : 64 * kR);  // or the partial sums
-  static constexpr int kZero = 32 * NB;                                  // h of a token that did not pick the expert
-  static constexpr int kFixed = (int)sizeof(ActiveList) + 16 * (kArea + kZero);
-  static constexpr int kHCap = (160 * 1024 - kFixed) / (512 * NB);       // entries whose h fits beside
-};
-
-template <int NB, int C8, bool HL>
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
     const uint16_t* __restrict__ gp, const ActiveList* __restrict__ batch, const uint8_t* __restrict__ w2,
     const uint8_t* __restrict__ s2, uint16_t* __restrict__ out, int M, int H, int k) {
-  typedef DownLds<NB, C8> Lds;
   typedef DownRows<NB> Rows;
-  constexpr int I = 128 * NB, R = Lds::kR;
-  constexpr int kChunks = 8 * C8 * 4 * NB;                               // of an expert's rows
-  constexpr int NL = (kChunks + 63) / 64;
-  constexpr int PE = NL >= 5 ? 2 : NL >= 3 ? 4 : NL == 2 ? 6 : 8;
+  constexpr int I = 128 * NB, R = (C8 + 1) / 2;      // R MFMA row tiles
+  constexpr int kRows = 8 * C8 * Rows::kStride;      // chunks of a wave's rows in LDS
+  constexpr int kWave = kRows > 64 * R ? kRows : 64 * R;  // (or its partial sums)
+  constexpr int NL = (8 * C8 * 4 * NB + 63) / 64;    // loads of an expert's rows
+  constexpr int PE = NL >= 5 ? 2 : NL >= 3 ? 4 : NB == 4 ? 4 : 8;
+  constexpr int UH = NB == 3 ? 3 : 4;
+  static_assert(PE * NB % UH == 0, "whole rounds of h");
   __shared__ __align__(16) ActiveList list;
-  __shared__ uint4 area[Lds::kArea + Lds::kZero];
-  __shared__ uint4 hs[HL ? Lds::kHCap * 32 * NB : 1];
+  __shared__ uint4 area[kLayerWaves * kWave];
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
-  for (int i = threadIdx.x; i < (int)sizeof(ActiveList) / 16; i += 64 * kLayerWaves)
+  for (int i = threadIdx.x; i < (int)offsetof(ActiveList, zero) / 16; i += 64 * kLayerWaves)
     reinterpret_cast<uint4*>(&list)[i] = reinterpret_cast<const uint4*>(batch)[i];
-  if (threadIdx.x < Lds::kZero) area[Lds::kArea + threadIdx.x] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   const int c0 = blockIdx.x * 8 * C8, cols = min(8 * C8, H - c0);
-  const int experts = (list.n - wave + kLayerWaves - 1) / kLayerWaves;   // of this wave
-  uint4* mine = area + wave * Lds::kRows;
+  const int experts = (list.n - wave + kLayerWaves - 1) / kLayerWaves;  // of this wave
+  uint4* mine = area + wave * kRows;
 
   typedef uint32_t scales __attribute__((ext_vector_type(NB == 1 ? 2 : NB), aligned(4)));
   uint4 q[PE][NL];
   uint32_t sc[PE][R][NB];
-  auto load = [&](int p, int i) {
+  auto load = [&](int p, int i) __attribute__((always_inline)) {
     const size_t row0 = (size_t)list.expert[wave + kLayerWaves * min(i, experts - 1)] * H + c0;
 #pragma unroll
     for (int l = 0; l < NL; ++l)  // columns past H: the last chunk again
@@ -432,38 +454,43 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
     bool both;
   };
   const int c8 = r & 7, part = r >> 3;
-  auto column = [&](int i) -> Column {
+  auto column = [&](int i) __attribute__((always_inline)) -> Column {
     const uint8_t* slots = list.slot[wave + kLayerWaves * min(i, experts - 1)];
     const int s0 = slots[c8], s1 = slots[c8 + 8];
     const bool both = __ballot(s0 != 255 && s1 != 255) != 0;
-    if (s0 != 255 || both) return Column{c8, s0, both};
-    return Column{c8 + 8, s1, both};
+    const bool lower = s0 != 255 || both;
+    return Column{lower ? c8 : c8 + 8, lower ? s0 : s1, both};
   };
-  if (experts > 0) {
+  auto load_h = [&](uint4(&hv)[4], const Column& c, int b) __attribute__((always_inline)) {
+    // (no branch round the loads: the compiler counts those under way)
+    const uint16_t* at = (c.slot != 255 ? gp + (size_t)((c.token * k + c.slot) * NB + b) * 256 : batch->zero) +
+                         (part * 4 + g) * 8;
 #pragma unroll
-    for (int p = 0; p < PE; ++p) load(p, p);
-  }
-  if constexpr (HL) {
-    // chunk c of token t's K-step is kept at c ^ t: a group's 16 tokens meet all
-    // banks. Four loads at a time: one by one, each waited for the one before.
-    const int total = M * k * 32 * NB, per = 64 * kLayerWaves;
-    const uint4* src = reinterpret_cast<const uint4*>(gp);
-    auto keep = [&](int i, uint4 v) __attribute__((always_inline)) {
-      if (i < total) hs[(i & ~15) | ((i & 15) ^ (i / (32 * NB) / k))] = v;
-    };
-    for (int i = threadIdx.x; i < total; i += 4 * per) {
-      const uint4 v0 = src[i], v1 = src[min(i + per, total - 1)];
-      const uint4 v2 = src[min(i + 2 * per, total - 1)], v3 = src[min(i + 3 * per, total - 1)];
-      keep(i, v0);
-      keep(i + per, v1);
-      keep(i + 2 * per, v2);
-      keep(i + 3 * per, v3);
-    }
-    __syncthreads();
+    for (int j = 0; j < 4; ++j) hv[j] = ld16(at + 64 * j);
+  };
+  uint4 hv[UH][4];
+  if (experts > 0) {
+    load(0, 0);
+#pragma unroll
+    for (int u = 0; u < UH; ++u) load_h(hv[u], column(u / NB), u % NB);
+#pragma unroll
+    for (int p = 1; p < PE; ++p) load(p, p);
   }
   v4f acc[2][R];  // tokens 0-7, tokens 8-15
 #pragma unroll
   for (int t = 0; t < R; ++t) acc[0][t] = acc[1][t] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](int p, int b, const uint4(&x)[4], v4f(&d)[R]) __attribute__((always_inline)) {
+    uint4 w[R];
+#pragma unroll
+    for (int t = 0; t < R; ++t) w[t] = mine[Rows::at(min(16 * t + r, 8 * C8 - 1), 4 * b + g)];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        const uint32_t c = j == 0 ? w[t].x : j == 1 ? w[t].y : j == 2 ? w[t].z : w[t].w;
+        d[t] = mfma_bf16(fp4x8_bf16(c, scale_operand<0>(sc[p][t][b] >> (8 * g))), __builtin_bit_cast(v8s, x[j]), d[t]);
+      }
+  };
   auto expert = [&](int p, int i) __attribute__((always_inline)) {
 #pragma unroll
     for (int l = 0; l < NL; ++l) {
@@ -471,53 +498,38 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
       mine[Rows::at(n / (4 * NB), n % (4 * NB))] = q[p][l];
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
-    Column col = column(i);
-    const bool both = col.both;
-    for (int pass = 0;; ++pass) {
-      const bool picked = col.slot != 255;
-      const uint4* h = HL && picked ? hs + ((col.token * k + col.slot) * NB * 2 + part) * 16 : area + Lds::kArea;
-      uint4 hv[2][4];
-      auto load_h = [&](int b) __attribute__((always_inline)) {
-        const uint16_t* at = gp + h_at(col.token * k + (picked ? col.slot : 0), NB, 128 * b + 32 * g, part);
+    const Column col = column(i);
+    v4f d[R];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) hv[b & 1][j] = picked ? ld16(at + 8 * j) : make_uint4(0, 0, 0, 0);
-      };
-      if constexpr (!HL) load_h(0);
-      v4f d[R];
+    for (int t = 0; t < R; ++t) d[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int u = p * NB + b;
+      multiply(p, b, hv[u % UH], d);
+      load_h(hv[u % UH], column(i + (b + UH) / NB), (b + UH) % NB);
+      if constexpr (NB * R > 4) __builtin_amdgcn_sched_barrier(0);  // one K-step's operands at a time in registers
+    }
+    // a token that did not pick the expert takes nothing from it, also where
+    // its weights are not finite
+    const bool low = col.slot != 255 && col.token < 8, high = col.slot != 255 && col.token >= 8;
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      if (low) acc[0][t] += d[t];
+      if (high) acc[1][t] += d[t];
+    }
+    if (col.both) {
+      const Column up{c8 + 8, list.slot[wave + kLayerWaves * i][c8 + 8], true};
 #pragma unroll
       for (int t = 0; t < R; ++t) d[t] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        if constexpr (!HL)
-          if (b + 1 < NB) load_h(b + 1);
-        uint4 w[R];
-#pragma unroll
-        for (int t = 0; t < R; ++t) w[t] = mine[Rows::at(min(16 * t + r, 8 * C8 - 1), 4 * b + g)];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 xw;
-          if constexpr (HL) xw = h[32 * b + ((4 * g + j) ^ col.token)];
-          else xw = hv[b & 1][j];
-          const v8s x = __builtin_bit_cast(v8s, xw);
-#pragma unroll
-          for (int t = 0; t < R; ++t) {
-            const uint32_t c = j == 0 ? w[t].x : j == 1 ? w[t].y : j == 2 ? w[t].z : w[t].w;
-            d[t] = mfma_bf16(fp4x8_bf16(c, scale_operand<0>(sc[p][t][b] >> (8 * g))), x, d[t]);
-          }
-        }
-        if constexpr (NB * R > 4) __builtin_amdgcn_sched_barrier(0);  // one K-step's operands at a time in registers
+        uint4 x[4];
+        load_h(x, up, b);
+        multiply(p, b, x, d);
       }
-      // a token that did not pick the expert takes nothing from it, also
-      // where its weights are not finite
-      const bool low = picked && col.token < 8, high = picked && col.token >= 8;
 #pragma unroll
-      for (int t = 0; t < R; ++t) {
-        if (low) acc[0][t] += d[t];
-        if (high) acc[1][t] += d[t];
-      }
-      if (!both || pass) break;
-      col.token = c8 + 8;
-      col.slot = list.slot[wave + kLayerWaves * i][c8 + 8];
+      for (int t = 0; t < R; ++t)
+        if (up.slot != 255) acc[1][t] += d[t];
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     load(p, i + PE);
@@ -537,8 +549,8 @@ done:
   for (int t = 0; t < R; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float lo = acc[0][t][e] + __shfl_xor(acc[0][t][e], 8, kWave);
-      const float hi = acc[1][t][e] + __shfl_xor(acc[1][t][e], 8, kWave);
+      const float lo = acc[0][t][e] + __shfl_xor(acc[0][t][e], 8, 64);
+      const float hi = acc[1][t][e] + __shfl_xor(acc[1][t][e], 8, 64);
       acc[0][t][e] = part ? hi : lo;
     }
   v4f(*const red)[R][64] = reinterpret_cast<v4f(*)[R][64]>(area);
@@ -578,12 +590,9 @@ template <int NB, int C8>
 static hipError_t launch_down_c8(const moe_plan* p, const LayerArgs& a, const uint16_t* gp) {
   const int H = (int)p->s.H;
   const dim3 grid((unsigned)((H + 8 * C8 - 1) / (8 * C8)));
-  auto go = [&](auto kern) {
-    return launch_k(kern, grid, dim3(64 * kLayerWaves), 0, a.stream, Ev{}, gp, wsp<ActiveList>(p, p->X.layer_list),
-                    (const uint8_t*)a.w2, (const uint8_t*)a.s2, (uint16_t*)a.out, (int)a.M, H, (int)p->s.top_k);
-  };
-  return a.M * p->s.top_k <= DownLds<NB, C8>::kHCap ? go(layer_down_kernel<NB, C8, true>)
-                                                    : go(layer_down_kernel<NB, C8, false>);
+  return launch_k(layer_down_kernel<NB, C8>, grid, dim3(64 * kLayerWaves), 0, a.stream, Ev{}, gp,
+                  wsp<ActiveList>(p, p->X.layer_list), (const uint8_t*)a.w2, (const uint8_t*)a.s2, (uint16_t*)a.out,
+                  (int)a.M, H, (int)p->s.top_k);
 }
 
 template <int NB>

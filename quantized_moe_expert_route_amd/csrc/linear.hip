@@ -192,8 +192,11 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a)
     load(0, s, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int k = 128 * (wave * S + s) + 8 * r, m = 4 * i + g;
-      xv[s][i] = m < a.M && k < K ? ld16(xp + m * a.ldx + k) : make_uint4(0, 0, 0, 0);
+      // rows past M and pieces past K: others again (no branch: the compiler
+      // counts the loads under way). Rows past M are not stored, pieces past K
+      // become zero on their way to LDS.
+      const int k = 128 * (wave * S + s) + 8 * r, m = min(4 * i + g, (int)a.M - 1);
+      xv[s][i] = ld16(xp + m * a.ldx + (k < K ? k : 0));
     }
   }
 #pragma unroll
@@ -203,7 +206,10 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a)
   auto operands = [&](int s) {
     uint4* mine = &xs[wave][0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mine[x_slot(0, r, 4 * i + g)] = xv[s][i];
+    for (int i = 0; i < 4; ++i) {
+      if (128 * (wave * S + s) + 128 > K && 128 * (wave * S + s) + 8 * r >= K) xv[s][i] = make_uint4(0, 0, 0, 0);
+      mine[x_slot(0, r, 4 * i + g)] = xv[s][i];
+    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
 #pragma unroll
     for (int j = 0; j < 4; ++j) xf[s][j][0] = mine[x_slot(0, 4 * j + g, r)];
@@ -296,14 +302,9 @@ __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int
   };
   auto load_x = [&](int p, int ks) {
     const int k = 128 * min(ks, nks - 1);
-    const bool in_k = k + 8 * r < K;
-    const int at = in_k ? k + 8 * r : 0;
+    const int at = k + 8 * r < K ? k + 8 * r : 0;
 #pragma unroll
     for (int i = 0; i < CT * 4; ++i) xv[p][i] = ld16(xr[i] + at);
-    if (k + 128 > K) {
-#pragma unroll
-      for (int i = 0; i < CT * 4; ++i) xv[p][i] = in_k ? xv[p][i] : make_uint4(0, 0, 0, 0);
-    }
   };
   v4f acc[R][CT];
 #pragma unroll
@@ -315,6 +316,10 @@ __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int
 #pragma unroll
   for (int p = 0; p < P; ++p) load_x(p, wave + p * W);
   auto step = [&](int p, int ks) __attribute__((always_inline)) {
+    if (128 * ks + 128 > K && 128 * ks + 8 * r >= K) {  // past K: zero (as the codes are)
+#pragma unroll
+      for (int i = 0; i < CT * 4; ++i) xv[p][i] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int i = 0; i < CT * 4; ++i) xs[wave][x_slot(i >> 2, r, 4 * (i & 3) + g)] = xv[p][i];
     // the wave's lanes read what its other lanes wrote: LDS keeps a wave's order
@@ -403,17 +408,17 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
   uint4 xv[2][NX];
   auto load_x = [&](uint4(&v)[NX], int ks) {
     const int k = 128 * min(ks, nks - 1);
-    // K's last step may end inside a row piece: zero there (as the codes are)
-    const bool in_k = k + 8 * r < K;
-    const int at = in_k ? k + 8 * r : 0;
+    const int at = k + 8 * r < K ? k + 8 * r : 0;
 #pragma unroll
     for (int i = 0; i < NX; ++i) v[i] = ld16(xr[i] + at);
-    if (k + 128 > K) {
-#pragma unroll
-      for (int i = 0; i < NX; ++i) v[i] = in_k ? v[i] : make_uint4(0, 0, 0, 0);
-    }
   };
-  auto put_x = [&](const uint4(&v)[NX], int buf) {
+  auto put_x = [&](uint4(&v)[NX], int buf, int ks) {
+    // K's last step may end inside a row piece: zero there (as the codes are;
+    // not at the load, which would be waited for)
+    if (128 * ks + 128 > K && 128 * ks + 8 * r >= K) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const int piece = wave * NX + i;
@@ -453,12 +458,12 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
   load_x(xv[1], 1);
 #pragma unroll
   for (int p = 0; p < PW; ++p) load_w(p, p);
-  put_x(xv[0], 0);
+  put_x(xv[0], 0, 0);
   load_x(xv[0], 2);
   barrier_lds();
   auto step = [&](int p, int ks) __attribute__((always_inline)) {
     // step ks + 1's x into the buffer that step ks - 1 was read from
-    put_x(xv[(p + 1) & 1], (p + 1) & 1);
+    put_x(xv[(p + 1) & 1], (p + 1) & 1, ks + 1);
     load_x(xv[(p + 1) & 1], ks + 3);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
