@@ -248,7 +248,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
   uint4 q[D][S];
   uint32_t sc[D][S];
   auto item_row = [&](int i) -> uint32_t {  // the item's (gate or up) row of this lane, in 16-row blocks' order
-    const int it = first + min(i, own - 1) * step, a = it / nit, c = it - a * nit;
+    const int it = own > 0 ? first + min(i, own - 1) * step : 0, a = it / nit, c = it - a * nit;
     return (uint32_t)list.expert[a] * (2 * I) + 8 * c + (r >= 8 ? I : 0) + (r & 7);
   };
   auto load = [&](int d, int s, uint32_t row) {
@@ -257,13 +257,13 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
     q[d][s] = ld16(w13p + (rb * nks + ks) * 1024 + 256 * g + 16 * (row & 15));
     sc[d][s] = ld4(s13p + (rb * nkq + (ks >> 2)) * 256 + 64 * g + 4 * (row & 15));
   };
-  if (own > 0) {
+  // (a workgroup without an item asks for the first one's: no branch, so that x
+  // is not waited for together with these)
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const uint32_t row = item_row(d);
+  for (int d = 0; d < D; ++d) {
+    const uint32_t row = item_row(d);
 #pragma unroll
-      for (int s = 0; s < S; ++s) load(d, s, row);
-    }
+    for (int s = 0; s < S; ++s) load(d, s, row);
   }
   // The routing weights, while the first weights are on their way: sigmoid
   // scores (float64, one rounding), renormalized over the token's slots in
@@ -426,22 +426,29 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
   const int c0 = blockIdx.x * 8 * C8, cols = min(8 * C8, H - c0);
   const int experts = (list.n - wave + kLayerWaves - 1) / kLayerWaves;  // of this wave
   uint4* mine = area + wave * kRows;
+  // The wave's expert i. Past its last, that one again (with none, the list's
+  // first), by one address for all lanes: asked for without a branch, but
+  // hardly any traffic.
+  auto at = [&](int i) __attribute__((always_inline)) {
+    return experts > 0 ? wave + kLayerWaves * min(i, experts - 1) : 0;
+  };
 
   typedef uint32_t scales __attribute__((ext_vector_type(NB == 1 ? 2 : NB), aligned(4)));
   uint4 q[PE][NL];
   uint32_t sc[PE][R][NB];
   auto load = [&](int p, int i) __attribute__((always_inline)) {
-    const size_t row0 = (size_t)list.expert[wave + kLayerWaves * min(i, experts - 1)] * H + c0;
+    const size_t row0 = (size_t)list.expert[at(i)] * H + c0;
+    const int used = i < experts ? ~0 : 0;
 #pragma unroll
     for (int l = 0; l < NL; ++l)  // columns past H: the last chunk again
-      q[p][l] = ld16(w2 + row0 * (I / 2) + 16 * min(64 * l + lane, cols * 4 * NB - 1));
+      q[p][l] = ld16(w2 + row0 * (I / 2) + 16 * (min(64 * l + lane, cols * 4 * NB - 1) & used));
 #pragma unroll
     for (int t = 0; t < R; ++t) {
-      const uint8_t* at = s2 + (row0 + min(16 * t + r, cols - 1)) * (I / 32);
+      const uint8_t* src = s2 + (row0 + (min(16 * t + r, cols - 1) & used)) * (I / 32);
       if constexpr (NB == 1) {
-        sc[p][t][0] = ld4(at);
+        sc[p][t][0] = ld4(src);
       } else {
-        const scales v = *reinterpret_cast<const scales*>(at);
+        const scales v = *reinterpret_cast<const scales*>(src);
 #pragma unroll
         for (int b = 0; b < NB; ++b) sc[p][t][b] = v[b];
       }
@@ -455,27 +462,25 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
   };
   const int c8 = r & 7, part = r >> 3;
   auto column = [&](int i) __attribute__((always_inline)) -> Column {
-    const uint8_t* slots = list.slot[wave + kLayerWaves * min(i, experts - 1)];
-    const int s0 = slots[c8], s1 = slots[c8 + 8];
+    const uint8_t* slots = list.slot[at(i)];
+    const int none = i < experts ? 0 : 255, s0 = slots[c8] | none, s1 = slots[c8 + 8] | none;
     const bool both = __ballot(s0 != 255 && s1 != 255) != 0;
     const bool lower = s0 != 255 || both;
     return Column{lower ? c8 : c8 + 8, lower ? s0 : s1, both};
   };
   auto load_h = [&](uint4(&hv)[4], const Column& c, int b) __attribute__((always_inline)) {
     // (no branch round the loads: the compiler counts those under way)
-    const uint16_t* at = (c.slot != 255 ? gp + (size_t)((c.token * k + c.slot) * NB + b) * 256 : batch->zero) +
-                         (part * 4 + g) * 8;
+    const uint16_t* src = (c.slot != 255 ? gp + (size_t)((c.token * k + c.slot) * NB + b) * 256 : batch->zero) +
+                          (part * 4 + g) * 8;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) hv[j] = ld16(at + 64 * j);
+    for (int j = 0; j < 4; ++j) hv[j] = ld16(src + 64 * j);
   };
   uint4 hv[UH][4];
-  if (experts > 0) {
-    load(0, 0);
+  load(0, 0);
 #pragma unroll
-    for (int u = 0; u < UH; ++u) load_h(hv[u], column(u / NB), u % NB);
+  for (int u = 0; u < UH; ++u) load_h(hv[u], column(u / NB), u % NB);
 #pragma unroll
-    for (int p = 1; p < PE; ++p) load(p, p);
-  }
+  for (int p = 1; p < PE; ++p) load(p, p);
   v4f acc[2][R];  // tokens 0-7, tokens 8-15
 #pragma unroll
   for (int t = 0; t < R; ++t) acc[0][t] = acc[1][t] = v4f{0.f, 0.f, 0.f, 0.f};

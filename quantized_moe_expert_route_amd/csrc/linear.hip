@@ -298,13 +298,15 @@ __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int
   uint4 xv[P][CT * 4];
   auto load_w = [&](int p, int ks) {
 #pragma unroll
-    for (int t = 0; t < R; ++t) w[p][t].load(a, (size_t)min(tile + t, last) * nks + min(ks, nks - 1), lane);
+    for (int t = 0; t < R; ++t)
+      w[p][t].load(a, (size_t)min(tile + t, last) * nks + min(ks, nks - 1), ks < nks ? lane : 0);
   };
   auto load_x = [&](int p, int ks) {
     const int k = 128 * min(ks, nks - 1);
     const int at = k + 8 * r < K ? k + 8 * r : 0;
+    // past the last step: one address for all lanes, hardly any traffic
 #pragma unroll
-    for (int i = 0; i < CT * 4; ++i) xv[p][i] = ld16(xr[i] + at);
+    for (int i = 0; i < CT * 4; ++i) xv[p][i] = ld16(ks < nks ? xr[i] + at : reinterpret_cast<const uint16_t*>(a.x));
   };
   v4f acc[R][CT];
 #pragma unroll
@@ -409,8 +411,9 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
   auto load_x = [&](uint4(&v)[NX], int ks) {
     const int k = 128 * min(ks, nks - 1);
     const int at = k + 8 * r < K ? k + 8 * r : 0;
+    // past the last step: one address for all lanes, hardly any traffic
 #pragma unroll
-    for (int i = 0; i < NX; ++i) v[i] = ld16(xr[i] + at);
+    for (int i = 0; i < NX; ++i) v[i] = ld16(ks < nks ? xr[i] + at : reinterpret_cast<const uint16_t*>(a.x));
   };
   auto put_x = [&](uint4(&v)[NX], int buf, int ks) {
     // K's last step may end inside a row piece: zero there (as the codes are;
@@ -441,11 +444,11 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
   uint4 q[PW][TN];
   uint32_t sc[PW][TN];
   auto load_w = [&](int p, int ks) {
-    const int kc = min(ks, nks - 1);
+    const int kc = min(ks, nks - 1), used = ks < nks ? ~0 : 0;
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
-      q[p][t] = ld16(a.wp + (rb[t] + kc) * 1024 + 16 * lane);
-      sc[p][t] = ld4(a.sp + (rb[t] + kc) * 64 + 4 * r);
+      q[p][t] = ld16(a.wp + (rb[t] + kc) * 1024 + 16 * (lane & used));
+      sc[p][t] = ld4(a.sp + (rb[t] + kc) * 64 + 4 * (r & used));
     }
   };
 
