@@ -253,9 +253,10 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
   };
   auto load = [&](int d, int s, uint32_t row) {
     const size_t rb = row >> 4;
-    const int ks = min(wave * S + s, nks - 1);
-    q[d][s] = ld16(w13p + (rb * nks + ks) * 1024 + 256 * g + 16 * (row & 15));
-    sc[d][s] = ld4(s13p + (rb * nkq + (ks >> 2)) * 256 + 64 * g + 4 * (row & 15));
+    // a step past the last: one address a block, hardly any traffic
+    const int ks = min(wave * S + s, nks - 1), used = wave * S + s < nks ? ~0 : 0;
+    q[d][s] = ld16(w13p + (rb * nks + ks) * 1024 + ((256 * g + 16 * (row & 15)) & used));
+    sc[d][s] = ld4(s13p + (rb * nkq + (ks >> 2)) * 256 + ((64 * g + 4 * (row & 15)) & used));
   };
   // (a workgroup without an item asks for the first one's: no branch, so that x
   // is not waited for together with these)
@@ -617,11 +618,16 @@ hipError_t launch_layer(const moe_plan* p, const moe_router* router, const Layer
   hipError_t e = launch_router(ra, p->num_cus, a.stream);
   if (e != hipSuccess) return e;
   const int H = (int)p->s.H, nks = H / 128;
-  e = nks <= 8    ? launch_gate_up_s<1>(p, a, logits, gp)
-      : nks <= 16 ? launch_gate_up_s<2>(p, a, logits, gp)
-      : nks <= 32 ? launch_gate_up_s<4>(p, a, logits, gp)
-      : nks <= 48 ? launch_gate_up_s<6>(p, a, logits, gp)
-                  : launch_gate_up_s<8>(p, a, logits, gp);
+  switch ((nks + kLayerWaves - 1) / kLayerWaves) {  // K-steps a wave
+    case 1: e = launch_gate_up_s<1>(p, a, logits, gp); break;
+    case 2: e = launch_gate_up_s<2>(p, a, logits, gp); break;
+    case 3: e = launch_gate_up_s<3>(p, a, logits, gp); break;
+    case 4: e = launch_gate_up_s<4>(p, a, logits, gp); break;
+    case 5: e = launch_gate_up_s<5>(p, a, logits, gp); break;
+    case 6: e = launch_gate_up_s<6>(p, a, logits, gp); break;
+    case 7: e = launch_gate_up_s<7>(p, a, logits, gp); break;
+    default: e = launch_gate_up_s<8>(p, a, logits, gp); break;
+  }
   if (e != hipSuccess) return e;
   // one workgroup a CU, each the same number of columns: a multiple of 8
   // (H 6144 on 256 CUs: 24)

@@ -532,6 +532,7 @@ static hipError_t launch_16_rows(const LinearArgs& a, int cus, hipStream_t strea
   // (fp16 carries four scale dwords a step: more steps do not fit the registers)
   if constexpr (!F16) {
     if (nks <= 32) return launch_rows<F16, 8, 4, 1>(a, cus, stream);
+    if (nks <= 40) return launch_rows<F16, 8, 5, 1>(a, cus, stream);
     if (nks <= 48) return launch_rows<F16, 8, 6, 1>(a, cus, stream);
   }
   // a longer K: x from the L2 for every 16 or 32 columns

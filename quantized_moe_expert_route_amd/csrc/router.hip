@@ -146,7 +146,7 @@ __device__ __forceinline__ void planes8(const Raw8<TYPE>& q, v8s (&out)[kPlanes<
   }
 }
 
-// Above 16 tokens: tiles of 16 TN experts x 16 TM tokens on the bf16 MFMA
+// Up to some hundred tokens: tiles of 16 TN experts x 16 TM tokens on the bf16 MFMA
 // (binary32 sums of exact products, planes as above). The W waves of a
 // workgroup split K in pieces of 64, so that no operand is shared between
 // them: each goes from memory to the wave's registers, without LDS or
@@ -241,6 +241,147 @@ __global__ __launch_bounds__(64 * W) void router_tile_kernel(const RouterArgs a,
   }
 }
 
+// Many tokens: 64 experts x 64 tokens a workgroup. x and the weights go through
+// LDS as they are (whole 256- or 512-byte row pieces are read, two K-steps of
+// 128 ahead in registers, two LDS buffers), each operand where lane 16 g + r
+// reads it, rows exchanged against bank conflicts as in the linear layer. Wave
+// w multiplies K's quarter w % 4 of every step for half of the tokens, so that
+// an operand read from LDS serves two or four MFMAs; planes are formed there.
+// (With every wave loading its own operands, 64 bytes of 16 rows each, 4096
+// tokens of H 6144 to 256 experts took 49 us: the memory pipeline's time.)
+template <int XT, int WT>
+__global__ __launch_bounds__(512) void router_wide_kernel(const RouterArgs a, int tiles_e) {
+  constexpr int NW = WT == MOE_FP32 ? 4 : 2;  // 16-byte pieces of a step's weights a thread
+  __shared__ uint4 sx[2][4 * 256], sw[2][NW * 512];
+  const int wave = wave_id(), lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+  const int wk = wave & 3, wm = wave >> 2;
+  const int H = (int)a.H, nks = (H + 127) / 128;
+  // XCD x (workgroups go to the eight in turn) takes a contiguous eighth of the
+  // tiles, the experts of the same tokens side by side
+  const int total = gridDim.x, per = total >> 3, rest = total & 7, xcd = blockIdx.x & 7;
+  const int id = xcd * per + min(xcd, rest) + (blockIdx.x >> 3);
+  const int e0 = id % tiles_e * 64;
+  const int64_t m0 = (int64_t)(id / tiles_e) * 64;
+
+  // piece i of this thread: row (thread + 512 i) / pieces of a row
+  const uint16_t* xr[2];
+  int64_t wr[NW];
+  constexpr int kWP = WT == MOE_FP32 ? 32 : 16;
+  const int xc = threadIdx.x & 15, wc = threadIdx.x & (kWP - 1);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    xr[i] = reinterpret_cast<const uint16_t*>(a.x) + min(m0 + (threadIdx.x >> 4) + 32 * i, a.M - 1) * a.ldx;
+#pragma unroll
+  for (int i = 0; i < NW; ++i)
+    wr[i] = (int64_t)min(e0 + (int)(threadIdx.x / kWP) + 512 / kWP * i, (int)a.E - 1) * H;
+  const int xe = 8 * xc, we = (kWP == 32 ? 4 : 8) * wc;  // first element of the piece
+  uint4 xv[2][2], wv[2][NW];
+  auto load = [&](int p, int ks) __attribute__((always_inline)) {
+    const int k = 128 * min(ks, nks - 1);  // pieces past H: the row's first (zero below)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) xv[p][i] = ld16(xr[i] + (k + xe < H ? k + xe : 0));
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int64_t at = wr[i] + (k + we < H ? k + we : 0);
+      if constexpr (WT == MOE_FP32) wv[p][i] = ld16(reinterpret_cast<const float*>(a.w) + at);
+      else wv[p][i] = ld16(reinterpret_cast<const uint16_t*>(a.w) + at);
+    }
+  };
+  // chunk c of row m of a 16-row block
+  auto slot = [](int block, int c, int m) { return (block * 4 + (c >> 2)) * 64 + 16 * (c & 3) + (m ^ c); };
+  auto put = [&](int p, int buf, int ks) __attribute__((always_inline)) {
+    const bool xin = 128 * ks + xe < H, win = 128 * ks + we < H;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = (threadIdx.x >> 4) + 32 * i;
+      sx[buf][slot(row >> 4, xc, row & 15)] = xin ? xv[p][i] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int row = threadIdx.x / kWP + 512 / kWP * i;
+      // fp32: an operand's 8 elements are two pieces, kept 1024 apart
+      const int at = kWP == 32 ? (wc & 1) * 1024 + slot(row >> 4, wc >> 1, row & 15) : slot(row >> 4, wc, row & 15);
+      sw[buf][at] = win ? wv[p][i] : make_uint4(0, 0, 0, 0);
+    }
+  };
+  v4f acc[4][2];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
+  load(0, 0);
+  load(1, 1);
+  put(0, 0, 0);
+  load(0, 2);
+  barrier_lds();
+  auto step = [&](int p, int ks) __attribute__((always_inline)) {
+    put(p ^ 1, p ^ 1, ks + 1);  // into the buffer that step ks - 1 was read from
+    load(p ^ 1, ks + 3);
+    v8s xf[2][kPlanes<XT>];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      Raw8<XT> q;
+      q.v[0] = sx[p][slot(2 * wm + u, 4 * wk + g, r)];
+      planes8<XT>(q, xf[u]);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      Raw8<WT> q;
+      q.v[0] = sw[p][slot(t, 4 * wk + g, r)];
+      if constexpr (WT == MOE_FP32) q.v[1] = sw[p][1024 + slot(t, 4 * wk + g, r)];
+      v8s wf[kPlanes<WT>];
+      planes8<WT>(q, wf);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = kPlanes<WT> - 1; i >= 0; --i)
+#pragma unroll
+          for (int j = kPlanes<XT> - 1; j >= 0; --j) acc[t][u] = mfma_bf16(wf[i], xf[u][j], acc[t][u]);
+    }
+    barrier_lds();
+  };
+  for (int k0 = 0;; k0 += 2) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      if (k0 + p >= nks) goto done;
+      step(p, k0 + p);
+    }
+  }
+done:
+  // the four quarters' sums in order, through LDS; lane (g, r): experts 4 g ..
+  // + 3 of token r
+  v4f(*const red)[8][64] = reinterpret_cast<v4f(*)[8][64]>(&sx[0][0]);  // [3][8][64]: 24 of sx's 32 KB
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    __syncthreads();
+    if (wm == half && wk > 0) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) red[wk - 1][2 * t + u][lane] = acc[t][u];
+    }
+    __syncthreads();
+    if (wm == half && wk == 0) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          v4f v = acc[t][u];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) v += red[i][2 * t + u][lane];
+          const int64_t m = m0 + 16 * (2 * wm + u) + r;
+          const int e = e0 + 16 * t + 4 * g;
+          if (m < a.M) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (e + q < a.E) a.logits[m * a.E + e + q] = v[q];
+          }
+        }
+    }
+  }
+}
+
 template <int XT, int WT, int TN, int TM, int W>
 static hipError_t launch_tiles(const RouterArgs& a, hipStream_t stream) {
   const int64_t te = (a.E + 16 * TN - 1) / (16 * TN), tm = (a.M + 16 * TM - 1) / (16 * TM);
@@ -257,9 +398,14 @@ static hipError_t launch_types(const RouterArgs& a, int cus, hipStream_t stream)
     if (a.M <= 8) return launch_k(router_kernel<XT, WT, 8>, grid, block, 0, stream, Ev{}, a);
     return launch_k(router_kernel<XT, WT, 16>, grid, block, 0, stream, Ev{}, a);
   }
-  // the largest tile that still gives every CU a workgroup
+  // 64 x 64 tiles where they occupy half of the CUs, else the larger of two that
+  // still give every CU a workgroup (H 6144, 256 experts, bf16: 2048 tokens 31
+  // us by the first, 49 by the second; 1024 tokens 30 and 25; 256 tokens 28 us
+  // by the first and 13 by the third)
   auto groups = [&](int t) { return ((a.E + 16 * t - 1) / (16 * t)) * ((a.M + 16 * t - 1) / (16 * t)); };
-  if (groups(4) >= cus) return launch_tiles<XT, WT, 4, 4, 8>(a, stream);
+  if (groups(4) >= cus / 2)
+    return launch_k(router_wide_kernel<XT, WT>, dim3((unsigned)groups(4)), dim3(512), 0, stream, Ev{}, a,
+                    (int)((a.E + 63) / 64));
   if (groups(2) >= cus) return launch_tiles<XT, WT, 2, 2, 8>(a, stream);
   return launch_tiles<XT, WT, 1, 1, 16>(a, stream);
 }
