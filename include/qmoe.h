@@ -349,7 +349,7 @@ typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
  *   w  [E, H]  bf16 or fp32 (w_type), kept by the handle, not copied: it must
  *              stay valid while the handle is used
  *   x  [M, H]  bf16 or fp16 (x_type), rows ldx elements apart (ldx >= H, a
- *              multiple of 8)
+ *              multiple of 8, at most 2^40)
  *   logits  fp32 [M, E], dense
  * max_M bounds a call's M. MOE_ERR_INVALID_ARG for null or misaligned
  * pointers (16 bytes), non-positive sizes, unknown types, M > max_M, a bad
@@ -387,7 +387,8 @@ moe_status moe_router_forward(const moe_router* router, int64_t M, const void* x
  * K, a multiple of 8; x 16-byte aligned); y [M, N], rows ldy >= N apart, of
  * x's type or MOE_FP32 (y_type); residual [M, N] of y's type, rows ldr >= N
  * apart, or NULL. residual may be y itself (same pointer and stride: added in
- * place); any other overlap of y with an input is MOE_ERR_INVALID_ARG.
+ * place); any other overlap of y with an input is MOE_ERR_INVALID_ARG, as is a
+ * row distance above 2^40.
  * M = 0 enqueues nothing. Calls on several streams may overlap. */
 typedef struct moe_linear moe_linear;
 moe_status moe_linear_pack_bytes(int64_t N, int64_t K, size_t* w_bytes, size_t* s_bytes);
@@ -408,7 +409,7 @@ moe_status moe_linear_forward(const moe_linear* linear, int64_t M, const void* x
  *   out    = bf16(sum over slots of weight * h W2^T)
  * `router` has the plan's E and H, bf16 x and the plan's device. x bf16
  * [M, H], out bf16 [M, H] fully overwritten, no overlap with an input or the
- * workspace. Leaves topk_ids and topk_w of moe_plan_layout; the other regions
+ * workspace, nor of x with the workspace. Leaves topk_ids and topk_w of moe_plan_layout; the other regions
  * are not written. MOE_ERR_UNSUPPORTED for M > 16, H > 8192, a plan with a
  * shared expert or shared slot, the tensor-parallel exchange, the MXFP4 mid or
  * a declared layout other than MOE_LAYOUT_W13_PACKED; other errors as

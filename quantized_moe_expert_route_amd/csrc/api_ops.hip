@@ -14,6 +14,7 @@ using namespace qmoe;
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 20;
+constexpr int64_t kMaxStride = (int64_t)1 << 40;  // elements between rows: kMaxRows of them stay below 2^63 bytes
 
 bool type16(int t) { return t == MOE_BF16 || t == MOE_FP16; }
 size_t type_bytes(int t) { return t == MOE_FP32 ? 4 : 2; }
@@ -75,7 +76,8 @@ moe_status moe_router_forward(const moe_router* r, int64_t M, const void* x, int
                               void* stream) {
   if (!r || M < 0 || M > r->max_M) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
-  if (!x || !aligned16(x) || !logits || !aligned16(logits) || ldx < r->H || ldx % 8 != 0) return MOE_ERR_INVALID_ARG;
+  if (!x || !aligned16(x) || !logits || !aligned16(logits) || ldx < r->H || ldx % 8 != 0 || ldx > kMaxStride)
+    return MOE_ERR_INVALID_ARG;
   if (ptr_device(x) != r->device || ptr_device(logits) != r->device) return MOE_ERR_DEVICE;
   const size_t out_bytes = 4 * (size_t)M * (size_t)r->E;
   if (overlaps(logits, out_bytes, x, span(M, ldx, r->H, 2)) ||
@@ -148,9 +150,10 @@ moe_status moe_linear_forward(const moe_linear* l, int64_t M, const void* x, int
   if (y_type != l->x_type && y_type != MOE_FP32) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
   const size_t es = type_bytes(y_type);
-  if (!x || !aligned16(x) || ldx < l->K || ldx % 8 != 0) return MOE_ERR_INVALID_ARG;
-  if (!y || ((uintptr_t)y & (es - 1)) || ldy < l->N) return MOE_ERR_INVALID_ARG;
-  if (residual && (((uintptr_t)residual & (es - 1)) || ldr < l->N)) return MOE_ERR_INVALID_ARG;
+  if (!x || !aligned16(x) || ldx < l->K || ldx % 8 != 0 || ldx > kMaxStride) return MOE_ERR_INVALID_ARG;
+  if (!y || ((uintptr_t)y & (es - 1)) || ldy < l->N || ldy > kMaxStride) return MOE_ERR_INVALID_ARG;
+  if (residual && (((uintptr_t)residual & (es - 1)) || ldr < l->N || ldr > kMaxStride))
+    return MOE_ERR_INVALID_ARG;
   if (ptr_device(x) != l->device || ptr_device(y) != l->device || (residual && ptr_device(residual) != l->device))
     return MOE_ERR_DEVICE;
   size_t wb, sb;
@@ -164,8 +167,13 @@ moe_status moe_linear_forward(const moe_linear* l, int64_t M, const void* x, int
     return MOE_ERR_INVALID_ARG;
   DeviceGuard guard(l->device);
   if (!guard.ok) return MOE_ERR_DEVICE;
-  const int vec = l->N % 4 == 0 && ldy % 4 == 0 && ((uintptr_t)y & (4 * es - 1)) == 0 &&
-                  (!residual || (ldr % 4 == 0 && ((uintptr_t)residual & (4 * es - 1)) == 0));
+  // columns that move together: groups of four, or pieces of 16 bytes
+  auto fits = [&](int64_t n) {
+    const uintptr_t bytes = (uintptr_t)n * es - 1;
+    return l->N % n == 0 && ldy % n == 0 && ((uintptr_t)y & bytes) == 0 &&
+           (!residual || (ldr % n == 0 && ((uintptr_t)residual & bytes) == 0));
+  };
+  const int vec = fits(16 / (int64_t)es) ? 2 : fits(4) ? 1 : 0;
   const LinearArgs a{M, l->N, l->K, ldx, ldr, ldy, x, l->wp, l->sp, l->bias, residual, y, l->x_type, y_type, vec};
   return launch_linear(a, l->num_cus, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -190,6 +198,7 @@ moe_status moe_layer_forward(moe_plan* plan, const moe_router* router, int64_t M
     if (ptr_device(q) != plan->device) return MOE_ERR_DEVICE;
   const size_t H = (size_t)plan->s.H, E = (size_t)plan->s.E, I = (size_t)plan->s.I, ob = (size_t)M * H * 2;
   if (overlaps(out, ob, x, ob) || overlaps(out, ob, plan->ws, plan->ws_bytes) ||
+      overlaps(x, ob, plan->ws, plan->ws_bytes) ||
       overlaps(out, ob, router->w, E * H * type_bytes(router->w_type)) || overlaps(out, ob, w13, E * I * H) ||
       overlaps(out, ob, s13, E * I * H / 16) || overlaps(out, ob, w2, E * I * H / 2) ||
       overlaps(out, ob, s2, E * I * H / 32))

@@ -43,7 +43,7 @@ struct LinearArgs {
   const void* residual;  // y's type, or NULL
   void* y;
   int x_type, y_type;
-  int vec;  // N, the strides and the addresses allow four columns in one access
+  int vec;  // N, the strides and the addresses allow four columns (1) or 16 bytes (2) in one access
 };
 hipError_t launch_pack_linear(const void* w, const void* s, int64_t N, int64_t K, void* wp, void* sp,
                               hipStream_t stream);

@@ -275,3 +275,70 @@ def test_refusals_on_the_device():
                    torch.zeros(2 * 4 * 8704, dtype=torch.uint8, device="cuda"),
                    torch.zeros(4, 8704, dtype=torch.bfloat16, device="cuda"))
     assert e.value.status == B.MOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("M,H,E,I,k", [(16, 8192, 20, 512, 16), (9, 3584, 300, 256, 7), (12, 8192, 260, 128, 4),
+                                       (16, 7168, 64, 384, 9), (6, 4608, 130, 512, 10)])
+def test_widest_and_slots_shared_by_both_halves(M, H, E, I, k):
+    """The widest hidden and expert sizes, K-steps that do not divide by the
+    waves, and experts that tokens of both halves of the batch picked."""
+    d = Layer(M, H, E, I, k, alike=0.5)
+    d.check(d.call())
+
+
+def test_two_graphs_share_a_plan():
+    """Two captured calls of different sizes on one plan's workspace, replayed
+    in turn with eager calls between them."""
+    import torch
+
+    d = Layer(16, 1024, 40, 256, 4)
+    x = d.x.cuda()
+    sizes = (3, 16)
+    want = [d.call(x=x[:M]).clone() for M in sizes]
+    outs = [torch.empty_like(w) for w in want]
+    graphs = []
+    for M, o in zip(sizes, outs):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            d.call(x=x[:M], out=o)
+        graphs.append(g)
+    for i in range(4):
+        for o in outs:
+            o.zero_()
+        for g in graphs[::1 if i % 2 else -1]:
+            g.replay()
+            d.call(x=x[:7])
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_inputs_inside_the_workspace_are_refused():
+    import torch
+    from quantized_moe_expert_route_amd import binding as B
+
+    d = Layer(4, 512, 8, 128, 2)
+    inside = d.plan.workspace.view(torch.bfloat16)[:4 * 512].view(4, 512)
+    for kw in (dict(x=inside), dict(out=inside)):
+        with pytest.raises(B.MoeError) as e:
+            d.call(**kw)
+        assert e.value.status == B.MOE_ERR_INVALID_ARG
+
+
+def test_every_logit_nan():
+    """Routing of a batch whose logits are all NaN (also the NaN of all ones)
+    stays inside the expert list; the next call is as before."""
+    import torch
+    from quantized_moe_expert_route_amd.binding import Router
+
+    for E in (8, 70, 300):
+        d = Layer(16, 512, E, 128, 5)
+        want = d.call().clone()
+        keep = d.router
+        for bits in (-1, 0x7FC00000):
+            d.router = Router(torch.full((E, 512), bits, dtype=torch.int32, device="cuda").view(torch.float32))
+            d.call()
+            ids = d.plan.view("topk_ids", torch.int32, (16, 5))
+            assert int(ids.min()) >= 0 and int(ids.max()) < E
+        d.router = keep
+        assert torch.equal(d.call(), want)

@@ -257,3 +257,74 @@ def test_refusals_on_the_device():
         lin.forward(strided, y)  # rows not 16-byte aligned
     with pytest.raises(ValueError):
         lin.forward(x.cpu(), y)
+
+
+@pytest.mark.parametrize("M", [20, 140, 300])
+@pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp16", "fp32")])
+def test_whole_pieces_in_place(M, xt, yt):
+    """Widths and strides whose pieces of 16 bytes are whole (N 264: in a row's
+    last tile only some are), bias and the residual in place, the columns
+    between the rows untouched; then the same from an address that allows
+    groups of four, and one that allows single elements only."""
+    import torch
+
+    rng = np.random.default_rng([M, 17])
+    N, K = 264, 160
+    d = _case(rng, M, N, K, xt, yt, bias=True, residual=True)
+    lin = _linear(d)
+    y, mag = _expect(d)
+    tol = R.sum_error(K) * mag * 1.01 + R.half_step(yt) * np.abs(y) + (2.0 ** -25 if yt == "fp16" else 0.0)
+    got = []
+    for start in (0, 4, 1):
+        buf = torch.full((M * 280 + 8,), 3.0, dtype=_dt(yt), device="cuda")
+        rows = buf[start:start + M * 280].view(M, 280)
+        rows[:, :N] = d["residual"].cuda()
+        lin.forward(d["x"].cuda(), rows[:, :N], residual=rows[:, :N])
+        assert bool((rows[:, N:] == 3.0).all()) and bool((buf[:start] == 3.0).all())
+        got.append(rows[:, :N].cpu())
+        assert np.all(np.abs(_f64(got[-1]) - y) <= tol)
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+@pytest.mark.parametrize("M", [3, 20, 130])
+def test_rows_more_than_32_bits_apart(M):
+    import torch
+
+    rng = np.random.default_rng([M, 19])
+    N, K = 48, 160
+    d = _case(rng, M, N, K, "bf16", "bf16", residual=True)
+    far = (5 << 30) // (2 * (M - 1)) // 8 * 8  # elements between rows: the last 5 GiB behind the first
+    big = torch.empty(far * (M - 1) + 512, dtype=torch.bfloat16, device="cuda")
+    x, y = (big[at:].as_strided((M, c), (far, 1)) for at, c in ((0, K), (256, N)))
+    with pytest.raises(Exception):  # the rows lie between each other: refused as overlapping
+        _linear(d).forward(x, y)
+    x.copy_(d["x"])
+    res = d["residual"].cuda()
+    out = torch.empty_like(res)
+    _linear(d).forward(x, out, residual=res)
+    _check(out.cpu(), d)
+    x = d["x"].cuda()
+    y.copy_(d["residual"])
+    _linear(d).forward(x, y, residual=y)
+    _check(y.cpu(), d)
+
+
+def test_most_rows_and_widest():
+    """The largest row count (2^20) and width (2^24) a call may have, exact sums."""
+    import torch
+
+    rng = np.random.default_rng(23)
+    d = _case(rng, 1 << 20, 8, 32, "bf16", "fp32", integers=True)
+    assert torch.equal(_run(d), torch.from_numpy(_expect(d)[0]).float())
+    codes = torch.randint(0, 256, (1 << 24, 16), dtype=torch.uint8, device="cuda")
+    scales = torch.full((1 << 24, 1), 127, dtype=torch.uint8, device="cuda")
+    from quantized_moe_expert_route_amd.binding import Linear
+
+    lin = Linear(codes, scales)
+    at = torch.from_numpy(np.r_[0:40, (1 << 24) - 40:1 << 24, rng.integers(0, 1 << 24, 200)]).cuda()
+    for M in (1, 20):
+        x = torch.from_numpy(rng.integers(-3, 4, (M, 32)).astype(np.float32)).bfloat16()
+        out = torch.empty(M, 1 << 24, dtype=torch.float32, device="cuda")
+        lin.forward(x.cuda(), out)
+        want = R.linear(_f64(x), codes[at].cpu().numpy(), scales[at].cpu().numpy())[0]
+        assert np.array_equal(_f64(out[:, at].cpu()), want)

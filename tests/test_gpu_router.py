@@ -124,3 +124,52 @@ def test_feeds_the_routed_call():
         want, _ = R.route((x.double().numpy() @ rw.double().numpy().T).astype(np.float32), k, 2.5)
         assert np.array_equal(ids, want)
         assert torch.isfinite(out.float()).all()
+
+
+def test_rows_more_than_32_bits_apart_and_most_rows():
+    import torch
+    from quantized_moe_expert_route_amd.binding import Router
+
+    for M, E in ((3, 40), (40, 40), (600, 300)):  # each of the three kernels
+        x, w = _case(M, E, 264, "bf16", "bf16")
+        far = (5 << 30) // (2 * (M - 1)) // 8 * 8
+        big = torch.empty(far * (M - 1) + 512, dtype=torch.bfloat16, device="cuda").as_strided((M, 264), (far, 1))
+        big.copy_(x)
+        out = torch.full((M, E), float("nan"), device="cuda")
+        Router(w.cuda()).forward(big, out)
+        _check(out.cpu().double().numpy(), x, w)
+    x, w = _case(1 << 20, 3, 8, "fp16", "fp32")
+    _check(_run(x, w), x, w)
+    x, w = _case(20, 5, 65536, "bf16", "fp32")
+    _check(_run(x, w), x, w)
+    _check(_run(x[:9], w), x[:9], w)
+
+
+def test_wide_tiles_of_every_type_and_non_finite_tokens():
+    """64 x 64 tiles, ragged in all three sizes; a NaN token stays alone."""
+    for xt, wt in (("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "bf16"), ("fp16", "fp32")):
+        x, w = _case(1100, 500, 328, xt, wt)
+        base = _run(x, w)
+        _check(base, x, w)
+        x[77, 100] = float("nan")
+        x[1099, 5] = float("inf")
+        got = _run(x, w)
+        rest = ~np.isin(np.arange(1100), (77, 1099))
+        assert np.array_equal(got[rest], base[rest]) and np.all(np.isnan(got[77])) and not np.isfinite(got[1099]).any()
+
+
+def test_one_handle_on_two_streams():
+    import torch
+    from quantized_moe_expert_route_amd.binding import Router
+
+    xs = [_case(M, 96, 1024, "bf16", "bf16")[0].cuda() for M in (9, 500)]
+    r = Router(_case(9, 96, 1024, "bf16", "bf16")[1].cuda())
+    want = [r.forward(x, torch.empty(x.shape[0], 96, device="cuda")).clone() for x in xs]
+    outs = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for x, o, s in zip(xs, outs, streams):
+            r.forward(x, o, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
