@@ -135,7 +135,9 @@ constexpr int kHoldItems = 16;  // finished items a gate/up workgroup holds befo
 // weights stream through a ring of two items' registers (one where x takes
 // more), each slot requested again as soon as its products are issued.
 // Results wait in LDS and are stored 16 items at a time: the compiler drains
-// all loads before it lets a store's counter mix with them.
+// all loads before it lets a store's counter mix with them. H 6144, I 256, 8 of
+// 256 experts: 4 tokens 16 us, of which 4.6 pass before weights move (logits,
+// top-k, list), 16 tokens 31 us (6.7); then 5.5 to 6.1 TB/s of them.
 //
 // T tokens a wave are routed, x comes operand-shaped up to 4 tokens (few
 // lines a load), else in whole row pieces turned round in LDS.
@@ -395,7 +397,9 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
 // picked the expert, column c + 8 its remainder (one MFMA, not two). Where
 // both did, tokens 8.. take a second pass over the same weights. A column's
 // result goes to the sum of tokens 0-7 or of tokens 8-15, and the two columns
-// of a token are added at the end.
+// of a token are added at the end. Bound by the weights' bytes, 5.6 TB/s of
+// them, and the spread of the waves' ends (their experts are fixed, so that the
+// sums' order is): H 6144, I 256, 8 of 256: 4 tokens 10.4 us, 16 tokens 18.4.
 template <int NB>
 struct DownRows {  // a row's 4 NB chunks of 16 bytes in LDS, exchanged against bank conflicts
   static constexpr int kStride = NB == 3 ? 16 : 4 * NB;

@@ -172,7 +172,10 @@ __device__ __forceinline__ int x_slot(int block, int c, int m) {
 // of the workgroup. Its weights stream through a ring of D tiles' registers:
 // the piece of a tile D ahead is requested as soon as a slot's products are
 // issued, so a wave has about S D KB under way at any time. The W partial
-// sums of a tile are added in wave order through LDS.
+// sums of a tile are added in wave order through LDS. Bound by the weights'
+// bytes once there are many (4 x 131072 x 6144: 73 us, 5.9 TB/s), by the start
+// and x's way to every CU below (16 x 8192 x 6144: 8.7 us, 3.1 TB/s; 1 x 6144 x
+// 2048: 4.5 us).
 template <bool F16>
 struct WeightStep {  // one K-step of 16 weight rows: a lane's codes and scales
   uint4 q;
@@ -322,7 +325,8 @@ static hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t stream) 
 // 256-byte row pieces are read: operand-shaped loads, 64 bytes of 16 rows
 // each, took three times as long), both P of the wave's steps ahead. The
 // partial sums are joined through LDS at the end. x is read once per 16 R
-// columns (from the L2): R = 2 where there are tiles enough.
+// columns (from the L2): R = 2 where there are tiles enough. Bound by x's L2
+// reads and the loads' latency: 32 x 6144 x 6144 9.7 us, 64 rows 16.6 us.
 template <bool F16, int CT, int R>
 __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int tiles_n) {
   constexpr int W = 8, P = CT == 1 ? 4 : 2;
@@ -415,8 +419,10 @@ done:
 // in registers for two steps until their buffer is free); weights go straight
 // from their packed form to registers, PW steps ahead, and are widened there:
 // a wave's rows are read by WM waves only. fp16 x is split into two bf16 on its
-// way into LDS (exact; the same products, twice the MFMAs). With one step ahead a step took
-// 2.2 us, the weights' latency, where its products take 0.85.
+// way into LDS (exact; the same products, twice the MFMAs). With one step of
+// weights ahead a K-step took 2.2 us, their latency, where its products take
+// 0.85. 4096 x 6144 x 6144: 241 us, 1280 TFLOP/s (fp16: 464 us), bound by MFMAs
+// and the widening between them; 256 rows 33 us, 192 workgroups for 256 CUs.
 template <bool F16, int TN, int TM, int WN, int WM>
 __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearArgs a, int tiles_m, int tiles_n) {
   constexpr int W = WN * WM, BM = 16 * TM * WM, BN = 16 * TN * WN;
@@ -610,9 +616,11 @@ template <bool F16>
 static hipError_t launch_type(const LinearArgs& a, int cus, hipStream_t stream) {
   if (a.M <= 16) return launch_16_rows<F16>(a, cus, stream);
   // Rounds of workgroups over the CUs times a round's time per K-step, in
-  // units of 10 ns (one workgroup a CU, K 6144; e.g. M 64, N 6144: 17.9 us by
-  // the second against 28.1 by the third; M 256: 50.5, 31.1 and 45.1 by the
-  // second to fourth; M 4096: 304, 298 and 248 by the last three).
+  // units of 10 ns (one workgroup a CU, N and K 6144, bf16 x; M 64: 16.6 us by
+  // the second against 32.6 by the third; M 256: 46.6, 33.2 and 46.2 by the
+  // second to fourth; M 1024: 83, 93 and 74, M 4096: 320, 296 and 241 by the
+  // last three. fp16 x: M 64 21 and 60, M 256 61, 61 and 105, M 4096 596, 623
+  // and 464).
   auto cost = [&](int64_t bm, int64_t bn, int per) {
     const int64_t groups = ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);
     return ((groups + cus - 1) / cus) * per;
