@@ -418,16 +418,20 @@ done:
 // buffers of one K-step of 128; whole 256-byte row pieces are read, and kept
 // in registers for two steps until their buffer is free); weights go straight
 // from their packed form to registers, PW steps ahead, and are widened there:
-// a wave's rows are read by WM waves only. fp16 x is split into two bf16 on its
+// a wave's rows are read by WM waves only. x's operands are read from LDS RD - 1
+// ahead of their MFMAs, in a fixed order: read where they are needed, two waves
+// a SIMD did not hide the LDS (with the rows of a tile in one wave 241 -> 235
+// us at 4096 x 6144 x 6144, fp16 464 -> 447). fp16 x is split into two bf16 on its
 // way into LDS (exact; the same products, twice the MFMAs). With one step of
 // weights ahead a K-step took 2.2 us, their latency, where its products take
-// 0.85. 4096 x 6144 x 6144: 241 us, 1280 TFLOP/s (fp16: 464 us), bound by MFMAs
-// and the widening between them; 256 rows 33 us, 192 workgroups for 256 CUs.
+// 0.85. 4096 x 6144 x 6144: 235 us, 1310 TFLOP/s (fp16: 447 us), bound by MFMAs
+// and the widening between them (the two overlap by a quarter only); 256 rows 31 us, 192 workgroups for 256 CUs.
 template <bool F16, int TN, int TM, int WN, int WM>
 __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearArgs a, int tiles_m, int tiles_n) {
   constexpr int W = WN * WM, BM = 16 * TM * WM, BN = 16 * TN * WN;
   constexpr int NX = BM / 4 / W;  // pieces of 4 rows x 128 K staged by a wave
   constexpr int PW = 4;           // weight steps in registers
+  constexpr int RD = 4;           // operands of x in registers
   static_assert(BM % (4 * W) == 0, "whole pieces");
   constexpr int P = F16 ? 2 : 1;  // bf16 planes of x
   __shared__ uint4 xs[2][P][BM * 16];
@@ -514,26 +518,33 @@ __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearA
   load_x(xv[0], 2);
   barrier_lds();
   auto step = [&](int p, int ks) __attribute__((always_inline)) {
-    // step ks + 1's x into the buffer that step ks - 1 was read from
-    put_x(xv[(p + 1) & 1], (p + 1) & 1, ks + 1);
-    load_x(xv[(p + 1) & 1], ks + 3);
+    constexpr int NF = 4 * TM * P;
+    v8s f[RD], wf[TN];
+    // operand i: MFMA j's of row tile u, the lower plane first
+    auto operand = [&](int i) __attribute__((always_inline)) {
+      const int j = i / (TM * P), u = i / P % TM, pl = P - 1 - i % P;
+      f[i % RD] = __builtin_bit_cast(v8s, xs[p & 1][pl][x_slot(wm * TM + u, 4 * j + g, r)]);
+    };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v8s wf[TN];
+    for (int i = 0; i < RD - 1; ++i) operand(i);
 #pragma unroll
-      for (int t = 0; t < TN; ++t) {
-        const uint32_t d = j == 0 ? q[p][t].x : j == 1 ? q[p][t].y : j == 2 ? q[p][t].z : q[p][t].w;
-        wf[t] = fp4x8_bf16(d, scale_of(sc[p][t], j));
+    for (int i = 0; i < NF; ++i) {
+      const int j = i / (TM * P), u = i / P % TM;
+      if (i + RD - 1 < NF) operand(i + RD - 1);
+      if (i % (TM * P) == 0) {
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+          const uint32_t d = j == 0 ? q[p][t].x : j == 1 ? q[p][t].y : j == 2 ? q[p][t].z : q[p][t].w;
+          wf[t] = fp4x8_bf16(d, scale_of(sc[p][t], j));
+        }
       }
 #pragma unroll
-      for (int u = 0; u < TM; ++u) {
-        const int at = x_slot(wm * TM + u, 4 * j + g, r);
-#pragma unroll
-        for (int pl = P - 1; pl >= 0; --pl) {
-          const v8s f = __builtin_bit_cast(v8s, xs[p & 1][pl][at]);
-#pragma unroll
-          for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], f, acc[t][u]);
-        }
+      for (int t = 0; t < TN; ++t) acc[t][u] = mfma_bf16(wf[t], f[i % RD], acc[t][u]);
+      __builtin_amdgcn_sched_barrier(0x16);  // ALU work and memory loads may move across, LDS and MFMAs not
+      if (i == TM * P - 1) {
+        // step ks + 1's x into the buffer that step ks - 1 was read from
+        put_x(xv[(p + 1) & 1], (p + 1) & 1, ks + 1);
+        load_x(xv[(p + 1) & 1], ks + 3);
       }
     }
     load_w(p, ks + PW);
@@ -617,10 +628,10 @@ static hipError_t launch_type(const LinearArgs& a, int cus, hipStream_t stream) 
   if (a.M <= 16) return launch_16_rows<F16>(a, cus, stream);
   // Rounds of workgroups over the CUs times a round's time per K-step, in
   // units of 10 ns (one workgroup a CU, N and K 6144, bf16 x; M 64: 16.6 us by
-  // the second against 32.6 by the third; M 256: 46.6, 33.2 and 46.2 by the
-  // second to fourth; M 1024: 83, 93 and 74, M 4096: 320, 296 and 241 by the
-  // last three. fp16 x: M 64 21 and 60, M 256 61, 61 and 105, M 4096 596, 623
-  // and 464).
+  // the second against 30.6 by the third; M 256: 46.6, 31.4 and 49 by the
+  // second to fourth; M 1024: 83, 98 and 72, M 4096: 312, 304 and 235 by the
+  // last three. fp16 x: M 64 21 and 58, M 256 61, 59 and 97, M 4096 604, 593
+  // and 447).
   auto cost = [&](int64_t bm, int64_t bn, int per) {
     const int64_t groups = ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);
     return ((groups + cus - 1) / cus) * per;
@@ -630,9 +641,14 @@ static hipError_t launch_type(const LinearArgs& a, int cus, hipStream_t stream) 
   switch (std::min_element(c, c + 5) - c) {
     case 0: return launch_mid<F16, 2, 1>(a, stream);
     case 1: return launch_mid<F16, 2, 2>(a, stream);
-    case 2: return launch_tile<F16, 2, 2, 4, 2>(a, stream);
+    // all rows of a tile by every wave (weights widened once a workgroup, not
+    // twice) where that measured faster: bf16 M 256 by the third 30.9 against
+    // 32.5 us, M 4096 by the fifth 235 against 246; by the fourth 310 against 304
+    case 2: return launch_tile<F16, 1, 4, 8, 1>(a, stream);
     case 3: return launch_tile<F16, 2, 4, 4, 2>(a, stream);
-    default: return launch_tile<F16, 4, 4, 4, 2>(a, stream);
+    default:
+      if constexpr (F16) return launch_tile<F16, 4, 4, 4, 2>(a, stream);
+      else return launch_tile<F16, 2, 8, 8, 1>(a, stream);
   }
 }
 
