@@ -627,17 +627,18 @@ template <bool F16>
 static hipError_t launch_type(const LinearArgs& a, int cus, hipStream_t stream) {
   if (a.M <= 16) return launch_16_rows<F16>(a, cus, stream);
   // Rounds of workgroups over the CUs times a round's time per K-step, in
-  // units of 10 ns (one workgroup a CU, N and K 6144, bf16 x; M 64: 16.6 us by
-  // the second against 30.6 by the third; M 256: 46.6, 31.4 and 49 by the
-  // second to fourth; M 1024: 83, 98 and 72, M 4096: 312, 304 and 235 by the
-  // last three. fp16 x: M 64 21 and 58, M 256 61, 59 and 97, M 4096 604, 593
-  // and 447).
+  // units of 10 ns (N and K 6144, bf16 x; M 32: 14.4 us by the first against 9.6
+  // by the second; M 64: 20.8, 16.9 and 30.7 by the first three; M 128: 26 and 31
+  // by the second and third, M 256: 46.6, 31.4 and 49 by the second to fourth;
+  // M 1024: 83, 98 and 71, M 4096: 312, 304 and 235 by the last three. fp16 x: M
+  // 64 25, 21 and 59 by the first three, M 256 61, 59 and 97 by the second to
+  // fourth, M 4096 604, 593 and 452 by the last three).
   auto cost = [&](int64_t bm, int64_t bn, int per) {
     const int64_t groups = ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);
     return ((groups + cus - 1) / cus) * per;
   };
-  const int64_t c[5] = {cost(32, 16, F16 ? 15 : 11), cost(32, 32, F16 ? 22 : 17), cost(64, 128, F16 ? 110 : 50),
-                        cost(128, 128, F16 ? 195 : 82), cost(128, 256, F16 ? 280 : 140)};
+  const int64_t c[5] = {cost(32, 16, F16 ? 16 : 14), cost(32, 32, F16 ? 22 : 16), cost(64, 128, F16 ? 105 : 60),
+                        cost(128, 128, F16 ? 195 : 97), cost(128, 256, F16 ? 280 : 150)};
   switch (std::min_element(c, c + 5) - c) {
     case 0: return launch_mid<F16, 2, 1>(a, stream);
     case 1: return launch_mid<F16, 2, 2>(a, stream);
