@@ -401,8 +401,8 @@ moe_status moe_linear_forward(const moe_linear* linear, int64_t M, const void* x
                               int64_t ldr, void* y, int64_t ldy, int y_type, void* stream);
 
 /* The whole MoE layer of up to 16 tokens from their hidden states, with the
- * activations kept in 16 bits (moe_forward takes logits and quantizes x and
- * mid). On the weights moe_forward reads (w13/s13 packed by moe_pack_w13,
+ * activations unquantized (moe_forward takes logits and quantizes x and mid):
+ * x as it is, h in binary32 with its routing weight, up to the down product. On the weights moe_forward reads (w13/s13 packed by moe_pack_w13,
  * w2/s2 row-major), so a decode step and a prefill share one copy:
  *   logits = fl32(x router^T), routed as in moe_forward (steps 1 of the call)
  *   h      = SiLU(x Wg^T) * (x Wu^T)  in fp32 per (token, slot)

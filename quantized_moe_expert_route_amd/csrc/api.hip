@@ -93,7 +93,7 @@ Layout make_layout(const moe_shape& s) {
   r.call_bytes = align256(off);
   const size_t Ml = std::min<size_t>(M, kSmallM);
   r.X.layer_logits = take(4 * Ml * E);
-  r.X.layer_g = take(4 * Ml * k * I);
+  r.X.layer_g = take(6 * Ml * k * I);
   r.X.layer_list = take(kLayerListBytes);
   r.L.total_bytes = align256(off);
   return r;

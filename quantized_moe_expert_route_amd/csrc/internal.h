@@ -32,8 +32,8 @@ struct Internal {
   size_t sync_begin, sync_bytes;  // region zeroed once when the workspace is bound
   // of moe_layer_forward, behind moe_forward's regions
   size_t layer_logits;  // fp32 [min(M, kSmallM), E]
-  size_t layer_g;       // bf16 [n, I/128, 256]: weighted h of its up to kSmallM tokens, values and remainders (h_at of layer.hip)
-  size_t layer_list;    // the picked experts and the tokens' slots (layer.hip)
+  size_t layer_g;       // bf16 [n, I/128, 3 * 128]: weighted h of its up to kSmallM tokens, in three parts (h_at of layer.hip)
+  size_t layer_list;    // the picked experts and their tokens (layer.hip)
 };
 
 }  // namespace qmoe

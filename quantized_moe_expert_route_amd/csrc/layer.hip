@@ -1,17 +1,16 @@
 // The whole MoE layer of up to 16 tokens from their hidden states, activations
-// kept in 16 bits:
+// unquantized:
 //   logits = x router^T (router.hip); top-k, weights as in route_common.h;
 //   h = SiLU(x Wg^T) (x Wu^T) per (token, slot), binary32;
 //   out[t] = sum_j w[t][j] h[t][j] W2[e_j]^T, one rounding to bf16.
-// h enters the down product scaled by its routing weight and split into two
-// bf16 (the value and the remainder, 16 significant bits: its rounding error
-// of 2^-17 stays far below the output's 2^-9).
+// h enters the down product scaled by its routing weight, in binary32, as the
+// three bf16 whose sum it is (8 significant bits each).
 //
 // With at most 16 tokens the MFMA's 16 columns hold the whole batch, so
 // nothing is sorted or gathered: an active expert's gate/up rows meet all
 // tokens' x, and the columns of tokens that did not pick it are dropped; the
-// down product of 16 output columns runs over every active expert, a token's
-// column being zero where it did not pick the expert, which also combines.
+// down product of some output columns runs over every active expert with the
+// tokens that picked it, which also combines.
 #include <stddef.h>
 
 #include <algorithm>
@@ -32,9 +31,18 @@ struct ActiveList {
   int pad[3];
   uint16_t expert[kLayerMaxEntries];        // active experts, ascending
   uint8_t slot[kLayerMaxEntries][kSmallM];  // [active][token]: the token's slot, 255: none
-  uint16_t zero[256];                       // h of a token that did not pick an expert
 };
-static_assert(sizeof(ActiveList) == kLayerListBytes && sizeof(ActiveList) % 16 == 0, "copied in 16-byte pieces");
+
+// The same for the down launch: which tokens picked an expert.
+struct PickList {
+  int n;
+  int pad[3];
+  uint16_t expert[kLayerMaxEntries];
+  uint8_t count[kLayerMaxEntries];          // tokens that picked it
+  uint8_t pick[kLayerMaxEntries][kSmallM];  // they, ascending: 16 token + slot
+};
+static_assert(sizeof(PickList) == kLayerListBytes && sizeof(PickList) % 16 == 0, "copied in 16-byte pieces");
+static_assert(offsetof(ActiveList, slot) == offsetof(PickList, count), "the same head");
 
 // Top-k of T tokens' keys by one wave (of two the second may be all zero:
 // unused), their rounds side by side so that one's lane exchanges hide the
@@ -119,10 +127,12 @@ __device__ __forceinline__ int x13_slot(int c, int m) { return (c & 3) * 64 + 16
 
 // Weighted h of the batch, as the down launch's lanes read it: per entry
 // t * k + j and K-step of 128, operand j (K 32 g + 8 j .. + 7 of lane group g)
-// is one line: the four groups' values, then their remainders.
+// is 192 bytes: the four groups' first bf16, then their second and third.
+constexpr int kHParts = 3;
+constexpr int kHStep = 128 * kHParts;
 __device__ __forceinline__ size_t h_at(int entry, int nb, int col, int part) {
   const int e = col & 127;
-  return ((size_t)entry * nb + (col >> 7)) * 256 + (((e >> 3) & 3) * 8 + part * 4 + (e >> 5)) * 8 + (e & 7);
+  return ((size_t)entry * nb + (col >> 7)) * kHStep + (((e >> 3) & 3) * (4 * kHParts) + part * 4 + (e >> 5)) * 8 + (e & 7);
 }
 
 constexpr int kHoldItems = 16;  // finished items a gate/up workgroup holds before it stores them
@@ -145,14 +155,14 @@ template <int S, int EC, int T>
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
     const uint16_t* __restrict__ x, const float* __restrict__ logits, const uint8_t* __restrict__ w13p,
     const uint8_t* __restrict__ s13p, int* __restrict__ topk_ids, float* __restrict__ topk_w,
-    uint16_t* __restrict__ gp, ActiveList* __restrict__ batch, int M, int H, int E, int I, int k, float scaling) {
+    uint16_t* __restrict__ gp, PickList* __restrict__ batch, int M, int H, int E, int I, int k, float scaling) {
   __shared__ __align__(16) ActiveList list;
   __shared__ __align__(16) uint32_t mask[kRouteMaxE / 32];  // picked experts
   __shared__ uint16_t ids[kLayerMaxEntries];
   __shared__ float wts[kLayerMaxEntries];
   __shared__ float red[2][kLayerWaves][4 * 80];
   __shared__ uint4 xs[kLayerWaves][256];
-  __shared__ uint32_t hold[kHoldItems * 128];
+  __shared__ float hold[kHoldItems * 128];
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int nks = H / 128, nkq = H / 512, nit = I / 8;
@@ -190,11 +200,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
 #pragma unroll
       for (int i = 0; i < 4; ++i) xv[s][i] = make_uint4(0, 0, 0, 0);
   }
-  if (threadIdx.x < kRouteMaxE / 32) {
-    mask[threadIdx.x] = 0;
-    reinterpret_cast<uint4*>(list.zero)[threadIdx.x] = make_uint4(0, 0, 0, 0);
-  }
-  static_assert(kRouteMaxE / 32 == sizeof(list.zero) / 16, "cleared together");
+  if (threadIdx.x < kRouteMaxE / 32) mask[threadIdx.x] = 0;
   for (int i = threadIdx.x; i < kLayerMaxEntries; i += 64 * kLayerWaves)
     reinterpret_cast<uint4*>(list.slot)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
   barrier_lds();
@@ -215,20 +221,21 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
       }
   }
   barrier_lds();
+  // an expert's place in the list: the picked ones below it
+  auto place_in = [](const uint32_t(&words)[2 * EC], int e) {
+    int at = 0;
+#pragma unroll
+    for (int w = 0; w < 2 * EC; ++w) {
+      const uint32_t below = w < (e >> 5) ? ~0u : w == (e >> 5) ? (1u << (e & 31)) - 1 : 0u;
+      at += __popc(words[w] & below);
+    }
+    return at;
+  };
   {
-    // an expert's place in the list: the picked ones below it
     uint32_t words[2 * EC];
 #pragma unroll
     for (int w = 0; w < 2 * EC; ++w) words[w] = mask[w];
-    auto place = [&](int e) {
-      int at = 0;
-#pragma unroll
-      for (int w = 0; w < 2 * EC; ++w) {
-        const uint32_t below = w < (e >> 5) ? ~0u : w == (e >> 5) ? (1u << (e & 31)) - 1 : 0u;
-        at += __popc(words[w] & below);
-      }
-      return at;
-    };
+    auto place = [&](int e) { return place_in(words, e); };
     for (int e = threadIdx.x; e < E; e += 64 * kLayerWaves)
       if ((mask[e >> 5] >> (e & 31)) & 1) list.expert[place(e)] = (uint16_t)e;
     if ((int)threadIdx.x < M * k) list.slot[place(ids[threadIdx.x])][threadIdx.x / k] = (uint8_t)(threadIdx.x % k);
@@ -312,9 +319,15 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
       const int it = first + (i0 + (v >> 7)) * step, a = it / nit, c = it - a * nit;
       const int t = (v & 127) >> 3, n = v & 7, slot = list.slot[a][t];
       if (slot == 255) continue;
-      const uint32_t u = hold[v];
-      gp[h_at(t * k + slot, I / 128, 8 * c + n, 0)] = (uint16_t)u;
-      gp[h_at(t * k + slot, I / 128, 8 * c + n, 1)] = (uint16_t)(u >> 16);
+      // the upper 8 significant bits of what is left, three times: exact (down
+      // to bf16's smallest number); an infinity or NaN stays in the first
+      float rest = hold[v];
+#pragma unroll
+      for (int p = 0; p < kHParts; ++p) {
+        const uint32_t u = __float_as_uint(rest) & 0xFFFF0000u;
+        gp[h_at(t * k + slot, I / 128, 8 * c + n, p)] = (uint16_t)(u >> 16);
+        rest = (u & 0x7F800000u) == 0x7F800000u ? 0.f : rest - __uint_as_float(u);
+      }
     }
   };
   auto compute = [&](int d, int i, auto reload) __attribute__((always_inline)) {
@@ -349,11 +362,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
           G += red[buf][w][at];
           U += red[buf][w][at + 160];
         }
-        const float v = G / (1.0f + expf(-G)) * U * wts[t * k + slot];
-        const uint16_t hi = bf16_bits(v);
-        const float rest = v - bf16_value(hi);
-        hold[(i % kHoldItems) * 128 + th] =
-            hi | ((uint32_t)(fabsf(rest) < INFINITY ? bf16_bits(rest) : (uint16_t)0) << 16);
+        hold[(i % kHoldItems) * 128 + th] = G / (1.0f + expf(-G)) * U * wts[t * k + slot];
       }
     }
     if ((i + 1) % kHoldItems == 0) {
@@ -377,8 +386,19 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
     if ((int)threadIdx.x < M * k) {
       topk_ids[threadIdx.x] = ids[threadIdx.x];
       topk_w[threadIdx.x] = wts[threadIdx.x];
+      // this token's rank among those that picked the expert
+      uint32_t words[2 * EC];
+#pragma unroll
+      for (int w = 0; w < 2 * EC; ++w) words[w] = mask[w];
+      const int at = place_in(words, ids[threadIdx.x]), t = threadIdx.x / k;
+      uint32_t tokens = 0;
+#pragma unroll
+      for (int m = 0; m < kSmallM; ++m) tokens |= (uint32_t)(list.slot[at][m] != 255) << m;
+      const int rank = __popc(tokens & ((1u << t) - 1));
+      batch->pick[at][rank] = (uint8_t)(16 * t + list.slot[at][t]);
+      if ((tokens >> t) == 1) batch->count[at] = (uint8_t)(rank + 1);
     }
-    for (int i = threadIdx.x; i < (int)sizeof(ActiveList) / 16; i += 64 * kLayerWaves)
+    for (int i = threadIdx.x; i < (int)offsetof(PickList, count) / 16; i += 64 * kLayerWaves)
       reinterpret_cast<uint4*>(batch)[i] = reinterpret_cast<const uint4*>(&list)[i];
   }
 }
@@ -392,14 +412,15 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
 // expert: loads return in order, so h asked for when it is needed would wait
 // for all weights under way (and copied to LDS beforehand, it cost 3 to 6 us
 // with nothing else moving).
-// An expert is picked by few of the tokens, so the 16 MFMA columns hold both
-// parts of h at once: column c < 8 the value of token c or c + 8, whichever
-// picked the expert, column c + 8 its remainder (one MFMA, not two). Where
-// both did, tokens 8.. take a second pass over the same weights. A column's
-// result goes to the sum of tokens 0-7 or of tokens 8-15, and the two columns
-// of a token are added at the end. Bound by the weights' bytes, 5.6 TB/s of
-// them, and the spread of the waves' ends (their experts are fixed, so that the
-// sums' order is): H 6144, I 256, 8 of 256: 4 tokens 10.4 us, 16 tokens 18.4.
+// An expert is picked by few of the tokens, so the 16 MFMA columns hold all three
+// parts of h at once: column c < 15 is part c / 5 of the (c % 5)th token that
+// picked the expert; more than five take further passes over the same weights.
+// Which tokens a column holds changes from expert to expert, so the sums stay in
+// LDS of the wave's own, per part and token, and the parts are added at the end.
+// Bound by the spread of the waves' ends (their experts are fixed, so that the
+// sums' order is) and the weights' way: H 6144, I 256, 8 of 256: 4 tokens 10.4
+// us, 16 tokens 18.4 where h was cut to two bf16 (half again the bytes of h and
+// the sums in LDS cost the whole layer 1 to 4 %).
 template <int NB>
 struct DownRows {  // a row's 4 NB chunks of 16 bytes in LDS, exchanged against bank conflicts
   static constexpr int kStride = NB == 3 ? 16 : 4 * NB;
@@ -411,21 +432,21 @@ struct DownRows {  // a row's 4 NB chunks of 16 bytes in LDS, exchanged against 
 
 template <int NB, int C8>
 __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
-    const uint16_t* __restrict__ gp, const ActiveList* __restrict__ batch, const uint8_t* __restrict__ w2,
+    const uint16_t* __restrict__ gp, const PickList* __restrict__ batch, const uint8_t* __restrict__ w2,
     const uint8_t* __restrict__ s2, uint16_t* __restrict__ out, int M, int H, int k) {
   typedef DownRows<NB> Rows;
   constexpr int I = 128 * NB, R = (C8 + 1) / 2;      // R MFMA row tiles
   constexpr int kRows = 8 * C8 * Rows::kStride;      // chunks of a wave's rows in LDS
-  constexpr int kWave = kRows > 64 * R ? kRows : 64 * R;  // (or its partial sums)
   constexpr int NL = (8 * C8 * 4 * NB + 63) / 64;    // loads of an expert's rows
   constexpr int PE = NL >= 5 ? 2 : NL >= 3 ? 4 : NB == 4 ? 4 : 8;
   constexpr int UH = NB == 3 ? 3 : 4;
   static_assert(PE * NB % UH == 0, "whole rounds of h");
-  __shared__ __align__(16) ActiveList list;
-  __shared__ uint4 area[kLayerWaves * kWave];
+  __shared__ __align__(16) PickList list;
+  __shared__ uint4 area[kLayerWaves * kRows];
+  __shared__ v4f sums[kLayerWaves][kHParts][kSmallM][4 * R];  // [.][.][token][4 t + g]: columns 16 t + 4 g .. + 3
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
-  for (int i = threadIdx.x; i < (int)offsetof(ActiveList, zero) / 16; i += 64 * kLayerWaves)
+  for (int i = threadIdx.x; i < (int)sizeof(PickList) / 16; i += 64 * kLayerWaves)
     reinterpret_cast<uint4*>(&list)[i] = reinterpret_cast<const uint4*>(batch)[i];
   __syncthreads();
   const int c0 = blockIdx.x * 8 * C8, cols = min(8 * C8, H - c0);
@@ -459,36 +480,35 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
       }
     }
   };
-  // token and slot of this lane's column for the wave's expert i; `both`: some
-  // column's two tokens picked it (uniform), the upper ones then left for later
-  struct Column {
-    int token, slot;
-    bool both;
+  // the tokens that picked the wave's expert i (uniform), none past its last
+  auto picked = [&](int i) __attribute__((always_inline)) -> int {
+    return i < experts ? __builtin_amdgcn_readfirstlane(list.count[at(i)]) : 0;
   };
-  const int c8 = r & 7, part = r >> 3;
-  auto column = [&](int i) __attribute__((always_inline)) -> Column {
-    const uint8_t* slots = list.slot[at(i)];
-    const int none = i < experts ? 0 : 255, s0 = slots[c8] | none, s1 = slots[c8 + 8] | none;
-    const bool both = __ballot(s0 != 255 && s1 != 255) != 0;
-    const bool lower = s0 != 255 || both;
-    return Column{lower ? c8 : c8 + 8, lower ? s0 : s1, both};
+  // Token and slot (16 token + slot) of this lane's column in a pass over the
+  // expert, -1: none. (Column 15 is nobody's and reads what column 10 does.)
+  const int c5 = r % 5, part = min(r / 5, kHParts - 1);
+  auto column = [&](int i, int pass) __attribute__((always_inline)) -> int {
+    const int q = 5 * pass + c5, who = list.pick[at(i)][min(q, kSmallM - 1)];
+    return q < picked(i) ? who : -1;
   };
-  auto load_h = [&](uint4(&hv)[4], const Column& c, int b) __attribute__((always_inline)) {
-    // (no branch round the loads: the compiler counts those under way)
-    const uint16_t* src = (c.slot != 255 ? gp + (size_t)((c.token * k + c.slot) * NB + b) * 256 : batch->zero) +
-                          (part * 4 + g) * 8;
+  auto load_h = [&](uint4(&hv)[4], int who, int b) __attribute__((always_inline)) {
+    // (no branch round the loads: the compiler counts those under way. Without a
+    // token the first entry's, for a column that is not used)
+    const int entry = who >= 0 ? (who >> 4) * k + (who & 15) : 0;
+    const uint16_t* src = gp + (size_t)(entry * NB + b) * kHStep + (part * 4 + g) * 8;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) hv[j] = ld16(src + 64 * j);
+    for (int j = 0; j < 4; ++j) hv[j] = ld16(src + 32 * kHParts * j);
   };
   uint4 hv[UH][4];
   load(0, 0);
 #pragma unroll
-  for (int u = 0; u < UH; ++u) load_h(hv[u], column(u / NB), u % NB);
+  for (int u = 0; u < UH; ++u) load_h(hv[u], column(u / NB, 0), u % NB);
 #pragma unroll
   for (int p = 1; p < PE; ++p) load(p, p);
-  v4f acc[2][R];  // tokens 0-7, tokens 8-15
+  constexpr int kSums = kHParts * kSmallM * 4 * R;  // of a wave
 #pragma unroll
-  for (int t = 0; t < R; ++t) acc[0][t] = acc[1][t] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < kSums / 64; ++i) (&sums[wave][0][0][0])[64 * i + lane] = v4f{0.f, 0.f, 0.f, 0.f};
+  static_assert(kSums % 64 == 0, "whole rounds");
   auto multiply = [&](int p, int b, const uint4(&x)[4], v4f(&d)[R]) __attribute__((always_inline)) {
     uint4 w[R];
 #pragma unroll
@@ -508,38 +528,42 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
       mine[Rows::at(n / (4 * NB), n % (4 * NB))] = q[p][l];
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
-    const Column col = column(i);
     v4f d[R];
+    // a token that did not pick the expert takes nothing from it, also where
+    // its weights are not finite
+    auto begin = [&](int who) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < R; ++t) d[t] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < R; ++t) d[t] = sums[wave][part][who >= 0 ? who >> 4 : 0][4 * t + g];
+    };
+    auto end = [&](int who) __attribute__((always_inline)) {
+      if (who >= 0 && r < 5 * kHParts) {
+#pragma unroll
+        for (int t = 0; t < R; ++t) sums[wave][part][who >> 4][4 * t + g] = d[t];
+      }
+    };
+    const int who = column(i, 0);
+    begin(who);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int u = p * NB + b;
       multiply(p, b, hv[u % UH], d);
-      load_h(hv[u % UH], column(i + (b + UH) / NB), (b + UH) % NB);
+      load_h(hv[u % UH], column(i + (b + UH) / NB, 0), (b + UH) % NB);
       if constexpr (NB * R > 4) __builtin_amdgcn_sched_barrier(0);  // one K-step's operands at a time in registers
     }
-    // a token that did not pick the expert takes nothing from it, also where
-    // its weights are not finite
-    const bool low = col.slot != 255 && col.token < 8, high = col.slot != 255 && col.token >= 8;
-#pragma unroll
-    for (int t = 0; t < R; ++t) {
-      if (low) acc[0][t] += d[t];
-      if (high) acc[1][t] += d[t];
-    }
-    if (col.both) {
-      const Column up{c8 + 8, list.slot[wave + kLayerWaves * i][c8 + 8], true};
-#pragma unroll
-      for (int t = 0; t < R; ++t) d[t] = v4f{0.f, 0.f, 0.f, 0.f};
+    end(who);
+    // (further passes ask for h when they need it, and so wait for the weights
+    // under way too: 16 tokens seldom pick one of many experts more than five times)
+    for (int pass = 1; 5 * pass < picked(i); ++pass) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // other lanes' sums than before
+      const int more = column(i, pass);
+      begin(more);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         uint4 x[4];
-        load_h(x, up, b);
+        load_h(x, more, b);
         multiply(p, b, x, d);
       }
-#pragma unroll
-      for (int t = 0; t < R; ++t)
-        if (up.slot != 255) acc[1][t] += d[t];
+      end(more);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     load(p, i + PE);
@@ -554,25 +578,17 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
     }
   }
 done:
-  // value and remainder columns of a token, each in its own lane's column
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  // a token's three parts, the smallest first, then the waves in order
 #pragma unroll
   for (int t = 0; t < R; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = acc[0][t][e] + __shfl_xor(acc[0][t][e], 8, 64);
-      const float hi = acc[1][t][e] + __shfl_xor(acc[1][t][e], 8, 64);
-      acc[0][t][e] = part ? hi : lo;
-    }
-  v4f(*const red)[R][64] = reinterpret_cast<v4f(*)[R][64]>(area);
-  __syncthreads();
-#pragma unroll
-  for (int t = 0; t < R; ++t) red[wave][t][lane] = acc[0][t];
+    sums[wave][0][r][4 * t + g] += sums[wave][1][r][4 * t + g] + sums[wave][2][r][4 * t + g];
   __syncthreads();
   if (wave < R && r < M) {
     const int n = 16 * wave + 4 * g;
-    v4f v = red[0][wave][lane];
+    v4f v = sums[0][0][r][4 * wave + g];
 #pragma unroll
-    for (int w = 1; w < kLayerWaves; ++w) v += red[w][wave][lane];
+    for (int w = 1; w < kLayerWaves; ++w) v += sums[w][0][r][4 * wave + g];
     if (n < cols) {
       uint2 o;
       o.x = (uint32_t)bf16_bits(v[0]) | ((uint32_t)bf16_bits(v[1]) << 16);
@@ -590,7 +606,7 @@ static hipError_t launch_gate_up_s(const moe_plan* p, const LayerArgs& a, const 
   auto go = [&](auto kern) {
     return launch_k(kern, grid, dim3(64 * kLayerWaves), 0, a.stream, Ev{}, (const uint16_t*)a.x, logits,
                     (const uint8_t*)a.w13, (const uint8_t*)a.s13, wsp<int>(p, p->L.topk_ids),
-                    wsp<float>(p, p->L.topk_w), gp, wsp<ActiveList>(p, p->X.layer_list), (int)a.M, (int)p->s.H, E, I, k, p->s.routed_scaling);
+                    wsp<float>(p, p->L.topk_w), gp, wsp<PickList>(p, p->X.layer_list), (int)a.M, (int)p->s.H, E, I, k, p->s.routed_scaling);
   };
   if (E <= 256) return a.M <= kLayerWaves ? go(layer_gate_up_kernel<S, 4, 1>) : go(layer_gate_up_kernel<S, 4, 2>);
   return a.M <= kLayerWaves ? go(layer_gate_up_kernel<S, 16, 1>) : go(layer_gate_up_kernel<S, 16, 2>);
@@ -601,7 +617,7 @@ static hipError_t launch_down_c8(const moe_plan* p, const LayerArgs& a, const ui
   const int H = (int)p->s.H;
   const dim3 grid((unsigned)((H + 8 * C8 - 1) / (8 * C8)));
   return launch_k(layer_down_kernel<NB, C8>, grid, dim3(64 * kLayerWaves), 0, a.stream, Ev{}, gp,
-                  wsp<ActiveList>(p, p->X.layer_list), (const uint8_t*)a.w2, (const uint8_t*)a.s2, (uint16_t*)a.out,
+                  wsp<PickList>(p, p->X.layer_list), (const uint8_t*)a.w2, (const uint8_t*)a.s2, (uint16_t*)a.out,
                   (int)a.M, H, (int)p->s.top_k);
 }
 

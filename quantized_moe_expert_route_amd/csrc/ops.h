@@ -53,7 +53,7 @@ hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream);
 // (8 waves hold at most 8 K-steps of 128 each as register operands).
 constexpr int kLayerMaxEntries = 256;
 constexpr int kLayerMaxH = 8192;
-constexpr int kLayerListBytes = 16 + 2 * kLayerMaxEntries + 16 * kLayerMaxEntries + 512;  // ActiveList of layer.hip
+constexpr int kLayerListBytes = 16 + (2 + 1 + 16) * kLayerMaxEntries;  // PickList of layer.hip
 
 struct LayerArgs {
   int64_t M;

@@ -342,3 +342,48 @@ def test_every_logit_nan():
             assert int(ids.min()) >= 0 and int(ids.max()) < E
         d.router = keep
         assert torch.equal(d.call(), want)
+
+
+@pytest.mark.parametrize("M,E,H,I", [(1, 1, 512, 128), (4, 1, 512, 256), (6, 2, 1024, 384), (16, 1, 512, 512),
+                                     (13, 3, 4608, 256)])
+def test_h_keeps_32_bits(M, E, H, I):
+    """Sums that cancel: every product and sum is a multiple of 1/4 below 2^22
+    (exact in binary32), and a row of W2 takes one h from another near to it, so
+    that an h held in fewer bits shows in the output's 8. Also more tokens on one
+    expert than one pass of the down product takes."""
+    import torch
+    from quantized_moe_expert_route_amd import binding as B
+
+    rng = np.random.default_rng([M, E, H, I, 29])
+    mags = np.array([0, .5, 1, 1.5, 2, 3, 4, 6])
+    x = rng.integers(1, 5, (M, H)).astype(np.float64)
+    keep = 512  # the other columns of W13 are zero
+    gate, up = rng.choice([2, 4, 5, 6], (E, I, H)), rng.choice([2, 4, 5, 6, 10, 12, 13, 14], (E, I, H))
+    w13 = np.concatenate([gate, up], 1)
+    w13[:, :, keep:] = 0
+    value = lambda c: np.where(c >= 8, -mags[c & 7], mags[c & 7])
+    rw = np.zeros((E, H))
+    rw[:, :8] = rng.integers(0, 5, (E, 8))  # scores above 1/2: the one slot's weight is exactly 1
+    picks = np.argmax(x @ rw.T, 1)  # ties go to the lower expert
+    h = np.stack([value(w13[picks[t]]) @ x[t] for t in range(M)])
+    h = h[:, :I] * h[:, I:]  # SiLU is its argument where that is above 104
+    assert (value(w13[:, :I]) @ x.T).min() > 104 and np.abs(h).max() < 2 ** 22
+    w2 = np.zeros((E, H, I), dtype=np.int64)
+    for e in range(E):
+        t = np.flatnonzero(picks == e)
+        order = np.argsort(h[t[0]] if len(t) else rng.random(I))
+        for n in range(H):  # n: neighbours of the expert's tokens in turn
+            if len(t):
+                order = np.argsort(h[t[n % len(t)]])
+            i = int(rng.integers(0, I - 1))
+            w2[e, n, order[i]], w2[e, n, order[i + 1]] = 2, 10  # 1 and -1
+    pack = lambda c: (c[..., ::2] | (c[..., 1::2] << 4)).astype(np.uint8)
+    cu = lambda a: torch.from_numpy(a).cuda()
+    one = lambda *s: torch.full(s, 127, dtype=torch.uint8, device="cuda")
+    plan = B.Plan(M, H, E, I, 1, routed_scaling=1.0)
+    out = torch.empty(M, H, dtype=torch.bfloat16, device="cuda")
+    plan.layer(torch.from_numpy(x).bfloat16().cuda(), B.Router(torch.from_numpy(rw).bfloat16().cuda()),
+               *B.pack_w13(cu(pack(w13)), one(E, 2 * I, H // 32)), cu(pack(w2)), one(E, H, I // 32), out)
+    want = np.stack([value(w2[picks[t]]) @ h[t] for t in range(M)])
+    assert np.abs(want).max() < 2 ** 22
+    assert torch.equal(out.cpu(), torch.from_numpy(want).float().bfloat16())
