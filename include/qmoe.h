@@ -376,8 +376,10 @@ moe_status moe_router_forward(const moe_router* router, int64_t M, const void* x
  *   w_packed [ceil(N/16)][ceil(K/128)][4 g][16 r][4 j] dwords: the 8 codes of
  *     K elements 128 ks + 32 j + 8 g .. + 7 of row 16 rb + r, zero past N or K
  *   s_packed [ceil(N/16)][ceil(K/128)][16 r][4 j]: the scale of MX block
- *     4 ks + j of row 16 rb + r, 127 past N or K
- * A scale byte of 255 (NaN) makes its row's results NaN.
+ *     4 ks + j of row 16 rb + r, 127 past N or K; bytes above 252 as 255
+ * A scale byte of 255 (NaN) makes its row's results NaN, and so do 253 and 254:
+ * bf16 does not hold all of their weights, and no binary32 weight has them by
+ * the MX rule (floor(log2 of a block's largest magnitude) - 2 + 127 <= 252).
  * Errors as moe_pack_w13; shapes: N 1 .. 2^24, K a multiple of 32 up to 65536,
  * else MOE_ERR_UNSUPPORTED.
  *

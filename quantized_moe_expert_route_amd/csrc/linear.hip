@@ -36,7 +36,11 @@ __global__ __launch_bounds__(256) void pack_linear_scale_kernel(const uint8_t* _
     const int j = (int)(o & 3), r = (int)((o >> 2) & 15);
     const int64_t rest = o >> 6;
     const int64_t n = rest / nks * 16 + r, b = rest % nks * 4 + j;
-    sp[o] = n < N && b < K / 32 ? s[n * (K / 32) + b] : (uint8_t)127;
+    // 253 and 254 become 255, NaN: 4 x 2^126 and 2 x 2^127 are above bf16's
+    // largest number, so the kernels that fold the scale into the weight would
+    // not agree with those that scale the sums
+    const uint8_t v = n < N && b < K / 32 ? s[n * (K / 32) + b] : (uint8_t)127;
+    sp[o] = v < 253 ? v : (uint8_t)255;
   }
 }
 

@@ -328,3 +328,27 @@ def test_most_rows_and_widest():
         lin.forward(x.cuda(), out)
         want = R.linear(_f64(x), codes[at].cpu().numpy(), scales[at].cpu().numpy())[0]
         assert np.array_equal(_f64(out[:, at].cpu()), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 48, 160), (16, 48, 8192), (20, 48, 160), (20, 5000, 160), (40, 16500, 160),
+                                   (129, 24600, 160), (65, 33000, 160)])
+@pytest.mark.parametrize("xt", ["bf16", "fp16"])
+def test_scales_above_bf16_make_their_row_nan(M, N, K, xt):
+    """Scale bytes 253 and 254 (no binary32 weight quantizes to them, and bf16
+    does not hold all of their weights) are NaN as 255 is, in every kernel:
+    their rows of w, and no other, have NaN results. 252 is a number."""
+    rng = np.random.default_rng([M, N, K, 31])
+    d = _case(rng, M, N, K, xt, "fp32")
+    base = _run(d)
+    rows = {5: 253, 17: 254, 30: 255, N - 1: 254}
+    d["scales"] = d["scales"].copy()
+    for n, v in rows.items():
+        d["scales"][n, int(rng.integers(0, K // 32))] = v
+    got = _run(d)
+    nan = np.zeros(N, dtype=bool)
+    nan[list(rows)] = True
+    assert bool(got[:, nan].isnan().all())
+    assert np.array_equal(got[:, ~nan].numpy(), base[:, ~nan].numpy())
+    d["scales"][list(rows)] = 252
+    d["x"] = (d["x"].float() * 2.0 ** -12).to(_dt(xt))
+    assert bool(_run(d).isfinite().all())
