@@ -344,8 +344,12 @@ moe_status moe_forward_noalloc(moe_plan* plan, int64_t M, const void* x, const f
 typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
 
 /* Router projection: the fp32 logits that moe_forward takes, from the hidden
- * states:  logits[m][e] = sum_h x[m][h] * w[e][h],  summed exactly enough
- * (float64 up to 16 tokens) and rounded to fp32.
+ * states:  logits[m][e] = sum_h x[m][h] * w[e][h],  rounded to fp32. Up to 16
+ * tokens the sums are float64; above, fp32 sums of exact products: logits
+ * nearer to each other than the fp32 sums' error (at most (48 + H/32) 2^-23 of
+ * the products' magnitudes) may then come in the other order, and the same token
+ * pick another of such two experts in a call of more tokens. Infinities and NaN
+ * come out as in float64 sums for any number of tokens.
  *   w  [E, H]  bf16 or fp32 (w_type), kept by the handle, not copied: it must
  *              stay valid while the handle is used
  *   x  [M, H]  bf16 or fp16 (x_type), rows ldx elements apart (ldx >= H, a

@@ -1,9 +1,11 @@
 // Router projection: logits[m][e] = sum_h x[m][h] w[e][h], one rounding to
 // binary32. x bf16 or fp16, w bf16 or fp32.
 //
-// The sums are float64: the routing compares logits, and with sums exact to
-// ~2^-50 two logits swap places only where their exact values round to the
-// same binary32 number, whatever order or split a kernel adds in.
+// Up to 16 tokens the sums are float64: the routing compares logits, and with
+// sums exact to ~2^-50 two logits swap places only where their exact values
+// round to the same binary32 number. Above, they are binary32 sums of exact
+// products, off by at most (48 + H / 32) 2^-23 of the products' magnitudes, so
+// that of two experts whose logits lie that near the other may be picked.
 #include <algorithm>
 
 #include "internal.h"
@@ -111,7 +113,9 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(const RouterA
 // 8 elements as P planes of bf16 whose sum they are: bf16 is one, fp16 two,
 // fp32 three (each plane keeps the upper 8 significant bits of what is left:
 // 24 = 3 x 8, exact down to bf16's smallest number). A value that is not
-// finite stays in the first.
+// finite is so in the first, the others zero: sums with it come out as an
+// infinity or a NaN, if not always the right one of the two (infinity times
+// another's zero plane), and are formed anew by redo_odd.
 template <int TYPE>
 constexpr int kPlanes = TYPE == MOE_BF16 ? 1 : TYPE == MOE_FP16 ? 2 : 3;
 
@@ -144,6 +148,36 @@ __device__ __forceinline__ void planes8(const Raw8<TYPE>& q, v8s (&out)[kPlanes<
     out[0] = as_v8s(h[0], h[1], h[2], h[3]);
     out[1] = as_v8s(m[0], m[1], m[2], m[3]);
     out[2] = as_v8s(l[0], l[1], l[2], l[3]);
+  }
+}
+
+__device__ __forceinline__ bool odd(float v) { return !(fabsf(v) < INFINITY); }
+
+// Logits e .. e + 3 of token m as the few-token kernel forms them, where what
+// this thread stored is not finite: planes of infinities, or a partial sum
+// above binary32's range. One logit a lane at a time: a call with an infinite
+// token takes some ms (4096 tokens, 256 experts, H 6144: 2.7, an infinity in
+// every token 6.3), with NaN, which end their sum, 10 to 20 us more.
+template <int XT, int WT>
+__device__ __forceinline__ void redo_odd(const RouterArgs& a, int64_t m, int e) {
+#pragma unroll 1
+  for (int i = e; i < min(e + 4, (int)a.E); ++i) {
+    float* const at = a.logits + m * a.E + i;
+    if (!odd(*at)) continue;
+    double sum = 0.0;
+#pragma unroll 1
+    for (int64_t c = 0; c < a.H && sum == sum; c += 8) {  // (a NaN stays one)
+      Raw8<WT> wr;
+      Raw8<XT> xr;
+      raw8<WT>(a.w, i * a.H + c, wr);
+      raw8<XT>(a.x, m * a.ldx + c, xr);
+      float w[8], x[8];
+      values8<WT>(wr, w);
+      values8<XT>(xr, x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum = fma((double)x[q], (double)w[q], sum);
+    }
+    *at = (float)sum;
   }
 }
 
@@ -236,9 +270,13 @@ __global__ __launch_bounds__(64 * W) void router_tile_kernel(const RouterArgs a,
       const int64_t m = m0 + 16 * ((s0 + s) % TM) + (l & 15);
       const int e = e0 + 16 * ((s0 + s) / TM) + 4 * (l >> 4);
       if (m < a.M) {
+        float odds = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 4; ++q) {
           if (e + q < a.E) a.logits[m * a.E + e + q] = v[q];
+          odds = fmaf(v[q], 0.f, odds);
+        }
+        if (odds != 0.f) redo_odd<XT, WT>(a, m, e);
       }
     }
   }
@@ -357,6 +395,7 @@ done:
   // the four quarters' sums in order, through LDS; lane (g, r): experts 4 g ..
   // + 3 of token r
   v4f(*const red)[8][64] = reinterpret_cast<v4f(*)[8][64]>(&sx[0][0]);  // [3][8][64]: 24 of sx's 32 KB
+  float odds = 0.f;  // NaN once a sum is not finite (columns past E repeat the last expert's)
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     __syncthreads();
@@ -375,6 +414,8 @@ done:
           v4f v = acc[t][u];
 #pragma unroll
           for (int i = 0; i < 3; ++i) v += red[i][2 * t + u][lane];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) odds = fmaf(v[q], 0.f, odds);
           const int64_t m = m0 + 16 * (2 * wm + u) + r;
           const int e = e0 + 16 * t + 4 * g;
           if (m < a.M) {
@@ -383,6 +424,13 @@ done:
               if (e + q < a.E) a.logits[m * a.E + e + q] = v[q];
           }
         }
+    }
+  }
+  if (odds != 0.f) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const int64_t m = m0 + 16 * (2 * wm + (i & 1)) + r;
+      if (m < a.M) redo_odd<XT, WT>(a, m, e0 + 16 * (i >> 1) + 4 * g);
     }
   }
 }

@@ -173,3 +173,62 @@ def test_one_handle_on_two_streams():
             r.forward(x, o, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def _row_checks(got, x, w, rows, cols):
+    """`got` of token rows and expert columns against 64-bit sums: the same
+    infinities and NaN (a sum at a time: no library's way through zeros)."""
+    xd, wd = x.double().numpy(), w.double().numpy()
+    with np.errstate(all="ignore"):
+        for m in rows:
+            for e in cols:
+                want = float(np.add.reduce(xd[m] * wd[e]))
+                assert np.isnan(got[m, e]) == np.isnan(want) and (np.isfinite(want) or np.isnan(want)
+                                                                  or got[m, e] == want), (m, e, got[m, e], want)
+                if np.isfinite(want):
+                    assert np.isfinite(got[m, e])
+
+
+@pytest.mark.parametrize("M,E,H", [(9, 40, 264), (40, 40, 264), (1024, 256, 328), (1100, 500, 328)])
+@pytest.mark.parametrize("xt,wt", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "bf16"), ("fp16", "fp32")])
+def test_infinities_and_nan_as_in_64_bits(M, E, H, xt, wt):
+    """Infinities in x and in w, met by weights and values that some of their
+    16-bit parts are zero of, and NaN of every payload, in each kernel."""
+    import torch
+
+    x, w = _case(M, E, H, xt, wt)
+    base = _run(x, w)
+    w[3] = torch.where(w[3] < 0, -0.5, 0.5).to(w.dtype)  # exact in 8 bits: the lower parts are zero
+    x[2], x[5] = 1.0, -2.0
+    clean = [m for m in range(M) if m not in (1, 2, 5, 6, M - 1)]
+    x[1, 17] = float("inf")
+    x[6, 100], x[6, 200] = float("inf"), float("-inf")
+    x[M - 1, H - 1] = float("-inf")
+    w[7, 30] = float("inf")
+    w[9, 31] = float("-inf")
+    w[11, 17] = 0.0  # meets x[1]'s infinity
+    if wt == "fp32":
+        w.view(torch.int32)[13, 5] = 0x7F800001  # a NaN by its low bits alone
+        w.view(torch.int32)[14, 6] = -1
+    else:
+        w[13, 5] = float("nan")
+    got = _run(x, w)
+    _row_checks(got, x, w, (0, 1, 2, 5, 6, M // 2, M - 1), range(min(E, 40)))
+    cols = [e for e in range(E) if e not in (3, 7, 9, 11, 13, 14)]
+    assert np.array_equal(got[np.ix_(clean, cols)], base[np.ix_(clean, cols)])
+
+
+@pytest.mark.parametrize("M,E", [(9, 40), (40, 40), (1024, 256), (1100, 500)])
+def test_partial_sums_above_binary32(M, E):
+    """Products of up to 2^126 whose partial sums pass binary32's range and
+    whose sum does not."""
+    import torch
+
+    x, w = _case(M, E, 264, "bf16", "bf16")
+    x[4] = 2.0 ** 126
+    w[6, :159], w[6, 159:263], w[6, 263] = 1.0, -1.0, -55.0
+    xd, wd = x.double().numpy(), w.double().numpy()
+    want = float(xd[4] @ wd[6])
+    assert want == 0.0
+    got = _run(x, w)
+    assert got[4, 6] == want
