@@ -423,7 +423,9 @@ moe_status moe_linear_forward(const moe_linear* linear, int64_t M, const void* x
 moe_status moe_layer_forward(moe_plan* plan, const moe_router* router, int64_t M, const void* x, const void* w13,
                              const void* s13, const void* w2, const void* s2, void* out, void* stream);
 
-/* Profiling aid: when `events` is non-NULL, moe_forward brackets stage i
+/* Profiling aid: when `events` is non-NULL, a call (moe_forward,
+ * moe_forward_noalloc or moe_layer_forward, whose stages are route: the router,
+ * gate_up: with the top-k, and down: with the combine) brackets stage i
  * with events[2i] (start of its first kernel) and events[2i+1] (end of its
  * last kernel), hipEvent_t handles, so hipEventElapsedTime(events[2i],
  * events[2i+1]) is the stage's execution time. A stage folded into another
@@ -431,8 +433,8 @@ moe_status moe_layer_forward(moe_plan* plan, const moe_router* router, int64_t M
  * 2 * moe_stage_count(). NULL disables. */
 moe_status moe_plan_set_stage_events(moe_plan* plan, void* const* events, int n);
 
-/* Profiling aid: when `start` and `stop` are non-NULL hipEvent_t handles,
- * moe_forward records `start` as its first kernel begins and `stop` as its
+/* Profiling aid: when `start` and `stop` are non-NULL hipEvent_t handles, a
+ * call (as above) records `start` as its first kernel begins and `stop` as its
  * last kernel ends, so hipEventElapsedTime(start, stop) is the call's device
  * time without the host's launch latency. Replaces the stage events above
  * (and they replace these); NULL, NULL disables. Both or neither must be
@@ -443,7 +445,7 @@ moe_status moe_plan_set_call_events(moe_plan* plan, void* start, void* stop);
 int moe_stage_count(void);
 const char* moe_stage_name(int i);
 
-/* Kernels that stage `stage` launches for a call of M tokens on this plan
+/* Kernels that stage `stage` of moe_forward launches for M tokens on this plan
  * with its current mid format (0 when the stage is folded into another
  * one), or -1 for bad arguments (M outside [0, the plan's M], an unknown
  * stage). */

@@ -17,7 +17,6 @@ using namespace qmoe;
 namespace {
 
 const char* kStageNames[] = {"route", "align", "gate_up", "act_quant", "shared", "down", "combine"};
-constexpr int kStages = 7;
 
 moe_status check_shape(const moe_shape* s) {
   if (!s) return MOE_ERR_INVALID_ARG;
@@ -140,12 +139,7 @@ hipError_t enqueue_call(const moe_plan* plan, const CallArgs& a) {
     // down (+ combine), the combine, or the exchange comes last
     ev[fused_combine && plan->tpx.tp == 0 ? 5 : 6].stop = plan->call_stop;
   }
-  // a stage with no launch of its own still records its (empty) interval
-  auto none = [&](int i) -> hipError_t {
-    if (!plan->n_events) return hipSuccess;
-    hipError_t e = hipEventRecord(ev[i].start, a.stream);
-    return e != hipSuccess ? e : hipEventRecord(ev[i].stop, a.stream);
-  };
+  auto none = [&](int i) { return record_empty(plan, ev[i], a.stream); };
   // Up to kSmallM tokens: routing + sort + x quantization in one launch
   // (workgroup 0 routes and sorts, the others quantize x); gate/up on 16-row
   // tiles; the mid quantization; down with the combine (a workgroup owns 16

@@ -70,6 +70,16 @@ struct Ev {
   hipEvent_t start = nullptr, stop = nullptr;
 };
 
+// Launch stages of a call (moe_stage_name), each with a pair of stage events.
+constexpr int kStages = 7;
+
+// A stage with no launch of its own still records its (empty) interval.
+inline hipError_t record_empty(const moe_plan* p, const Ev& ev, hipStream_t s) {
+  if (!p->n_events) return hipSuccess;
+  const hipError_t e = hipEventRecord(ev.start, s);
+  return e != hipSuccess ? e : hipEventRecord(ev.stop, s);
+}
+
 template <typename... KArgs, typename... Args>
 inline hipError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t lds, hipStream_t s, Ev ev,
                            Args... args) {

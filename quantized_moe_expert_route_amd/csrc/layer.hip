@@ -599,12 +599,12 @@ done:
 }
 
 template <int S>
-static hipError_t launch_gate_up_s(const moe_plan* p, const LayerArgs& a, const float* logits, uint16_t* gp) {
+static hipError_t launch_gate_up_s(const moe_plan* p, const LayerArgs& a, const float* logits, uint16_t* gp, Ev ev) {
   const int E = (int)p->s.E, I = (int)p->s.I, k = (int)p->s.top_k;
   const int64_t items = std::min<int64_t>(E, a.M * k) * (I / 8);
   const dim3 grid((unsigned)std::min<int64_t>(items, p->num_cus));
   auto go = [&](auto kern) {
-    return launch_k(kern, grid, dim3(64 * kLayerWaves), 0, a.stream, Ev{}, (const uint16_t*)a.x, logits,
+    return launch_k(kern, grid, dim3(64 * kLayerWaves), 0, a.stream, ev, (const uint16_t*)a.x, logits,
                     (const uint8_t*)a.w13, (const uint8_t*)a.s13, wsp<int>(p, p->L.topk_ids),
                     wsp<float>(p, p->L.topk_w), gp, wsp<PickList>(p, p->X.layer_list), (int)a.M, (int)p->s.H, E, I, k, p->s.routed_scaling);
   };
@@ -613,21 +613,21 @@ static hipError_t launch_gate_up_s(const moe_plan* p, const LayerArgs& a, const 
 }
 
 template <int NB, int C8>
-static hipError_t launch_down_c8(const moe_plan* p, const LayerArgs& a, const uint16_t* gp) {
+static hipError_t launch_down_c8(const moe_plan* p, const LayerArgs& a, const uint16_t* gp, Ev ev) {
   const int H = (int)p->s.H;
   const dim3 grid((unsigned)((H + 8 * C8 - 1) / (8 * C8)));
-  return launch_k(layer_down_kernel<NB, C8>, grid, dim3(64 * kLayerWaves), 0, a.stream, Ev{}, gp,
+  return launch_k(layer_down_kernel<NB, C8>, grid, dim3(64 * kLayerWaves), 0, a.stream, ev, gp,
                   wsp<PickList>(p, p->X.layer_list), (const uint8_t*)a.w2, (const uint8_t*)a.s2, (uint16_t*)a.out,
                   (int)a.M, H, (int)p->s.top_k);
 }
 
 template <int NB>
-static hipError_t launch_down_nb(const moe_plan* p, const LayerArgs& a, int c8, const uint16_t* gp) {
+static hipError_t launch_down_nb(const moe_plan* p, const LayerArgs& a, int c8, const uint16_t* gp, Ev ev) {
   switch (c8) {
-    case 1: return launch_down_c8<NB, 1>(p, a, gp);
-    case 2: return launch_down_c8<NB, 2>(p, a, gp);
-    case 3: return launch_down_c8<NB, 3>(p, a, gp);
-    default: return launch_down_c8<NB, 4>(p, a, gp);
+    case 1: return launch_down_c8<NB, 1>(p, a, gp, ev);
+    case 2: return launch_down_c8<NB, 2>(p, a, gp, ev);
+    case 3: return launch_down_c8<NB, 3>(p, a, gp, ev);
+    default: return launch_down_c8<NB, 4>(p, a, gp, ev);
   }
 }
 
@@ -635,29 +635,41 @@ hipError_t launch_layer(const moe_plan* p, const moe_router* router, const Layer
   float* logits = wsp<float>(p, p->X.layer_logits);
   uint16_t* gp = wsp<uint16_t>(p, p->X.layer_g);
   const RouterArgs ra{a.M, p->s.E, p->s.H, p->s.H, a.x, router->w, logits, router->x_type, router->w_type};
-  hipError_t e = launch_router(ra, p->num_cus, a.stream);
+  // stages: route (the router), gate_up (with the top-k), down (with the
+  // combine); the others record empty intervals
+  Ev ev[kStages];
+  if (p->n_events)
+    for (int i = 0; i < kStages; ++i) ev[i] = Ev{p->events[2 * i], p->events[2 * i + 1]};
+  if (p->call_start) {
+    ev[0].start = p->call_start;
+    ev[5].stop = p->call_stop;
+  }
+  hipError_t e = launch_router(ra, p->num_cus, a.stream, ev[0]);
+  if (e == hipSuccess) e = record_empty(p, ev[1], a.stream);
   if (e != hipSuccess) return e;
   const int H = (int)p->s.H, nks = H / 128;
   switch ((nks + kLayerWaves - 1) / kLayerWaves) {  // K-steps a wave
-    case 1: e = launch_gate_up_s<1>(p, a, logits, gp); break;
-    case 2: e = launch_gate_up_s<2>(p, a, logits, gp); break;
-    case 3: e = launch_gate_up_s<3>(p, a, logits, gp); break;
-    case 4: e = launch_gate_up_s<4>(p, a, logits, gp); break;
-    case 5: e = launch_gate_up_s<5>(p, a, logits, gp); break;
-    case 6: e = launch_gate_up_s<6>(p, a, logits, gp); break;
-    case 7: e = launch_gate_up_s<7>(p, a, logits, gp); break;
-    default: e = launch_gate_up_s<8>(p, a, logits, gp); break;
+    case 1: e = launch_gate_up_s<1>(p, a, logits, gp, ev[2]); break;
+    case 2: e = launch_gate_up_s<2>(p, a, logits, gp, ev[2]); break;
+    case 3: e = launch_gate_up_s<3>(p, a, logits, gp, ev[2]); break;
+    case 4: e = launch_gate_up_s<4>(p, a, logits, gp, ev[2]); break;
+    case 5: e = launch_gate_up_s<5>(p, a, logits, gp, ev[2]); break;
+    case 6: e = launch_gate_up_s<6>(p, a, logits, gp, ev[2]); break;
+    case 7: e = launch_gate_up_s<7>(p, a, logits, gp, ev[2]); break;
+    default: e = launch_gate_up_s<8>(p, a, logits, gp, ev[2]); break;
   }
+  for (int i = 3; i <= 4 && e == hipSuccess; ++i) e = record_empty(p, ev[i], a.stream);
   if (e != hipSuccess) return e;
   // one workgroup a CU, each the same number of columns: a multiple of 8
   // (H 6144 on 256 CUs: 24)
   const int c8 = std::min(4, (H / 8 + p->num_cus - 1) / p->num_cus);
   switch (p->s.I / 128) {
-    case 1: return launch_down_nb<1>(p, a, c8, gp);
-    case 2: return launch_down_nb<2>(p, a, c8, gp);
-    case 3: return launch_down_nb<3>(p, a, c8, gp);
-    default: return launch_down_nb<4>(p, a, c8, gp);
+    case 1: e = launch_down_nb<1>(p, a, c8, gp, ev[5]); break;
+    case 2: e = launch_down_nb<2>(p, a, c8, gp, ev[5]); break;
+    case 3: e = launch_down_nb<3>(p, a, c8, gp, ev[5]); break;
+    default: e = launch_down_nb<4>(p, a, c8, gp, ev[5]); break;
   }
+  return e == hipSuccess ? record_empty(p, ev[6], a.stream) : e;
 }
 
 }  // namespace qmoe

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "internal.h"
 #include "qmoe.h"
 
 struct moe_router {
@@ -32,7 +33,7 @@ struct RouterArgs {
   float* logits;
   int x_type, w_type;
 };
-hipError_t launch_router(const RouterArgs& a, int cus, hipStream_t stream);
+hipError_t launch_router(const RouterArgs& a, int cus, hipStream_t stream, Ev ev = {});
 
 struct LinearArgs {
   int64_t M, N, K, ldx, ldr, ldy;

@@ -436,20 +436,20 @@ done:
 }
 
 template <int XT, int WT, int TN, int TM, int W>
-static hipError_t launch_tiles(const RouterArgs& a, hipStream_t stream) {
+static hipError_t launch_tiles(const RouterArgs& a, hipStream_t stream, Ev ev) {
   const int64_t te = (a.E + 16 * TN - 1) / (16 * TN), tm = (a.M + 16 * TM - 1) / (16 * TM);
-  return launch_k(router_tile_kernel<XT, WT, TN, TM, W>, dim3((unsigned)(te * tm)), dim3(64 * W), 0, stream, Ev{}, a,
+  return launch_k(router_tile_kernel<XT, WT, TN, TM, W>, dim3((unsigned)(te * tm)), dim3(64 * W), 0, stream, ev, a,
                   (int)te);
 }
 
 template <int XT, int WT>
-static hipError_t launch_types(const RouterArgs& a, int cus, hipStream_t stream) {
+static hipError_t launch_types(const RouterArgs& a, int cus, hipStream_t stream, Ev ev) {
   if (a.M <= 16) {
     const dim3 grid((unsigned)a.E), block(64 * (unsigned)std::min<int64_t>(kRouterWaves, (a.H + 511) / 512));
-    if (a.M <= 1) return launch_k(router_kernel<XT, WT, 1>, grid, block, 0, stream, Ev{}, a);
-    if (a.M <= 4) return launch_k(router_kernel<XT, WT, 4>, grid, block, 0, stream, Ev{}, a);
-    if (a.M <= 8) return launch_k(router_kernel<XT, WT, 8>, grid, block, 0, stream, Ev{}, a);
-    return launch_k(router_kernel<XT, WT, 16>, grid, block, 0, stream, Ev{}, a);
+    if (a.M <= 1) return launch_k(router_kernel<XT, WT, 1>, grid, block, 0, stream, ev, a);
+    if (a.M <= 4) return launch_k(router_kernel<XT, WT, 4>, grid, block, 0, stream, ev, a);
+    if (a.M <= 8) return launch_k(router_kernel<XT, WT, 8>, grid, block, 0, stream, ev, a);
+    return launch_k(router_kernel<XT, WT, 16>, grid, block, 0, stream, ev, a);
   }
   // 64 x 64 tiles where they occupy half of the CUs, else the larger of two that
   // still give every CU a workgroup (H 6144, 256 experts, bf16: 2048 tokens 31
@@ -457,18 +457,18 @@ static hipError_t launch_types(const RouterArgs& a, int cus, hipStream_t stream)
   // by the first and 13 by the third)
   auto groups = [&](int t) { return ((a.E + 16 * t - 1) / (16 * t)) * ((a.M + 16 * t - 1) / (16 * t)); };
   if (groups(4) >= cus / 2)
-    return launch_k(router_wide_kernel<XT, WT>, dim3((unsigned)groups(4)), dim3(512), 0, stream, Ev{}, a,
+    return launch_k(router_wide_kernel<XT, WT>, dim3((unsigned)groups(4)), dim3(512), 0, stream, ev, a,
                     (int)((a.E + 63) / 64));
-  if (groups(2) >= cus) return launch_tiles<XT, WT, 2, 2, 8>(a, stream);
-  return launch_tiles<XT, WT, 1, 1, 16>(a, stream);
+  if (groups(2) >= cus) return launch_tiles<XT, WT, 2, 2, 8>(a, stream, ev);
+  return launch_tiles<XT, WT, 1, 1, 16>(a, stream, ev);
 }
 
-hipError_t launch_router(const RouterArgs& a, int cus, hipStream_t stream) {
+hipError_t launch_router(const RouterArgs& a, int cus, hipStream_t stream, Ev ev) {
   if (a.x_type == MOE_BF16)
-    return a.w_type == MOE_BF16 ? launch_types<MOE_BF16, MOE_BF16>(a, cus, stream)
-                                : launch_types<MOE_BF16, MOE_FP32>(a, cus, stream);
-  return a.w_type == MOE_BF16 ? launch_types<MOE_FP16, MOE_BF16>(a, cus, stream)
-                              : launch_types<MOE_FP16, MOE_FP32>(a, cus, stream);
+    return a.w_type == MOE_BF16 ? launch_types<MOE_BF16, MOE_BF16>(a, cus, stream, ev)
+                                : launch_types<MOE_BF16, MOE_FP32>(a, cus, stream, ev);
+  return a.w_type == MOE_BF16 ? launch_types<MOE_FP16, MOE_BF16>(a, cus, stream, ev)
+                              : launch_types<MOE_FP16, MOE_FP32>(a, cus, stream, ev);
 }
 
 }  // namespace qmoe

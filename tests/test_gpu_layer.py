@@ -387,3 +387,42 @@ def test_h_keeps_32_bits(M, E, H, I):
     want = np.stack([value(w2[picks[t]]) @ h[t] for t in range(M)])
     assert np.abs(want).max() < 2 ** 22
     assert torch.equal(out.cpu(), torch.from_numpy(want).float().bfloat16())
+
+
+@pytest.mark.parametrize("M", [1, 16])
+def test_stage_and_call_events(M):
+    """Events set on the plan are recorded by a layer call too, not left with
+    an earlier call's times."""
+    import torch
+    from quantized_moe_expert_route_amd import binding as B
+
+    d = Layer(M, 1024, 24, 256, 4)
+    d.call()
+    n = len(B.stage_names())
+    ev = B.HipEvents(2 * n + 2)
+    s = torch.cuda.current_stream()
+    try:
+        for _ in range(2):
+            d.plan.set_stage_events(ev.handles[:2 * n])
+            ev.record(2 * n, s)
+            want = d.call()
+            ev.record(2 * n + 1, s)
+            torch.cuda.synchronize()
+            used = [i for i, name in enumerate(B.stage_names()) if name in ("route", "gate_up", "down")]
+            for i in range(n):
+                assert ev.elapsed_ms(2 * n, 2 * i) >= 0 and ev.elapsed_ms(2 * i + 1, 2 * n + 1) >= 0
+                assert ev.elapsed_ms(2 * i, 2 * i + 1) > 0 if i in used else ev.elapsed_ms(2 * i, 2 * i + 1) >= 0
+            for a, b in zip(used, used[1:]):  # in order
+                assert ev.elapsed_ms(2 * a + 1, 2 * b) >= 0
+            d.check(want)
+            d.plan.set_call_events(*ev.handles[:2])
+            ev.record(2 * n, s)
+            d.call()
+            ev.record(2 * n + 1, s)
+            torch.cuda.synchronize()
+            assert ev.elapsed_ms(2 * n, 0) >= 0 and ev.elapsed_ms(0, 1) > 0 and ev.elapsed_ms(1, 2 * n + 1) >= 0
+        d.plan.set_call_events(None, None)
+        d.check(d.call())
+    finally:
+        d.plan.set_call_events(None, None)
+        ev.close()
