@@ -83,11 +83,16 @@ inline hipError_t record_empty(const moe_plan* p, const Ev& ev, hipStream_t s) {
 template <typename... KArgs, typename... Args>
 inline hipError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t lds, hipStream_t s, Ev ev,
                            Args... args) {
-  if (ev.start || ev.stop)
-    hipExtLaunchKernelGGL(kern, grid, block, lds, s, ev.start, ev.stop, 0, static_cast<KArgs>(args)...);
-  else
-    hipLaunchKernelGGL(kern, grid, block, lds, s, static_cast<KArgs>(args)...);
-  return hipGetLastError();
+  // The launch's own status: hipGetLastError would also return (and clear) what
+  // an earlier HIP call of the caller's has left behind.
+  const hipError_t e = [&](KArgs... a) {
+    void* argv[] = {const_cast<void*>(static_cast<const void*>(&a))...};
+    const void* f = reinterpret_cast<const void*>(kern);
+    return ev.start || ev.stop ? hipExtLaunchKernel(f, grid, block, argv, lds, s, ev.start, ev.stop, 0)
+                               : hipLaunchKernel(f, grid, block, argv, lds, s);
+  }(static_cast<KArgs>(args)...);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
 }
 
 // Largest M (and M * top_k) served by the single-workgroup routing/sort

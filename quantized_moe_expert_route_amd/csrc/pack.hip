@@ -74,15 +74,13 @@ hipError_t launch_pack_w2(const void* w2, const void* s2, int64_t E, int64_t I, 
   const int64_t units = rows * (I / 32);  // 16-byte units of w2
   const int64_t dwords = rows * 4;        // one dword per lane per 16-row block
   auto blocks = [](int64_t n) { return (int)std::min<int64_t>((n + 255) / 256, 65536); };
-  hipLaunchKernelGGL(pack_w13_kernel, dim3(blocks(units)), dim3(256), 0, stream,
+  hipError_t e = launch_k(pack_w13_kernel, dim3(blocks(units)), dim3(256), 0, stream, Ev{},
                      reinterpret_cast<const uint8_t*>(w2), reinterpret_cast<uint8_t*>(w2p), units, (int)(I / 128),
                      I / 2);
-  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pack_s2_kernel, dim3(blocks(dwords)), dim3(256), 0, stream,
+  return launch_k(pack_s2_kernel, dim3(blocks(dwords)), dim3(256), 0, stream, Ev{},
                      reinterpret_cast<const uint8_t*>(s2), reinterpret_cast<uint32_t*>(s2p), dwords, (int)(I / 128),
                      I / 32);
-  return hipGetLastError();
 }
 
 hipError_t launch_pack_w13(const void* w13, const void* s13, int64_t E, int64_t I, int64_t H, void* w13p, void* s13p,
@@ -91,15 +89,13 @@ hipError_t launch_pack_w13(const void* w13, const void* s13, int64_t E, int64_t 
   const int64_t units = rows * (H / 32);   // 16-byte units of w13
   const int64_t dwords = rows * (H / 128); // dwords of s13
   auto blocks = [](int64_t n) { return (int)std::min<int64_t>((n + 255) / 256, 65536); };
-  hipLaunchKernelGGL(pack_w13_kernel, dim3(blocks(units)), dim3(256), 0, stream,
+  hipError_t e = launch_k(pack_w13_kernel, dim3(blocks(units)), dim3(256), 0, stream, Ev{},
                      reinterpret_cast<const uint8_t*>(w13), reinterpret_cast<uint8_t*>(w13p), units, (int)(H / 128),
                      H / 2);
-  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pack_s13_kernel, dim3(blocks(dwords)), dim3(256), 0, stream,
+  return launch_k(pack_s13_kernel, dim3(blocks(dwords)), dim3(256), 0, stream, Ev{},
                      reinterpret_cast<const uint8_t*>(s13), reinterpret_cast<uint32_t*>(s13p), dwords, (int)(H / 512),
                      H / 32);
-  return hipGetLastError();
 }
 
 }  // namespace qmoe
