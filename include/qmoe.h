@@ -119,7 +119,9 @@ moe_status moe_shape_workspace_bytes(const moe_shape* shape, size_t* bytes);
 /* Free the plan (not the caller's workspace). NULL is accepted. */
 void moe_plan_destroy(moe_plan* plan);
 
-/* Bytes of device workspace the plan needs (multiple of 256). */
+/* Bytes of device workspace the plan needs (multiple of 256), with the regions
+ * of moe_layer_forward where the shape allows that call (no shared_I, H up to
+ * 8192). */
 size_t moe_plan_workspace_bytes(const moe_plan* plan);
 
 /* Offsets of the intermediates inside the workspace. */

@@ -90,10 +90,12 @@ Layout make_layout(const moe_shape& s) {
     r.X.sh_part = take(8 * std::min<size_t>(M, kSmallM) * (H / 128) * 2 * Is);
   }
   r.call_bytes = align256(off);
-  const size_t Ml = std::min<size_t>(M, kSmallM);
-  r.X.layer_logits = take(4 * Ml * E);
-  r.X.layer_g = take(6 * Ml * k * I);
-  r.X.layer_list = take(kLayerListBytes);
+  if (M > 0 && layer_shape(s)) {
+    const size_t Ml = std::min<size_t>(M, kSmallM);
+    r.X.layer_logits = take(4 * Ml * E);
+    r.X.layer_g = take(6 * Ml * k * I);
+    r.X.layer_list = take(kLayerListBytes);
+  }
   r.L.total_bytes = align256(off);
   return r;
 }

@@ -185,8 +185,8 @@ moe_status moe_layer_forward(moe_plan* plan, const moe_router* router, int64_t M
   if (M < 0 || M > plan->s.M) return MOE_ERR_INVALID_ARG;
   if (router->E != plan->s.E || router->H != plan->s.H || router->x_type != MOE_BF16) return MOE_ERR_INVALID_ARG;
   if (router->device != plan->device) return MOE_ERR_DEVICE;
-  if (M > kSmallM || plan->s.H > kLayerMaxH) return MOE_ERR_UNSUPPORTED;
-  if (plan->s.shared_I > 0 || plan->shared_slot || plan->tpx.tp > 0 || plan->mid_fmt != MOE_MID_E4M3 ||
+  if (M > kSmallM || !layer_shape(plan->s)) return MOE_ERR_UNSUPPORTED;
+  if (plan->shared_slot || plan->tpx.tp > 0 || plan->mid_fmt != MOE_MID_E4M3 ||
       plan->layout != MOE_LAYOUT_W13_PACKED)
     return MOE_ERR_UNSUPPORTED;
   if (!plan->ws) return MOE_ERR_WORKSPACE;

@@ -56,6 +56,9 @@ constexpr int kLayerMaxEntries = 256;
 constexpr int kLayerMaxH = 8192;
 constexpr int kLayerListBytes = 16 + (2 + 1 + 16) * kLayerMaxEntries;  // PickList of layer.hip
 
+// Shapes of plans that moe_layer_forward may run on (others have no workspace for it).
+inline bool layer_shape(const moe_shape& s) { return s.shared_I == 0 && s.H <= kLayerMaxH; }
+
 struct LayerArgs {
   int64_t M;
   const void* x;

@@ -200,3 +200,15 @@ def test_reference_layer_against_the_dense_definition():
         dense += y * (wt * (ids == e)).sum(1)[:, None]
     assert np.allclose(out, dense, rtol=1e-12, atol=1e-12)
     assert np.all(err > 0) and np.median(err / np.abs(out)) < 2e-2
+
+
+@pytest.mark.parametrize("kw,nbytes", [
+    (dict(M=4, H=6144, E=256, I=256, top_k=8, shared_I=256), 4208640),
+    (dict(M=4096, H=6144, E=256, I=512, top_k=8, shared_I=512), 1102433536),
+    (dict(M=64, H=16384, E=64, I=128, top_k=4), 17579264),
+    (dict(M=0, H=512, E=16, I=128, top_k=2), 1024),
+])
+def test_plans_without_the_layer_pay_nothing_for_it(kw, nbytes):
+    """Shapes that moe_layer_forward refuses need the workspace they needed
+    before it was there."""
+    assert B.shape_workspace_bytes(**kw) == nbytes
