@@ -30,6 +30,17 @@ __device__ __forceinline__ void barrier_lds() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Between a wave's lanes writing LDS and others of them reading it (or the other
+// way round), without a workgroup barrier. The LDS serves a wave's instructions in
+// their order; the fences keep the compiler from changing that order, and the wave
+// barrier keeps it from running lanes apart: after code that only some lanes
+// enter, it may otherwise let the others' next write go ahead of these lanes' read.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ----------------------------------------------------------------- wave reductions
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll

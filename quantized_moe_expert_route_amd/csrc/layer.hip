@@ -298,10 +298,10 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
     for (int s = 0; s < S; ++s) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) mine[x13_slot(r, 4 * i + g)] = xv[s][i];
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
+      wave_lds_order();
 #pragma unroll
       for (int j = 0; j < 4; ++j) xf[s][j] = mine[x13_slot(4 * g + j, r)];
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      wave_lds_order();
     }
   }
   // x is waited for here, once: left to its first use, inside the loop, the
@@ -527,7 +527,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
       const int n = min(64 * l + lane, cols * 4 * NB - 1);
       mine[Rows::at(n / (4 * NB), n % (4 * NB))] = q[p][l];
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
+    wave_lds_order();
     v4f d[R];
     // a token that did not pick the expert takes nothing from it, also where
     // its weights are not finite
@@ -554,7 +554,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
     // (further passes ask for h when they need it, and so wait for the weights
     // under way too: 16 tokens seldom pick one of many experts more than five times)
     for (int pass = 1; 5 * pass < picked(i); ++pass) {
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // other lanes' sums than before
+      wave_lds_order();  // other lanes' sums than before
       const int more = column(i, pass);
       begin(more);
 #pragma unroll
@@ -565,7 +565,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
       }
       end(more);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    wave_lds_order();
     load(p, i + PE);
   };
   // out of the loop itself, not round its end: paths that met there would make
@@ -578,7 +578,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
     }
   }
 done:
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  wave_lds_order();
   // a token's three parts, the smallest first, then the waves in order
 #pragma unroll
   for (int t = 0; t < R; ++t)

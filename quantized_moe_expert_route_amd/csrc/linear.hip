@@ -260,10 +260,10 @@ __global__ __launch_bounds__(64 * W) void linear_rows_kernel(const LinearArgs a)
       if (128 * (wave * S + s) + 128 > K && 128 * (wave * S + s) + 8 * r >= K) xv[s][i] = make_uint4(0, 0, 0, 0);
       mine[x_slot(0, r, 4 * i + g)] = xv[s][i];
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
+    wave_lds_order();
 #pragma unroll
     for (int j = 0; j < 4; ++j) xf[s][j][0] = mine[x_slot(0, 4 * j + g, r)];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    wave_lds_order();
   };
 
   auto tile_done = [&](int i, const v4f& acc) {
@@ -375,8 +375,7 @@ __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int
     }
 #pragma unroll
     for (int i = 0; i < CT * 4; ++i) xs[wave][x_slot(i >> 2, r, 4 * (i & 3) + g)] = xv[p][i];
-    // the wave's lanes read what its other lanes wrote: LDS keeps a wave's order
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    wave_lds_order();
     load_x(p, ks + P * W);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -386,7 +385,7 @@ __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int
 #pragma unroll
       for (int t = 0; t < R; ++t) w[p][t].template mul<CT>(j, x, acc[t]);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    wave_lds_order();
     load_w(p, ks + P * W);
   };
   // out of the loop itself, not round its end: paths that met there would make
@@ -578,13 +577,13 @@ done:
     for (int u = 0; u < TM; ++u) {
 #pragma unroll
       for (int t = 0; t < TN; ++t) *reinterpret_cast<v4f*>(&mine[r * S + 16 * t + 4 * g]) = acc[t][u];
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS keeps a wave's order
+      wave_lds_order();
       for (int i = lane; i < 16 * per_row; i += 64) {
         const int row = i / per_row, c = i % per_row * e;
         const int64_t m = m0 + 16 * (wm * TM + u) + row, n = n0 + C * wn + c;
         if (m < a.M && n < a.N) store_piece(a, m, n, &mine[row * S + c]);
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      wave_lds_order();
     }
     return;
   }

@@ -352,3 +352,20 @@ def test_scales_above_bf16_make_their_row_nan(M, N, K, xt):
     d["scales"][list(rows)] = 252
     d["x"] = (d["x"].float() * 2.0 ** -12).to(_dt(xt))
     assert bool(_run(d).isfinite().all())
+
+
+@pytest.mark.parametrize("xt,M,N,K", [("bf16", 300, 2600, 160), ("bf16", 140, 8000, 224), ("bf16", 256, 6144, 96),
+                                      ("fp16", 300, 4000, 160), ("fp16", 140, 8192, 96)])
+def test_narrow_tiles_with_whole_pieces(xt, M, N, K):
+    """64 x 128 tiles whose rows of 16-bit y are whole 16-byte pieces: only half
+    of a wave's lanes move a piece of a tile's 16 rows, between writes of the
+    sums by all of them."""
+    import torch
+
+    for extra in (False, True):
+        d = _case(np.random.default_rng([M, N, K, 41]), M, N, K, xt, xt, bias=extra, residual=extra, integers=True)
+        if xt == "fp16":
+            d["scales"] -= np.uint8(6)
+        y, mag = _expect(d)
+        assert mag.max() < 2.0 ** 22
+        assert torch.equal(_run(d), torch.from_numpy(y).float().to(_dt(xt)))
