@@ -453,6 +453,12 @@ const char* moe_stage_name(int i);
  * stage). */
 int moe_plan_stage_launches(const moe_plan* plan, int64_t M, int stage);
 
+/* Profiling aid: which of its kernels a call of M rows on this handle launches,
+ * as static text ("64 x 128 tile"); NULL for a NULL handle or M outside
+ * 1 .. max_M. The choice goes by the sizes, x's type and the device's CUs. */
+const char* moe_router_kernel(const moe_router* router, int64_t M);
+const char* moe_linear_kernel(const moe_linear* linear, int64_t M);
+
 /* Static text for a status code. */
 const char* moe_status_str(moe_status status);
 

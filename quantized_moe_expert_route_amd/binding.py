@@ -116,6 +116,9 @@ def lib() -> ctypes.CDLL:
     L.moe_router_destroy.argtypes = [vp]
     L.moe_router_forward.restype = st
     L.moe_router_forward.argtypes = [vp, i64, vp, i64, vp, vp]
+    for f in (L.moe_router_kernel, L.moe_linear_kernel):
+        f.restype = ctypes.c_char_p
+        f.argtypes = [vp, i64]
     L.moe_linear_pack_bytes.restype = st
     L.moe_linear_pack_bytes.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)]
     L.moe_pack_linear.restype = st
@@ -238,6 +241,13 @@ class _Handle:
         if not 0 <= M <= self.max_M:
             raise ValueError(f"M = {M} outside [0, {self.max_M}]")
         return M
+
+    def kernel(self, M: int) -> str:
+        """Which of its kernels a call of M rows launches (profiling aid)."""
+        name = getattr(lib(), self._destroy.replace("destroy", "kernel"))(self._h, int(M))
+        if name is None:
+            raise ValueError(f"M = {M} outside [1, {self.max_M}], or no handle")
+        return name.decode()
 
     def _stream(self, stream):
         return _raw_stream(self.device) if stream is None else stream.cuda_stream

@@ -72,6 +72,10 @@ moe_status moe_router_create(int64_t E, int64_t H, int x_type, const void* w, in
 
 void moe_router_destroy(moe_router* r) { delete r; }
 
+const char* moe_router_kernel(const moe_router* r, int64_t M) {
+  return r && M > 0 && M <= r->max_M ? router_kernel_name(M, r->E, r->num_cus) : nullptr;
+}
+
 moe_status moe_router_forward(const moe_router* r, int64_t M, const void* x, int64_t ldx, float* logits,
                               void* stream) {
   if (!r || M < 0 || M > r->max_M) return MOE_ERR_INVALID_ARG;
@@ -143,6 +147,10 @@ moe_status moe_linear_create(int64_t N, int64_t K, int x_type, const void* w_pac
 }
 
 void moe_linear_destroy(moe_linear* l) { delete l; }
+
+const char* moe_linear_kernel(const moe_linear* l, int64_t M) {
+  return l && M > 0 && M <= l->max_M ? linear_kernel_name(M, l->N, l->K, l->x_type == MOE_FP16, l->num_cus) : nullptr;
+}
 
 moe_status moe_linear_forward(const moe_linear* l, int64_t M, const void* x, int64_t ldx, const void* residual,
                               int64_t ldr, void* y, int64_t ldy, int y_type, void* stream) {

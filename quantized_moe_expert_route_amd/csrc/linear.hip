@@ -610,25 +610,59 @@ static hipError_t launch_mid(const LinearArgs& a, hipStream_t stream) {
                   (int)tiles);
 }
 
-template <bool F16>
-static hipError_t launch_16_rows(const LinearArgs& a, int cus, hipStream_t stream) {
-  const int64_t nks = (a.K + 127) / 128;
-  if (nks <= 8) return launch_rows<F16, 8, 1, 3>(a, cus, stream);
-  if (nks <= 16) return launch_rows<F16, 8, 2, 2>(a, cus, stream);
-  if (nks <= 24) return launch_rows<F16, 8, 3, 1>(a, cus, stream);
-  // (fp16 carries four scale dwords a step: more steps do not fit the registers)
-  if constexpr (!F16) {
-    if (nks <= 32) return launch_rows<F16, 8, 4, 1>(a, cus, stream);
-    if (nks <= 40) return launch_rows<F16, 8, 5, 1>(a, cus, stream);
-    if (nks <= 48) return launch_rows<F16, 8, 6, 1>(a, cus, stream);
-  }
-  // a longer K: x from the L2 for every 16 or 32 columns
-  return (a.N + 15) / 16 <= cus ? launch_mid<F16, 1, 1>(a, stream) : launch_mid<F16, 1, 2>(a, stream);
+// The kernels a call may run, by the rules of `choose`: name, and per type of x
+// the launch (NULL: not for that type).
+namespace {
+
+typedef hipError_t (*Launch)(const LinearArgs& a, int cus, hipStream_t stream);
+struct Choice {
+  const char* name;
+  Launch launch[2];  // bf16, fp16 x
+};
+
+// up to 16 rows: K-steps a wave, workgroups a CU
+template <bool F16, int S, int OCC>
+hipError_t rows(const LinearArgs& a, int cus, hipStream_t stream) {
+  return launch_rows<F16, 8, S, OCC>(a, cus, stream);
+}
+template <bool F16, int CT, int R>
+hipError_t mid(const LinearArgs& a, int, hipStream_t stream) {
+  return launch_mid<F16, CT, R>(a, stream);
+}
+template <bool F16, int TN, int TM, int WN, int WM>
+hipError_t tile(const LinearArgs& a, int, hipStream_t stream) {
+  return launch_tile<F16, TN, TM, WN, WM>(a, stream);
 }
 
-template <bool F16>
-static hipError_t launch_type(const LinearArgs& a, int cus, hipStream_t stream) {
-  if (a.M <= 16) return launch_16_rows<F16>(a, cus, stream);
+enum { kMid1 = 6, kMidRows = 8, kChoices = 13 };
+constexpr Choice kChoice[kChoices] = {
+    {"rows, 1 K-step a wave", {rows<false, 1, 3>, rows<true, 1, 3>}},
+    {"rows, 2 K-steps a wave", {rows<false, 2, 2>, rows<true, 2, 2>}},
+    {"rows, 3 K-steps a wave", {rows<false, 3, 1>, rows<true, 3, 1>}},
+    // (fp16 carries four scale dwords a step)
+    {"rows, 4 K-steps a wave", {rows<false, 4, 1>, nullptr}},
+    {"rows, 5 K-steps a wave", {rows<false, 5, 1>, nullptr}},
+    {"rows, 6 K-steps a wave", {rows<false, 6, 1>, nullptr}},
+    {"16 x 16, K split over the waves", {mid<false, 1, 1>, mid<true, 1, 1>}},
+    {"16 x 32, K split over the waves", {mid<false, 1, 2>, mid<true, 1, 2>}},
+    {"32 x 16, K split over the waves", {mid<false, 2, 1>, mid<true, 2, 1>}},
+    {"32 x 32, K split over the waves", {mid<false, 2, 2>, mid<true, 2, 2>}},
+    // all rows of a tile by every wave (weights widened once a workgroup, not
+    // twice) where that measured faster: bf16 M 256 by the first 30.9 against
+    // 32.5 us, M 4096 by the third 235 against 246; by the second 310 against 304
+    {"64 x 128 tile", {tile<false, 1, 4, 8, 1>, tile<true, 1, 4, 8, 1>}},
+    {"128 x 128 tile", {tile<false, 2, 4, 4, 2>, tile<true, 2, 4, 4, 2>}},
+    {"128 x 256 tile", {tile<false, 2, 8, 8, 1>, tile<true, 4, 4, 4, 2>}},
+};
+
+int choose(int64_t M, int64_t N, int64_t K, bool f16, int cus) {
+  const int64_t tiles = (N + 15) / 16;
+  if (M <= 16) {
+    const int64_t S = ((K + 127) / 128 + 7) / 8;
+    if (S <= (f16 ? 3 : 6)) return (int)S - 1;
+    // a longer K: x from the L2 for every 16 or 32 columns
+    return tiles <= cus ? kMid1 : kMid1 + 1;
+  }
   // Rounds of workgroups over the CUs times a round's time per K-step, in
   // units of 10 ns (N and K 6144, bf16 x; M 32: 14.4 us by the first against 9.6
   // by the second; M 64: 20.8, 16.9 and 30.7 by the first three; M 128: 26 and 31
@@ -637,27 +671,23 @@ static hipError_t launch_type(const LinearArgs& a, int cus, hipStream_t stream) 
   // 64 25, 21 and 59 by the first three, M 256 61, 59 and 97 by the second to
   // fourth, M 4096 604, 593 and 452 by the last three).
   auto cost = [&](int64_t bm, int64_t bn, int per) {
-    const int64_t groups = ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn);
+    const int64_t groups = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
     return ((groups + cus - 1) / cus) * per;
   };
-  const int64_t c[5] = {cost(32, 16, F16 ? 16 : 14), cost(32, 32, F16 ? 22 : 16), cost(64, 128, F16 ? 105 : 60),
-                        cost(128, 128, F16 ? 195 : 97), cost(128, 256, F16 ? 280 : 150)};
-  switch (std::min_element(c, c + 5) - c) {
-    case 0: return launch_mid<F16, 2, 1>(a, stream);
-    case 1: return launch_mid<F16, 2, 2>(a, stream);
-    // all rows of a tile by every wave (weights widened once a workgroup, not
-    // twice) where that measured faster: bf16 M 256 by the third 30.9 against
-    // 32.5 us, M 4096 by the fifth 235 against 246; by the fourth 310 against 304
-    case 2: return launch_tile<F16, 1, 4, 8, 1>(a, stream);
-    case 3: return launch_tile<F16, 2, 4, 4, 2>(a, stream);
-    default:
-      if constexpr (F16) return launch_tile<F16, 4, 4, 4, 2>(a, stream);
-      else return launch_tile<F16, 2, 8, 8, 1>(a, stream);
-  }
+  const int64_t c[5] = {cost(32, 16, f16 ? 16 : 14), cost(32, 32, f16 ? 22 : 16), cost(64, 128, f16 ? 105 : 60),
+                        cost(128, 128, f16 ? 195 : 97), cost(128, 256, f16 ? 280 : 150)};
+  return kMidRows + (int)(std::min_element(c, c + 5) - c);
 }
 
+}  // namespace
+
 hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream) {
-  return a.x_type == MOE_FP16 ? launch_type<true>(a, cus, stream) : launch_type<false>(a, cus, stream);
+  const bool f16 = a.x_type == MOE_FP16;
+  return kChoice[choose(a.M, a.N, a.K, f16, cus)].launch[f16](a, cus, stream);
+}
+
+const char* linear_kernel_name(int64_t M, int64_t N, int64_t K, bool f16, int cus) {
+  return kChoice[choose(M, N, K, f16, cus)].name;
 }
 
 }  // namespace qmoe

@@ -34,6 +34,7 @@ struct RouterArgs {
   int x_type, w_type;
 };
 hipError_t launch_router(const RouterArgs& a, int cus, hipStream_t stream, Ev ev = {});
+const char* router_kernel_name(int64_t M, int64_t E, int cus);  // that it launches, M > 0
 
 struct LinearArgs {
   int64_t M, N, K, ldx, ldr, ldy;
@@ -49,6 +50,7 @@ struct LinearArgs {
 hipError_t launch_pack_linear(const void* w, const void* s, int64_t N, int64_t K, void* wp, void* sp,
                               hipStream_t stream);
 hipError_t launch_linear(const LinearArgs& a, int cus, hipStream_t stream);
+const char* linear_kernel_name(int64_t M, int64_t N, int64_t K, bool f16, int cus);  // that it launches, M > 0
 
 // Few-token MoE layer: most (token, slot) entries and the widest x a call takes
 // (8 waves hold at most 8 K-steps of 128 each as register operands).

@@ -442,26 +442,37 @@ static hipError_t launch_tiles(const RouterArgs& a, hipStream_t stream, Ev ev) {
                   (int)te);
 }
 
+// Up to 16 tokens by 1, 4, 8 or 16 of them a workgroup. Above, 64 x 64 tiles where
+// they occupy half of the CUs, else the larger of two that still give every CU a
+// workgroup (H 6144, 256 experts, bf16: 2048 tokens 31 us by the first, 49 by the
+// second; 1024 tokens 30 and 25; 256 tokens 28 us by the first and 13 by the third)
+enum { kTokens1, kTokens4, kTokens8, kTokens16, kWide, kTiles2, kTiles1 };
+static const char* const kNames[] = {"1 token", "4 tokens", "8 tokens", "16 tokens",
+                                     "64 x 64 tile", "32 x 32, K split over the waves",
+                                     "16 x 16, K split over the waves"};
+static int64_t tiles_of(int64_t M, int64_t E, int t) { return ((E + t - 1) / t) * ((M + t - 1) / t); }
+static int choose(int64_t M, int64_t E, int cus) {
+  if (M <= 16) return M <= 1 ? kTokens1 : M <= 4 ? kTokens4 : M <= 8 ? kTokens8 : kTokens16;
+  return tiles_of(M, E, 64) >= cus / 2 ? kWide : tiles_of(M, E, 32) >= cus ? kTiles2 : kTiles1;
+}
+
 template <int XT, int WT>
 static hipError_t launch_types(const RouterArgs& a, int cus, hipStream_t stream, Ev ev) {
-  if (a.M <= 16) {
-    const dim3 grid((unsigned)a.E), block(64 * (unsigned)std::min<int64_t>(kRouterWaves, (a.H + 511) / 512));
-    if (a.M <= 1) return launch_k(router_kernel<XT, WT, 1>, grid, block, 0, stream, ev, a);
-    if (a.M <= 4) return launch_k(router_kernel<XT, WT, 4>, grid, block, 0, stream, ev, a);
-    if (a.M <= 8) return launch_k(router_kernel<XT, WT, 8>, grid, block, 0, stream, ev, a);
-    return launch_k(router_kernel<XT, WT, 16>, grid, block, 0, stream, ev, a);
+  const dim3 grid((unsigned)a.E), block(64 * (unsigned)std::min<int64_t>(kRouterWaves, (a.H + 511) / 512));
+  switch (choose(a.M, a.E, cus)) {
+    case kTokens1: return launch_k(router_kernel<XT, WT, 1>, grid, block, 0, stream, ev, a);
+    case kTokens4: return launch_k(router_kernel<XT, WT, 4>, grid, block, 0, stream, ev, a);
+    case kTokens8: return launch_k(router_kernel<XT, WT, 8>, grid, block, 0, stream, ev, a);
+    case kTokens16: return launch_k(router_kernel<XT, WT, 16>, grid, block, 0, stream, ev, a);
+    case kWide:
+      return launch_k(router_wide_kernel<XT, WT>, dim3((unsigned)tiles_of(a.M, a.E, 64)), dim3(512), 0, stream, ev, a,
+                      (int)((a.E + 63) / 64));
+    case kTiles2: return launch_tiles<XT, WT, 2, 2, 8>(a, stream, ev);
+    default: return launch_tiles<XT, WT, 1, 1, 16>(a, stream, ev);
   }
-  // 64 x 64 tiles where they occupy half of the CUs, else the larger of two that
-  // still give every CU a workgroup (H 6144, 256 experts, bf16: 2048 tokens 31
-  // us by the first, 49 by the second; 1024 tokens 30 and 25; 256 tokens 28 us
-  // by the first and 13 by the third)
-  auto groups = [&](int t) { return ((a.E + 16 * t - 1) / (16 * t)) * ((a.M + 16 * t - 1) / (16 * t)); };
-  if (groups(4) >= cus / 2)
-    return launch_k(router_wide_kernel<XT, WT>, dim3((unsigned)groups(4)), dim3(512), 0, stream, ev, a,
-                    (int)((a.E + 63) / 64));
-  if (groups(2) >= cus) return launch_tiles<XT, WT, 2, 2, 8>(a, stream, ev);
-  return launch_tiles<XT, WT, 1, 1, 16>(a, stream, ev);
 }
+
+const char* router_kernel_name(int64_t M, int64_t E, int cus) { return kNames[choose(M, E, cus)]; }
 
 hipError_t launch_router(const RouterArgs& a, int cus, hipStream_t stream, Ev ev) {
   if (a.x_type == MOE_BF16)

@@ -48,6 +48,7 @@ def test_null_handles():
     assert L.moe_linear_create(16, 32, B.BF16, A, A2, None, 16, None) == B.MOE_ERR_INVALID_ARG
     assert L.moe_linear_forward(None, 1, A, 32, None, 0, A2, 16, B.BF16, None) == B.MOE_ERR_INVALID_ARG
     assert L.moe_layer_forward(None, None, 1, A, A, A, A, A, A2, None) == B.MOE_ERR_INVALID_ARG
+    assert L.moe_router_kernel(None, 1) is None and L.moe_linear_kernel(None, 1) is None
     L.moe_router_destroy(None)
     L.moe_linear_destroy(None)
 
