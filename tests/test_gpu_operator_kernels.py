@@ -227,3 +227,36 @@ def test_kernel_names_and_bad_counts():
     lin.close()
     with pytest.raises(ValueError):
         lin.kernel(1)
+
+
+@pytest.mark.parametrize("xt,M,N,K", [(xt, M, N, K) for xt in ("bf16", "fp16")
+                                      for M, N, K in ((4, 50, 352), (16, 100, 8192), (20, 300, 352), (300, 2600, 160),
+                                                      (300, 7000, 160), (385, 10000, 160))])
+def test_linear_subnormal_x(xt, M, N, K):
+    """Subnormal numbers of x's type keep their value in every kernel."""
+    import torch
+
+    d = _case(np.random.default_rng([M, N, K, 9]), M, N, K, xt, "fp32", integers=True)
+    unit = 2.0 ** -24 if xt == "fp16" else 2.0 ** -133
+    d["x"] = (d["x"].double() * unit).to(_dt(xt))
+    assert np.count_nonzero(_f64(d["x"])) > M * K // 2
+    if xt == "bf16":
+        d["scales"] += np.uint8(100)
+    y, _ = _expect(d)
+    lin = _linear(d)
+    out = torch.empty(M, N, device="cuda")
+    lin.forward(d["x"].cuda(), out)
+    assert np.array_equal(_f64(out.cpu()), y)
+
+
+@pytest.mark.parametrize("M,E,H", [(4, 50, 264), (16, 50, 264), (40, 50, 264), (1024, 256, 136), (1100, 500, 136)])
+@pytest.mark.parametrize("xt,wt", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "bf16"), ("fp16", "fp32")])
+def test_router_subnormal_x(M, E, H, xt, wt):
+    import torch
+
+    g = torch.Generator().manual_seed(M + E)
+    unit = 2.0 ** -24 if xt == "fp16" else 2.0 ** -133
+    x = (torch.randint(-3, 4, (M, H), generator=g).double() * unit).to(_dt(xt))
+    w = torch.randint(-9, 10, (E, H), generator=g).to(_dt(wt)) * 2.0 ** 60
+    want = x.double().numpy() @ w.double().numpy().T
+    assert np.array_equal(_router_run(x, w), want)
