@@ -26,6 +26,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import sys
 import time
 
@@ -72,11 +73,24 @@ def call_flops(shape):
     return f
 
 
-def kernel_source_hash():
+# the sources of the routed call's kernels; the operators beside it (router,
+# linear layer, few-token layer) have files of their own
+CALL_SOURCES = ("a4w4.hip", "down.hip", "gate_up.hip", "gemm_big.hip", "route_align.hip", "shared.hip",
+                "tp_exchange.hip")
+
+
+def kernel_source_hash(root=ROOT):
+    """Hash of the files the routed call's kernels are built from: CALL_SOURCES
+    and what they include of the library's own headers."""
+    d = os.path.join(root, "quantized_moe_expert_route_amd", "csrc")
+    files, new = set(), set(CALL_SOURCES)
+    while new:
+        files |= new
+        text = "".join(open(os.path.join(d, f)).read() for f in new)
+        new = {f for f in re.findall(r'^#include "(.*)"', text, re.M) if os.path.exists(os.path.join(d, f))} - files
     h = hashlib.sha256()
-    d = os.path.join(ROOT, "quantized_moe_expert_route_amd", "csrc")
-    for f in sorted(os.listdir(d)):
-        h.update(open(os.path.join(d, f), "rb").read())
+    for f in sorted(files):
+        h.update(f.encode() + b"\0" + open(os.path.join(d, f), "rb").read())
     return h.hexdigest()[:16]
 
 
