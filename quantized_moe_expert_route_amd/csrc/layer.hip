@@ -438,12 +438,14 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
   constexpr int I = 128 * NB, R = (C8 + 1) / 2;      // R MFMA row tiles
   constexpr int kRows = 8 * C8 * Rows::kStride;      // chunks of a wave's rows in LDS
   constexpr int NL = (8 * C8 * 4 * NB + 63) / 64;    // loads of an expert's rows
-  constexpr int PE = NL >= 5 ? 2 : NL >= 3 ? 4 : NB == 4 ? 4 : 8;
+  // (H 4096, I 256, 16 tokens: 21.1 us with 4 experts ahead, 22.0 with 6, no registers for 8)
+  constexpr int PE = NL >= 5 ? 2 : NL >= 3 || NB == 4 || NL * NB == 4 ? 4 : 8;
   constexpr int UH = NB == 3 ? 3 : 4;
   static_assert(PE * NB % UH == 0, "whole rounds of h");
   __shared__ __align__(16) PickList list;
   __shared__ uint4 area[kLayerWaves * kRows];
-  __shared__ v4f sums[kLayerWaves][kHParts][kSmallM][4 * R];  // [.][.][token][4 t + g]: columns 16 t + 4 g .. + 3
+  // [.][.][token][4 t + g]: columns 16 t + 4 g .. + 3 (one more, or all tokens met the same banks)
+  __shared__ v4f sums[kLayerWaves][kHParts][kSmallM][4 * R + 1];
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   for (int i = threadIdx.x; i < (int)sizeof(PickList) / 16; i += 64 * kLayerWaves)
@@ -480,35 +482,33 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
       }
     }
   };
-  // the tokens that picked the wave's expert i (uniform), none past its last
-  auto picked = [&](int i) __attribute__((always_inline)) -> int {
-    return i < experts ? __builtin_amdgcn_readfirstlane(list.count[at(i)]) : 0;
-  };
   // Token and slot (16 token + slot) of this lane's column in a pass over the
-  // expert, -1: none. (Column 15 is nobody's and reads what column 10 does.)
+  // wave's expert i, -1: none; n: the tokens that picked it, none past the last
+  // expert. Both bytes are read whatever comes of them: a branch would wait for
+  // the one and then for the other. (Column 15 is nobody's and reads what column
+  // 10 does.)
   const int c5 = r % 5, part = min(r / 5, kHParts - 1);
-  auto column = [&](int i, int pass) __attribute__((always_inline)) -> int {
+  auto column = [&](int i, int pass, int& n) __attribute__((always_inline)) -> int {
     const int q = 5 * pass + c5, who = list.pick[at(i)][min(q, kSmallM - 1)];
-    return q < picked(i) ? who : -1;
+    n = list.count[at(i)] & (i < experts ? 255 : 0);
+    return who | (q < n ? 0 : -1);
   };
   auto load_h = [&](uint4(&hv)[4], int who, int b) __attribute__((always_inline)) {
     // (no branch round the loads: the compiler counts those under way. Without a
     // token the first entry's, for a column that is not used)
-    const int entry = who >= 0 ? (who >> 4) * k + (who & 15) : 0;
+    const int w = max(who, 0), entry = (w >> 4) * k + (w & 15);
     const uint16_t* src = gp + (size_t)(entry * NB + b) * kHStep + (part * 4 + g) * 8;
 #pragma unroll
     for (int j = 0; j < 4; ++j) hv[j] = ld16(src + 32 * kHParts * j);
   };
+  int n_ahead;
   uint4 hv[UH][4];
   load(0, 0);
 #pragma unroll
-  for (int u = 0; u < UH; ++u) load_h(hv[u], column(u / NB, 0), u % NB);
+  for (int u = 0; u < UH; ++u) load_h(hv[u], column(u / NB, 0, n_ahead), u % NB);
 #pragma unroll
   for (int p = 1; p < PE; ++p) load(p, p);
-  constexpr int kSums = kHParts * kSmallM * 4 * R;  // of a wave
-#pragma unroll
-  for (int i = 0; i < kSums / 64; ++i) (&sums[wave][0][0][0])[64 * i + lane] = v4f{0.f, 0.f, 0.f, 0.f};
-  static_assert(kSums % 64 == 0, "whole rounds");
+  for (int i = lane; i < kHParts * kSmallM * (4 * R + 1); i += 64) (&sums[wave][0][0][0])[i] = v4f{0.f, 0.f, 0.f, 0.f};
   auto multiply = [&](int p, int b, const uint4(&x)[4], v4f(&d)[R]) __attribute__((always_inline)) {
     uint4 w[R];
 #pragma unroll
@@ -533,7 +533,7 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
     // its weights are not finite
     auto begin = [&](int who) __attribute__((always_inline)) {
 #pragma unroll
-      for (int t = 0; t < R; ++t) d[t] = sums[wave][part][who >= 0 ? who >> 4 : 0][4 * t + g];
+      for (int t = 0; t < R; ++t) d[t] = sums[wave][part][max(who, 0) >> 4][4 * t + g];
     };
     auto end = [&](int who) __attribute__((always_inline)) {
       if (who >= 0 && r < 5 * kHParts) {
@@ -541,21 +541,23 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_down_kernel(
         for (int t = 0; t < R; ++t) sums[wave][part][who >> 4][4 * t + g] = d[t];
       }
     };
-    const int who = column(i, 0);
+    int n, n_same;
+    const int who = column(i, 0, n);
     begin(who);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int u = p * NB + b;
       multiply(p, b, hv[u % UH], d);
-      load_h(hv[u % UH], column(i + (b + UH) / NB, 0), (b + UH) % NB);
-      if constexpr (NB * R > 4) __builtin_amdgcn_sched_barrier(0);  // one K-step's operands at a time in registers
+      load_h(hv[u % UH], column(i + (b + UH) / NB, 0, n_ahead), (b + UH) % NB);
+      if constexpr (NB * R > 4 || C8 == 2) __builtin_amdgcn_sched_barrier(0);  // one K-step's operands at a time in registers
     }
     end(who);
     // (further passes ask for h when they need it, and so wait for the weights
     // under way too: 16 tokens seldom pick one of many experts more than five times)
-    for (int pass = 1; 5 * pass < picked(i); ++pass) {
+    const int tokens = __builtin_amdgcn_readfirstlane(n);
+    for (int pass = 1; 5 * pass < tokens; ++pass) {
       wave_lds_order();  // other lanes' sums than before
-      const int more = column(i, pass);
+      const int more = column(i, pass, n_same);
       begin(more);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
