@@ -147,7 +147,8 @@ constexpr int kHoldItems = 16;  // finished items a gate/up workgroup holds befo
 // Results wait in LDS and are stored 16 items at a time: the compiler drains
 // all loads before it lets a store's counter mix with them. H 6144, I 256, 8 of
 // 256 experts: 4 tokens 16 us, of which 4.6 pass before weights move (logits,
-// top-k, list), 16 tokens 31 us (6.7); then 5.5 to 6.1 TB/s of them.
+// top-k, list), 16 tokens 31 us (6.7); then 4.4 TB/s of them (51 and 108 MB), a
+// third of the time with the vector ALUs at work and a twelfth with the MFMAs.
 //
 // T tokens a wave are routed, x comes operand-shaped up to 4 tokens (few
 // lines a load), else in whole row pieces turned round in LDS.
@@ -417,10 +418,11 @@ __global__ __launch_bounds__(64 * kLayerWaves) void layer_gate_up_kernel(
 // picked the expert; more than five take further passes over the same weights.
 // Which tokens a column holds changes from expert to expert, so the sums stay in
 // LDS of the wave's own, per part and token, and the parts are added at the end.
-// Bound by the spread of the waves' ends (their experts are fixed, so that the
-// sums' order is) and the weights' way: H 6144, I 256, 8 of 256: 4 tokens 10.4
-// us, 16 tokens 18.4 where h was cut to two bf16 (half again the bytes of h and
-// the sums in LDS cost the whole layer 1 to 4 %).
+// Bound by loads' latency, not by a rate: few experts a wave, and the waves' ends
+// spread (their experts are fixed, so that the sums' order is). H 6144, I 256, 8
+// of 256 experts: 4 tokens 11.2 us (26 MB of weights, 2.3 TB/s; with h 41 MB from
+// the L2s), 16 tokens 20.3 (54 MB, 2.6 TB/s; 108 MB); where h was cut to two bf16
+// and the sums stayed in registers 10.6 and 18.5.
 template <int NB>
 struct DownRows {  // a row's 4 NB chunks of 16 bytes in LDS, exchanged against bank conflicts
   static constexpr int kStride = NB == 3 ? 16 : 4 * NB;

@@ -329,8 +329,11 @@ static hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t stream) 
 // 256-byte row pieces are read: operand-shaped loads, 64 bytes of 16 rows
 // each, took three times as long), both P of the wave's steps ahead. The
 // partial sums are joined through LDS at the end. x is read once per 16 R
-// columns (from the L2): R = 2 where there are tiles enough. Bound by x's L2
-// reads and the loads' latency: 32 x 6144 x 6144 9.7 us, 64 rows 16.6 us.
+// columns (from the L2): R = 2 where there are tiles enough. Bound by the L2
+// reads and the loads' latency: 32 x 6144 x 6144 9.7 us, 64 rows 16.9 us (192 MB
+// from the L2s, 11 TB/s). 16 rows of a K that the kernel above does not take: 16 x
+// 8192 x 7168 10.9 us, x 8192 11.2, x 16384 18.4; 4 x 131072 x 8192 143 us (4.0 TB/s
+// of weights; the kernel above at K 6144 5.9).
 template <bool F16, int CT, int R>
 __global__ __launch_bounds__(512) void linear_mid_kernel(const LinearArgs a, int tiles_n) {
   constexpr int W = 8, P = CT == 1 ? 4 : 2;
@@ -428,7 +431,9 @@ done:
 // way into LDS (exact; the same products, twice the MFMAs). With one step of
 // weights ahead a K-step took 2.2 us, their latency, where its products take
 // 0.85. 4096 x 6144 x 6144: 235 us, 1310 TFLOP/s (fp16: 447 us), bound by MFMAs
-// and the widening between them (the two overlap by a quarter only); 256 rows 31 us, 192 workgroups for 256 CUs.
+// and the widening between them (with the residual, 253 us: MFMAs busy 49 % of the
+// SIMDs' time, vector ALUs 28 %, and the two overlap by a quarter only; fp16 54 and
+// 54 %); 256 rows 31 us, 192 workgroups for 256 CUs, MFMAs busy 25 %.
 template <bool F16, int TN, int TM, int WN, int WM>
 __global__ __launch_bounds__(64 * WN * WM) void linear_tile_kernel(const LinearArgs a, int tiles_m, int tiles_n) {
   constexpr int W = WN * WM, BM = 16 * TM * WM, BN = 16 * TN * WN;
@@ -639,7 +644,8 @@ constexpr Choice kChoice[kChoices] = {
     {"rows, 1 K-step a wave", {rows<false, 1, 3>, rows<true, 1, 3>}},
     {"rows, 2 K-steps a wave", {rows<false, 2, 2>, rows<true, 2, 2>}},
     {"rows, 3 K-steps a wave", {rows<false, 3, 1>, rows<true, 3, 1>}},
-    // (fp16 carries four scale dwords a step)
+    // more K-steps a wave (fp16 4, bf16 7 and 8) fit the registers as well, are not
+    // there, and go to the ones below
     {"rows, 4 K-steps a wave", {rows<false, 4, 1>, nullptr}},
     {"rows, 5 K-steps a wave", {rows<false, 5, 1>, nullptr}},
     {"rows, 6 K-steps a wave", {rows<false, 6, 1>, nullptr}},

@@ -185,9 +185,11 @@ __device__ __forceinline__ void redo_odd(const RouterArgs& a, int64_t m, int e) 
 // (binary32 sums of exact products, planes as above). The W waves of a
 // workgroup split K in pieces of 64, so that no operand is shared between
 // them: each goes from memory to the wave's registers, without LDS or
-// barriers in the loop. The W partial tiles are added in wave order. Bound by
-// the operands' latency: 77 tokens, 161 experts, H 2056 5.3 us (fp16 x); 256
-// tokens, 256 experts, H 6144 13 us.
+// barriers in the loop. The W partial tiles are added in wave order. 77 tokens,
+// 161 experts, H 2056 5.3 us (fp16 x); 256 tokens, 256 experts, H 6144 13 us, 1024
+// tokens 25: no rate is near its limit (107 and 245 MB from the L2s, MFMAs busy 2
+// and 5 % of the time); what is left are the latency of loads of 64 bytes from each
+// of 16 rows and the start.
 template <int XT, int WT, int TN, int TM, int W>
 __global__ __launch_bounds__(64 * W) void router_tile_kernel(const RouterArgs a, int tiles_e) {
   __shared__ v4f red[W][TN * TM > 4 ? 4 : TN * TM][64];
@@ -288,8 +290,10 @@ __global__ __launch_bounds__(64 * W) void router_tile_kernel(const RouterArgs a,
 // reads it, rows exchanged against bank conflicts as in the linear layer. Wave
 // w multiplies K's quarter w % 4 of every step for half of the tokens, so that
 // an operand read from LDS serves two or four MFMAs; planes are formed there.
-// 4096 tokens, 256 experts, H 6144, bf16: 31 us, bound by reading x once (50 MB)
-// and the weights once per 64 tokens (200 MB from the L2s) through 256 workgroups.
+// 4096 tokens, 256 experts, H 6144, bf16: 31 us for 411 MB from the L2s (x once per
+// 64 experts, the weights once per 64 tokens, 201 MB each) through 256 workgroups,
+// one a CU; MFMAs busy 15 % of the time. fp32 weights: 92 us, three MFMAs a product
+// and the planes' vector work.
 // (With every wave loading its own operands, 64 bytes of 16 rows each, 4096
 // tokens of H 6144 to 256 experts took 49 us: the memory pipeline's time.)
 template <int XT, int WT>
