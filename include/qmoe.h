@@ -421,7 +421,9 @@ moe_status moe_linear_forward(const moe_linear* linear, int64_t M, const void* x
  * are not written. MOE_ERR_UNSUPPORTED for M > 16, H > 8192, a plan with a
  * shared expert or shared slot, the tensor-parallel exchange, the MXFP4 mid or
  * a declared layout other than MOE_LAYOUT_W13_PACKED; other errors as
- * moe_forward. Weights must be finite (scale bytes up to 252). */
+ * moe_forward, but for MOE_ERR_HIP, after which the workspace stays bound (a
+ * call forms all that it reads there). Weights must be finite (scale bytes up to
+ * 252). */
 moe_status moe_layer_forward(moe_plan* plan, const moe_router* router, int64_t M, const void* x, const void* w13,
                              const void* s13, const void* w2, const void* s2, void* out, void* stream);
 
