@@ -427,6 +427,131 @@ moe_status moe_linear_forward(const moe_linear* linear, int64_t M, const void* x
 moe_status moe_layer_forward(moe_plan* plan, const moe_router* router, int64_t M, const void* x, const void* w13,
                              const void* s13, const void* w2, const void* s2, void* out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Layers in 16 bits and the output head. The parts of a model around the experts
+ * that stay in 16 bits: dense products, the gated block of the dense layers, and
+ * what reads the head's logits, with the gradients that train them.
+ *
+ * `workspace` of these calls is caller-owned device memory, 256-byte aligned, of
+ * at least the handle's workspace bytes for the call's M (its contents need not
+ * be kept between calls; NULL where none are needed). Handles hold no mutable
+ * state; calls that may overlap (other streams, captured graphs replayed side by
+ * side) need workspaces of their own. MOE_ERR_WORKSPACE for a workspace that is
+ * missing, short or misaligned.
+ *
+ * Activations. gelu is z Phi(z), Phi the normal distribution function; gelu_tanh
+ * is z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; silu is z / (1 + exp(-z));
+ * relu's slope at 0 is 0. */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4 } moe_activation;
+
+/* Matrix product with bias, activation and residual in its epilogue:
+ *   z = x w^T (+ bias),  y = act(z) (+ residual)
+ * products exact, summed in fp32, y rounded once. `type` (MOE_BF16 or MOE_FP16)
+ * is that of x, w and bias.
+ *   w [N, K] dense and bias [N] (or NULL) are kept by the handle, not copied: an
+ *   optimizer may update them in place between calls.
+ * moe_dense_forward: x [M, K], rows ldx apart (ldx >= K); y [M, N], rows ldy >= N
+ * apart, of x's type or MOE_FP32 (y_type); residual [M, N] of y's type or NULL;
+ * it may be y itself (same pointer and stride). `pre`, or NULL: z [M, N] rounded
+ * to x's type, rows ldp >= N apart, for moe_dense_backward.
+ * moe_dense_backward, of y for the upstream gradient dy [M, N] of x's type (the
+ * residual's gradient is dy itself):
+ *   dz = dy act'(pre), dx = dz w, dw = dz^T x, dbias = sum over rows of dz
+ * dx [M, K], rows lddx apart, dw [N, K] and dbias [N] dense, all of x's type; each
+ * may be NULL where it is not wanted, not all. `pre` is what the forward call
+ * saved, ignored without an activation (may be NULL then). Without an activation
+ * dz is dy; with one it is rounded to x's type before the two products (their
+ * operands have 16 bits), not for dbias. M = 0 writes zeros to dw and dbias.
+ * Rows of 16-bit matrices that products read (x; w) start on 16 bytes: K and ldx
+ * multiples of 8, K up to 65536, ldx up to 2^22 elements; N any up to 2^22; dy,
+ * pre, residual, y and dx aligned to their elements, rows up to 2^40 apart.
+ * moe_dense_workspace_bytes: for moe_dense_forward (train = 0) or for both (1).
+ * Errors as the linear layer's. */
+typedef struct moe_dense moe_dense;
+moe_status moe_dense_create(int64_t N, int64_t K, int type, const void* w, const void* bias, int activation,
+                            int64_t max_M, moe_dense** out);
+void moe_dense_destroy(moe_dense* dense);
+moe_status moe_dense_workspace_bytes(const moe_dense* dense, int64_t M, int train, size_t* bytes);
+moe_status moe_dense_forward(const moe_dense* dense, int64_t M, const void* x, int64_t ldx, const void* residual,
+                             int64_t ldr, void* y, int64_t ldy, int y_type, void* pre, int64_t ldp, void* workspace,
+                             size_t workspace_bytes, void* stream);
+moe_status moe_dense_backward(const moe_dense* dense, int64_t M, const void* dy, int64_t lddy, const void* pre,
+                              int64_t ldp, const void* x, int64_t ldx, void* dx, int64_t lddx, void* dw, void* dbias,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gated feed-forward block: both projections, the activation and the product,
+ *   [g u] = x w13^T,  h = act(g) u
+ * w13 [2I, H] dense, rows [0, I) gate, [I, 2I) up (as the experts'), kept by the
+ * handle, not copied; act any but MOE_ACT_NONE. x [M, H], rows ldx apart; h [M, I],
+ * rows ldh >= I apart, of x's type, rounded once from fp32 g and u. `pre`, or
+ * NULL: [M, 2I] dense, g and u rounded to x's type, for moe_gated_backward:
+ *   dg = dh u act'(g), du = dh act(g), dx = [dg du] w13, dw13 = [dg du]^T x
+ * dg and du rounded to x's type before the products. dx [M, H], rows lddx apart,
+ * dw13 [2I, H] dense, of x's type; one of them may be NULL. Sizes, alignment,
+ * M = 0, workspace and errors as moe_dense (H for K; I up to 2^21). */
+typedef struct moe_gated moe_gated;
+moe_status moe_gated_create(int64_t I, int64_t H, int type, const void* w13, int activation, int64_t max_M,
+                            moe_gated** out);
+void moe_gated_destroy(moe_gated* gated);
+moe_status moe_gated_workspace_bytes(const moe_gated* gated, int64_t M, int train, size_t* bytes);
+moe_status moe_gated_forward(const moe_gated* gated, int64_t M, const void* x, int64_t ldx, void* h, int64_t ldh,
+                             void* pre, void* workspace, size_t workspace_bytes, void* stream);
+moe_status moe_gated_backward(const moe_gated* gated, int64_t M, const void* dh, int64_t lddh, const void* pre,
+                              const void* x, int64_t ldx, void* dx, int64_t lddx, void* dw13, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Scores of given tokens from the head's logits z [M, V] (bf16, fp16 or fp32,
+ * rows ldz >= V elements apart, at most 2^40, aligned to their elements):
+ *   lse = log sum_v exp(z_v), logprobs = z_token - lse, entropy = -sum_v q_v log q_v
+ *   (q = exp(z - lse); a token of z = -inf takes no part), and the row's top_k
+ *   largest logits in falling order, equal ones by rising id: top_logprobs [M, k]
+ *   (z - lse) and top_ids int32 [M, k]; all other outputs fp32 [M], dense.
+ * tokens int32 [M]; a token outside [0, V) has the log probability NaN. tokens and
+ * logprobs both or neither NULL; entropy and lse may be NULL; top_logprobs and
+ * top_ids are NULL exactly if top_k is 0. A row that holds a NaN or +inf, or
+ * nothing but -inf, has NaN for all its scores (lse is NaN, +inf or -inf); its
+ * top_ids are some ids in [0, V).
+ * top_k 0 .. 64 and up to V, V up to 2^24, max_M up to 2^20. The handle belongs to
+ * the current device. Sums in fp32 and float64. Errors as the router's. */
+typedef struct moe_scores moe_scores;
+moe_status moe_scores_create(int64_t V, int64_t top_k, int type, int64_t max_M, moe_scores** out);
+void moe_scores_destroy(moe_scores* scores);
+moe_status moe_scores_workspace_bytes(const moe_scores* scores, int64_t M, size_t* bytes);
+moe_status moe_scores_forward(const moe_scores* scores, int64_t M, const void* z, int64_t ldz, const int32_t* tokens,
+                              float* logprobs, float* entropy, float* lse, float* top_logprobs, int32_t* top_ids,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Distillation from a teacher's top logits. Of row m, the teacher gives k logits
+ * (or log probabilities: only their differences count) t [M, k] fp32 at tokens ids
+ * int32 [M, k]; a slot whose id is outside [0, V) is empty. With temperature T,
+ * p the softmax of t/T over the row's filled slots and q that of z/T over all V:
+ *   loss = sum_j p_j (log p_j - log q_ids[j])                     fp32 [M]
+ *   dz   = weight/T (q - sum_j p_j [v = ids_j])                    [M, V]
+ * weight fp32 [M] is the gradient of the rows' losses. A token in two slots has
+ * the sum of both. A row without a filled slot (padding) has loss 0 and gradient
+ * 0, whatever its logits and weight; one whose logits hold a NaN or +inf, or nothing
+ * but -inf, NaN. A slot of t = -inf has p 0 and takes no part in the loss.
+ * moe_distill_forward writes loss and lse (fp32 [M], log sum exp(z/T), for the
+ * backward call; may be NULL); moe_distill_backward reads it;
+ * moe_distill_forward_backward does both at once, for weights known beforehand
+ * (1/rows, say). dz of type grad_type: z's own, MOE_BF16 or MOE_FP16, rows lddz
+ * apart; it may be z itself (same pointer, stride and type). k 1 .. 64, T finite
+ * and > 0; sizes, strides and errors as moe_scores (dz as z). */
+typedef struct moe_distill moe_distill;
+moe_status moe_distill_create(int64_t V, int64_t k, int type, int grad_type, float temperature, int64_t max_M,
+                              moe_distill** out);
+void moe_distill_destroy(moe_distill* distill);
+moe_status moe_distill_workspace_bytes(const moe_distill* distill, int64_t M, size_t* bytes);
+moe_status moe_distill_forward(const moe_distill* distill, int64_t M, const void* z, int64_t ldz, const int32_t* ids,
+                               const float* t, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream);
+moe_status moe_distill_backward(const moe_distill* distill, int64_t M, const void* z, int64_t ldz, const int32_t* ids,
+                                const float* t, const float* lse, const float* weight, void* dz, int64_t lddz,
+                                void* stream);
+moe_status moe_distill_forward_backward(const moe_distill* distill, int64_t M, const void* z, int64_t ldz,
+                                        const int32_t* ids, const float* t, const float* weight, float* loss, void* dz,
+                                        int64_t lddz, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Profiling aid: when `events` is non-NULL, a call (moe_forward,
  * moe_forward_noalloc or moe_layer_forward, whose stages are route: the router,
  * gate_up: with the top-k, and down: with the combine) brackets stage i

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "lib
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE, MOE_ERR_HIP = range(6)
 MID_E4M3, MID_MXFP4 = 0, 1  # moe_mid_format
 BF16, FP16, FP32 = range(3)  # moe_dtype
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # moe_activation
 LAYOUT_W13_PACKED, LAYOUT_W2_PACKED = 1, 2  # moe_weight_layout flags
 
 
@@ -131,6 +132,29 @@ def lib() -> ctypes.CDLL:
     L.moe_linear_forward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, ctypes.c_int, vp]
     L.moe_layer_forward.restype = st
     L.moe_layer_forward.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+    sz, psz, ph, ci, cf = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(vp), ctypes.c_int, ctypes.c_float
+    for name, args in {
+        "moe_dense_create": [i64, i64, ci, vp, vp, ci, i64, ph],
+        "moe_dense_workspace_bytes": [vp, i64, ci, psz],
+        "moe_dense_forward": [vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, i64, vp, sz, vp],
+        "moe_dense_backward": [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, sz, vp],
+        "moe_gated_create": [i64, i64, ci, vp, ci, i64, ph],
+        "moe_gated_workspace_bytes": [vp, i64, ci, psz],
+        "moe_gated_forward": [vp, i64, vp, i64, vp, i64, vp, vp, sz, vp],
+        "moe_gated_backward": [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, sz, vp],
+        "moe_scores_create": [i64, i64, ci, i64, ph],
+        "moe_scores_workspace_bytes": [vp, i64, psz],
+        "moe_scores_forward": [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "moe_distill_create": [i64, i64, ci, ci, cf, i64, ph],
+        "moe_distill_workspace_bytes": [vp, i64, psz],
+        "moe_distill_forward": [vp, i64, vp, i64, vp, vp, vp, vp, vp, sz, vp],
+        "moe_distill_backward": [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp],
+        "moe_distill_forward_backward": [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp],
+    }.items():
+        f = getattr(L, name)
+        f.restype, f.argtypes = st, args
+    for f in (L.moe_dense_destroy, L.moe_gated_destroy, L.moe_scores_destroy, L.moe_distill_destroy):
+        f.restype, f.argtypes = None, [vp]
     L.moe_plan_set_tp_exchange.restype = st
     L.moe_plan_set_tp_exchange.argtypes = [vp, ctypes.POINTER(moe_tp_exchange)]
     _lib = L
@@ -377,6 +401,288 @@ class Linear(_Handle):
         if st != MOE_OK:
             raise MoeError(st, "moe_linear_forward")
         return out
+
+
+class _Sized(_Handle):
+    """A handle whose calls may take a workspace: a uint8 tensor of at least
+    workspace_bytes(M), the caller's; calls that may overlap need one each."""
+
+    def _create(self, name, *args):
+        h = ctypes.c_void_p()
+        st = getattr(lib(), name)(*args, ctypes.byref(h))
+        if st != MOE_OK:
+            raise MoeError(st, name)
+        self._h = h
+
+    def _bytes(self, name, *args):
+        n = ctypes.c_size_t(0)
+        st = getattr(lib(), name)(self._h, *args, ctypes.byref(n))
+        if st != MOE_OK:
+            raise MoeError(st, name)
+        return n.value
+
+    def _call(self, name, *args):
+        st = getattr(lib(), name)(self._h, *args)
+        if st != MOE_OK:
+            raise MoeError(st, name)
+
+    def _workspace(self, t):
+        """(pointer, bytes) of a workspace tensor or None."""
+        if t is None:
+            return None, 0
+        import torch
+
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {self.device}")
+        return t.data_ptr(), t.numel()
+
+    def _vector(self, name, t, dtype, n):
+        """Pointer of a dense vector of at least n elements."""
+        import torch
+
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.dtype is not dtype or t.dim() != 1 or t.shape[0] < n or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} elements on {self.device}")
+        return t.data_ptr()
+
+
+def _weight(name, w, rows_even=False):
+    import torch
+
+    if (not isinstance(w, torch.Tensor) or w.dim() != 2 or not w.is_contiguous()
+            or w.dtype not in (torch.bfloat16, torch.float16) or (rows_even and w.shape[0] % 2)):
+        raise ValueError(f"{name} must be a contiguous 2-d bfloat16 or float16 tensor" + (" of 2 I rows" if rows_even else ""))
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation {name!r} is none of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+class Dense(_Sized):
+    """Matrix product on 16-bit weights w [N, K] with bias [N], activation and
+    residual in its epilogue, and its backward pass. w and bias are kept by
+    reference: an optimizer may update them in place."""
+
+    _destroy = "moe_dense_destroy"
+
+    def __init__(self, w, bias=None, activation: str = "none", max_M: int = 1 << 20):
+        _weight("w", w)
+        act = _activation(activation)
+        self.N, self.K = w.shape
+        if bias is not None and (bias.dtype != w.dtype or tuple(bias.shape) != (self.N,) or bias.device != w.device
+                                 or not bias.is_contiguous()):
+            raise ValueError("bias must be a contiguous [N] tensor of w's type beside it")
+        self.w, self.bias, self.dtype, self.device, self.max_M = w, bias, w.dtype, w.device, int(max_M)
+        self.activation, self._code = activation, _dtype_code(w.dtype)
+        self._create("moe_dense_create", self.N, self.K, self._code, _ptr(w), None if bias is None else _ptr(bias), act,
+                     self.max_M)
+
+    def workspace_bytes(self, M: int, train: bool = False) -> int:
+        """Workspace of forward, with `train` of backward too, for M rows."""
+        return self._bytes("moe_dense_workspace_bytes", int(M), int(bool(train)))
+
+    def forward(self, x, out, residual=None, pre=None, workspace=None, M: Optional[int] = None, stream=None):
+        """out[:M] = act(x[:M] w^T + bias) (+ residual[:M]); out is of x's type or
+        float32, residual of out's, and may be out itself. `pre` [M, N] of x's type
+        takes the activation's argument, for backward."""
+        import torch
+
+        M = self._rows(x, M)
+        ldx = self._check("x", x, self.dtype, M, self.K)
+        wide = getattr(out, "dtype", None) is torch.float32
+        y_dtype = torch.float32 if wide else self.dtype
+        ldy = self._check("out", out, y_dtype, M, self.N)
+        ldr = 0 if residual is None else self._check("residual", residual, y_dtype, M, self.N)
+        ldp = 0 if pre is None else self._check("pre", pre, self.dtype, M, self.N)
+        ws, nws = self._workspace(workspace)
+        self._call("moe_dense_forward", M, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
+                   out.data_ptr(), ldy, FP32 if wide else self._code, None if pre is None else pre.data_ptr(), ldp, ws, nws,
+                   self._stream(stream))
+        return out
+
+    def backward(self, dy, x, dx=None, dw=None, dbias=None, pre=None, workspace=None, M: Optional[int] = None, stream=None):
+        """The gradients of x into dx[:M], of w into dw and of the bias into dbias
+        (each may be None), for dy[:M] = the gradient of forward's out (in w's type);
+        `pre` is what forward saved, needed with an activation."""
+        M = self._rows(dy, M)
+        lddy = self._check("dy", dy, self.dtype, M, self.N)
+        ldx = self._check("x", x, self.dtype, M, self.K)
+        ldp = lddx = 0
+        if self.activation != "none":
+            if pre is None:
+                raise ValueError("backward through an activation needs pre")
+            ldp = self._check("pre", pre, self.dtype, M, self.N)
+        else:
+            pre = None
+        if dx is not None:
+            lddx = self._check("dx", dx, self.dtype, M, self.K)
+        if dw is not None:
+            self._check("dw", dw, self.dtype, self.N, self.K, dense=True)
+        ws, nws = self._workspace(workspace)
+        self._call("moe_dense_backward", M, dy.data_ptr(), lddy, None if pre is None else pre.data_ptr(), ldp, x.data_ptr(),
+                   ldx, None if dx is None else dx.data_ptr(), lddx, None if dw is None else dw.data_ptr(),
+                   None if dbias is None else self._vector("dbias", dbias, self.dtype, self.N), ws, nws,
+                   self._stream(stream))
+
+
+class Gated(_Sized):
+    """Gated feed-forward block on 16-bit weights w13 [2I, H] (rows [0, I) gate, [I,
+    2I) up): h = act(x Wg^T) * (x Wu^T), and its backward pass. w13 is kept by reference."""
+
+    _destroy = "moe_gated_destroy"
+
+    def __init__(self, w13, activation: str = "silu", max_M: int = 1 << 20):
+        _weight("w13", w13, rows_even=True)
+        act = _activation(activation)
+        self.I, self.H = w13.shape[0] // 2, w13.shape[1]
+        self.w13, self.dtype, self.device, self.max_M = w13, w13.dtype, w13.device, int(max_M)
+        self.activation = activation
+        self._create("moe_gated_create", self.I, self.H, _dtype_code(w13.dtype), _ptr(w13), act, self.max_M)
+
+    def workspace_bytes(self, M: int, train: bool = False) -> int:
+        """Workspace of forward, with `train` of backward too, for M rows."""
+        return self._bytes("moe_gated_workspace_bytes", int(M), int(bool(train)))
+
+    def forward(self, x, out, pre=None, workspace=None, M: Optional[int] = None, stream=None):
+        """out[:M] [M, I]; `pre` [M, 2I] (contiguous) takes [g u], for backward."""
+        M = self._rows(x, M)
+        ldx = self._check("x", x, self.dtype, M, self.H)
+        ldh = self._check("out", out, self.dtype, M, self.I)
+        if pre is not None:
+            self._check("pre", pre, self.dtype, M, 2 * self.I, dense=True)
+        ws, nws = self._workspace(workspace)
+        self._call("moe_gated_forward", M, x.data_ptr(), ldx, out.data_ptr(), ldh, None if pre is None else pre.data_ptr(), ws,
+                   nws, self._stream(stream))
+        return out
+
+    def backward(self, dh, x, pre, dx=None, dw=None, workspace=None, M: Optional[int] = None, stream=None):
+        """The gradients of x into dx[:M] and of w13 into dw (one may be None), for
+        dh[:M] = the gradient of forward's out, `pre` what forward saved."""
+        M = self._rows(dh, M)
+        lddh = self._check("dh", dh, self.dtype, M, self.I)
+        ldx = self._check("x", x, self.dtype, M, self.H)
+        self._check("pre", pre, self.dtype, M, 2 * self.I, dense=True)
+        lddx = 0 if dx is None else self._check("dx", dx, self.dtype, M, self.H)
+        if dw is not None:
+            self._check("dw", dw, self.dtype, 2 * self.I, self.H, dense=True)
+        ws, nws = self._workspace(workspace)
+        self._call("moe_gated_backward", M, dh.data_ptr(), lddh, pre.data_ptr(), x.data_ptr(), ldx,
+                   None if dx is None else dx.data_ptr(), lddx, None if dw is None else dw.data_ptr(), ws, nws,
+                   self._stream(stream))
+
+
+class _Head(_Sized):
+    """What TokenScores and Distill share: logits [M, V] of one type on one device."""
+
+    def _init(self, V, dtype, device, max_M):
+        import torch
+
+        self.V, self.max_M = int(V), int(max_M)
+        self.dtype = torch.float32 if dtype is None else dtype
+        device = torch.device("cuda") if device is None else torch.device(device)
+        if device.type == "cuda" and device.index is None and torch.cuda.is_available():
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device, self._i32, self._fp32 = device, torch.int32, torch.float32
+
+    def _create_here(self, name, *args):
+        import torch
+
+        if self.device.type == "cuda" and torch.cuda.is_available():
+            with torch.cuda.device(self.device):
+                return self._create(name, *args)
+        return self._create(name, *args)
+
+    def _out(self, name, t, M, dtype=None):
+        return None if t is None else self._vector(name, t, dtype or self._fp32, M)
+
+
+class TokenScores(_Head):
+    """Scores of given tokens from logits [M, V] of `dtype`: their log probabilities,
+    the rows' entropies and top_k largest alternatives."""
+
+    _destroy = "moe_scores_destroy"
+
+    def __init__(self, V: int, top_k: int = 0, dtype=None, device=None, max_M: int = 1 << 20):
+        self._init(V, dtype, device, max_M)
+        self.top_k = int(top_k)
+        self._create_here("moe_scores_create", self.V, self.top_k, _dtype_code(self.dtype), self.max_M)
+
+    def workspace_bytes(self, M: int) -> int:
+        return self._bytes("moe_scores_workspace_bytes", int(M))
+
+    def forward(self, logits, tokens, logprobs, entropy=None, lse=None, top_logprobs=None, top_ids=None, workspace=None,
+                M: Optional[int] = None, stream=None):
+        """tokens (int32 [M]) to their logprobs [M], float32; entropy and lse [M] where
+        given; top_logprobs and top_ids (int32) [M, top_k], equal logits by rising id.
+        tokens and logprobs may both be None."""
+        M = self._rows(logits, M)
+        ldz = self._check("logits", logits, self.dtype, M, self.V)
+        if self.top_k and (top_logprobs is None or top_ids is None):
+            raise ValueError("top_logprobs and top_ids are needed with top_k above 0")
+        tp = ti = None
+        if self.top_k:
+            self._check("top_logprobs", top_logprobs, self._fp32, M, self.top_k, dense=True)
+            self._check("top_ids", top_ids, self._i32, M, self.top_k, dense=True)
+            tp, ti = top_logprobs.data_ptr(), top_ids.data_ptr()
+        ws, nws = self._workspace(workspace)
+        self._call("moe_scores_forward", M, logits.data_ptr(), ldz, self._out("tokens", tokens, M, self._i32),
+                   self._out("logprobs", logprobs, M), self._out("entropy", entropy, M), self._out("lse", lse, M), tp, ti, ws,
+                   nws, self._stream(stream))
+        return logprobs
+
+
+class Distill(_Head):
+    """Distillation of logits [M, V] from a teacher's k logits a row (t [M, k] float32 at
+    tokens ids [M, k] int32, a negative id an empty slot) at a temperature."""
+
+    _destroy = "moe_distill_destroy"
+
+    def __init__(self, V: int, k: int, dtype=None, grad_dtype=None, temperature: float = 1.0, device=None,
+                 max_M: int = 1 << 20):
+        self._init(V, dtype, device, max_M)
+        self.k, self.temperature = int(k), float(temperature)
+        self.grad_dtype = self.dtype if grad_dtype is None else grad_dtype
+        self._create_here("moe_distill_create", self.V, self.k, _dtype_code(self.dtype), _dtype_code(self.grad_dtype),
+                          self.temperature, self.max_M)
+
+    def workspace_bytes(self, M: int) -> int:
+        return self._bytes("moe_distill_workspace_bytes", int(M))
+
+    def _inputs(self, logits, ids, t, M):
+        M = self._rows(logits, M)
+        ldz = self._check("logits", logits, self.dtype, M, self.V)
+        self._check("ids", ids, self._i32, M, self.k, dense=True)
+        self._check("t", t, self._fp32, M, self.k, dense=True)
+        return M, (logits.data_ptr(), ldz, ids.data_ptr(), t.data_ptr())
+
+    def forward(self, logits, ids, t, loss, lse=None, workspace=None, M: Optional[int] = None, stream=None):
+        """The rows' losses [M], and lse [M] for backward, float32."""
+        M, args = self._inputs(logits, ids, t, M)
+        ws, nws = self._workspace(workspace)
+        self._call("moe_distill_forward", M, *args, self._vector("loss", loss, self._fp32, M), self._out("lse", lse, M), ws,
+                   nws, self._stream(stream))
+        return loss
+
+    def backward(self, logits, ids, t, lse, weight, grad, M: Optional[int] = None, stream=None):
+        """The logits' gradient into grad[:M] (may be logits itself), for weight [M] =
+        the gradient of the rows' losses, lse what forward wrote."""
+        M, args = self._inputs(logits, ids, t, M)
+        ldg = self._check("grad", grad, self.grad_dtype, M, self.V)
+        self._call("moe_distill_backward", M, *args, self._vector("lse", lse, self._fp32, M),
+                   self._vector("weight", weight, self._fp32, M), grad.data_ptr(), ldg, self._stream(stream))
+        return grad
+
+    def forward_backward(self, logits, ids, t, weight, loss, grad, workspace=None, M: Optional[int] = None, stream=None):
+        """Losses and gradient at once, for weights known beforehand."""
+        M, args = self._inputs(logits, ids, t, M)
+        ldg = self._check("grad", grad, self.grad_dtype, M, self.V)
+        ws, nws = self._workspace(workspace)
+        self._call("moe_distill_forward_backward", M, *args, self._vector("weight", weight, self._fp32, M),
+                   self._vector("loss", loss, self._fp32, M), grad.data_ptr(), ldg, ws, nws, self._stream(stream))
+        return loss
 
 
 class Plan:

@@ -1,8 +1,6 @@
 // C ABI of the operators beside the routed-MoE call: the router, the MXFP4
 // linear layer and the few-token MoE layer. Validation only; nothing here
 // allocates device memory or synchronizes a stream.
-#include <string.h>
-
 #include <new>
 
 #include "api_util.h"
@@ -12,34 +10,6 @@
 using namespace qmoe;
 
 namespace {
-
-constexpr int64_t kMaxRows = (int64_t)1 << 20;
-constexpr int64_t kMaxStride = (int64_t)1 << 40;  // elements between rows: kMaxRows of them stay below 2^63 bytes
-
-bool type16(int t) { return t == MOE_BF16 || t == MOE_FP16; }
-size_t type_bytes(int t) { return t == MOE_FP32 ? 4 : 2; }
-
-// Bytes from a [rows, cols] tensor's first element to behind its last.
-size_t span(int64_t rows, int64_t ld, int64_t cols, size_t elem) {
-  return rows > 0 ? ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * elem : 0;
-}
-
-// The device of gfx950 pointers `ptrs`, all on one: MOE_OK and *dev, *cus.
-moe_status device_of(const void* const* ptrs, int n, int* dev, int* cus) {
-  const int d = ptr_device(ptrs[0]);
-  if (d < 0) return MOE_ERR_DEVICE;
-  for (int i = 1; i < n; ++i)
-    if (ptrs[i] && ptr_device(ptrs[i]) != d) return MOE_ERR_DEVICE;
-  hipDeviceProp_t prop;
-  if (hipGetDeviceProperties(&prop, d) != hipSuccess) {
-    (void)hipGetLastError();
-    return MOE_ERR_DEVICE;
-  }
-  if (strncmp(prop.gcnArchName, "gfx950", 6) != 0) return MOE_ERR_DEVICE;
-  *dev = d;
-  *cus = prop.multiProcessorCount > 0 ? prop.multiProcessorCount : 256;
-  return MOE_OK;
-}
 
 moe_status check_linear_shape(int64_t N, int64_t K) {
   if (N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
