@@ -41,6 +41,7 @@ struct GemmArgs {
   void* pre;
   int64_t ldr, ldy, ldp;
   int act, y_type;
+  int vec;  // set by launch_gemm: which of the matrices move in 16-byte pieces
   // workspace of split sums
   void* ws;
   size_t ws_bytes;

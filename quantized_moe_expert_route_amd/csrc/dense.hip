@@ -7,21 +7,9 @@
 // and summed there by the MFMA, whose operand of a lane is 8 elements along K.
 #include <algorithm>
 
-#include "act.h"
-#include "dense.h"
-#include "mxfp4.h"
+#include "gemm_tile.h"
 
 namespace qmoe {
-
-template <bool F16>
-__device__ __forceinline__ v4f mfma16(uint4 a, uint4 b, v4f c) {
-  if constexpr (F16) return mfma_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c);
-  else return mfma_bf16(__builtin_bit_cast(v8s, a), __builtin_bit_cast(v8s, b), c);
-}
-template <bool F16>
-__device__ __forceinline__ float value16(uint16_t b) { return F16 ? fp16_value(b) : bf16_value(b); }
-template <bool F16>
-__device__ __forceinline__ uint16_t bits16(float v) { return F16 ? fp16_bits(v) : bf16_bits(v); }
 
 // One element of C into y (and pre).
 template <bool F16, GemmKind KIND>
@@ -95,13 +83,24 @@ static hipError_t simple(const GemmArgs& a, hipStream_t stream) {
 
 size_t gemm_ws_bytes(GemmKind, int64_t, int64_t, int64_t, int, int) { return 0; }
 
-hipError_t launch_gemm(GemmKind kind, const GemmArgs& a, int, hipStream_t stream) {
+template <bool F16, GemmKind KIND>
+static hipError_t launch(const GemmArgs& a, hipStream_t stream) {
+  if (a.rows <= 64) return simple<F16, KIND>(a, stream);
+  return launch_tile<F16, KIND, 8, 4, 2, 4>(a, stream);
+}
+
+hipError_t launch_gemm(GemmKind kind, const GemmArgs& args, int, hipStream_t stream) {
+  GemmArgs a = args;
+  const int64_t es = a.y_type == MOE_FP32 ? 4 : 2;
+  auto vec = [](const void* p, int64_t ld, int64_t elem) { return p && ((uintptr_t)p & 15) == 0 && ld * elem % 16 == 0; };
+  a.vec = (vec(a.y, a.ldy, es) ? kVecY : 0) | (vec(a.residual, a.ldr, es) ? kVecResidual : 0) |
+          (vec(a.pre, a.ldp, 2) && (kind != kGemmGated || a.cols % 8 == 0) ? kVecPre : 0) | (vec(a.bias, 0, 2) ? kVecBias : 0);
   const bool f16 = a.type == MOE_FP16;
   switch (kind) {
-    case kGemmForward: return f16 ? simple<true, kGemmForward>(a, stream) : simple<false, kGemmForward>(a, stream);
-    case kGemmGated: return f16 ? simple<true, kGemmGated>(a, stream) : simple<false, kGemmGated>(a, stream);
-    case kGemmInput: return f16 ? simple<true, kGemmInput>(a, stream) : simple<false, kGemmInput>(a, stream);
-    default: return f16 ? simple<true, kGemmWeight>(a, stream) : simple<false, kGemmWeight>(a, stream);
+    case kGemmForward: return f16 ? launch<true, kGemmForward>(a, stream) : launch<false, kGemmForward>(a, stream);
+    case kGemmGated: return f16 ? launch<true, kGemmGated>(a, stream) : launch<false, kGemmGated>(a, stream);
+    case kGemmInput: return f16 ? launch<true, kGemmInput>(a, stream) : launch<false, kGemmInput>(a, stream);
+    default: return f16 ? launch<true, kGemmWeight>(a, stream) : launch<false, kGemmWeight>(a, stream);
   }
 }
 

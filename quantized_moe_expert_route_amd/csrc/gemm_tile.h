@@ -1,0 +1,363 @@
+// Tiles of C [rows, cols] = A B^T of 16-bit operands: staging, fragments, the main
+// loop and the epilogue, for operands that lie along K or across it.
+//
+// A workgroup of WM x WN waves computes BM = 16 TM WM rows by BN = 16 TN WN columns,
+// a wave 16 TM x 16 TN of them, in K-steps of 64 from two buffers of LDS. Memory goes
+// straight to LDS (16 bytes a lane, 1 KB an instruction, in LDS in lane order), so
+// the tile's way through LDS needs no registers and what lies past a matrix's edge
+// comes as zeros from the buffer's bound.
+//
+// LDS of an operand of R rows (or columns) and 64 k:
+//  along K:  [R][64], 128-byte rows of eight 16-byte chunks; chunk c of row r lies at
+//            c ^ (r >> 1 & 7): the 16 lanes that read a chunk column meet all banks.
+//            A lane's MFMA operand, 8 k of its row, is one 16-byte read.
+//  across K: [64][R]; the lane's 8 k come by two transposing reads, of which 16 lanes
+//            take 4 k by 16 rows (32 bytes a k). The 32-byte blocks of k are exchanged
+//            by the bits of k that tell apart the 8 k a half wave reads at a time.
+#pragma once
+
+#include <type_traits>
+
+#include "act.h"
+#include "dense.h"
+#include "mxfp4.h"
+
+namespace qmoe {
+
+template <bool F16>
+__device__ __forceinline__ v4f mfma16(uint4 a, uint4 b, v4f c) {
+  if constexpr (F16) return mfma_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c);
+  else return mfma_bf16(__builtin_bit_cast(v8s, a), __builtin_bit_cast(v8s, b), c);
+}
+template <bool F16>
+__device__ __forceinline__ float value16(uint16_t b) { return F16 ? fp16_value(b) : bf16_value(b); }
+template <bool F16>
+__device__ __forceinline__ uint16_t bits16(float v) { return F16 ? fp16_bits(v) : bf16_bits(v); }
+
+// ----------------------------------------------------------------- memory to LDS
+constexpr uint32_t kOutside = 0x80000000u;  // an offset past every buffer's bound
+
+// Buffer descriptor of 2^31 bytes from p on (raw, 32-bit elements).
+__device__ __forceinline__ v4i buffer_at(const void* p) {
+  const uint64_t u = (uint64_t)p;
+  return v4i{(int)__builtin_amdgcn_readfirstlane((uint32_t)u),
+             (int)(__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) & 0xFFFF), (int)kOutside, 0x00020000};
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// 16 bytes a lane from `offset` to LDS at `lds` + 16 lane; zeros where the offset is
+// kOutside. In assembly, so that the compiler does not wait for it before every
+// read of LDS: wait_and_barrier does that. No register is written.
+__device__ __forceinline__ void load_lds16(v4i buffer, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(offset), "s"(buffer)
+               : "memory");
+}
+
+// All but the N newest of the wave's loads to LDS have arrived, its reads of LDS too; then the
+// workgroup's barrier.
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+// ----------------------------------------------------------------- an operand's tile
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+template <bool BY_K, int R, int W>
+struct Operand {
+  static constexpr int kBytes = R * 128;
+  static constexpr int kLoads = R / 8 / W;  // load instructions a wave
+  static_assert(R % (8 * W) == 0, "whole loads");
+  static_assert(!BY_K || R % 64 == 0, "whole groups of blocks");
+  uint32_t off[kLoads];
+  int left[kLoads];  // K from this lane's piece on, at the start
+
+  // across K: how the 32-byte blocks of row k are exchanged
+  static __device__ __forceinline__ int swap(int k) {
+    if constexpr (R % 128 == 0) return (k & 3) | ((k >> 3 & 1) << 2);
+    else return (k >> 1 & 1) | ((k >> 3 & 1) << 1);  // rows of an odd multiple of 128 bytes: k & 1 is another half of the banks
+  }
+
+  // rows: how many of the tile's rows the matrix has
+  __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int64_t rows) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int piece = (i * W + wave) * 64 + lane;
+      if constexpr (BY_K) {
+        const int k = piece / (R / 8), at = piece % (R / 8);
+        const int col = (((at >> 1) ^ swap(k)) << 1 | (at & 1)) * 8;
+        off[i] = col < rows ? (uint32_t)(k * ld * 2 + col * 2) : kOutside;
+        left[i] = -k;
+      } else {
+        const int row = piece >> 3, chunk = (piece & 7) ^ (row >> 1 & 7);
+        off[i] = row < rows ? (uint32_t)(row * ld * 2 + chunk * 16) : kOutside;
+        left[i] = -8 * chunk;
+      }
+    }
+  }
+  // the tile's last step, with `k` of K left: what is past them comes as zeros
+  __device__ __forceinline__ void last(int k) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (left[i] + k <= 0) off[i] = kOutside;
+  }
+  // second: buffer of the rows from R / 2 on (gated: the other half of B's rows)
+  __device__ __forceinline__ void load(v4i buffer, v4i second, uint32_t lds, int wave) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      load_lds16(!BY_K && i * W + wave >= R / 16 ? second : buffer, off[i], lds + (uint32_t)(i * W + wave) * 1024);
+  }
+
+  // MFMA operand of K 32 j .. + 31 of the tile's row block b (16 rows)
+  static __device__ __forceinline__ uint4 fragment(const uint8_t* lds, int b, int j, int r, int g) {
+    if constexpr (BY_K) {
+      const int k = 32 * j + 8 * g + (r >> 2);
+      const uint8_t* p = lds + k * (2 * R) + ((b ^ swap(8 * g + (r >> 2))) * 32) + (r & 3) * 8;
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)p);
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * 2 * R));
+      const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
+      return make_uint4(l.x, l.y, h.x, h.y);
+    } else {
+      return ld16(lds + (16 * b + r) * 128 + (((4 * j + g) ^ (r >> 1)) * 16));
+    }
+  }
+};
+
+// ----------------------------------------------------------------- epilogue
+// What of a call's matrices moves in 16-byte pieces along a row.
+enum { kVecY = 1, kVecResidual = 2, kVecPre = 4, kVecBias = 8 };
+
+// Up to 8 values at p, of 16 bits (WIDE: of 32).
+template <bool F16, bool WIDE>
+__device__ __forceinline__ void read8(const void* p, bool vec, int n, float (&v)[8]) {
+  if constexpr (WIDE) {
+    const float* f = reinterpret_cast<const float*>(p);
+    if (vec && n == 8) {
+      *reinterpret_cast<v4f*>(v) = *reinterpret_cast<const v4f*>(f);
+      *reinterpret_cast<v4f*>(v + 4) = *reinterpret_cast<const v4f*>(f + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < n ? f[i] : 0.f;
+    }
+  } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    union {
+      uint4 q;
+      uint16_t b[8];
+    } w;
+    if (vec && n == 8) {
+      w.q = ld16(h);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w.b[i] = i < n ? h[i] : (uint16_t)0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = value16<F16>(w.b[i]);
+  }
+}
+template <bool F16, bool WIDE>
+__device__ __forceinline__ void write8(void* p, bool vec, int n, const float (&v)[8]) {
+  if constexpr (WIDE) {
+    float* f = reinterpret_cast<float*>(p);
+    if (vec && n == 8) {
+      *reinterpret_cast<v4f*>(f) = *reinterpret_cast<const v4f*>(v);
+      *reinterpret_cast<v4f*>(f + 4) = *reinterpret_cast<const v4f*>(v + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) f[i] = v[i];
+    }
+  } else {
+    uint16_t* h = reinterpret_cast<uint16_t*>(p);
+    union {
+      uint4 q;
+      uint16_t b[8];
+    } w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w.b[i] = bits16<F16>(v[i]);
+    if (vec && n == 8) {
+      *reinterpret_cast<uint4*>(h) = w.q;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) h[i] = w.b[i];
+    }
+  }
+}
+
+// Eight columns n .. n + 7 of row m from their sums (n < cols); gated: `up` the
+// second product's.
+template <bool F16, GemmKind KIND>
+__device__ __forceinline__ void store8(const GemmArgs& a, int64_t m, int64_t n, float (&c)[8], const float (&up)[8]) {
+  const int left = (int)min((int64_t)8, a.cols - n);
+  const bool vy = a.vec & kVecY;
+  uint16_t* y16 = reinterpret_cast<uint16_t*>(a.y) + m * a.ldy + n;
+  if constexpr (KIND == kGemmGated) {
+    if (a.pre) {
+      uint16_t* p = reinterpret_cast<uint16_t*>(a.pre) + m * a.ldp + n;
+      write8<F16, false>(p, a.vec & kVecPre, left, c);
+      write8<F16, false>(p + a.cols, a.vec & kVecPre, left, up);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = act_value(a.act, c[i]) * up[i];
+    write8<F16, false>(y16, vy, left, c);
+  } else if constexpr (KIND == kGemmForward) {
+    float t[8];
+    if (a.bias) {
+      read8<F16, false>(reinterpret_cast<const uint16_t*>(a.bias) + n, a.vec & kVecBias, left, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] += t[i];
+    }
+    if (a.pre) write8<F16, false>(reinterpret_cast<uint16_t*>(a.pre) + m * a.ldp + n, a.vec & kVecPre, left, c);
+    if (a.act) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = act_value(a.act, c[i]);
+    }
+    if (a.y_type == MOE_FP32) {
+      if (a.residual) {
+        read8<F16, true>(reinterpret_cast<const float*>(a.residual) + m * a.ldr + n, a.vec & kVecResidual, left, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] += t[i];
+      }
+      write8<F16, true>(reinterpret_cast<float*>(a.y) + m * a.ldy + n, vy, left, c);
+    } else {
+      if (a.residual) {
+        read8<F16, false>(reinterpret_cast<const uint16_t*>(a.residual) + m * a.ldr + n, a.vec & kVecResidual, left, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] += t[i];
+      }
+      write8<F16, false>(y16, vy, left, c);
+    }
+  } else {
+    write8<F16, false>(y16, vy, left, c);
+  }
+}
+
+// Tile of workgroup `block`. Workgroups go to the eight XCDs in turn: XCD x takes a
+// contiguous eighth of the tiles, walked in groups of GM row blocks, so that the tiles
+// it runs at a time share operands in its L2.
+__device__ __forceinline__ void tile_of(int block, int tiles_m, int tiles_n, int& tm, int& tn) {
+  constexpr int GM = 8;
+  const int total = tiles_m * tiles_n;
+  const int xcd = block & 7, at = block >> 3, per = total >> 3, rest = total & 7;
+  const int id = xcd * per + min(xcd, rest) + at;
+  const int group = id / (GM * tiles_n), first = group * GM, rows = min(GM, tiles_m - first);
+  const int in = id - group * GM * tiles_n;
+  tm = first + in % rows;
+  tn = in / rows;
+}
+
+template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_tile_kernel(const GemmArgs a, int tiles_m, int tiles_n) {
+  constexpr int W = WM * WN, BM = 16 * TM * WM, BN = 16 * TN * WN;
+  constexpr bool gated = KIND == kGemmGated;
+  constexpr int cols = gated ? BN / 2 : BN;  // columns of y a tile
+  typedef Operand<KIND == kGemmWeight, BM, W> OpA;
+  typedef Operand<KIND == kGemmInput || KIND == kGemmWeight, BN, W> OpB;
+  constexpr int kStage = OpA::kBytes + OpB::kBytes;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+  const int wave = wave_id(), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wm = wave / WN, wn = wave % WN;
+  int tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * cols;
+
+  OpA la;
+  OpB lb;
+  la.init(wave, lane, a.lda, a.rows - m0);
+  if constexpr (gated) {
+    // rows [0, BN / 2) of B's tile: gate; from BN / 2 on: up, the same columns
+    lb.init(wave, lane, a.ldb, BN);
+#pragma unroll
+    for (int i = 0; i < OpB::kLoads; ++i) {
+      const int piece = (i * W + wave) * 64 + lane, row = (piece >> 3) % (BN / 2), chunk = (piece & 7) ^ (piece >> 4 & 7);
+      lb.off[i] = n0 + row < a.cols ? (uint32_t)(row * a.ldb * 2 + chunk * 16) : kOutside;
+    }
+  } else {
+    lb.init(wave, lane, a.ldb, a.cols - n0);
+  }
+  const uint16_t* pa = reinterpret_cast<const uint16_t*>(a.a) + (KIND == kGemmWeight ? m0 : m0 * a.lda);
+  const uint16_t* pb = reinterpret_cast<const uint16_t*>(a.b) + (KIND >= kGemmInput ? n0 : n0 * a.ldb);
+  const int64_t step_a = KIND == kGemmWeight ? 64 * a.lda : 64, step_b = KIND >= kGemmInput ? 64 * a.ldb : 64;
+  const int steps = (int)((a.K + 63) / 64);
+  const uint32_t base = __builtin_amdgcn_readfirstlane(lds_address(lds));
+  auto load = [&](int t) {
+    if (t + 1 == steps) {
+      la.last((int)(a.K - (int64_t)t * 64));
+      lb.last((int)(a.K - (int64_t)t * 64));
+    }
+    const uint32_t at = base + (uint32_t)(t & 1) * kStage;
+    const v4i ba = buffer_at(pa + t * step_a), bb = buffer_at(pb + t * step_b);
+    la.load(ba, ba, at, wave);
+    lb.load(bb, gated ? buffer_at(pb + a.cols * a.ldb + t * step_b) : bb, at + OpA::kBytes, wave);
+  };
+
+  v4f acc[TN][TM];
+#pragma unroll
+  for (int t = 0; t < TN; ++t)
+#pragma unroll
+    for (int u = 0; u < TM; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
+  // column block t of the wave in B's tile
+  auto block_n = [&](int t) { return gated ? (t < TN / 2 ? wn * (TN / 2) + t : BN / 32 + wn * (TN / 2) + t - TN / 2) : wn * TN + t; };
+  if (steps > 0) load(0);
+  for (int t = 0; t < steps; ++t) {
+    wait_and_barrier<0>();
+    if (t + 1 < steps) load(t + 1);
+    const uint8_t* sa = lds + (t & 1) * kStage;
+    const uint8_t* sb = sa + OpA::kBytes;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint4 fa[TM], fb[TN];
+#pragma unroll
+      for (int t = 0; t < TN; ++t) fb[t] = OpB::fragment(sb, block_n(t), j, r, g);
+#pragma unroll
+      for (int u = 0; u < TM; ++u) fa[u] = OpA::fragment(sa, wm * TM + u, j, r, g);
+#pragma unroll
+      for (int u = 0; u < TM; ++u)
+#pragma unroll
+        for (int t = 0; t < TN; ++t) acc[t][u] = mfma16<F16>(fb[t], fa[u], acc[t][u]);
+    }
+  }
+  // 16 rows of sums at a time through LDS of the wave's own, so that all that moves
+  // in the epilogue moves in 16-byte pieces along a row
+  wait_and_barrier<0>();
+  constexpr int C = 16 * TN, S = C + 4;
+  static_assert(2 * kStage >= W * 16 * S * 4, "the sums fit the operands' buffers");
+  float* mine = reinterpret_cast<float*>(lds) + wave * 16 * S;
+  constexpr int pieces = (gated ? C / 2 : C) / 8;
+#pragma unroll
+  for (int u = 0; u < TM; ++u) {
+#pragma unroll
+    for (int t = 0; t < TN; ++t) *reinterpret_cast<v4f*>(&mine[r * S + 16 * t + 4 * g]) = acc[t][u];
+    wave_lds_order();
+#pragma unroll
+    for (int i = lane; i < 16 * pieces; i += 64) {
+      const int row = i / pieces, c = i % pieces * 8;
+      const int64_t m = m0 + 16 * (wm * TM + u) + row, n = n0 + (gated ? C / 2 : C) * wn + c;
+      float v[8], up[8];
+#pragma unroll
+      for (int q = 0; q < 8; q += 4) {
+        *reinterpret_cast<v4f*>(v + q) = *reinterpret_cast<const v4f*>(&mine[row * S + c + q]);
+        if constexpr (gated) *reinterpret_cast<v4f*>(up + q) = *reinterpret_cast<const v4f*>(&mine[row * S + C / 2 + c + q]);
+      }
+      if (m < a.rows && n < a.cols) store8<F16, KIND>(a, m, n, v, up);
+    }
+    wave_lds_order();
+  }
+}
+
+template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN>
+hipError_t launch_tile(const GemmArgs& a, hipStream_t stream) {
+  constexpr int BM = 16 * TM * WM, cols = 16 * TN * WN / (KIND == kGemmGated ? 2 : 1);
+  const int64_t tm = (a.rows + BM - 1) / BM, tn = (a.cols + cols - 1) / cols;
+  return launch_k(gemm_tile_kernel<F16, KIND, TM, TN, WM, WN>, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), 0, stream,
+                  Ev{}, a, (int)tm, (int)tn);
+}
+
+}  // namespace qmoe
