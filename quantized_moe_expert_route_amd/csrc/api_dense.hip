@@ -131,7 +131,7 @@ moe_status moe_dense_forward(const moe_dense* d, int64_t M, const void* x, int64
   if (st != MOE_OK) return st;
   DeviceGuard guard(d->device);
   if (!guard.ok) return MOE_ERR_DEVICE;
-  GemmArgs g{M, d->N, d->K, x, d->w, ldx, d->K, d->type, d->bias, residual, y, pre, ldr, ldy, ldp, d->act, y_type, 0,
+  GemmArgs g{M, d->N, d->K, x, d->w, ldx, d->K, d->type, d->bias, residual, y, pre, ldr, ldy, ldp, d->act, y_type, 0, 1,
              workspace, need};
   return launch_gemm(kGemmForward, g, d->num_cus, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -227,7 +227,7 @@ moe_status moe_gated_forward(const moe_gated* d, int64_t M, const void* x, int64
   if (st != MOE_OK) return st;
   DeviceGuard guard(d->device);
   if (!guard.ok) return MOE_ERR_DEVICE;
-  GemmArgs g{M, d->I, d->H, x, d->w13, ldx, d->H, d->type, nullptr, nullptr, h, pre, 0, ldh, 2 * d->I, d->act, d->type, 0,
+  GemmArgs g{M, d->I, d->H, x, d->w13, ldx, d->H, d->type, nullptr, nullptr, h, pre, 0, ldh, 2 * d->I, d->act, d->type, 0, 1,
              workspace, need};
   return launch_gemm(kGemmGated, g, d->num_cus, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

@@ -42,7 +42,8 @@ struct GemmArgs {
   int64_t ldr, ldy, ldp;
   int act, y_type;
   int vec;  // set by launch_gemm: which of the matrices move in 16-byte pieces
-  // workspace of split sums
+  int splits;  // parts of K, set by launch_gemm
+  // workspace of the splits' sums
   void* ws;
   size_t ws_bytes;
 };

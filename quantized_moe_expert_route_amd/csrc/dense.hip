@@ -11,96 +11,80 @@
 
 namespace qmoe {
 
-// One element of C into y (and pre).
-template <bool F16, GemmKind KIND>
-__device__ __forceinline__ void store1(const GemmArgs& a, int64_t m, int64_t n, float c, float up) {
-  uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + m * a.ldy + n;
-  if constexpr (KIND == kGemmGated) {
-    if (a.pre) {
-      uint16_t* p = reinterpret_cast<uint16_t*>(a.pre) + m * a.ldp + n;
-      p[0] = bits16<F16>(c);
-      p[a.cols] = bits16<F16>(up);
-    }
-    *y = bits16<F16>(act_value(a.act, c) * up);
-  } else if constexpr (KIND == kGemmForward) {
-    if (a.bias) c += value16<F16>(reinterpret_cast<const uint16_t*>(a.bias)[n]);
-    if (a.pre) reinterpret_cast<uint16_t*>(a.pre)[m * a.ldp + n] = bits16<F16>(c);
-    c = act_value(a.act, c);
-    if (a.y_type == MOE_FP32) {
-      if (a.residual) c += reinterpret_cast<const float*>(a.residual)[m * a.ldr + n];
-      reinterpret_cast<float*>(a.y)[m * a.ldy + n] = c;
-    } else {
-      if (a.residual) c += value16<F16>(reinterpret_cast<const uint16_t*>(a.residual)[m * a.ldr + n]);
-      *y = bits16<F16>(c);
-    }
-  } else {
-    *y = bits16<F16>(c);
+namespace {
+
+// The tiles a product may run on.
+struct Tile {
+  int rows, cols;  // of C (gated: of both products, half of them columns of y)
+};
+enum { k256x256, k256x192, k128x128, k64x64, kTiles };
+constexpr Tile kTile[kTiles] = {{256, 256}, {256, 192}, {128, 128}, {64, 64}};
+
+struct Choice {
+  int tile, splits;
+};
+
+Choice choose(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int cus) {
+  // Rounds of workgroups over the CUs times a round's time per K-step
+  constexpr int per[kTiles] = {100, 76, 36, 18};
+  constexpr int wide[kTiles] = {1, 1, 2, 2};  // workgroups a CU
+  const int64_t steps = std::max<int64_t>((K + 63) / 64, 1);
+  Choice best{0, 1};
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < kTiles; ++i) {
+    const int64_t bn = kind == kGemmGated ? kTile[i].cols / 2 : kTile[i].cols;
+    const int64_t tiles = ((rows + kTile[i].rows - 1) / kTile[i].rows) * ((cols + bn - 1) / bn);
+    // splits of at least 8 steps each, while they fit the chip at once
+    int64_t splits = std::min(std::max<int64_t>(cus * wide[i] / tiles, 1), std::max<int64_t>(steps / 8, 1));
+    splits = std::min<int64_t>(splits, 32);
+    const int64_t part = (steps + splits - 1) / splits;
+    splits = (steps + part - 1) / part;  // none of them empty
+    const int64_t rounds = (tiles * splits + cus * wide[i] - 1) / (cus * wide[i]);
+    const int64_t cost = rounds * (part + 8) * per[i] * wide[i] + (splits > 1 ? 800 : 0);
+    if (cost < least) least = cost, best = {i, (int)splits};
   }
+  return best;
 }
 
-// 64 x 64 of C a workgroup, through LDS in K-steps of 32, every access checked.
 template <bool F16, GemmKind KIND>
-__global__ __launch_bounds__(256) void gemm_simple_kernel(const GemmArgs a, int tiles_m) {
-  constexpr int B = KIND == kGemmGated ? 2 : 1;
-  __shared__ uint16_t as[64][40], bs[B][64][40];  // rows of 32 K (and 8 of padding)
-  const int wave = wave_id(), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * 64, n0 = (int64_t)(blockIdx.x / tiles_m) * 64;
-  auto stage = [&](uint16_t(&dst)[64][40], const void* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, bool by_k) {
-    const uint16_t* src = reinterpret_cast<const uint16_t*>(p);
-    for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-      const int row = by_k ? i & 63 : i >> 5, k = by_k ? i >> 6 : i & 31;
-      const bool in = r0 + row < rows && k0 + k < a.K;
-      dst[row][k] = in ? src[by_k ? (k0 + k) * ld + r0 + row : (r0 + row) * ld + k0 + k] : (uint16_t)0;
-    }
-  };
-  v4f acc[B][4];
-  for (int q = 0; q < B; ++q)
-    for (int t = 0; t < 4; ++t) acc[q][t] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int64_t k0 = 0; k0 < a.K; k0 += 32) {
-    stage(as, a.a, a.lda, m0, a.rows, k0, KIND == kGemmWeight);
-    for (int q = 0; q < B; ++q)
-      stage(bs[q], reinterpret_cast<const uint16_t*>(a.b) + q * a.cols * a.ldb, a.ldb, n0, a.cols, k0, KIND >= kGemmInput);
-    __syncthreads();
-    const uint4 x = ld16(&as[16 * wave + r][8 * g]);
-    for (int q = 0; q < B; ++q)
-      for (int t = 0; t < 4; ++t) acc[q][t] = mfma16<F16>(ld16(&bs[q][16 * t + r][8 * g]), x, acc[q][t]);
-    __syncthreads();
+hipError_t launch(GemmArgs a, const Choice& c, hipStream_t stream) {
+  a.splits = c.splits;
+  hipError_t e;
+  switch (c.tile) {
+    case k256x256: e = launch_tile<F16, KIND, 8, 4, 2, 4, 2>(a, stream); break;
+    case k256x192: e = launch_tile<F16, KIND, 4, 6, 4, 2, 2>(a, stream); break;
+    case k128x128: e = launch_tile<F16, KIND, 4, 4, 2, 2, 2>(a, stream); break;
+    default: e = launch_tile<F16, KIND, 2, 2, 2, 2, 4>(a, stream); break;
   }
-  const int64_t m = m0 + 16 * wave + r;
-  if (m >= a.rows) return;
-  for (int t = 0; t < 4; ++t)
-    for (int i = 0; i < 4; ++i) {
-      const int64_t n = n0 + 16 * t + 4 * g + i;
-      if (n < a.cols) store1<F16, KIND>(a, m, n, acc[0][t][i], acc[B - 1][t][i]);
-    }
+  if (e == hipSuccess && c.splits > 1) {
+    const int64_t pieces = a.rows * ((a.cols + 7) / 8);
+    e = launch_k(split_join_kernel<F16, KIND>, dim3((unsigned)std::min<int64_t>((pieces + 255) / 256, 4096)), dim3(256),
+                 0, stream, Ev{}, a);
+  }
+  return e;
 }
 
-template <bool F16, GemmKind KIND>
-static hipError_t simple(const GemmArgs& a, hipStream_t stream) {
-  const int64_t tm = (a.rows + 63) / 64, tn = (a.cols + 63) / 64;
-  return launch_k(gemm_simple_kernel<F16, KIND>, dim3((unsigned)(tm * tn)), dim3(256), 0, stream, Ev{}, a, (int)tm);
+}  // namespace
+
+size_t gemm_ws_bytes(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int, int cus) {
+  if (rows == 0 || cols == 0) return 0;
+  const Choice c = choose(kind, rows, cols, K, cus);
+  return c.splits > 1 ? (size_t)c.splits * rows * ((cols + 7) / 8 * 8) * (kind == kGemmGated ? 8 : 4) : 0;
 }
 
-size_t gemm_ws_bytes(GemmKind, int64_t, int64_t, int64_t, int, int) { return 0; }
-
-template <bool F16, GemmKind KIND>
-static hipError_t launch(const GemmArgs& a, hipStream_t stream) {
-  if (a.rows <= 64) return simple<F16, KIND>(a, stream);
-  return launch_tile<F16, KIND, 8, 4, 2, 4>(a, stream);
-}
-
-hipError_t launch_gemm(GemmKind kind, const GemmArgs& args, int, hipStream_t stream) {
+hipError_t launch_gemm(GemmKind kind, const GemmArgs& args, int cus, hipStream_t stream) {
   GemmArgs a = args;
   const int64_t es = a.y_type == MOE_FP32 ? 4 : 2;
   auto vec = [](const void* p, int64_t ld, int64_t elem) { return p && ((uintptr_t)p & 15) == 0 && ld * elem % 16 == 0; };
   a.vec = (vec(a.y, a.ldy, es) ? kVecY : 0) | (vec(a.residual, a.ldr, es) ? kVecResidual : 0) |
           (vec(a.pre, a.ldp, 2) && (kind != kGemmGated || a.cols % 8 == 0) ? kVecPre : 0) | (vec(a.bias, 0, 2) ? kVecBias : 0);
   const bool f16 = a.type == MOE_FP16;
+  const Choice c = choose(kind, a.rows, a.cols, a.K, cus);
   switch (kind) {
-    case kGemmForward: return f16 ? launch<true, kGemmForward>(a, stream) : launch<false, kGemmForward>(a, stream);
-    case kGemmGated: return f16 ? launch<true, kGemmGated>(a, stream) : launch<false, kGemmGated>(a, stream);
-    case kGemmInput: return f16 ? launch<true, kGemmInput>(a, stream) : launch<false, kGemmInput>(a, stream);
-    default: return f16 ? launch<true, kGemmWeight>(a, stream) : launch<false, kGemmWeight>(a, stream);
+    case kGemmForward: return f16 ? launch<true, kGemmForward>(a, c, stream) : launch<false, kGemmForward>(a, c, stream);
+    case kGemmGated: return f16 ? launch<true, kGemmGated>(a, c, stream) : launch<false, kGemmGated>(a, c, stream);
+    case kGemmInput: return f16 ? launch<true, kGemmInput>(a, c, stream) : launch<false, kGemmInput>(a, c, stream);
+    default: return f16 ? launch<true, kGemmWeight>(a, c, stream) : launch<false, kGemmWeight>(a, c, stream);
   }
 }
 

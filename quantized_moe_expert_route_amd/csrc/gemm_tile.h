@@ -2,7 +2,7 @@
 // loop and the epilogue, for operands that lie along K or across it.
 //
 // A workgroup of WM x WN waves computes BM = 16 TM WM rows by BN = 16 TN WN columns,
-// a wave 16 TM x 16 TN of them, in K-steps of 64 from two buffers of LDS. Memory goes
+// a wave 16 TM x 16 TN of them, in K-steps of 64 from S buffers of LDS. Memory goes
 // straight to LDS (16 bytes a lane, 1 KB an instruction, in LDS in lane order), so
 // the tile's way through LDS needs no registers and what lies past a matrix's edge
 // comes as zeros from the buffer's bound.
@@ -107,11 +107,9 @@ struct Operand {
     for (int i = 0; i < kLoads; ++i)
       if (left[i] + k <= 0) off[i] = kOutside;
   }
-  // second: buffer of the rows from R / 2 on (gated: the other half of B's rows)
-  __device__ __forceinline__ void load(v4i buffer, v4i second, uint32_t lds, int wave) const {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      load_lds16(!BY_K && i * W + wave >= R / 16 ? second : buffer, off[i], lds + (uint32_t)(i * W + wave) * 1024);
+  // load i of the wave's. second: buffer of the rows from R / 2 on (gated: the other half of B's rows)
+  __device__ __forceinline__ void load(int i, v4i buffer, v4i second, uint32_t lds, int wave) const {
+    load_lds16(!BY_K && i * W + wave >= R / 16 ? second : buffer, off[i], lds + (uint32_t)(i * W + wave) * 1024);
   }
 
   // MFMA operand of K 32 j .. + 31 of the tile's row block b (16 rows)
@@ -253,19 +251,27 @@ __device__ __forceinline__ void tile_of(int block, int tiles_m, int tiles_n, int
   tn = in / rows;
 }
 
-template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_tile_kernel(const GemmArgs a, int tiles_m, int tiles_n) {
+// A split's sums (a.splits > 1: workgroups take parts of K, joined by split_join_kernel):
+// fp32 [split][rows][columns of B's rows, padded to 8].
+__device__ __forceinline__ float* split_sums(const GemmArgs& a, int split, int64_t m, bool gated) {
+  const int64_t ld = (a.cols + 7) / 8 * 8 * (gated ? 2 : 1);
+  return reinterpret_cast<float*>(a.ws) + (split * a.rows + m) * ld;
+}
+
+template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN, int S>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(const GemmArgs a, int tiles_m, int tiles_n) {
   constexpr int W = WM * WN, BM = 16 * TM * WM, BN = 16 * TN * WN;
   constexpr bool gated = KIND == kGemmGated;
   constexpr int cols = gated ? BN / 2 : BN;  // columns of y a tile
   typedef Operand<KIND == kGemmWeight, BM, W> OpA;
   typedef Operand<KIND == kGemmInput || KIND == kGemmWeight, BN, W> OpB;
-  constexpr int kStage = OpA::kBytes + OpB::kBytes;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+  constexpr int kStage = OpA::kBytes + OpB::kBytes, kLoads = OpA::kLoads + OpB::kLoads;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kStage];
   const int wave = wave_id(), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wm = wave / WN, wn = wave % WN;
+  const int tiles = tiles_m * tiles_n, split = blockIdx.x / tiles;
   int tm, tn;
-  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  tile_of(blockIdx.x - split * tiles, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * cols;
 
   OpA la;
@@ -282,20 +288,30 @@ __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_tile_kernel(
   } else {
     lb.init(wave, lane, a.ldb, a.cols - n0);
   }
-  const uint16_t* pa = reinterpret_cast<const uint16_t*>(a.a) + (KIND == kGemmWeight ? m0 : m0 * a.lda);
-  const uint16_t* pb = reinterpret_cast<const uint16_t*>(a.b) + (KIND >= kGemmInput ? n0 : n0 * a.ldb);
+  // this split's part of K
+  const int64_t part = ((a.K + 63) / 64 + a.splits - 1) / a.splits * 64, k0 = split * part;
+  const int64_t K = min(part, a.K - k0);
+  const int steps = (int)((K + 63) / 64);
   const int64_t step_a = KIND == kGemmWeight ? 64 * a.lda : 64, step_b = KIND >= kGemmInput ? 64 * a.ldb : 64;
-  const int steps = (int)((a.K + 63) / 64);
+  const uint16_t* pa = reinterpret_cast<const uint16_t*>(a.a) + (KIND == kGemmWeight ? m0 : m0 * a.lda) + k0 / 64 * step_a;
+  const uint16_t* pb = reinterpret_cast<const uint16_t*>(a.b) + (KIND >= kGemmInput ? n0 : n0 * a.ldb) + k0 / 64 * step_b;
   const uint32_t base = __builtin_amdgcn_readfirstlane(lds_address(lds));
-  auto load = [&](int t) {
-    if (t + 1 == steps) {
-      la.last((int)(a.K - (int64_t)t * 64));
-      lb.last((int)(a.K - (int64_t)t * 64));
+
+  // Loads of step t to buffer t % S, one at a time.
+  v4i ba, bb, bc;
+  uint32_t at;
+  auto begin_loads = [&](int t, int buffer) __attribute__((always_inline)) {
+    if (t + 1 >= steps) {  // past the last step: zeros, not used
+      la.last((int)(K - (int64_t)t * 64));
+      lb.last((int)(K - (int64_t)t * 64));
     }
-    const uint32_t at = base + (uint32_t)(t & 1) * kStage;
-    const v4i ba = buffer_at(pa + t * step_a), bb = buffer_at(pb + t * step_b);
-    la.load(ba, ba, at, wave);
-    lb.load(bb, gated ? buffer_at(pb + a.cols * a.ldb + t * step_b) : bb, at + OpA::kBytes, wave);
+    at = base + (uint32_t)buffer * kStage;
+    ba = buffer_at(pa + t * step_a), bb = buffer_at(pb + t * step_b);
+    bc = gated ? buffer_at(pb + a.cols * a.ldb + t * step_b) : bb;
+  };
+  auto load = [&](int n) __attribute__((always_inline)) {
+    if (n < OpA::kLoads) la.load(n, ba, ba, at, wave);
+    else lb.load(n - OpA::kLoads, bb, bc, at + OpA::kBytes, wave);
   };
 
   v4f acc[TN][TM];
@@ -305,36 +321,60 @@ __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_tile_kernel(
     for (int u = 0; u < TM; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
   // column block t of the wave in B's tile
   auto block_n = [&](int t) { return gated ? (t < TN / 2 ? wn * (TN / 2) + t : BN / 32 + wn * (TN / 2) + t - TN / 2) : wn * TN + t; };
-  if (steps > 0) load(0);
-  for (int t = 0; t < steps; ++t) {
-    wait_and_barrier<0>();
-    if (t + 1 < steps) load(t + 1);
-    const uint8_t* sa = lds + (t & 1) * kStage;
-    const uint8_t* sb = sa + OpA::kBytes;
+  // A step is two halves of 32 k. While the MFMAs of one half run, the operands of the
+  // next are read from LDS, so that they are there when the step's one barrier ends.
+  uint4 fa[2][TM], fb[2][TN];
+  auto read = [&](int i, int j, int buffer) __attribute__((always_inline)) {  // operand i of half j of a step
+    const uint8_t* sa = lds + buffer * kStage;
+    if (i < TN) fb[j][i] = OpB::fragment(sa + OpA::kBytes, block_n(i), j, r, g);
+    else fa[j][i - TN] = OpA::fragment(sa, wm * TM + i - TN, j, r, g);
+  };
+  // The reads go among the first three quarters of the MFMAs; so do, over all of the
+  // second half's, the loads: issued in a row after the barrier they held up all waves
+  // at once (4096 x 4096 x 6144 190 -> 172 us).
+  auto half = [&](int j, int next) __attribute__((always_inline)) {
+    constexpr int all = TM * TN, reads = TM + TN;
+    constexpr int gap = all * 3 / 4 / reads > 0 ? all * 3 / 4 / reads : 1, every = all / kLoads > 0 ? all / kLoads : 1;
+    static_assert(all >= reads && all >= kLoads, "one read and one load an MFMA at most");
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint4 fa[TM], fb[TN];
-#pragma unroll
-      for (int t = 0; t < TN; ++t) fb[t] = OpB::fragment(sb, block_n(t), j, r, g);
-#pragma unroll
-      for (int u = 0; u < TM; ++u) fa[u] = OpA::fragment(sa, wm * TM + u, j, r, g);
-#pragma unroll
-      for (int u = 0; u < TM; ++u)
-#pragma unroll
-        for (int t = 0; t < TN; ++t) acc[t][u] = mfma16<F16>(fb[t], fa[u], acc[t][u]);
+    for (int i = 0; i < all; ++i) {
+      const int u = i / TN, t = i % TN;
+      if (i % gap == 0 && i / gap < reads) read(i / gap, j ^ 1, next);
+      acc[t][u] = mfma16<F16>(fb[j][t], fa[j][u], acc[t][u]);
+      if (j == 1 && i % every == every - 1 && i / every < kLoads) load(i / every);
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+#pragma unroll
+  for (int t = 0; t < S; ++t) {
+    begin_loads(t, t);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) load(n);
+  }
+  wait_and_barrier<(S - 1) * kLoads>();
+#pragma unroll
+  for (int i = 0; i < TM + TN; ++i) read(i, 0, 0);
+  int buffer = 0;
+  for (int t = 0; t < steps; ++t) {
+    const int next = buffer + 1 == S ? 0 : buffer + 1;
+    half(0, buffer);
+    // step t has been read by all waves, step t + 1 has arrived
+    wait_and_barrier<(S - 2) * kLoads>();
+    begin_loads(t + S, buffer);
+    half(1, next);
+    buffer = next;
   }
   // 16 rows of sums at a time through LDS of the wave's own, so that all that moves
   // in the epilogue moves in 16-byte pieces along a row
   wait_and_barrier<0>();
-  constexpr int C = 16 * TN, S = C + 4;
-  static_assert(2 * kStage >= W * 16 * S * 4, "the sums fit the operands' buffers");
-  float* mine = reinterpret_cast<float*>(lds) + wave * 16 * S;
+  constexpr int C = 16 * TN, P = C + 4;
+  static_assert(S * kStage >= W * 16 * P * 4, "the sums fit the operands' buffers");
+  float* mine = reinterpret_cast<float*>(lds) + wave * 16 * P;
   constexpr int pieces = (gated ? C / 2 : C) / 8;
 #pragma unroll
   for (int u = 0; u < TM; ++u) {
 #pragma unroll
-    for (int t = 0; t < TN; ++t) *reinterpret_cast<v4f*>(&mine[r * S + 16 * t + 4 * g]) = acc[t][u];
+    for (int t = 0; t < TN; ++t) *reinterpret_cast<v4f*>(&mine[r * P + 16 * t + 4 * g]) = acc[t][u];
     wave_lds_order();
 #pragma unroll
     for (int i = lane; i < 16 * pieces; i += 64) {
@@ -343,21 +383,53 @@ __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_tile_kernel(
       float v[8], up[8];
 #pragma unroll
       for (int q = 0; q < 8; q += 4) {
-        *reinterpret_cast<v4f*>(v + q) = *reinterpret_cast<const v4f*>(&mine[row * S + c + q]);
-        if constexpr (gated) *reinterpret_cast<v4f*>(up + q) = *reinterpret_cast<const v4f*>(&mine[row * S + C / 2 + c + q]);
+        *reinterpret_cast<v4f*>(v + q) = *reinterpret_cast<const v4f*>(&mine[row * P + c + q]);
+        if constexpr (gated) *reinterpret_cast<v4f*>(up + q) = *reinterpret_cast<const v4f*>(&mine[row * P + C / 2 + c + q]);
       }
-      if (m < a.rows && n < a.cols) store8<F16, KIND>(a, m, n, v, up);
+      if (m < a.rows && n < a.cols) {
+        if (a.splits > 1) {
+          float* p = split_sums(a, split, m, gated) + n;
+          write8<F16, true>(p, true, 8, v);
+          if constexpr (gated) write8<F16, true>(p + (a.cols + 7) / 8 * 8, true, 8, up);
+        } else {
+          store8<F16, KIND>(a, m, n, v, up);
+        }
+      }
     }
     wave_lds_order();
   }
 }
 
-template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN>
+// The splits' sums, added in their order, and the epilogue.
+template <bool F16, GemmKind KIND>
+__global__ __launch_bounds__(256) void split_join_kernel(const GemmArgs a) {
+  constexpr bool gated = KIND == kGemmGated;
+  const int64_t pieces = (a.cols + 7) / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.rows * pieces; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / pieces, n = (i - m * pieces) * 8;
+    float v[8] = {}, up[8] = {};
+    for (int s = 0; s < a.splits; ++s) {
+      float t[8];
+      const float* p = split_sums(a, s, m, gated) + n;
+      read8<F16, true>(p, true, 8, t);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += t[q];
+      if constexpr (gated) {
+        read8<F16, true>(p + pieces * 8, true, 8, t);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) up[q] += t[q];
+      }
+    }
+    store8<F16, KIND>(a, m, n, v, up);
+  }
+}
+
+template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN, int S>
 hipError_t launch_tile(const GemmArgs& a, hipStream_t stream) {
   constexpr int BM = 16 * TM * WM, cols = 16 * TN * WN / (KIND == kGemmGated ? 2 : 1);
   const int64_t tm = (a.rows + BM - 1) / BM, tn = (a.cols + cols - 1) / cols;
-  return launch_k(gemm_tile_kernel<F16, KIND, TM, TN, WM, WN>, dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), 0, stream,
-                  Ev{}, a, (int)tm, (int)tn);
+  return launch_k(gemm_tile_kernel<F16, KIND, TM, TN, WM, WN, S>, dim3((unsigned)(tm * tn * a.splits)),
+                  dim3(64 * WM * WN), 0, stream, Ev{}, a, (int)tm, (int)tn);
 }
 
 }  // namespace qmoe
