@@ -535,8 +535,8 @@ moe_status moe_scores_forward(const moe_scores* scores, int64_t M, const void* z
  * backward call; may be NULL); moe_distill_backward reads it;
  * moe_distill_forward_backward does both at once, for weights known beforehand
  * (1/rows, say). dz of type grad_type: z's own, MOE_BF16 or MOE_FP16, rows lddz
- * apart; it may be z itself (same pointer, stride and type). k 1 .. 64, T finite
- * and > 0; sizes, strides and errors as moe_scores (dz as z). */
+ * apart; it may be z itself (same pointer, stride and type). k 1 .. 64, T 1e-6
+ * .. 1e6; sizes, strides and errors as moe_scores (dz as z). */
 typedef struct moe_distill moe_distill;
 moe_status moe_distill_create(int64_t V, int64_t k, int type, int grad_type, float temperature, int64_t max_M,
                               moe_distill** out);

@@ -1,8 +1,6 @@
 // C ABI of the operators on the output head's logits: scores of given tokens and
 // distillation. Validation only; nothing here allocates device memory or
 // synchronizes a stream.
-#include <math.h>
-
 #include <new>
 
 #include "api_util.h"
@@ -85,7 +83,7 @@ moe_status moe_distill_create(int64_t V, int64_t k, int type, int grad_type, flo
   moe_status st = check_head(V, k, 1, type, max_M);
   if (st != MOE_OK) return st;
   if (grad_type != type && !type16(grad_type)) return MOE_ERR_INVALID_ARG;
-  if (!(temperature > 0.f) || !(1.f / temperature < INFINITY) || !(1.f / temperature > 0.f)) return MOE_ERR_INVALID_ARG;
+  if (!(temperature >= 1e-6f && temperature <= 1e6f)) return MOE_ERR_INVALID_ARG;
   int dev, cus;
   st = current_device(&dev, &cus);
   if (st != MOE_OK) return st;
