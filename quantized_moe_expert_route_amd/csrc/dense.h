@@ -71,7 +71,7 @@ struct SlopeArgs {
   float* part;
   int type, act;
 };
-constexpr int kBiasRows = 64;  // rows a partial sum of dbias takes
+constexpr int kBiasRows = 16;  // rows a partial sum of dbias takes
 inline int64_t dbias_parts(int64_t M) { return (M + kBiasRows - 1) / kBiasRows; }
 hipError_t launch_slope(const SlopeArgs& a, hipStream_t stream);
 

@@ -89,78 +89,128 @@ hipError_t launch_gemm(GemmKind kind, const GemmArgs& args, int cus, hipStream_t
 }
 
 // ----------------------------------------------------------------- backward, elementwise
-// A thread takes one column of kBiasRows rows. dbias's partial sums are joined in
-// the order of the rows by a second launch.
+// A lane takes eight columns, a wave a row's 512 at a time; the four waves of a
+// workgroup take kBiasRows rows in turn. dbias's sums of a workgroup are joined in the
+// order of its waves, those of all workgroups in the order of the rows by a second
+// launch. Bound by memory.
 template <bool F16>
-__global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a, int vec) {
+  __shared__ float sums[4][512];
+  const int wave = wave_id(), lane = threadIdx.x & 63;
+  const int64_t n = ((int64_t)blockIdx.x * 64 + lane) * 8;
   const int64_t m0 = (int64_t)blockIdx.y * kBiasRows, m1 = min(m0 + kBiasRows, a.M);
-  const int64_t cols = a.dz ? a.ldz : a.N;
-  if (n >= cols) return;
-  float sum = 0.f;
-  for (int64_t m = m0; m < m1; ++m) {
-    float v = 0.f;
-    if (n < a.N) {
-      v = value16<F16>(reinterpret_cast<const uint16_t*>(a.dy)[m * a.lddy + n]);
-      float y;
-      if (a.act) v *= act_slope(a.act, value16<F16>(reinterpret_cast<const uint16_t*>(a.pre)[m * a.ldp + n]), y);
-    }
-    if (a.dz) reinterpret_cast<uint16_t*>(a.dz)[m * a.ldz + n] = bits16<F16>(v);
-    sum += v;
+  const int left = (int)max((int64_t)0, min((int64_t)8, a.N - n));
+  float sum[8] = {};
+  if (left > 0) {
+    with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll 4
+      for (int64_t m = m0 + wave; m < m1; m += 4) {
+        float v[8], p[8];
+        read8<F16, false>(reinterpret_cast<const uint16_t*>(a.dy) + m * a.lddy + n, vec & 1, left, v);
+        if constexpr (act != MOE_ACT_NONE) {
+          read8<F16, false>(reinterpret_cast<const uint16_t*>(a.pre) + m * a.ldp + n, vec & 2, left, p);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float y;
+            v[i] *= act_slope<act>(p[i], y);
+          }
+        }
+        // (columns past N hold zeros)
+        if (a.dz) write8<F16, false>(reinterpret_cast<uint16_t*>(a.dz) + m * a.ldz + n, true, 8, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += v[i];
+      }
+    });
   }
-  if (a.dbias && n < a.N) a.part[blockIdx.y * a.N + n] = sum;
+  if (!a.dbias) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[wave][i * 64 + lane] = sum[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int64_t c = (int64_t)blockIdx.x * 512 + (i & 63) * 8 + (i >> 6);
+    if (c < a.N) a.part[blockIdx.y * a.N + c] = sums[0][i] + sums[1][i] + sums[2][i] + sums[3][i];
+  }
 }
 
+// 64 columns a workgroup; its 16 waves take the partial sums in turn.
 template <bool F16>
-__global__ __launch_bounds__(256) void dbias_kernel(const float* __restrict__ part, uint16_t* __restrict__ dbias, int64_t N,
-                                                    int64_t parts) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+__global__ __launch_bounds__(1024) void dbias_kernel(const float* __restrict__ part, uint16_t* __restrict__ dbias, int64_t N,
+                                                     int64_t parts) {
+  __shared__ float sums[16][64];
+  const int wave = wave_id(), lane = threadIdx.x & 63;
+  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
   float sum = 0.f;
-  for (int64_t p = 0; p < parts; ++p) sum += part[p * N + n];
-  dbias[n] = bits16<F16>(sum);
+  if (n < N) {
+#pragma unroll 8
+    for (int64_t p = wave; p < parts; p += 16) sum += part[p * N + n];
+  }
+  sums[wave][lane] = sum;
+  __syncthreads();
+  if (wave == 0 && n < N) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) sum += sums[w][lane];
+    dbias[n] = bits16<F16>(sum);
+  }
 }
+
+static bool on16(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
 
 hipError_t launch_slope(const SlopeArgs& a, hipStream_t stream) {
   const bool f16 = a.type == MOE_FP16;
   const int64_t parts = dbias_parts(a.M);
   hipError_t e = hipSuccess;
   if (a.M > 0) {
-    const dim3 grid((unsigned)(((a.dz ? a.ldz : a.N) + 255) / 256), (unsigned)parts);
-    e = f16 ? launch_k(slope_kernel<true>, grid, dim3(256), 0, stream, Ev{}, a)
-            : launch_k(slope_kernel<false>, grid, dim3(256), 0, stream, Ev{}, a);
+    const int vec = (on16(a.dy, a.lddy) ? 1 : 0) | (a.pre && on16(a.pre, a.ldp) ? 2 : 0);
+    const dim3 grid((unsigned)((a.N + 511) / 512), (unsigned)parts);
+    e = f16 ? launch_k(slope_kernel<true>, grid, dim3(256), 0, stream, Ev{}, a, vec)
+            : launch_k(slope_kernel<false>, grid, dim3(256), 0, stream, Ev{}, a, vec);
   }
   if (e == hipSuccess && a.dbias) {
-    const dim3 grid((unsigned)((a.N + 255) / 256));
-    e = f16 ? launch_k(dbias_kernel<true>, grid, dim3(256), 0, stream, Ev{}, (const float*)a.part, (uint16_t*)a.dbias, a.N, parts)
-            : launch_k(dbias_kernel<false>, grid, dim3(256), 0, stream, Ev{}, (const float*)a.part, (uint16_t*)a.dbias, a.N, parts);
+    const dim3 grid((unsigned)((a.N + 63) / 64));
+    e = f16 ? launch_k(dbias_kernel<true>, grid, dim3(1024), 0, stream, Ev{}, (const float*)a.part, (uint16_t*)a.dbias, a.N, parts)
+            : launch_k(dbias_kernel<false>, grid, dim3(1024), 0, stream, Ev{}, (const float*)a.part, (uint16_t*)a.dbias, a.N, parts);
   }
   return e;
 }
 
+// Eight columns of I of a row a lane, both halves of dz. vec: 1 dh, 2 pre's and dz's
+// rows and halves move in 16-byte pieces.
 template <bool F16>
-__global__ __launch_bounds__(256) void gated_slope_kernel(const GatedSlopeArgs a) {
-  const int64_t total = a.M * a.ldz;
-  for (int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x; o < total; o += (int64_t)gridDim.x * 256) {
-    const int64_t m = o / a.ldz, n = o - m * a.ldz;
-    float v = 0.f;
-    if (n < 2 * a.I) {
-      const int64_t i = n < a.I ? n : n - a.I;
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(a.pre) + m * 2 * a.I + i;
-      const float d = value16<F16>(reinterpret_cast<const uint16_t*>(a.dh)[m * a.lddh + i]);
-      float value;
-      const float slope = act_slope(a.act, value16<F16>(p[0]), value);
-      v = n < a.I ? d * value16<F16>(p[a.I]) * slope : d * value;
-    }
-    reinterpret_cast<uint16_t*>(a.dz)[o] = bits16<F16>(v);
-  }
+__global__ __launch_bounds__(256) void gated_slope_kernel(const GatedSlopeArgs a, int vec) {
+  const int64_t pieces = (a.I + 7) / 8;
+  with_act(a.act, [&](auto act) __attribute__((always_inline)) {
+    if constexpr (act != MOE_ACT_NONE)
+      for (int64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = i * 8;
+        if (i >= pieces) break;
+        const int left = (int)min((int64_t)8, a.I - n);
+        float d[8], g[8], u[8];
+        const uint16_t* pre = reinterpret_cast<const uint16_t*>(a.pre) + m * 2 * a.I + n;
+        uint16_t* dz = reinterpret_cast<uint16_t*>(a.dz) + m * a.ldz + n;
+        read8<F16, false>(reinterpret_cast<const uint16_t*>(a.dh) + m * a.lddh + n, vec & 1, left, d);
+        read8<F16, false>(pre, vec & 2, left, g);
+        read8<F16, false>(pre + a.I, vec & 2, left, u);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float value;
+          const float s = act_slope<act>(g[q], value);
+          g[q] = d[q] * u[q] * s;
+          u[q] = d[q] * value;
+        }
+        write8<F16, false>(dz, vec & 2, left, g);
+        write8<F16, false>(dz + a.I, vec & 2, left, u);
+        if (i == 0)  // what pads the row
+          for (int64_t c = 2 * a.I; c < a.ldz; ++c) reinterpret_cast<uint16_t*>(a.dz)[m * a.ldz + c] = 0;
+      }
+  });
 }
 
 hipError_t launch_gated_slope(const GatedSlopeArgs& a, hipStream_t stream) {
   if (a.M == 0) return hipSuccess;
-  const dim3 grid((unsigned)std::min<int64_t>((a.M * a.ldz + 255) / 256, 1 << 16));
-  return a.type == MOE_FP16 ? launch_k(gated_slope_kernel<true>, grid, dim3(256), 0, stream, Ev{}, a)
-                            : launch_k(gated_slope_kernel<false>, grid, dim3(256), 0, stream, Ev{}, a);
+  const int vec = (on16(a.dh, a.lddh) ? 1 : 0) | (on16(a.pre, a.I) ? 2 : 0);
+  const dim3 grid((unsigned)((a.I + 2047) / 2048), (unsigned)std::min<int64_t>(a.M, 65535));
+  return a.type == MOE_FP16 ? launch_k(gated_slope_kernel<true>, grid, dim3(256), 0, stream, Ev{}, a, vec)
+                            : launch_k(gated_slope_kernel<false>, grid, dim3(256), 0, stream, Ev{}, a, vec);
 }
 
 }  // namespace qmoe

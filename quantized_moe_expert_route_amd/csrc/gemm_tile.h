@@ -202,8 +202,10 @@ __device__ __forceinline__ void store8(const GemmArgs& a, int64_t m, int64_t n, 
       write8<F16, false>(p, a.vec & kVecPre, left, c);
       write8<F16, false>(p + a.cols, a.vec & kVecPre, left, up);
     }
+    with_act(a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = act_value(a.act, c[i]) * up[i];
+      for (int i = 0; i < 8; ++i) c[i] = act_value<act>(c[i]) * up[i];
+    });
     write8<F16, false>(y16, vy, left, c);
   } else if constexpr (KIND == kGemmForward) {
     float t[8];
@@ -213,10 +215,10 @@ __device__ __forceinline__ void store8(const GemmArgs& a, int64_t m, int64_t n, 
       for (int i = 0; i < 8; ++i) c[i] += t[i];
     }
     if (a.pre) write8<F16, false>(reinterpret_cast<uint16_t*>(a.pre) + m * a.ldp + n, a.vec & kVecPre, left, c);
-    if (a.act) {
+    with_act(a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = act_value(a.act, c[i]);
-    }
+      for (int i = 0; i < 8; ++i) c[i] = act_value<act>(c[i]);
+    });
     if (a.y_type == MOE_FP32) {
       if (a.residual) {
         read8<F16, true>(reinterpret_cast<const float*>(a.residual) + m * a.ldr + n, a.vec & kVecResidual, left, t);

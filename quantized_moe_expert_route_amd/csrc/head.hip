@@ -113,21 +113,19 @@ __device__ __forceinline__ Total join(const Sums<MEAN>& a, float cl) {
   float m = wave_max(a.m);
   if (lane == 0) lm[wave] = m;
   __syncthreads();
-  m = lm[0];
-#pragma unroll
-  for (int w = 1; w < W; ++w) m = fmaxf(m, lm[w]);
+  m = wave_max(lm[lane % W]);
   const float back = fmaxf((a.m - m) * cl, -1e4f);
   const double f = __builtin_amdgcn_exp2f(back);
-  double s = a.s * f, t = 0;
-  if constexpr (MEAN) t = ((double)a.t + (double)a.s * back) * f;
-  s = wave_sum(s);
-  if constexpr (MEAN) t = wave_sum(t);
-  if (lane == 0) ls[wave] = s, lt[wave] = t;
+  const double s = wave_sum(a.s * f);
+  if (lane == 0) ls[wave] = s;
+  if constexpr (MEAN) {
+    const double t = wave_sum(((double)a.t + (double)a.s * back) * f);
+    if (lane == 0) lt[wave] = t;
+  }
   __syncthreads();
-  s = t = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) s += ls[w], t += lt[w];
-  return {m, s, t * 0.69314718055994531};
+  Total r{m, wave_sum(lane < W ? ls[lane] : 0.0), 0};
+  if constexpr (MEAN) r.t = wave_sum(lane < W ? lt[lane] : 0.0) * 0.69314718055994531;
+  return r;
 }
 
 // ----------------------------------------------------------------- the k largest
@@ -140,31 +138,13 @@ __device__ __forceinline__ uint64_t key_of(float v, int64_t id) {
 constexpr int kKeys = 2048;  // candidates held
 struct Candidates {
   uint64_t key[kKeys];
-  uint64_t at_least;  // the threshold
-  uint64_t wave[16];
-  int n;              // candidates met; those past kKeys are not held
+  uint64_t top[kMaxTop];  // the k largest, in order
+  uint64_t at_least;      // the threshold
+  int n;                  // candidates met; those past kKeys are not held
+  int threads;            // threads whose best element reaches the threshold,
+  uint16_t thread[1024];  // in no order
+  uint32_t best[1024];    // the threads' best elements (order_key)
 };
-
-// The threshold that a tile's best elements give, `best` a thread's: every wave has q
-// threads at or above its q-th best, all waves together at least k above the least of
-// these.
-template <int THREADS>
-__device__ __forceinline__ void raise_threshold(Candidates& c, uint64_t best, int k) {
-  constexpr int W = THREADS / 64;
-  const int q = (k + W - 1) / W;
-  uint64_t at = 0;
-  for (int i = 0; i < q; ++i) {
-    at = wave_max_u64(best);
-    if (best == at) best = 0;  // keys differ, but for 0
-  }
-  if ((threadIdx.x & 63) == 0) c.wave[wave_id()] = at;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < W; ++w) at = c.wave[w] < at ? c.wave[w] : at;
-    if (at > c.at_least) c.at_least = at;
-  }
-  __syncthreads();
-}
 
 // The candidates held, largest first, c.n of them at most k; the threshold is the k-th.
 template <int THREADS>
@@ -173,12 +153,16 @@ __device__ void sort_candidates(Candidates& c, int k) {
   const int n = min(c.n, kKeys);
   int size = 2;
   while (size < n) size *= 2;
+#pragma unroll 1
   for (int i = n + threadIdx.x; i < size; i += THREADS) c.key[i] = 0;
   __syncthreads();
+#pragma unroll 1
   for (int run = 2; run <= size; run *= 2)
+#pragma unroll 1
     for (int step = run / 2; step > 0; step /= 2) {
+#pragma unroll 1
       for (int i = threadIdx.x; i < size / 2; i += THREADS) {
-        const int lo = (i / step) * 2 * step + i % step, hi = lo + step;
+        const int lo = (i & ~(step - 1)) * 2 | (i & (step - 1)), hi = lo + step;
         const uint64_t a = c.key[lo], b = c.key[hi];
         if ((a < b) == ((lo & run) == 0)) c.key[lo] = b, c.key[hi] = a;
       }
@@ -187,6 +171,28 @@ __device__ void sort_candidates(Candidates& c, int k) {
   if (threadIdx.x == 0) {
     c.n = min(n, k);
     if (n >= k) c.at_least = c.key[k - 1];
+  }
+  __syncthreads();
+}
+
+// c.top: the k largest of the candidates (zeros behind fewer). A few hundred are
+// ranked by counting the larger ones, more are sorted.
+template <int THREADS>
+__device__ void rank_candidates(Candidates& c, int k) {
+  __syncthreads();
+  const int n = c.n;
+  if (n > THREADS) {
+    sort_candidates<THREADS>(c, k);
+    for (int j = threadIdx.x; j < k; j += THREADS) c.top[j] = j < c.n ? c.key[j] : 0;
+  } else {
+    for (int j = n + threadIdx.x; j < k; j += THREADS) c.top[j] = 0;
+    if ((int)threadIdx.x < n) {
+      const uint64_t key = c.key[threadIdx.x];
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) rank += c.key[j] > key;
+      if (rank < k) c.top[rank] = key;
+    }
   }
   __syncthreads();
 }
@@ -209,42 +215,21 @@ __device__ __forceinline__ void offer(Candidates& c, const float (&v)[N], int64_
   }
 }
 
-// The k largest of a segment again, for rows whose candidates were more than fit: the
-// threshold is raised by every tile, and whenever the candidates are full they are
-// sorted and all but k dropped.
+// The k largest of a segment again, of which more candidates reach the threshold than
+// fit (or fewer than k: `from` is 0 then): whenever they are full, they are sorted, all
+// but k dropped and the threshold raised.
 template <int TYPE, int THREADS>
-__device__ void reselect(Candidates& c, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, int k) {
-  constexpr int E = Logit<TYPE>::kPiece;
+__device__ __forceinline__ void reselect(Candidates& c, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, uint64_t from, int k) {
+  if (threadIdx.x == 0) c.n = 0, c.at_least = from;
   __syncthreads();
-  if (threadIdx.x == 0) c.n = 0, c.at_least = 0;
-  __syncthreads();
-  for (int64_t base = edges ? p0 - THREADS : p0; base < p1; base += THREADS) {
-    float v[E];
-    uint32_t left = 0;
-    int64_t first = 0;
-    if (base < p0) {  // the elements outside the pieces
-      const bool in = (int)threadIdx.x < row.edges();
-      first = row.edge(in ? threadIdx.x : 0);
-      v[0] = in ? Logit<TYPE>::load(row.p, first) : 0.f;
-#pragma unroll
-      for (int i = 1; i < E; ++i) v[i] = 0.f;
-      left = in;
-    } else {
-      const int64_t p = base + threadIdx.x;
-      const uint4 q = row.piece(p < p1 ? p : p0);
-      first = row.first(p);
-      left = p < p1 ? (1u << E) - 1 : 0;
-#pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = Logit<TYPE>::value(q, i);
-    }
-    uint64_t best = 0;
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (left >> i & 1) {
-        const uint64_t key = key_of(v[i], first + i);
-        best = key > best ? key : best;
-      }
-    raise_threshold<THREADS>(c, best, k);
+  const int64_t inner = (p1 - p0) * Logit<TYPE>::kPiece, all = inner + (edges ? row.edges() : 0);
+#pragma unroll 1
+  for (int64_t base = 0; base < all; base += THREADS) {
+    const int64_t i = base + threadIdx.x;
+    uint32_t left = i < all;
+    const int64_t first = !left ? 0 : i < inner ? row.first(p0) + i : row.edge((int)(i - inner));
+    const float v[1] = {left ? Logit<TYPE>::load(row.p, first) : 0.f};
+#pragma unroll 1
     for (;;) {
       offer(c, v, first, left);
       __syncthreads();
@@ -254,6 +239,67 @@ __device__ void reselect(Candidates& c, const Row<TYPE>& row, int64_t p0, int64_
       sort_candidates<THREADS>(c, k);
     }
   }
+}
+
+// The k largest of a segment whose threads hold their own elements' maxima: at least k
+// elements reach the k-th largest of these, and hardly more do (131072 elements of 512
+// threads, k 32: 33 where nothing ties), all of them elements of threads whose maximum
+// reaches it. Those threads' pieces are read again. The threshold is taken from the
+// maxima's upper 16 bits.
+template <int TYPE, int THREADS>
+__device__ void select(Candidates& c, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, float edge, float best, int k) {
+  constexpr int E = Logit<TYPE>::kPiece, W = THREADS / 64;
+  const uint32_t mine = order_key(best);
+  c.best[threadIdx.x] = mine;
+  if (threadIdx.x == 0) c.n = 0, c.threads = 0;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    uint32_t b[W], at = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) b[w] = c.best[64 * w + threadIdx.x] >> 16;
+#pragma unroll 1
+    for (uint32_t bit = 1u << 15; bit > 0; bit >>= 1) {
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) n += __popcll(__ballot(b[w] >= (at | bit)));
+      if (n >= k) at |= bit;
+    }
+    if (threadIdx.x == 0) c.at_least = (uint64_t)at << 48;
+  }
+  __syncthreads();
+  const uint64_t at_least = c.at_least;
+  if (mine >= (uint32_t)(at_least >> 32)) c.thread[atomicAdd(&c.threads, 1)] = (uint16_t)threadIdx.x;
+  if (edges && (int)threadIdx.x < row.edges()) {
+    float v[1] = {edge};
+    uint32_t left = 1;
+    offer(c, v, row.edge(threadIdx.x), left);
+  }
+  __syncthreads();
+  const int n = c.threads;
+  const int rounds = (int)((p1 - p0 + THREADS - 1) / THREADS);  // pieces a thread
+#pragma unroll 1
+  for (int i = threadIdx.x; i < rounds * n; i += THREADS) {
+    const int r = i / n;
+    const int64_t p = p0 + r * THREADS + c.thread[i - r * n];
+    if (p >= p1) continue;
+    const uint4 q = row.piece(p);
+    float v[E], top;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      v[e] = Logit<TYPE>::value(q, e);
+      top = e ? fmaxf(top, v[e]) : v[e];
+    }
+    if (order_key(top) < (uint32_t)(at_least >> 32)) continue;
+    uint32_t left = (1u << E) - 1;
+    offer(c, v, row.first(p), left);
+  }
+  __syncthreads();
+  // too few where elements are NaN or -inf (the maxima start above -inf), too many of
+  // equal ones
+  const int met = c.n;
+  __syncthreads();
+  if (met < k || met > kKeys) reselect<TYPE, THREADS>(c, row, p0, p1, edges, met < k ? 0 : at_least, k);
+  rank_candidates<THREADS>(c, k);
 }
 
 // ----------------------------------------------------------------- scores
@@ -277,7 +323,7 @@ __device__ void write_scores(const ScoresArgs& a, int64_t m, const Total& r, flo
     if (a.lse) a.lse[m] = ok ? (float)lse : r.m == INFINITY ? INFINITY : r.s == 0 ? -INFINITY : NAN;
   }
   for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
-    const uint64_t key = c.key[j];
+    const uint64_t key = c.top[j];
     a.top_ids[m * a.k + j] = (int32_t)~(uint32_t)key;
     a.top_logprobs[m * a.k + j] = ok ? (float)(key_to_float((uint32_t)(key >> 32)) - lse) : NAN;
   }
@@ -289,8 +335,9 @@ __device__ __forceinline__ float given_logit(const ScoresArgs& a, const Row<TYPE
   return t >= 0 && t < a.V ? Logit<TYPE>::load(row.p, t) : 0.f;
 }
 
+// (at most 64 registers: four workgroups of 512 threads a CU)
 template <int TYPE, int THREADS, bool TOP>
-__global__ __launch_bounds__(THREADS) void scores_kernel(const ScoresArgs a, int parts) {
+__global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel(const ScoresArgs a, int parts) {
   constexpr int E = Logit<TYPE>::kPiece, NP = 16 / E, N = NP * E;  // pieces, elements a thread and tile
   __shared__ Candidates c;
   const int64_t m = blockIdx.x / parts;
@@ -300,7 +347,6 @@ __global__ __launch_bounds__(THREADS) void scores_kernel(const ScoresArgs a, int
   const int64_t p0 = min(per * part, row.pieces), p1 = min(p0 + per, row.pieces);
   const bool edges = part == 0;
   const float given = parts == 1 ? given_logit<TYPE>(a, row, m) : 0.f;
-  if (TOP && threadIdx.x == 0) c.n = 0, c.at_least = 0;
   Sums<true> sums;
 
   uint4 q[NP];
@@ -319,49 +365,17 @@ __global__ __launch_bounds__(THREADS) void scores_kernel(const ScoresArgs a, int
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = Logit<TYPE>::value(q[i / E], i % E);
     load(base + NP * THREADS);
-    const float top = sums.add(v, kLog2e);
-    if constexpr (TOP) {
-      if (base == p0) {
-        uint64_t best = edges && (int)threadIdx.x < row.edges() ? key_of(edge[0], row.edge(threadIdx.x)) : 0;
-#pragma unroll
-        for (int u = 0; u < NP; ++u) {
-          const int64_t p = base + u * THREADS + threadIdx.x;
-#pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const uint64_t key = p < p1 ? key_of(v[u * E + i], row.first(p) + i) : 0;
-            best = key > best ? key : best;
-          }
-        }
-        raise_threshold<THREADS>(c, best, a.k);
-        uint32_t left = edges && (int)threadIdx.x < row.edges();
-        offer(c, edge, row.edge(threadIdx.x), left);
-      }
-      // (the first tile's NaN raise the threshold, but not `top`; a NaN threshold lets all pass)
-      if (base == p0 || !(top < key_to_float((uint32_t)(c.at_least >> 32)))) {
-#pragma unroll
-        for (int u = 0; u < NP; ++u) {
-          const int64_t p = base + u * THREADS + threadIdx.x;
-          float w[E];
-#pragma unroll
-          for (int i = 0; i < E; ++i) w[i] = v[u * E + i];
-          uint32_t left = p < p1 ? (1u << E) - 1 : 0;
-          offer(c, w, row.first(p), left);
-        }
-      }
-    }
+    sums.add(v, kLog2e);
   }
-  const Total r = join<THREADS>(sums, kLog2e);  // (its barriers: all candidates are in)
-  if constexpr (TOP) {
-    if (c.n > kKeys) reselect<TYPE, THREADS>(c, row, p0, p1, edges, a.k);
-    sort_candidates<THREADS>(c, a.k);
-  }
+  const Total r = join<THREADS>(sums, kLog2e);
+  if constexpr (TOP) select<TYPE, THREADS>(c, row, p0, p1, edges, edge[0], sums.m, a.k);
   if (parts == 1) {
     write_scores(a, m, r, given, c);
     return;
   }
   if (threadIdx.x == 0) reinterpret_cast<ScoresPart*>(a.ws)[blockIdx.x] = {r.m, 0.f, r.s, r.t};
   uint64_t* keys = reinterpret_cast<uint64_t*>(reinterpret_cast<ScoresPart*>(a.ws) + a.M * parts) + (int64_t)blockIdx.x * a.k;
-  for (int j = threadIdx.x; j < a.k; j += THREADS) keys[j] = j < c.n ? c.key[j] : 0;
+  for (int j = threadIdx.x; j < a.k; j += THREADS) keys[j] = c.top[j];
 }
 
 constexpr int kMaxParts = 32;
@@ -375,16 +389,29 @@ __global__ __launch_bounds__(256) void scores_join_kernel(const ScoresArgs a, in
   const float given = given_logit<TYPE>(a, row, m);
   const ScoresPart* p = reinterpret_cast<const ScoresPart*>(a.ws) + m * parts;
   const uint64_t* keys = reinterpret_cast<const uint64_t*>(reinterpret_cast<const ScoresPart*>(a.ws) + a.M * parts) + m * parts * a.k;
-  for (int j = threadIdx.x; j < parts * a.k; j += 256) c.key[j] = keys[j];
-  if (threadIdx.x == 0) c.n = parts * a.k, c.at_least = 0;
-  Total r{-FLT_MAX, 0, 0};
-  for (int i = 0; i < parts; ++i) r.m = fmaxf(r.m, p[i].m);
-  for (int i = 0; i < parts; ++i) {
-    const double back = fmax((double)p[i].m - r.m, -1e4), f = exp(back);
-    r.s += p[i].s * f;
-    r.t += (p[i].t + p[i].s * back) * f;
+  if (threadIdx.x == 0) c.n = 0;
+  __syncthreads();
+  if (a.k) {
+    // at least k of the keys reach the least of the parts' q-th, and the largest of their k-th
+    const int i = threadIdx.x & 63, q = (a.k + parts - 1) / parts;
+    const uint64_t least = ~wave_max_u64(i < parts ? ~keys[(int64_t)i * a.k + q - 1] : 0);
+    const uint64_t last = wave_max_u64(i < parts ? keys[(int64_t)i * a.k + a.k - 1] : 0);
+    const uint64_t at_least = least > last ? least : last;
+    for (int j = threadIdx.x; j < parts * a.k; j += 256) {
+      const uint64_t key = keys[j];
+      if (key >= at_least && key) c.key[atomicAdd(&c.n, 1)] = key;
+    }
   }
-  if (a.k) sort_candidates<256>(c, a.k);
+  Total r{-FLT_MAX, 0, 0};
+  {  // every wave the same
+    const int i = threadIdx.x & 63;
+    const ScoresPart mine = i < parts ? p[i] : ScoresPart{-FLT_MAX, 0.f, 0, 0};
+    r.m = wave_max(mine.m);
+    const double back = fmax((double)mine.m - r.m, -1e4), f = exp(back);
+    r.s = wave_sum(mine.s * f);
+    r.t = wave_sum((mine.t + mine.s * back) * f);
+  }
+  if (a.k) rank_candidates<256>(c, a.k);
   write_scores(a, m, r, given, c);
 }
 
@@ -452,53 +479,100 @@ __device__ void read_teacher(const DistillArgs& a, int64_t m, Teacher& w) {
   __syncthreads();
 }
 
-// The loss, and lse where asked for, of a row with these sums (first wave).
-template <int TYPE>
-__device__ void write_loss(const DistillArgs& a, int64_t m, const Row<TYPE>& row, const Teacher& w, const Total& r) {
+// The loss, and lse where asked for, of a row with these sums; z the logit at the
+// thread's slot (first wave).
+__device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t m, const Teacher& w, const Total& r, float z) {
   if (threadIdx.x >= 64) return;
   const int j = threadIdx.x;
   const double c = 1.f / a.temperature;
   const bool ok = r.m < INFINITY && r.s > 0;
   const double lse = r.m * c + log(r.s);
   double l = 0;
-  if (w.p[j] != 0) l = w.p[j] * (w.logp[j] - (Logit<TYPE>::load(row.p, w.id[j]) * c - lse));
+  if (w.p[j] != 0) l = w.p[j] * (w.logp[j] - (z * c - lse));
   l = wave_sum(l);
   if (j == 0) {
     a.loss[m] = !w.some ? 0.f : ok ? (float)l : NAN;
     if (a.lse) a.lse[m] = ok ? (float)lse : r.m == INFINITY ? INFINITY : r.s == 0 ? -INFINITY : NAN;
   }
 }
+template <int TYPE>
+__device__ __forceinline__ float slot_logit(const Row<TYPE>& row, const Teacher& w) {
+  return threadIdx.x < 64 && w.id[threadIdx.x] >= 0 ? Logit<TYPE>::load(row.p, w.id[threadIdx.x]) : 0.f;
+}
 
-// Gradient of pieces [p0, p1) of a row (and of the elements outside the pieces):
-// f exp2(z cl - at), the teacher's tokens by themselves. Every logit is read before its
-// gradient is written (dz may be z).
+// A row's gradient f exp2((z - shift) cl), zero for a row without a slot (some = 0).
+struct Slope {
+  float shift, f, cl;
+  int some;
+  __device__ __forceinline__ float at(float z) const { return some ? f * __builtin_amdgcn_exp2f((z - shift) * cl) : 0.f; }
+};
+
+// The gradient at the thread's slot's token, where the logit is z; `mine`: this is the
+// first of the token's slots.
+__device__ __forceinline__ float slot_grad(const DistillArgs& a, int64_t m, const Teacher& w, const Slope& g, float z, bool& mine) {
+  const int j = threadIdx.x;
+  double q = 0;
+  mine = true;
+#pragma unroll 1
+  for (int i = 0; i < a.k; ++i)
+    if (w.id[i] == w.id[j]) {
+      if (i < j) mine = false;
+      q += w.p[i];
+    }
+  return (float)(g.at(z) - a.weight[m] / a.temperature * q);
+}
+
+// A piece's gradients to elements o .. of a row of dz; `vec`: on 16 bytes for whole
+// pieces of dz's type.
+template <int GRAD, int E>
+__device__ __forceinline__ void store_grads(uint8_t* out, uint32_t o, bool vec, const float (&g)[E]) {
+  if constexpr (GRAD == MOE_FP32) {
+    if (vec) *reinterpret_cast<float4*>(out + o * 4) = make_float4(g[0], g[1], g[2], g[3]);
+    else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) Logit<GRAD>::store(out, o + i, g[i]);
+    }
+  } else {
+    union {
+      uint16_t b[E];
+      uint4 q4;
+      uint2 q2;
+    } s;
+#pragma unroll
+    for (int i = 0; i < E; ++i) s.b[i] = GRAD == MOE_FP16 ? fp16_bits(g[i]) : bf16_bits(g[i]);
+    if (E == 8 && vec) *reinterpret_cast<uint4*>(out + o * 2) = s.q4;
+    else if (E == 4 && ((uintptr_t)(out + o * 2) & 7) == 0) *reinterpret_cast<uint2*>(out + o * 2) = s.q2;
+    else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) reinterpret_cast<uint16_t*>(out)[o + i] = s.b[i];
+    }
+  }
+}
+template <int GRAD>
+__device__ __forceinline__ uint8_t* grad_row(const DistillArgs& a, int64_t m) {
+  return reinterpret_cast<uint8_t*>(a.dz) + m * a.lddz * Logit<GRAD>::kBytes;
+}
+
+// The gradient of pieces [p0, p1) of a row (and of the elements outside the pieces).
 template <int TYPE, int GRAD, int THREADS>
 __device__ void write_grad(const DistillArgs& a, int64_t m, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges,
-                           const Teacher& w, float shift, float f, float cl) {
-  constexpr int E = Logit<TYPE>::kPiece;
-  uint8_t* out = reinterpret_cast<uint8_t*>(a.dz) + m * a.lddz * Logit<GRAD>::kBytes;
-  auto grad = [&](float z) __attribute__((always_inline)) { return f * __builtin_amdgcn_exp2f((z - shift) * cl); };
-  // the gradient at a slot's token, by the first of its slots
-  float at = 0.f;
+                           const Teacher& w, const Slope& g) {
+  constexpr int E = Logit<TYPE>::kPiece, NP = 2;
+  uint8_t* out = grad_row<GRAD>(a, m);
+  // every logit is read before its gradient is written (dz may be z); other workgroups
+  // write the slots of other pieces
+  float slot = 0.f;
   bool mine = false;
   if (threadIdx.x < 64 && w.id[threadIdx.x] >= 0) {
-    const int j = threadIdx.x;
-    const int64_t v = w.id[j], p = v - row.head;
-    mine = v < row.head || v >= row.V - row.tail ? edges : p / E >= p0 && p / E < p1;
-    double s = 0;
-    for (int i = 0; i < a.k; ++i)
-      if (w.id[i] == w.id[j]) {
-        if (i < j) mine = false;
-        s += w.p[i];
-      }
-    if (mine) at = (float)(grad(Logit<TYPE>::load(row.p, v)) - a.weight[m] / a.temperature * s);
+    const int64_t v = w.id[threadIdx.x], p = (v - row.head) / E;
+    if (v < row.head || v >= row.V - row.tail ? edges : p >= p0 && p < p1)
+      slot = slot_grad(a, m, w, g, Logit<TYPE>::load(row.p, v), mine);
   }
-  const float edge = edges && (int)threadIdx.x < row.edges() ? Logit<TYPE>::load(row.p, row.edge(threadIdx.x)) : 0.f;
+  const bool at_edge = edges && (int)threadIdx.x < row.edges();
+  const float edge = at_edge ? Logit<TYPE>::load(row.p, row.edge(threadIdx.x)) : 0.f;
   __syncthreads();
-  if (edges && (int)threadIdx.x < row.edges()) Logit<GRAD>::store(out, row.edge(threadIdx.x), w.some ? grad(edge) : 0.f);
-  const int64_t o0 = row.head;
-  const bool vec = ((uintptr_t)(out + o0 * Logit<GRAD>::kBytes) & 15) == 0;  // dz's pieces lie as z's
-  constexpr int NP = 2;
+  if (at_edge) Logit<GRAD>::store(out, row.edge(threadIdx.x), g.at(edge));
+  const bool vec = ((uintptr_t)(out + (int64_t)row.head * Logit<GRAD>::kBytes) & 15) == 0;  // dz's pieces lie as z's
   for (int64_t base = p0; base < p1; base += NP * THREADS) {
     uint4 q[NP];
 #pragma unroll
@@ -510,35 +584,14 @@ __device__ void write_grad(const DistillArgs& a, int64_t m, const Row<TYPE>& row
     for (int u = 0; u < NP; ++u) {
       const int64_t p = base + u * THREADS + threadIdx.x;
       if (p >= p1) continue;
-      float g[E];
+      float v[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) g[i] = w.some ? grad(Logit<TYPE>::value(q[u], i)) : 0.f;
-      const int64_t o = row.first(p);
-      if constexpr (GRAD == MOE_FP32) {
-        if (vec) *reinterpret_cast<float4*>(out + o * 4) = make_float4(g[0], g[1], g[2], g[3]);
-        else {
-#pragma unroll
-          for (int i = 0; i < E; ++i) Logit<GRAD>::store(out, o + i, g[i]);
-        }
-      } else {
-        union {
-          uint16_t b[E];
-          uint4 q4;
-          uint2 q2;
-        } s;
-#pragma unroll
-        for (int i = 0; i < E; ++i) s.b[i] = GRAD == MOE_FP16 ? fp16_bits(g[i]) : bf16_bits(g[i]);
-        if (E == 8 && vec) *reinterpret_cast<uint4*>(out + o * 2) = s.q4;
-        else if (E == 4 && ((uintptr_t)(out + o * 2) & 7) == 0) *reinterpret_cast<uint2*>(out + o * 2) = s.q2;
-        else {
-#pragma unroll
-          for (int i = 0; i < E; ++i) reinterpret_cast<uint16_t*>(out)[o + i] = s.b[i];
-        }
-      }
+      for (int i = 0; i < E; ++i) v[i] = g.at(Logit<TYPE>::value(q[u], i));
+      store_grads<GRAD>(out, (uint32_t)row.first(p), vec, v);
     }
   }
   __syncthreads();
-  if (mine) Logit<GRAD>::store(out, w.id[threadIdx.x], at);
+  if (mine) Logit<GRAD>::store(out, w.id[threadIdx.x], slot);
 }
 
 template <int TYPE, int THREADS>
@@ -579,19 +632,19 @@ __global__ __launch_bounds__(THREADS) void distill_sums_kernel(const DistillArgs
   const Total r = join<THREADS>(sum_pieces<TYPE, THREADS>(row, p0, p1, part == 0, cl), cl);
   if (parts == 1) {
     read_teacher(a, m, w);
-    write_loss<TYPE>(a, m, row, w, r);
+    write_loss(a, m, w, r, slot_logit(row, w));
   } else if (threadIdx.x == 0) {
     reinterpret_cast<ScoresPart*>(a.ws)[blockIdx.x] = {r.m, 0.f, r.s, 0};
   }
 }
 
-__device__ Total joined(const DistillArgs& a, int64_t m, int parts) {
-  const ScoresPart* p = reinterpret_cast<const ScoresPart*>(a.ws) + m * parts;
-  Total r{-FLT_MAX, 0, 0};
+__device__ Total joined(const DistillArgs& a, int64_t row, int parts) {
+  const ScoresPart* p = reinterpret_cast<const ScoresPart*>(a.ws) + row * parts;
   const double c = 1.f / a.temperature;
-  for (int i = 0; i < parts; ++i) r.m = fmaxf(r.m, p[i].m);
-  for (int i = 0; i < parts; ++i) r.s += p[i].s * exp(((double)p[i].m - r.m) * c);
-  return r;
+  const int i = threadIdx.x & 63;  // every wave the same
+  const float m = i < parts ? p[i].m : -FLT_MAX;
+  const float top = wave_max(m);
+  return {top, wave_sum(i < parts ? p[i].s * exp(((double)m - top) * c) : 0.0), 0};
 }
 
 // Forward, the parts' sums joined: the loss. (PARTS workgroups with the gradient.)
@@ -600,7 +653,7 @@ __global__ __launch_bounds__(64) void distill_loss_kernel(const DistillArgs a, i
   __shared__ Teacher w;
   const int64_t m = blockIdx.x;
   read_teacher(a, m, w);
-  write_loss<TYPE>(a, m, Row<TYPE>(a.z, m, a.ldz, a.V), w, joined(a, m, parts));
+  write_loss(a, m, w, joined(a, m, parts), slot_logit(Row<TYPE>(a.z, m, a.ldz, a.V), w));
 }
 
 // The gradient from lse (backward), or from the parts' sums.
@@ -625,7 +678,7 @@ __global__ __launch_bounds__(THREADS) void distill_grad_kernel(const DistillArgs
     shift = lse * a.temperature;
     f = fabsf(lse) < INFINITY ? f * expf(__builtin_fmaf(shift, c, -lse)) : NAN;
   }
-  write_grad<TYPE, GRAD, THREADS>(a, m, row, p0, p1, part == 0, w, shift, f, c * kLog2e);
+  write_grad<TYPE, GRAD, THREADS>(a, m, row, p0, p1, part == 0, w, Slope{shift, f, c * kLog2e, w.some});
 }
 
 // Forward and backward: a row a workgroup.
@@ -637,14 +690,129 @@ __global__ __launch_bounds__(THREADS) void distill_both_kernel(const DistillArgs
   const Row<TYPE> row(a.z, m, a.ldz, a.V);
   const Total r = join<THREADS>(sum_pieces<TYPE, THREADS>(row, 0, row.pieces, true, cl), cl);
   read_teacher(a, m, w);
-  write_loss<TYPE>(a, m, row, w, r);
+  write_loss(a, m, w, r, slot_logit(row, w));
   const float f = r.m < INFINITY && r.s > 0 ? (float)(a.weight[m] * c / r.s) : NAN;
-  write_grad<TYPE, GRAD, THREADS>(a, m, row, 0, row.pieces, true, w, r.m, f, cl);
+  write_grad<TYPE, GRAD, THREADS>(a, m, row, 0, row.pieces, true, w, Slope{r.m, f, cl, w.some});
 }
+
+// The same for rows of at most 1024 H pieces, which the threads hold between the sums
+// and the gradient: every logit is read once. A workgroup takes rows one after another
+// and loads a piece of the next as soon as that piece's gradient is on its way. dz's
+// elements have z's size and its rows z's alignment. The rows' sums and their logits at
+// the slots go to the workspace for distill_finish_kernel, which writes the loss and
+// the gradient at the slots: 64-bit functions here left no registers for the pieces.
+__device__ __forceinline__ float* slot_logits(const DistillArgs& a, int64_t m) {
+  return reinterpret_cast<float*>(reinterpret_cast<ScoresPart*>(a.ws) + a.M) + m * kMaxTop;
+}
+
+template <int TYPE, int GRAD, int H>
+__global__ __launch_bounds__(1024, TYPE == MOE_FP32 && H <= 8 ? 8 : 4) void distill_held_kernel(const DistillArgs a) {
+  constexpr int E = Logit<TYPE>::kPiece, G = 16 / E, W = 16;  // pieces summed at a time, waves
+  static_assert(H % G == 0, "whole groups");
+  __shared__ float lm[W];
+  __shared__ double ls[W];
+  __shared__ int some;
+  const float c = 1.f / a.temperature, cl = c * kLog2e;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
+  uint4 q[H];
+  uint32_t tid = threadIdx.x;
+  // Offsets are formed anew for every row, and the pieces' values for the sums and
+  // again for the gradient: kept over either they would not fit the registers.
+  auto fresh = [](uint4& p) __attribute__((always_inline)) { asm volatile("" : "+v"(p.x), "+v"(p.y), "+v"(p.z), "+v"(p.w)); };
+  auto load = [&](const Row<TYPE>& row, int h) __attribute__((always_inline)) {
+    const uint32_t p = h * 1024 + tid;
+    q[h] = p < (uint32_t)row.pieces ? ld16(row.p + row.head * Logit<TYPE>::kBytes + p * 16u) : Logit<TYPE>::none();
+  };
+  {
+    const Row<TYPE> row(a.z, blockIdx.x, a.ldz, a.V);
+#pragma unroll
+    for (int h = 0; h < H; ++h) load(row, h);
+  }
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+    const Row<TYPE> row(a.z, m, a.ldz, a.V);
+    if (threadIdx.x < 64) {
+      const int32_t id = lane < a.k ? a.ids[m * a.k + lane] : -1;
+      const bool in = id >= 0 && id < a.V;
+      if (in) slot_logits(a, m)[lane] = Logit<TYPE>::load(row.p, id);
+      const bool any = __ballot(in) != 0;
+      if (lane == 0) some = any;
+    }
+    asm volatile("" : "+v"(tid));
+    const bool at_edge = (int)tid < row.edges();
+    const float edge[1] = {at_edge ? Logit<TYPE>::load(row.p, row.edge(tid)) : -INFINITY};
+    Sums<false> sums;
+    sums.add(edge, cl);
+#pragma unroll
+    for (int h = 0; h < H; h += G) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        // (after the last group's sums: else all groups' values come first)
+        asm volatile("" : "+v"(q[h + i].x), "+v"(q[h + i].y), "+v"(q[h + i].z), "+v"(q[h + i].w), "+v"(sums.s), "+v"(sums.m));
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = Logit<TYPE>::value(q[h + i / E], i % E);
+      sums.add(v, cl);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // the sums of the threads, in 64 bits
+    float top = wave_max(sums.m);
+    if (lane == 0) lm[wave] = top;
+    __syncthreads();
+    top = wave_max(lm[lane % W]);
+    const float part = sums.s * __builtin_amdgcn_exp2f(fmaxf((sums.m - top) * cl, -1e4f));
+    const double ws = wave_sum((double)part);
+    if (lane == 0) ls[wave] = ws;
+    __syncthreads();
+    const double s = wave_sum(lane < W ? ls[lane] : 0.0);
+    if (threadIdx.x == 0) reinterpret_cast<ScoresPart*>(a.ws)[m] = {top, 0.f, s, 0};
+    const Slope g{top, top < INFINITY && s > 0 ? (float)(a.weight[m] * c / s) : NAN, cl, some};
+    uint8_t* out = grad_row<GRAD>(a, m);
+    if (at_edge) Logit<GRAD>::store(out, row.edge(tid), g.at(edge[0]));
+    const int64_t mn = m + gridDim.x;
+    const Row<TYPE> next(a.z, mn < a.M ? mn : m, a.ldz, mn < a.M ? a.V : 0);
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const uint32_t p = h * 1024 + tid;
+      fresh(q[h]);
+      if (p < (uint32_t)row.pieces) {
+        float v[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = g.at(Logit<TYPE>::value(q[h], i));
+        store_grads<GRAD>(out + row.head * Logit<GRAD>::kBytes, p * (uint32_t)E, true, v);
+      }
+      load(next, h);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();  // (all have read `some`)
+  }
+}
+
+// A row a wave: the loss, and the gradient at the slots over what stands there.
+template <int TYPE, int GRAD>
+__global__ __launch_bounds__(64) void distill_finish_kernel(const DistillArgs a) {
+  __shared__ Teacher w;
+  const int64_t m = blockIdx.x;
+  const int j = threadIdx.x;
+  const ScoresPart r = reinterpret_cast<const ScoresPart*>(a.ws)[m];
+  const float c = 1.f / a.temperature;
+  read_teacher(a, m, w);
+  const float z = w.id[j] >= 0 ? slot_logits(a, m)[j] : 0.f;
+  write_loss(a, m, w, Total{r.m, r.s, 0}, z);
+  if (w.id[j] < 0) return;
+  const Slope g{r.m, r.m < INFINITY && r.s > 0 ? (float)(a.weight[m] * c / r.s) : NAN, c * kLog2e, w.some};
+  bool mine;
+  const float v = slot_grad(a, m, w, g, z, mine);
+  if (mine) Logit<GRAD>::store(grad_row<GRAD>(a, m), w.id[j], v);
+}
+
+// Rows up to this are read again for the gradient, from the L2 (32000 of 16 bits: ).
+constexpr int64_t kHeldV = 16384;
 
 size_t distill_ws_bytes(int64_t M, int64_t V, int, int cus) {
   const int parts = parts_of(M, V, cus);
-  return parts > 1 ? (size_t)M * parts * sizeof(ScoresPart) : 0;
+  // (one part: the held rows' sums and slots)
+  return (size_t)M * (parts * sizeof(ScoresPart) + (parts == 1 && V > kHeldV ? kMaxTop * sizeof(float) : 0));
 }
 
 namespace {
@@ -658,9 +826,21 @@ hipError_t distill(DistillPass pass, const DistillArgs& a, int cus, hipStream_t 
   if (pass == kDistillBackward)
     return small ? launch_k(distill_grad_kernel<TYPE, GRAD, 128, false>, grid, block, 0, stream, Ev{}, a, parts)
                  : launch_k(distill_grad_kernel<TYPE, GRAD, 512, false>, grid, block, 0, stream, Ev{}, a, parts);
-  if (pass == kDistillBoth && parts == 1)
-    return small ? launch_k(distill_both_kernel<TYPE, GRAD, 128>, grid, block, 0, stream, Ev{}, a)
-                 : launch_k(distill_both_kernel<TYPE, GRAD, 512>, grid, block, 0, stream, Ev{}, a);
+  if (pass == kDistillBoth && parts == 1) {
+    if (small) return launch_k(distill_both_kernel<TYPE, GRAD, 128>, grid, block, 0, stream, Ev{}, a);
+    if constexpr (Logit<TYPE>::kBytes == Logit<GRAD>::kBytes) {
+      const int64_t held = (a.V / Logit<TYPE>::kPiece + 1023) / 1024;  // pieces a thread of 1024
+      const bool alike = (((uintptr_t)a.z - (uintptr_t)a.dz) & 15) == 0 && (a.ldz - a.lddz) * Logit<TYPE>::kBytes % 16 == 0;
+      if (a.V > kHeldV && alike && held <= 16) {
+        const dim3 rows((unsigned)std::min<int64_t>(a.M, a.type == MOE_FP32 && held <= 8 ? 2 * cus : cus));  // that fit at once
+        const hipError_t e = held <= 8 ? launch_k(distill_held_kernel<TYPE, GRAD, 8>, rows, dim3(1024), 0, stream, Ev{}, a)
+                                       : launch_k(distill_held_kernel<TYPE, GRAD, 16>, rows, dim3(1024), 0, stream, Ev{}, a);
+        return e != hipSuccess ? e : launch_k(distill_finish_kernel<TYPE, GRAD>, dim3((unsigned)a.M), dim3(64), 0, stream, Ev{}, a);
+      }
+    }
+    if (a.V <= 32768) return launch_k(distill_both_kernel<TYPE, GRAD, 512>, grid, block, 0, stream, Ev{}, a);
+    return launch_k(distill_both_kernel<TYPE, GRAD, 1024>, grid, dim3(1024), 0, stream, Ev{}, a);
+  }
   hipError_t e = small ? launch_k(distill_sums_kernel<TYPE, 128>, grid, block, 0, stream, Ev{}, a, parts)
                        : launch_k(distill_sums_kernel<TYPE, 512>, grid, block, 0, stream, Ev{}, a, parts);
   if (e == hipSuccess && parts > 1)
