@@ -452,8 +452,8 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  *   optimizer may update them in place between calls.
  * moe_dense_forward: x [M, K], rows ldx apart (ldx >= K); y [M, N], rows ldy >= N
  * apart, of x's type or MOE_FP32 (y_type); residual [M, N] of y's type or NULL;
- * it may be y itself (same pointer and stride). `pre`, or NULL: z [M, N] rounded
- * to x's type, rows ldp >= N apart, for moe_dense_backward.
+ * it may be y itself (same pointer and stride). `pre`, or NULL: z [M, N] in
+ * x's type or MOE_FP32 (pre_type), rows ldp >= N apart, for moe_dense_backward.
  * moe_dense_backward, of y for the upstream gradient dy [M, N] of x's type (the
  * residual's gradient is dy itself):
  *   dz = dy act'(pre), dx = dz w, dw = dz^T x, dbias = sum over rows of dz
@@ -473,18 +473,20 @@ moe_status moe_dense_create(int64_t N, int64_t K, int type, const void* w, const
 void moe_dense_destroy(moe_dense* dense);
 moe_status moe_dense_workspace_bytes(const moe_dense* dense, int64_t M, int train, size_t* bytes);
 moe_status moe_dense_forward(const moe_dense* dense, int64_t M, const void* x, int64_t ldx, const void* residual,
-                             int64_t ldr, void* y, int64_t ldy, int y_type, void* pre, int64_t ldp, void* workspace,
-                             size_t workspace_bytes, void* stream);
+                             int64_t ldr, void* y, int64_t ldy, int y_type, void* pre, int64_t ldp, int pre_type,
+                             void* workspace, size_t workspace_bytes, void* stream);
 moe_status moe_dense_backward(const moe_dense* dense, int64_t M, const void* dy, int64_t lddy, const void* pre,
-                              int64_t ldp, const void* x, int64_t ldx, void* dx, int64_t lddx, void* dw, void* dbias,
-                              void* workspace, size_t workspace_bytes, void* stream);
+                              int64_t ldp, int pre_type, const void* x, int64_t ldx, void* dx, int64_t lddx, void* dw,
+                              void* dbias, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gated feed-forward block: both projections, the activation and the product,
  *   [g u] = x w13^T,  h = act(g) u
  * w13 [2I, H] dense, rows [0, I) gate, [I, 2I) up (as the experts'), kept by the
  * handle, not copied; act any but MOE_ACT_NONE. x [M, H], rows ldx apart; h [M, I],
  * rows ldh >= I apart, of x's type, rounded once from fp32 g and u. `pre`, or
- * NULL: [M, 2I] dense, g and u rounded to x's type, for moe_gated_backward:
+ * NULL: [M, 2I] dense, g and u in x's type or MOE_FP32 (pre_type: 16 bits make the
+ * gradients' relative error 1.7 times the rounding of their own type, 32 bits 1.4
+ * times), for moe_gated_backward:
  *   dg = dh u act'(g), du = dh act(g), dx = [dg du] w13, dw13 = [dg du]^T x
  * dg and du rounded to x's type before the products. dx [M, H], rows lddx apart,
  * dw13 [2I, H] dense, of x's type; one of them may be NULL. Sizes, alignment,
@@ -495,9 +497,9 @@ moe_status moe_gated_create(int64_t I, int64_t H, int type, const void* w13, int
 void moe_gated_destroy(moe_gated* gated);
 moe_status moe_gated_workspace_bytes(const moe_gated* gated, int64_t M, int train, size_t* bytes);
 moe_status moe_gated_forward(const moe_gated* gated, int64_t M, const void* x, int64_t ldx, void* h, int64_t ldh,
-                             void* pre, void* workspace, size_t workspace_bytes, void* stream);
+                             void* pre, int pre_type, void* workspace, size_t workspace_bytes, void* stream);
 moe_status moe_gated_backward(const moe_gated* gated, int64_t M, const void* dh, int64_t lddh, const void* pre,
-                              const void* x, int64_t ldx, void* dx, int64_t lddx, void* dw13, void* workspace,
+                              int pre_type, const void* x, int64_t ldx, void* dx, int64_t lddx, void* dw13, void* workspace,
                               size_t workspace_bytes, void* stream);
 
 /* Scores of given tokens from the head's logits z [M, V] (bf16, fp16 or fp32,
@@ -585,6 +587,10 @@ int moe_plan_stage_launches(const moe_plan* plan, int64_t M, int stage);
  * 1 .. max_M. The choice goes by the sizes, x's type and the device's CUs. */
 const char* moe_router_kernel(const moe_router* router, int64_t M);
 const char* moe_linear_kernel(const moe_linear* linear, int64_t M);
+/* Of the 16-bit layers, by product: 0 forward, 1 the input's gradient, 2 the weight's
+ * (NULL for another number). */
+const char* moe_dense_kernel(const moe_dense* dense, int64_t M, int product);
+const char* moe_gated_kernel(const moe_gated* gated, int64_t M, int product);
 
 /* Static text for a status code. */
 const char* moe_status_str(moe_status status);

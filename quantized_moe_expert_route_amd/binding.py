@@ -136,12 +136,12 @@ def lib() -> ctypes.CDLL:
     for name, args in {
         "moe_dense_create": [i64, i64, ci, vp, vp, ci, i64, ph],
         "moe_dense_workspace_bytes": [vp, i64, ci, psz],
-        "moe_dense_forward": [vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, i64, vp, sz, vp],
-        "moe_dense_backward": [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, sz, vp],
+        "moe_dense_forward": [vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, i64, ci, vp, sz, vp],
+        "moe_dense_backward": [vp, i64, vp, i64, vp, i64, ci, vp, i64, vp, i64, vp, vp, vp, sz, vp],
         "moe_gated_create": [i64, i64, ci, vp, ci, i64, ph],
         "moe_gated_workspace_bytes": [vp, i64, ci, psz],
-        "moe_gated_forward": [vp, i64, vp, i64, vp, i64, vp, vp, sz, vp],
-        "moe_gated_backward": [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, sz, vp],
+        "moe_gated_forward": [vp, i64, vp, i64, vp, i64, vp, ci, vp, sz, vp],
+        "moe_gated_backward": [vp, i64, vp, i64, vp, ci, vp, i64, vp, i64, vp, vp, sz, vp],
         "moe_scores_create": [i64, i64, ci, i64, ph],
         "moe_scores_workspace_bytes": [vp, i64, psz],
         "moe_scores_forward": [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp],
@@ -153,6 +153,8 @@ def lib() -> ctypes.CDLL:
     }.items():
         f = getattr(L, name)
         f.restype, f.argtypes = st, args
+    for f in (L.moe_dense_kernel, L.moe_gated_kernel):
+        f.restype, f.argtypes = ctypes.c_char_p, [vp, i64, ci]
     for f in (L.moe_dense_destroy, L.moe_gated_destroy, L.moe_scores_destroy, L.moe_distill_destroy):
         f.restype, f.argtypes = None, [vp]
     L.moe_plan_set_tp_exchange.restype = st
@@ -430,7 +432,7 @@ class _Sized(_Handle):
         """(pointer, bytes) of a workspace tensor or None."""
         if t is None:
             return None, 0
-        import torch
+        import torch  # (a module loaded long before: a dictionary's look-up)
 
         if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or not t.is_contiguous() or t.device != self.device:
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {self.device}")
@@ -438,13 +440,32 @@ class _Sized(_Handle):
 
     def _vector(self, name, t, dtype, n):
         """Pointer of a dense vector of at least n elements."""
+        try:
+            if t.dtype is dtype and t.dim() == 1 and t.shape[0] >= n and t.device == self.device and t.is_contiguous():
+                return t.data_ptr()
+        except AttributeError:
+            raise TypeError(f"{name} must be a torch tensor") from None
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} elements on {self.device}")
+
+
+class _Product(_Sized):
+    """What Dense and Gated share."""
+
+    def _pre(self, pre, M, cols, dense=False):
+        """Row distance and type of the saved arguments: of x's type or float32."""
         import torch
 
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch tensor")
-        if t.dtype is not dtype or t.dim() != 1 or t.shape[0] < n or t.device != self.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} elements on {self.device}")
-        return t.data_ptr()
+        wide = getattr(pre, "dtype", None) is torch.float32
+        ld = self._check("pre", pre, torch.float32 if wide else self.dtype, M, cols, dense=dense)
+        return ld, FP32 if wide else self._code
+
+    def kernel(self, M: int, product: int = 0) -> str:
+        """Which of its kernels a call of M rows launches for the forward product (0),
+        the input's gradient (1) or the weight's (2) (profiling aid)."""
+        name = getattr(lib(), self._destroy.replace("destroy", "kernel"))(self._h, int(M), int(product))
+        if name is None:
+            raise ValueError(f"M = {M} outside [1, {self.max_M}], product {product} not 0, 1 or 2, or no handle")
+        return name.decode()
 
 
 def _weight(name, w, rows_even=False):
@@ -461,7 +482,7 @@ def _activation(name):
     return ACTIVATIONS[name]
 
 
-class Dense(_Sized):
+class Dense(_Product):
     """Matrix product on 16-bit weights w [N, K] with bias [N], activation and
     residual in its epilogue, and its backward pass. w and bias are kept by
     reference: an optimizer may update them in place."""
@@ -486,8 +507,8 @@ class Dense(_Sized):
 
     def forward(self, x, out, residual=None, pre=None, workspace=None, M: Optional[int] = None, stream=None):
         """out[:M] = act(x[:M] w^T + bias) (+ residual[:M]); out is of x's type or
-        float32, residual of out's, and may be out itself. `pre` [M, N] of x's type
-        takes the activation's argument, for backward."""
+        float32, residual of out's, and may be out itself. `pre` [M, N] of x's type or
+        float32 takes the activation's argument, for backward."""
         import torch
 
         M = self._rows(x, M)
@@ -496,11 +517,11 @@ class Dense(_Sized):
         y_dtype = torch.float32 if wide else self.dtype
         ldy = self._check("out", out, y_dtype, M, self.N)
         ldr = 0 if residual is None else self._check("residual", residual, y_dtype, M, self.N)
-        ldp = 0 if pre is None else self._check("pre", pre, self.dtype, M, self.N)
+        ldp, p_code = (0, self._code) if pre is None else self._pre(pre, M, self.N)
         ws, nws = self._workspace(workspace)
         self._call("moe_dense_forward", M, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
-                   out.data_ptr(), ldy, FP32 if wide else self._code, None if pre is None else pre.data_ptr(), ldp, ws, nws,
-                   self._stream(stream))
+                   out.data_ptr(), ldy, FP32 if wide else self._code, None if pre is None else pre.data_ptr(), ldp, p_code, ws,
+                   nws, self._stream(stream))
         return out
 
     def backward(self, dy, x, dx=None, dw=None, dbias=None, pre=None, workspace=None, M: Optional[int] = None, stream=None):
@@ -510,11 +531,11 @@ class Dense(_Sized):
         M = self._rows(dy, M)
         lddy = self._check("dy", dy, self.dtype, M, self.N)
         ldx = self._check("x", x, self.dtype, M, self.K)
-        ldp = lddx = 0
+        ldp, lddx, p_code = 0, 0, self._code
         if self.activation != "none":
             if pre is None:
                 raise ValueError("backward through an activation needs pre")
-            ldp = self._check("pre", pre, self.dtype, M, self.N)
+            ldp, p_code = self._pre(pre, M, self.N)
         else:
             pre = None
         if dx is not None:
@@ -522,13 +543,13 @@ class Dense(_Sized):
         if dw is not None:
             self._check("dw", dw, self.dtype, self.N, self.K, dense=True)
         ws, nws = self._workspace(workspace)
-        self._call("moe_dense_backward", M, dy.data_ptr(), lddy, None if pre is None else pre.data_ptr(), ldp, x.data_ptr(),
-                   ldx, None if dx is None else dx.data_ptr(), lddx, None if dw is None else dw.data_ptr(),
+        self._call("moe_dense_backward", M, dy.data_ptr(), lddy, None if pre is None else pre.data_ptr(), ldp, p_code,
+                   x.data_ptr(), ldx, None if dx is None else dx.data_ptr(), lddx, None if dw is None else dw.data_ptr(),
                    None if dbias is None else self._vector("dbias", dbias, self.dtype, self.N), ws, nws,
                    self._stream(stream))
 
 
-class Gated(_Sized):
+class Gated(_Product):
     """Gated feed-forward block on 16-bit weights w13 [2I, H] (rows [0, I) gate, [I,
     2I) up): h = act(x Wg^T) * (x Wu^T), and its backward pass. w13 is kept by reference."""
 
@@ -539,23 +560,23 @@ class Gated(_Sized):
         act = _activation(activation)
         self.I, self.H = w13.shape[0] // 2, w13.shape[1]
         self.w13, self.dtype, self.device, self.max_M = w13, w13.dtype, w13.device, int(max_M)
-        self.activation = activation
-        self._create("moe_gated_create", self.I, self.H, _dtype_code(w13.dtype), _ptr(w13), act, self.max_M)
+        self.activation, self._code = activation, _dtype_code(w13.dtype)
+        self._create("moe_gated_create", self.I, self.H, self._code, _ptr(w13), act, self.max_M)
 
     def workspace_bytes(self, M: int, train: bool = False) -> int:
         """Workspace of forward, with `train` of backward too, for M rows."""
         return self._bytes("moe_gated_workspace_bytes", int(M), int(bool(train)))
 
     def forward(self, x, out, pre=None, workspace=None, M: Optional[int] = None, stream=None):
-        """out[:M] [M, I]; `pre` [M, 2I] (contiguous) takes [g u], for backward."""
+        """out[:M] [M, I]; `pre` [M, 2I] (contiguous, of x's type or float32) takes [g u],
+        for backward."""
         M = self._rows(x, M)
         ldx = self._check("x", x, self.dtype, M, self.H)
         ldh = self._check("out", out, self.dtype, M, self.I)
-        if pre is not None:
-            self._check("pre", pre, self.dtype, M, 2 * self.I, dense=True)
+        p_code = self._code if pre is None else self._pre(pre, M, 2 * self.I, dense=True)[1]
         ws, nws = self._workspace(workspace)
-        self._call("moe_gated_forward", M, x.data_ptr(), ldx, out.data_ptr(), ldh, None if pre is None else pre.data_ptr(), ws,
-                   nws, self._stream(stream))
+        self._call("moe_gated_forward", M, x.data_ptr(), ldx, out.data_ptr(), ldh, None if pre is None else pre.data_ptr(),
+                   p_code, ws, nws, self._stream(stream))
         return out
 
     def backward(self, dh, x, pre, dx=None, dw=None, workspace=None, M: Optional[int] = None, stream=None):
@@ -564,12 +585,12 @@ class Gated(_Sized):
         M = self._rows(dh, M)
         lddh = self._check("dh", dh, self.dtype, M, self.I)
         ldx = self._check("x", x, self.dtype, M, self.H)
-        self._check("pre", pre, self.dtype, M, 2 * self.I, dense=True)
+        p_code = self._pre(pre, M, 2 * self.I, dense=True)[1]
         lddx = 0 if dx is None else self._check("dx", dx, self.dtype, M, self.H)
         if dw is not None:
             self._check("dw", dw, self.dtype, 2 * self.I, self.H, dense=True)
         ws, nws = self._workspace(workspace)
-        self._call("moe_gated_backward", M, dh.data_ptr(), lddh, pre.data_ptr(), x.data_ptr(), ldx,
+        self._call("moe_gated_backward", M, dh.data_ptr(), lddh, pre.data_ptr(), p_code, x.data_ptr(), ldx,
                    None if dx is None else dx.data_ptr(), lddx, None if dw is None else dw.data_ptr(), ws, nws,
                    self._stream(stream))
 

@@ -28,6 +28,16 @@ bool matrix_ok(const void* p, int64_t ld, int64_t cols, size_t elem, int64_t max
   return p && ((uintptr_t)p & (elem - 1)) == 0 && ld >= cols && ld <= max_ld;
 }
 
+// Kernel of product 0 (forward, of this kind and N columns), 1 (dx) or 2 (dw [Nw, K]).
+const char* kernel_of(GemmKind kind, int64_t M, int64_t N, int64_t Nw, int64_t K, int cus, int product) {
+  switch (product) {
+    case 0: return gemm_kernel_name(kind, M, N, K, cus);
+    case 1: return gemm_kernel_name(kGemmInput, M, K, Nw, cus);
+    case 2: return gemm_kernel_name(kGemmWeight, Nw, K, M, cus);
+  }
+  return nullptr;
+}
+
 int64_t up8(int64_t n) { return (n + 7) & ~(int64_t)7; }
 
 // Workspace of a backward pass: dz, the partial sums of dbias, split sums.
@@ -97,6 +107,10 @@ moe_status moe_dense_create(int64_t N, int64_t K, int type, const void* w, const
 
 void moe_dense_destroy(moe_dense* d) { delete d; }
 
+const char* moe_dense_kernel(const moe_dense* d, int64_t M, int product) {
+  return d && M > 0 && M <= d->max_M ? kernel_of(kGemmForward, M, d->N, d->N, d->K, d->num_cus, product) : nullptr;
+}
+
 moe_status moe_dense_workspace_bytes(const moe_dense* d, int64_t M, int train, size_t* bytes) {
   if (!d || !bytes || M < 0 || M > d->max_M || (train != 0 && train != 1)) return MOE_ERR_INVALID_ARG;
   const size_t f = gemm_ws_bytes(kGemmForward, M, d->N, d->K, d->type, d->num_cus);
@@ -106,22 +120,24 @@ moe_status moe_dense_workspace_bytes(const moe_dense* d, int64_t M, int train, s
 }
 
 moe_status moe_dense_forward(const moe_dense* d, int64_t M, const void* x, int64_t ldx, const void* residual,
-                             int64_t ldr, void* y, int64_t ldy, int y_type, void* pre, int64_t ldp, void* workspace,
+                             int64_t ldr, void* y, int64_t ldy, int y_type, void* pre, int64_t ldp, int pre_type, void* workspace,
                              size_t workspace_bytes, void* stream) {
   if (!d || M < 0 || M > d->max_M) return MOE_ERR_INVALID_ARG;
   if (y_type != d->type && y_type != MOE_FP32) return MOE_ERR_INVALID_ARG;
+  if (pre && pre_type != d->type && pre_type != MOE_FP32) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
   const size_t es = type_bytes(y_type);
   if (!operand_ok(x, ldx, d->K) || !matrix_ok(y, ldy, d->N, es)) return MOE_ERR_INVALID_ARG;
   if (residual && !matrix_ok(residual, ldr, d->N, es)) return MOE_ERR_INVALID_ARG;
-  if (pre && !matrix_ok(pre, ldp, d->N, 2)) return MOE_ERR_INVALID_ARG;
+  const size_t ps = type_bytes(pre_type);
+  if (pre && !matrix_ok(pre, ldp, d->N, ps)) return MOE_ERR_INVALID_ARG;
   const size_t need = gemm_ws_bytes(kGemmForward, M, d->N, d->K, d->type, d->num_cus);
   moe_status st = check_ws(workspace, workspace_bytes, need);
   if (st != MOE_OK) return st;
   // in place (y is the residual itself) every element is read before it is written
   const bool in_place = residual == y && ldr == ldy;
   const Buf b[] = {{y, span(M, ldy, d->N, es), true},
-                   {pre, span(M, ldp, d->N, 2), true},
+                   {pre, span(M, ldp, d->N, ps), true},
                    {workspace, need, true},
                    {residual, in_place ? 0 : span(M, ldr, d->N, es), false},
                    {x, span(M, ldx, d->K, 2), false},
@@ -131,19 +147,21 @@ moe_status moe_dense_forward(const moe_dense* d, int64_t M, const void* x, int64
   if (st != MOE_OK) return st;
   DeviceGuard guard(d->device);
   if (!guard.ok) return MOE_ERR_DEVICE;
-  GemmArgs g{M, d->N, d->K, x, d->w, ldx, d->K, d->type, d->bias, residual, y, pre, ldr, ldy, ldp, d->act, y_type, 0, 1,
+  GemmArgs g{M, d->N, d->K, x, d->w, ldx, d->K, d->type, d->bias, residual, y, pre, ldr, ldy, ldp, d->act, y_type, pre_type, 0, 1,
              workspace, need};
   return launch_gemm(kGemmForward, g, d->num_cus, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 moe_status moe_dense_backward(const moe_dense* d, int64_t M, const void* dy, int64_t lddy, const void* pre,
-                              int64_t ldp, const void* x, int64_t ldx, void* dx, int64_t lddx, void* dw, void* dbias,
+                              int64_t ldp, int pre_type, const void* x, int64_t ldx, void* dx, int64_t lddx, void* dw, void* dbias,
                               void* workspace, size_t workspace_bytes, void* stream) {
   if (!d || M < 0 || M > d->max_M || (!dx && !dw && !dbias)) return MOE_ERR_INVALID_ARG;
   const int64_t N = d->N, K = d->K;
   if (d->act == MOE_ACT_NONE) pre = nullptr;
+  if (pre && pre_type != d->type && pre_type != MOE_FP32) return MOE_ERR_INVALID_ARG;
+  const size_t ps = type_bytes(pre_type);
   if (M > 0) {
-    if (!matrix_ok(dy, lddy, N, 2) || (d->act != MOE_ACT_NONE && !matrix_ok(pre, ldp, N, 2))) return MOE_ERR_INVALID_ARG;
+    if (!matrix_ok(dy, lddy, N, 2) || (d->act != MOE_ACT_NONE && !matrix_ok(pre, ldp, N, ps))) return MOE_ERR_INVALID_ARG;
     if (dw && !operand_ok(x, ldx, K)) return MOE_ERR_INVALID_ARG;
     if (dx && !matrix_ok(dx, lddx, K, 2)) return MOE_ERR_INVALID_ARG;
   }
@@ -156,7 +174,7 @@ moe_status moe_dense_backward(const moe_dense* d, int64_t M, const void* dy, int
                    {dbias, 2 * (size_t)N, true},
                    {workspace, l.bytes, true},
                    {dy, span(M, lddy, N, 2), false},
-                   {pre, span(M, ldp, N, 2), false},
+                   {pre, span(M, ldp, N, ps), false},
                    {dw ? x : nullptr, span(M, ldx, K, 2), false},
                    {d->w, 2 * (size_t)N * K, false},
                    {d->bias, 2 * (size_t)N, false}};
@@ -171,7 +189,7 @@ moe_status moe_dense_backward(const moe_dense* d, int64_t M, const void* dy, int
   const bool need_dz = !direct && (dx || dw);
   hipError_t e = hipSuccess;
   if (need_dz || dbias) {
-    const SlopeArgs a{M, N, lddy, ldp, up8(N), dy, pre, need_dz ? ws + l.dz : nullptr, dbias, (float*)(ws + l.part), d->type, d->act};
+    const SlopeArgs a{M, N, lddy, ldp, up8(N), dy, pre, need_dz ? ws + l.dz : nullptr, dbias, (float*)(ws + l.part), d->type, d->act, pre_type};
     e = launch_slope(a, s);
   }
   if (e == hipSuccess)
@@ -202,6 +220,10 @@ moe_status moe_gated_create(int64_t I, int64_t H, int type, const void* w13, int
 
 void moe_gated_destroy(moe_gated* d) { delete d; }
 
+const char* moe_gated_kernel(const moe_gated* d, int64_t M, int product) {
+  return d && M > 0 && M <= d->max_M ? kernel_of(kGemmGated, M, d->I, 2 * d->I, d->H, d->num_cus, product) : nullptr;
+}
+
 moe_status moe_gated_workspace_bytes(const moe_gated* d, int64_t M, int train, size_t* bytes) {
   if (!d || !bytes || M < 0 || M > d->max_M || (train != 0 && train != 1)) return MOE_ERR_INVALID_ARG;
   const size_t f = gemm_ws_bytes(kGemmGated, M, d->I, d->H, d->type, d->num_cus);
@@ -211,15 +233,17 @@ moe_status moe_gated_workspace_bytes(const moe_gated* d, int64_t M, int train, s
 }
 
 moe_status moe_gated_forward(const moe_gated* d, int64_t M, const void* x, int64_t ldx, void* h, int64_t ldh,
-                             void* pre, void* workspace, size_t workspace_bytes, void* stream) {
+                             void* pre, int pre_type, void* workspace, size_t workspace_bytes, void* stream) {
   if (!d || M < 0 || M > d->max_M) return MOE_ERR_INVALID_ARG;
+  if (pre && pre_type != d->type && pre_type != MOE_FP32) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
-  if (!operand_ok(x, ldx, d->H) || !matrix_ok(h, ldh, d->I, 2) || ((uintptr_t)pre & 1)) return MOE_ERR_INVALID_ARG;
+  const size_t ps = type_bytes(pre_type);
+  if (!operand_ok(x, ldx, d->H) || !matrix_ok(h, ldh, d->I, 2) || ((uintptr_t)pre & (ps - 1))) return MOE_ERR_INVALID_ARG;
   const size_t need = gemm_ws_bytes(kGemmGated, M, d->I, d->H, d->type, d->num_cus);
   moe_status st = check_ws(workspace, workspace_bytes, need);
   if (st != MOE_OK) return st;
   const Buf b[] = {{h, span(M, ldh, d->I, 2), true},
-                   {pre, span(M, 2 * d->I, 2 * d->I, 2), true},
+                   {pre, span(M, 2 * d->I, 2 * d->I, ps), true},
                    {workspace, need, true},
                    {x, span(M, ldx, d->H, 2), false},
                    {d->w13, 4 * (size_t)d->I * d->H, false}};
@@ -227,18 +251,20 @@ moe_status moe_gated_forward(const moe_gated* d, int64_t M, const void* x, int64
   if (st != MOE_OK) return st;
   DeviceGuard guard(d->device);
   if (!guard.ok) return MOE_ERR_DEVICE;
-  GemmArgs g{M, d->I, d->H, x, d->w13, ldx, d->H, d->type, nullptr, nullptr, h, pre, 0, ldh, 2 * d->I, d->act, d->type, 0, 1,
+  GemmArgs g{M, d->I, d->H, x, d->w13, ldx, d->H, d->type, nullptr, nullptr, h, pre, 0, ldh, 2 * d->I, d->act, d->type, pre_type, 0, 1,
              workspace, need};
   return launch_gemm(kGemmGated, g, d->num_cus, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 moe_status moe_gated_backward(const moe_gated* d, int64_t M, const void* dh, int64_t lddh, const void* pre,
-                              const void* x, int64_t ldx, void* dx, int64_t lddx, void* dw13, void* workspace,
+                              int pre_type, const void* x, int64_t ldx, void* dx, int64_t lddx, void* dw13, void* workspace,
                               size_t workspace_bytes, void* stream) {
   if (!d || M < 0 || M > d->max_M || (!dx && !dw13)) return MOE_ERR_INVALID_ARG;
+  if (pre_type != d->type && pre_type != MOE_FP32) return MOE_ERR_INVALID_ARG;
+  const size_t ps = type_bytes(pre_type);
   const int64_t N = 2 * d->I, H = d->H;
   if (M > 0) {
-    if (!matrix_ok(dh, lddh, d->I, 2) || !pre || ((uintptr_t)pre & 1)) return MOE_ERR_INVALID_ARG;
+    if (!matrix_ok(dh, lddh, d->I, 2) || !pre || ((uintptr_t)pre & (ps - 1))) return MOE_ERR_INVALID_ARG;
     if (dw13 && !operand_ok(x, ldx, H)) return MOE_ERR_INVALID_ARG;
     if (dx && !matrix_ok(dx, lddx, H, 2)) return MOE_ERR_INVALID_ARG;
   }
@@ -250,7 +276,7 @@ moe_status moe_gated_backward(const moe_gated* d, int64_t M, const void* dh, int
                    {dw13, 2 * (size_t)N * H, true},
                    {workspace, l.bytes, true},
                    {dh, span(M, lddh, d->I, 2), false},
-                   {pre, span(M, N, N, 2), false},
+                   {pre, span(M, N, N, ps), false},
                    {dw13 ? x : nullptr, span(M, ldx, H, 2), false},
                    {d->w13, 2 * (size_t)N * H, false}};
   st = check_buffers(b, 7, d->device);
@@ -259,7 +285,7 @@ moe_status moe_gated_backward(const moe_gated* d, int64_t M, const void* dh, int
   if (!guard.ok) return MOE_ERR_DEVICE;
   hipStream_t s = (hipStream_t)stream;
   uint8_t* ws = (uint8_t*)workspace;
-  const GatedSlopeArgs a{M, d->I, lddh, up8(N), dh, pre, ws + l.dz, d->type, d->act};
+  const GatedSlopeArgs a{M, d->I, lddh, up8(N), dh, pre, ws + l.dz, d->type, d->act, pre_type};
   hipError_t e = launch_gated_slope(a, s);
   if (e == hipSuccess)
     e = products(M, N, H, d->type, d->num_cus, ws + l.dz, up8(N), d->w13, x, ldx, dx, lddx, dw13, ws, l, s);

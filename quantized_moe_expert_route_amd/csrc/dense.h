@@ -40,7 +40,7 @@ struct GemmArgs {
   void* y;
   void* pre;
   int64_t ldr, ldy, ldp;
-  int act, y_type;
+  int act, y_type, pre_type;
   int vec;  // set by launch_gemm: which of the matrices move in 16-byte pieces
   int splits;  // parts of K, set by launch_gemm
   // workspace of the splits' sums
@@ -59,6 +59,8 @@ hipError_t launch_gemm(GemmKind kind, const GemmArgs& a, int cus, hipStream_t st
 // bytes of GemmArgs::ws that the launch wants for these sizes
 size_t gemm_ws_bytes(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int type, int cus);
 
+const char* gemm_kernel_name(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int cus);  // rows, cols > 0
+
 // dz [M, ldz] (ldz a multiple of 8 from N on, columns past N zero) = dy act'(pre),
 // or dy itself without an activation; dbias [N] = its column sums before the rounding
 // (NULL: none; dz NULL: only dbias). part: fp32 [dbias_parts(M), N].
@@ -69,9 +71,9 @@ struct SlopeArgs {
   void* dz;
   void* dbias;
   float* part;
-  int type, act;
+  int type, act, pre_type;
 };
-constexpr int kBiasRows = 16;  // rows a partial sum of dbias takes
+constexpr int kBiasRows = 128;  // rows a partial sum of dbias takes
 inline int64_t dbias_parts(int64_t M) { return (M + kBiasRows - 1) / kBiasRows; }
 hipError_t launch_slope(const SlopeArgs& a, hipStream_t stream);
 
@@ -81,7 +83,7 @@ struct GatedSlopeArgs {
   const void* dh;
   const void* pre;
   void* dz;
-  int type, act;
+  int type, act, pre_type;
 };
 hipError_t launch_gated_slope(const GatedSlopeArgs& a, hipStream_t stream);
 

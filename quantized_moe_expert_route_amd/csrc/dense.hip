@@ -13,27 +13,54 @@ namespace qmoe {
 
 namespace {
 
-// The tiles a product may run on.
-struct Tile {
-  int rows, cols;  // of C (gated: of both products, half of them columns of y)
-};
-enum { k256x256, k256x192, k128x128, k64x64, kTiles };
-constexpr Tile kTile[kTiles] = {{256, 256}, {256, 192}, {128, 128}, {64, 64}};
-
+// The kernels a product may run on: 16 TM rows by 16 TN columns a wave (gated: of both
+// products, so half of them columns of y).
+enum { k256x256, k256x192, k128x128, k64x64, kTiles, kWave16x16 = kTiles, kWave16x32, kWave32x16, kWave32x32, kChoices };
 struct Choice {
-  int tile, splits;
+  int kernel, splits;
+};
+struct Size {
+  const char* name;
+  int rows, cols;
+};
+constexpr Size kSize[kChoices] = {
+    {"256 x 256 tile", 256, 256},
+    {"256 x 192 tile", 256, 192},
+    {"128 x 128 tile", 128, 128},
+    {"64 x 64 tile", 64, 64},
+    {"16 x 16, K split over the waves", 16, 16},
+    {"16 x 32, K split over the waves", 16, 32},
+    {"32 x 16, K split over the waves", 32, 16},
+    {"32 x 32, K split over the waves", 32, 32},
 };
 
 Choice choose(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int cus) {
-  // Rounds of workgroups over the CUs times a round's time per K-step
+  auto tiles_of = [&](int i) {
+    const int64_t bn = kind == kGemmGated ? kSize[i].cols / 2 : kSize[i].cols;
+    return ((rows + kSize[i].rows - 1) / kSize[i].rows) * ((cols + bn - 1) / bn);
+  };
+  auto rounds_of = [&](int i) { return (tiles_of(i) + cus - 1) / cus; };
+  if (kind == kGemmForward || kind == kGemmGated) {
+    // Few rows: no split sums to join by a second launch (weights from memory: 1 x 6144
+    // x 2048 12.5 us by the 64 x 64 tiles, 9.1 by 16 x 32; 16 x 16384 x 6144 56.7 and 48.5; 4
+    // x 512 x 8192 12.1, 10.9 and by 16 x 16 8.6; gated 4 x 2048 x 6144 19.3, 18.2 and 14.9).
+    if (rows <= 16) return {rounds_of(kWave16x16) * 10 <= rounds_of(kWave16x32) * 18 ? kWave16x16 : kWave16x32, 1};
+    // Tens of rows, while one round does (48 x 1536 x 1536: 9.5 us by 64 x 64, 7.4 by 32 x
+    // 32, 5.9 by 32 x 16; 77 x 1543 x 1448 11.4, 9.3 and in two rounds 10.9; 64 x 6144 x 6144
+    // 29.4, in two rounds 36.5), or weights are read once either way (24 x 16384 x 6144 55.3 and 51.4).
+    if (rows <= 128) {
+      if (rounds_of(kWave32x16) == 1) return {kWave32x16, 1};
+      if (rounds_of(kWave32x32) == 1 || rows <= 32) return {kWave32x32, 1};
+    }
+  }
+  // Rounds of workgroups over the CUs times a round's time per K-step, in units of 10 ns
   constexpr int per[kTiles] = {100, 76, 36, 18};
   constexpr int wide[kTiles] = {1, 1, 2, 2};  // workgroups a CU
   const int64_t steps = std::max<int64_t>((K + 63) / 64, 1);
   Choice best{0, 1};
   int64_t least = INT64_MAX;
   for (int i = 0; i < kTiles; ++i) {
-    const int64_t bn = kind == kGemmGated ? kTile[i].cols / 2 : kTile[i].cols;
-    const int64_t tiles = ((rows + kTile[i].rows - 1) / kTile[i].rows) * ((cols + bn - 1) / bn);
+    const int64_t tiles = tiles_of(i);
     // splits of at least 8 steps each, while they fit the chip at once
     int64_t splits = std::min(std::max<int64_t>(cus * wide[i] / tiles, 1), std::max<int64_t>(steps / 8, 1));
     splits = std::min<int64_t>(splits, 32);
@@ -47,10 +74,18 @@ Choice choose(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int cus) {
 }
 
 template <bool F16, GemmKind KIND>
-hipError_t launch(GemmArgs a, const Choice& c, hipStream_t stream) {
+hipError_t launch(GemmArgs a, const Choice& c, int cus, hipStream_t stream) {
   a.splits = c.splits;
+  if constexpr (KIND == kGemmForward || KIND == kGemmGated) {
+    switch (c.kernel) {
+      case kWave16x16: return launch_wave<F16, KIND, 1, 1, 4>(a, cus, stream);
+      case kWave16x32: return launch_wave<F16, KIND, 1, 2, 3>(a, cus, stream);
+      case kWave32x16: return launch_wave<F16, KIND, 2, 1, 2>(a, cus, stream);
+      case kWave32x32: return launch_wave<F16, KIND, 2, 2, 2>(a, cus, stream);
+    }
+  }
   hipError_t e;
-  switch (c.tile) {
+  switch (c.kernel) {
     case k256x256: e = launch_tile<F16, KIND, 8, 4, 2, 4, 2>(a, stream); break;
     case k256x192: e = launch_tile<F16, KIND, 4, 6, 4, 2, 2>(a, stream); break;
     case k128x128: e = launch_tile<F16, KIND, 4, 4, 2, 2, 2>(a, stream); break;
@@ -72,43 +107,53 @@ size_t gemm_ws_bytes(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int, 
   return c.splits > 1 ? (size_t)c.splits * rows * ((cols + 7) / 8 * 8) * (kind == kGemmGated ? 8 : 4) : 0;
 }
 
+const char* gemm_kernel_name(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int cus) {
+  return kSize[choose(kind, rows, cols, K, cus).kernel].name;
+}
+
 hipError_t launch_gemm(GemmKind kind, const GemmArgs& args, int cus, hipStream_t stream) {
   GemmArgs a = args;
-  const int64_t es = a.y_type == MOE_FP32 ? 4 : 2;
+  const int64_t es = a.y_type == MOE_FP32 ? 4 : 2, ps = a.pre_type == MOE_FP32 ? 4 : 2;
   auto vec = [](const void* p, int64_t ld, int64_t elem) { return p && ((uintptr_t)p & 15) == 0 && ld * elem % 16 == 0; };
   a.vec = (vec(a.y, a.ldy, es) ? kVecY : 0) | (vec(a.residual, a.ldr, es) ? kVecResidual : 0) |
-          (vec(a.pre, a.ldp, 2) && (kind != kGemmGated || a.cols % 8 == 0) ? kVecPre : 0) | (vec(a.bias, 0, 2) ? kVecBias : 0);
+          (vec(a.pre, a.ldp, ps) && (kind != kGemmGated || a.cols * ps % 16 == 0) ? kVecPre : 0) | (vec(a.bias, 0, 2) ? kVecBias : 0);
   const bool f16 = a.type == MOE_FP16;
   const Choice c = choose(kind, a.rows, a.cols, a.K, cus);
   switch (kind) {
-    case kGemmForward: return f16 ? launch<true, kGemmForward>(a, c, stream) : launch<false, kGemmForward>(a, c, stream);
-    case kGemmGated: return f16 ? launch<true, kGemmGated>(a, c, stream) : launch<false, kGemmGated>(a, c, stream);
-    case kGemmInput: return f16 ? launch<true, kGemmInput>(a, c, stream) : launch<false, kGemmInput>(a, c, stream);
-    default: return f16 ? launch<true, kGemmWeight>(a, c, stream) : launch<false, kGemmWeight>(a, c, stream);
+    case kGemmForward: return f16 ? launch<true, kGemmForward>(a, c, cus, stream) : launch<false, kGemmForward>(a, c, cus, stream);
+    case kGemmGated: return f16 ? launch<true, kGemmGated>(a, c, cus, stream) : launch<false, kGemmGated>(a, c, cus, stream);
+    case kGemmInput: return f16 ? launch<true, kGemmInput>(a, c, cus, stream) : launch<false, kGemmInput>(a, c, cus, stream);
+    default: return f16 ? launch<true, kGemmWeight>(a, c, cus, stream) : launch<false, kGemmWeight>(a, c, cus, stream);
   }
 }
 
 // ----------------------------------------------------------------- backward, elementwise
-// A lane takes eight columns, a wave a row's 512 at a time; the four waves of a
-// workgroup take kBiasRows rows in turn. dbias's sums of a workgroup are joined in the
-// order of its waves, those of all workgroups in the order of the rows by a second
-// launch. Bound by memory.
+// Up to 8 values of pre.
 template <bool F16>
-__global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a, int vec) {
-  __shared__ float sums[4][512];
+__device__ __forceinline__ void read_pre(const void* pre, int type, int64_t at, bool vec, int n, float (&v)[8]) {
+  if (type == MOE_FP32) read8<F16, true>(reinterpret_cast<const float*>(pre) + at, vec, n, v);
+  else read8<F16, false>(reinterpret_cast<const uint16_t*>(pre) + at, vec, n, v);
+}
+
+// 64 columns a workgroup, eight a lane: a wave takes eight rows of them at a time, the
+// 16 waves 128. dbias's sums of a workgroup are joined in a fixed order, those of
+// several workgroups (kBiasRows rows each) by a second launch. Bound by memory.
+template <bool F16>
+__global__ __launch_bounds__(1024) void slope_kernel(const SlopeArgs a, int vec) {
+  __shared__ float sums[16][64];
   const int wave = wave_id(), lane = threadIdx.x & 63;
-  const int64_t n = ((int64_t)blockIdx.x * 64 + lane) * 8;
+  const int64_t n = (int64_t)blockIdx.x * 64 + (lane & 7) * 8;
   const int64_t m0 = (int64_t)blockIdx.y * kBiasRows, m1 = min(m0 + kBiasRows, a.M);
   const int left = (int)max((int64_t)0, min((int64_t)8, a.N - n));
   float sum[8] = {};
   if (left > 0) {
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
-#pragma unroll 4
-      for (int64_t m = m0 + wave; m < m1; m += 4) {
+#pragma unroll 2
+      for (int64_t m = m0 + 8 * wave + (lane >> 3); m < m1; m += 128) {
         float v[8], p[8];
         read8<F16, false>(reinterpret_cast<const uint16_t*>(a.dy) + m * a.lddy + n, vec & 1, left, v);
         if constexpr (act != MOE_ACT_NONE) {
-          read8<F16, false>(reinterpret_cast<const uint16_t*>(a.pre) + m * a.ldp + n, vec & 2, left, p);
+          read_pre<F16>(a.pre, a.pre_type, m * a.ldp + n, vec & 2, left, p);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float y;
@@ -124,12 +169,19 @@ __global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a, int vec) 
   }
   if (!a.dbias) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sums[wave][i * 64 + lane] = sum[i];
-  __syncthreads();
-  for (int i = threadIdx.x; i < 512; i += 256) {
-    const int64_t c = (int64_t)blockIdx.x * 512 + (i & 63) * 8 + (i >> 6);
-    if (c < a.N) a.part[blockIdx.y * a.N + c] = sums[0][i] + sums[1][i] + sums[2][i] + sums[3][i];
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int o = 8; o < 64; o *= 2) sum[i] += __shfl_xor(sum[i], o, kWave);
+    if (lane < 8) sums[wave][lane * 8 + i] = sum[i];
   }
+  __syncthreads();
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  if (wave > 0 || c >= a.N) return;
+  float v = sums[0][lane];
+#pragma unroll
+  for (int w = 1; w < 16; ++w) v += sums[w][lane];
+  if (gridDim.y == 1) reinterpret_cast<uint16_t*>(a.dbias)[c] = bits16<F16>(v);
+  else a.part[blockIdx.y * a.N + c] = v;
 }
 
 // 64 columns a workgroup; its 16 waves take the partial sums in turn.
@@ -153,28 +205,25 @@ __global__ __launch_bounds__(1024) void dbias_kernel(const float* __restrict__ p
   }
 }
 
-static bool on16(const void* p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
+static bool on16(const void* p, int64_t ld, int64_t elem) { return ((uintptr_t)p & 15) == 0 && ld * elem % 16 == 0; }
 
 hipError_t launch_slope(const SlopeArgs& a, hipStream_t stream) {
   const bool f16 = a.type == MOE_FP16;
-  const int64_t parts = dbias_parts(a.M);
-  hipError_t e = hipSuccess;
-  if (a.M > 0) {
-    const int vec = (on16(a.dy, a.lddy) ? 1 : 0) | (a.pre && on16(a.pre, a.ldp) ? 2 : 0);
-    const dim3 grid((unsigned)((a.N + 511) / 512), (unsigned)parts);
-    e = f16 ? launch_k(slope_kernel<true>, grid, dim3(256), 0, stream, Ev{}, a, vec)
-            : launch_k(slope_kernel<false>, grid, dim3(256), 0, stream, Ev{}, a, vec);
-  }
-  if (e == hipSuccess && a.dbias) {
-    const dim3 grid((unsigned)((a.N + 63) / 64));
-    e = f16 ? launch_k(dbias_kernel<true>, grid, dim3(1024), 0, stream, Ev{}, (const float*)a.part, (uint16_t*)a.dbias, a.N, parts)
-            : launch_k(dbias_kernel<false>, grid, dim3(1024), 0, stream, Ev{}, (const float*)a.part, (uint16_t*)a.dbias, a.N, parts);
+  const int vec = (on16(a.dy, a.lddy, 2) ? 1 : 0) | (a.pre && on16(a.pre, a.ldp, a.pre_type == MOE_FP32 ? 4 : 2) ? 2 : 0);
+  const int64_t parts = std::max<int64_t>(dbias_parts(a.M), 1);  // (no rows: dbias is zero)
+  const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)parts);
+  hipError_t e = f16 ? launch_k(slope_kernel<true>, grid, dim3(1024), 0, stream, Ev{}, a, vec)
+                     : launch_k(slope_kernel<false>, grid, dim3(1024), 0, stream, Ev{}, a, vec);
+  if (e == hipSuccess && a.dbias && parts > 1) {
+    const dim3 cols((unsigned)((a.N + 63) / 64));
+    e = f16 ? launch_k(dbias_kernel<true>, cols, dim3(1024), 0, stream, Ev{}, (const float*)a.part, (uint16_t*)a.dbias, a.N, parts)
+            : launch_k(dbias_kernel<false>, cols, dim3(1024), 0, stream, Ev{}, (const float*)a.part, (uint16_t*)a.dbias, a.N, parts);
   }
   return e;
 }
 
-// Eight columns of I of a row a lane, both halves of dz. vec: 1 dh, 2 pre's and dz's
-// rows and halves move in 16-byte pieces.
+// Eight columns of I of a row a lane, both halves of dz. vec: the rows and halves of dh
+// (1), pre (2) and dz (4) move in 16-byte pieces.
 template <bool F16>
 __global__ __launch_bounds__(256) void gated_slope_kernel(const GatedSlopeArgs a, int vec) {
   const int64_t pieces = (a.I + 7) / 8;
@@ -185,11 +234,10 @@ __global__ __launch_bounds__(256) void gated_slope_kernel(const GatedSlopeArgs a
         if (i >= pieces) break;
         const int left = (int)min((int64_t)8, a.I - n);
         float d[8], g[8], u[8];
-        const uint16_t* pre = reinterpret_cast<const uint16_t*>(a.pre) + m * 2 * a.I + n;
         uint16_t* dz = reinterpret_cast<uint16_t*>(a.dz) + m * a.ldz + n;
         read8<F16, false>(reinterpret_cast<const uint16_t*>(a.dh) + m * a.lddh + n, vec & 1, left, d);
-        read8<F16, false>(pre, vec & 2, left, g);
-        read8<F16, false>(pre + a.I, vec & 2, left, u);
+        read_pre<F16>(a.pre, a.pre_type, m * 2 * a.I + n, vec & 2, left, g);
+        read_pre<F16>(a.pre, a.pre_type, m * 2 * a.I + a.I + n, vec & 2, left, u);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           float value;
@@ -197,8 +245,8 @@ __global__ __launch_bounds__(256) void gated_slope_kernel(const GatedSlopeArgs a
           g[q] = d[q] * u[q] * s;
           u[q] = d[q] * value;
         }
-        write8<F16, false>(dz, vec & 2, left, g);
-        write8<F16, false>(dz + a.I, vec & 2, left, u);
+        write8<F16, false>(dz, vec & 4, left, g);
+        write8<F16, false>(dz + a.I, vec & 4, left, u);
         if (i == 0)  // what pads the row
           for (int64_t c = 2 * a.I; c < a.ldz; ++c) reinterpret_cast<uint16_t*>(a.dz)[m * a.ldz + c] = 0;
       }
@@ -207,7 +255,7 @@ __global__ __launch_bounds__(256) void gated_slope_kernel(const GatedSlopeArgs a
 
 hipError_t launch_gated_slope(const GatedSlopeArgs& a, hipStream_t stream) {
   if (a.M == 0) return hipSuccess;
-  const int vec = (on16(a.dh, a.lddh) ? 1 : 0) | (on16(a.pre, a.I) ? 2 : 0);
+  const int vec = (on16(a.dh, a.lddh, 2) ? 1 : 0) | (on16(a.pre, a.I, a.pre_type == MOE_FP32 ? 4 : 2) ? 2 : 0) | (a.I % 8 == 0 ? 4 : 0);
   const dim3 grid((unsigned)((a.I + 2047) / 2048), (unsigned)std::min<int64_t>(a.M, 65535));
   return a.type == MOE_FP16 ? launch_k(gated_slope_kernel<true>, grid, dim3(256), 0, stream, Ev{}, a, vec)
                             : launch_k(gated_slope_kernel<false>, grid, dim3(256), 0, stream, Ev{}, a, vec);

@@ -16,6 +16,7 @@
 //            by the bits of k that tell apart the 8 k a half wave reads at a time.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "act.h"
@@ -107,6 +108,8 @@ struct Operand {
     for (int i = 0; i < kLoads; ++i)
       if (left[i] + k <= 0) off[i] = kOutside;
   }
+  // offset i with k of K left
+  __device__ __forceinline__ uint32_t offset(int i, int k) const { return left[i] + k > 0 ? off[i] : kOutside; }
   // load i of the wave's. second: buffer of the rows from R / 2 on (gated: the other half of B's rows)
   __device__ __forceinline__ void load(int i, v4i buffer, v4i second, uint32_t lds, int wave) const {
     load_lds16(!BY_K && i * W + wave >= R / 16 ? second : buffer, off[i], lds + (uint32_t)(i * W + wave) * 1024);
@@ -189,6 +192,12 @@ __device__ __forceinline__ void write8(void* p, bool vec, int n, const float (&v
   }
 }
 
+template <bool F16>
+__device__ __forceinline__ void write_pre(const GemmArgs& a, int64_t at, int n, const float (&v)[8]) {
+  if (a.pre_type == MOE_FP32) write8<F16, true>(reinterpret_cast<float*>(a.pre) + at, a.vec & kVecPre, n, v);
+  else write8<F16, false>(reinterpret_cast<uint16_t*>(a.pre) + at, a.vec & kVecPre, n, v);
+}
+
 // Eight columns n .. n + 7 of row m from their sums (n < cols); gated: `up` the
 // second product's.
 template <bool F16, GemmKind KIND>
@@ -198,9 +207,8 @@ __device__ __forceinline__ void store8(const GemmArgs& a, int64_t m, int64_t n, 
   uint16_t* y16 = reinterpret_cast<uint16_t*>(a.y) + m * a.ldy + n;
   if constexpr (KIND == kGemmGated) {
     if (a.pre) {
-      uint16_t* p = reinterpret_cast<uint16_t*>(a.pre) + m * a.ldp + n;
-      write8<F16, false>(p, a.vec & kVecPre, left, c);
-      write8<F16, false>(p + a.cols, a.vec & kVecPre, left, up);
+      write_pre<F16>(a, m * a.ldp + n, left, c);
+      write_pre<F16>(a, m * a.ldp + a.cols + n, left, up);
     }
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
@@ -214,7 +222,7 @@ __device__ __forceinline__ void store8(const GemmArgs& a, int64_t m, int64_t n, 
 #pragma unroll
       for (int i = 0; i < 8; ++i) c[i] += t[i];
     }
-    if (a.pre) write8<F16, false>(reinterpret_cast<uint16_t*>(a.pre) + m * a.ldp + n, a.vec & kVecPre, left, c);
+    if (a.pre) write_pre<F16>(a, m * a.ldp + n, left, c);
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) c[i] = act_value<act>(c[i]);
@@ -424,6 +432,132 @@ __global__ __launch_bounds__(256) void split_join_kernel(const GemmArgs a) {
     }
     store8<F16, KIND>(a, m, n, v, up);
   }
+}
+
+// ----------------------------------------------------------------- few rows
+// 16 TM rows by 16 TN columns (gated: 8 TN of both products) a workgroup at a time. Its
+// eight waves share no operand: they take the K-steps of 64 in turn, each through S
+// buffers of its own, without a barrier, and join their sums through LDS at the end of a
+// tile. A workgroup takes tiles one after another; the loads run on over their ends.
+template <bool F16, GemmKind KIND, int TM, int TN, int S>
+__global__ __launch_bounds__(512) void gemm_wave_kernel(const GemmArgs a, int tiles_m, int tiles_n) {
+  constexpr int W = 8, BM = 16 * TM, BN = 16 * TN;
+  constexpr bool gated = KIND == kGemmGated;
+  constexpr int cols = gated ? BN / 2 : BN;
+  static_assert(KIND == kGemmForward || gated, "operands along K");
+  typedef Operand<false, BM, 1> OpA;
+  typedef Operand<false, BN, 1> OpB;
+  constexpr int kStage = OpA::kBytes + OpB::kBytes, kLoads = OpA::kLoads + OpB::kLoads;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[W * S * kStage];
+  __shared__ float sums[W][BM][BN];
+  const int wave = wave_id(), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int tiles = tiles_m * tiles_n, step = gridDim.x;
+  const int steps = (int)((a.K + 63) / 64), per = (steps + W - 1) / W;  // K-steps, of a wave (some of them past K)
+  const uint32_t base = __builtin_amdgcn_readfirstlane(lds_address(lds)) + wave * (S * kStage);
+  const uint8_t* mine = lds + wave * (S * kStage);
+
+  // Loads run S steps ahead: those of step `at` of tile `tile`.
+  OpA la;
+  OpB lb;
+  const uint16_t *pa, *pb;
+  int tile = blockIdx.x, at = 0, buffer = 0;
+  auto begin_tile = [&]() __attribute__((always_inline)) {
+    if (tile >= tiles) return;
+    const int64_t m0 = (int64_t)(tile / tiles_n) * BM, n0 = (int64_t)(tile % tiles_n) * cols;
+    la.init(0, lane, a.lda, a.rows - m0);
+    if constexpr (gated) {
+      lb.init(0, lane, a.ldb, BN);
+#pragma unroll
+      for (int i = 0; i < OpB::kLoads; ++i) {
+        const int piece = i * 64 + lane, row = (piece >> 3) % (BN / 2), chunk = (piece & 7) ^ (piece >> 4 & 7);
+        lb.off[i] = n0 + row < a.cols ? (uint32_t)(row * a.ldb * 2 + chunk * 16) : kOutside;
+      }
+    } else {
+      lb.init(0, lane, a.ldb, a.cols - n0);
+    }
+    pa = reinterpret_cast<const uint16_t*>(a.a) + m0 * a.lda;
+    pb = reinterpret_cast<const uint16_t*>(a.b) + n0 * a.ldb;
+  };
+  auto load = [&]() __attribute__((always_inline)) {
+    const int t = at * W + wave, left = tile < tiles ? (int)min(a.K - (int64_t)t * 64, (int64_t)64) : 0;
+    const int64_t k = left > 0 ? (int64_t)t * 64 : 0;
+    const v4i ba = buffer_at(pa + k), bb = buffer_at(pb + k);
+    const v4i bc = gated ? buffer_at(pb + a.cols * a.ldb + k) : bb;
+    const uint32_t to = base + (uint32_t)buffer * kStage;
+#pragma unroll
+    for (int i = 0; i < OpA::kLoads; ++i) load_lds16(ba, la.offset(i, left), to + i * 1024);
+#pragma unroll
+    for (int i = 0; i < OpB::kLoads; ++i)
+      load_lds16(gated && i >= OpB::kLoads / 2 ? bc : bb, lb.offset(i, left), to + OpA::kBytes + i * 1024);
+    buffer = buffer + 1 == S ? 0 : buffer + 1;
+    if (++at == per) {
+      at = 0;
+      tile += step;
+      begin_tile();
+    }
+  };
+  begin_tile();
+#pragma unroll
+  for (int i = 0; i < S; ++i) load();
+  int from = 0;
+  for (int now = blockIdx.x; now < tiles; now += step) {
+    v4f acc[TN][TM];
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+      for (int u = 0; u < TM; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < per; ++i) {
+      asm volatile("s_waitcnt vmcnt(%0)" : : "n"((S - 1) * kLoads) : "memory");
+      const uint8_t* sa = mine + from * kStage;
+      const uint8_t* sb = sa + OpA::kBytes;
+      uint4 fa[2][TM], fb[2][TN];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int t = 0; t < TN; ++t) fb[j][t] = OpB::fragment(sb, t, j, r, g);
+#pragma unroll
+        for (int u = 0; u < TM; ++u) fa[j][u] = OpA::fragment(sa, u, j, r, g);
+      }
+      from = from + 1 == S ? 0 : from + 1;
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // read before it is loaded anew
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+#pragma unroll
+          for (int u = 0; u < TM; ++u) acc[t][u] = mfma16<F16>(fb[j][t], fa[j][u], acc[t][u]);
+      load();
+    }
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+      for (int u = 0; u < TM; ++u) *reinterpret_cast<v4f*>(&sums[wave][16 * u + r][16 * t + 4 * g]) = acc[t][u];
+    barrier_lds();
+    const int64_t m0 = (int64_t)(now / tiles_n) * BM, n0 = (int64_t)(now % tiles_n) * cols;
+    constexpr int pieces = cols / 8;
+    for (int i = threadIdx.x; i < BM * pieces; i += 64 * W) {
+      const int row = i / pieces, c = i % pieces * 8;
+      float v[8] = {}, up[8] = {};
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          v[q] += sums[w][row][c + q];
+          if constexpr (gated) up[q] += sums[w][row][cols + c + q];
+        }
+      if (m0 + row < a.rows && n0 + c < a.cols) store8<F16, KIND>(a, m0 + row, n0 + c, v, up);
+    }
+    barrier_lds();
+  }
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // no load to LDS outlives the workgroup
+}
+
+template <bool F16, GemmKind KIND, int TM, int TN, int S>
+hipError_t launch_wave(const GemmArgs& a, int cus, hipStream_t stream) {
+  constexpr int cols = 16 * TN / (KIND == kGemmGated ? 2 : 1);
+  const int64_t tm = (a.rows + 16 * TM - 1) / (16 * TM), tn = (a.cols + cols - 1) / cols;
+  return launch_k(gemm_wave_kernel<F16, KIND, TM, TN, S>, dim3((unsigned)std::min<int64_t>(tm * tn, cus)), dim3(512), 0,
+                  stream, Ev{}, a, (int)tm, (int)tn);
 }
 
 template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN, int S>

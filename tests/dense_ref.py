@@ -61,8 +61,9 @@ def rounding(t, v):
     return half_step(t) * v.abs() + (2.0 ** -25 if t == "fp16" else 2.0 ** -134)
 
 
-def dense(x, w, bias, name, residual, t, yt):
-    """(y, bound, z, bound of z saved in type t)."""
+def dense(x, w, bias, name, residual, t, yt, pt=None):
+    """(y, bound, z, bound of z saved in type pt, t by itself)."""
+    pt = pt or t
     z, mag = x @ w.T, x.abs() @ w.abs().T
     if bias is not None:
         z, mag = z + bias, mag + bias.abs()
@@ -72,7 +73,7 @@ def dense(x, w, bias, name, residual, t, yt):
     if residual is not None:
         y = y + residual
         ey = ey + U * (y.abs() + ey)
-    return y, ey * (1 + half_step(yt)) + rounding(yt, y), z, ez * (1 + half_step(t)) + rounding(t, z)
+    return y, ey * (1 + half_step(yt)) + rounding(yt, y), z, ez * (1 + half_step(pt)) + rounding(pt, z)
 
 
 def products(dz, edz, x, w, t):
@@ -95,8 +96,9 @@ def dense_backward(dy, pre, x, w, name, t):
     return products(dz, edz, x, w, t) + [(db, eb * (1 + half_step(t)) + rounding(t, db))]
 
 
-def gated(x, w13, name, t):
-    """(h, bound, pre, bound)."""
+def gated(x, w13, name, t, pt=None):
+    """(h, bound, pre, bound of pre in type pt, t by itself)."""
+    pt = pt or t
     gu, mag = x @ w13.T, x.abs() @ w13.abs().T
     e = sum_error(x.shape[1]) * mag
     (g, u), (eg, eu) = gu.chunk(2, 1), e.chunk(2, 1)
@@ -104,7 +106,7 @@ def gated(x, w13, name, t):
     ea = MAX_SLOPE * eg + act_error(g.abs() + eg)
     h = a * u
     eh = ea * (u.abs() + eu) + a.abs() * eu + U * h.abs()
-    return h, eh * (1 + half_step(t)) + rounding(t, h), gu, e * (1 + half_step(t)) + rounding(t, gu)
+    return h, eh * (1 + half_step(t)) + rounding(t, h), gu, e * (1 + half_step(pt)) + rounding(pt, gu)
 
 
 def gated_backward(dh, pre, x, w13, name, t):

@@ -75,10 +75,10 @@ def test_null_handles():
     assert L.moe_gated_workspace_bytes(None, 1, 0, ctypes.byref(n)) == BAD
     assert L.moe_scores_workspace_bytes(None, 1, ctypes.byref(n)) == BAD
     assert L.moe_distill_workspace_bytes(None, 1, ctypes.byref(n)) == BAD
-    assert L.moe_dense_forward(None, 1, A, 64, None, 0, A2, 16, 0, None, 0, None, 0, None) == BAD
-    assert L.moe_dense_backward(None, 1, A, 16, None, 0, A2, 64, A3, 64, None, None, None, 0, None) == BAD
-    assert L.moe_gated_forward(None, 1, A, 64, A2, 16, None, None, 0, None) == BAD
-    assert L.moe_gated_backward(None, 1, A, 16, A2, A3, 64, None, 0, A, None, 0, None) == BAD
+    assert L.moe_dense_forward(None, 1, A, 64, None, 0, A2, 16, 0, None, 0, 0, None, 0, None) == BAD
+    assert L.moe_dense_backward(None, 1, A, 16, None, 0, 0, A2, 64, A3, 64, None, None, None, 0, None) == BAD
+    assert L.moe_gated_forward(None, 1, A, 64, A2, 16, None, 0, None, 0, None) == BAD
+    assert L.moe_gated_backward(None, 1, A, 16, A2, 0, A3, 64, None, 0, A, None, 0, None) == BAD
     assert L.moe_scores_forward(None, 1, A, 16, A2, A3, None, None, None, None, None, 0, None) == BAD
     assert L.moe_distill_forward(None, 1, A, 16, A2, A3, A, None, None, 0, None) == BAD
     assert L.moe_distill_backward(None, 1, A, 16, A2, A3, A, A, A, 16, None) == BAD
@@ -104,7 +104,7 @@ def test_binding_refuses_bad_tensors_dense():
     base = dict(x=x, out=y, residual=y, pre=y)
     for bad in (dict(x=x.float()), dict(x=x[:, :32]), dict(x=torch.zeros(64, 4, dtype=BF).t()), dict(x=None), dict(x=x[:0], M=1),
                 dict(x=torch.zeros(5, 64, dtype=BF)), dict(out=y.half()), dict(out=y[:2]), dict(residual=y.float()),
-                dict(residual=y[:, :20]), dict(pre=y.float()), dict(pre=y[:3]), dict(M=-1), dict(M=5),
+                dict(residual=y[:, :20]), dict(pre=y.double()), dict(pre=y[:3]), dict(M=-1), dict(M=5),
                 dict(workspace=torch.zeros(8)), dict(workspace=torch.zeros(16, dtype=torch.uint8)[::2])):
         with pytest.raises((ValueError, TypeError, AttributeError)):
             op.forward(**{**base, **bad})
@@ -117,7 +117,7 @@ def test_binding_refuses_bad_tensors_dense():
 
 
 def test_binding_refuses_bad_tensors_gated():
-    op = _bare(B.Gated, device=CPU, max_M=4, I=12, H=64, dtype=BF)
+    op = _bare(B.Gated, device=CPU, max_M=4, I=12, H=64, dtype=BF, _code=B.BF16)
     x, h, pre, w = torch.zeros(4, 64, dtype=BF), torch.zeros(4, 12, dtype=BF), torch.zeros(4, 24, dtype=BF), torch.zeros(24, 64, dtype=BF)
     for bad in (dict(x=x.half()), dict(out=h[:, :8]), dict(pre=pre[:, :12]), dict(pre=torch.zeros(4, 48, dtype=BF)[:, :24]),
                 dict(pre=pre[:3]), dict(M=5), dict(workspace=x)):

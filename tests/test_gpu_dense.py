@@ -62,7 +62,7 @@ def _f64(t):
 
 def _forward(d, op):
     M, N = d["dy"].shape
-    y, pre = _nan((M, N), DT[d["yt"]]), _nan((M, N), DT[d["t"]])
+    y, pre = _nan((M, N), DT[d["yt"]]), _nan((M, N), DT[d.get("pt", d["t"])])
     op.forward(_cuda(d["x"]), y, residual=_cuda(d["residual"]), pre=pre, workspace=_ws(op.workspace_bytes(M)))
     return y, pre
 
@@ -106,6 +106,20 @@ def test_random_within_the_bound(M, N, K, t, yt, act):
     op = _dense(d, max_M=M)
     y, pre = _forward(d, op)
     ye, ey, z, ez = R.dense(_f64(d["x"]), _f64(d["w"]), _f64(d["bias"]), act, _f64(d["residual"]), t, yt)
+    _within(y, ye, ey, "y")
+    _within(pre, z, ez, "pre")
+    grads = R.dense_backward(_f64(d["dy"]), _f64(pre.cpu()), _f64(d["x"]), _f64(d["w"]), act, t)
+    for got, (want, bound), what in zip(_backward(d, op, pre), grads, ("dx", "dw", "dbias")):
+        _within(got, want, bound, what)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 24, 72), (40, 83, 264), (130, 200, 328)])
+@pytest.mark.parametrize("t,act", [("bf16", "gelu"), ("fp16", "silu")])
+def test_pre_in_32_bits(M, N, K, t, act):
+    d = dict(_case(M, M, N, K, t, act), pt="fp32")
+    op = _dense(d, max_M=M)
+    y, pre = _forward(d, op)
+    ye, ey, z, ez = R.dense(_f64(d["x"]), _f64(d["w"]), _f64(d["bias"]), act, _f64(d["residual"]), t, t, pt="fp32")
     _within(y, ye, ey, "y")
     _within(pre, z, ez, "pre")
     grads = R.dense_backward(_f64(d["dy"]), _f64(pre.cpu()), _f64(d["x"]), _f64(d["w"]), act, t)
@@ -225,16 +239,17 @@ def _gated_case(seed, M, I, H, t, ints=False):
 
 
 @pytest.mark.parametrize("M,I,H", GATED)
-@pytest.mark.parametrize("t,act", [("bf16", "silu"), ("fp16", "gelu_tanh"), ("bf16", "gelu"), ("fp16", "relu")])
-def test_gated_within_the_bound(M, I, H, t, act):
+@pytest.mark.parametrize("t,act,pt", [("bf16", "silu", "bf16"), ("fp16", "gelu_tanh", "fp32"), ("bf16", "gelu", "fp32"),
+                                      ("fp16", "relu", "fp16")])
+def test_gated_within_the_bound(M, I, H, t, act, pt):
     from quantized_moe_expert_route_amd.binding import Gated
 
     d = _gated_case(M + I, M, I, H, t)
     op = Gated(_cuda(d["w"]), activation=act, max_M=M)
-    h, pre, dx, dw = _nan((M, I), DT[t]), _nan((M, 2 * I), DT[t]), _nan((M, H), DT[t]), _nan((2 * I, H), DT[t])
+    h, pre, dx, dw = _nan((M, I), DT[t]), _nan((M, 2 * I), DT[pt]), _nan((M, H), DT[t]), _nan((2 * I, H), DT[t])
     ws = _ws(op.workspace_bytes(M, train=True))
     op.forward(_cuda(d["x"]), h, pre=pre, workspace=ws)
-    he, eh, gu, egu = R.gated(_f64(d["x"]), _f64(d["w"]), act, t)
+    he, eh, gu, egu = R.gated(_f64(d["x"]), _f64(d["w"]), act, t, pt)
     _within(h, he, eh, "h")
     _within(pre, gu, egu, "pre")
     op.backward(_cuda(d["dh"]), _cuda(d["x"]), pre, dx=dx, dw=dw, workspace=ws)
