@@ -53,22 +53,29 @@ Choice choose(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int cus) {
       if (rounds_of(kWave32x32) == 1 || rows <= 32) return {kWave32x32, 1};
     }
   }
-  // Rounds of workgroups over the CUs times a round's time per K-step, in units of 10 ns
-  constexpr int per[kTiles] = {100, 76, 36, 18};
+  // Tiles: rounds of workgroups over the CUs times a round's time, a K-step's per tile
+  // and 20 steps' for its start and end, in units of 10 ns; split sums are written, read
+  // and joined by a second launch besides. Fitted to 52 products of 8 .. 4096 rows, on which
+  // the kernels chosen take 1.2 % longer than the best of 4 tiles by 8 splits on average, 17 %
+  // at most (512 x 1024 x 1024: 64 x 64 whole 9.1 us, in 2 splits 11.0; 512 x 6144 x 6144: 256 x
+  // 192 in 4 splits 51, 128 x 128 in 2 58; 1024 x 6144 x 2048 39.5 by 128 x 128, 42 by 256 x 192;
+  // 4096 x 6144 x 2048 89, by 256 x 256 114).
+  constexpr int per[kTiles] = {167, 146, 63, 27};
   constexpr int wide[kTiles] = {1, 1, 2, 2};  // workgroups a CU
   const int64_t steps = std::max<int64_t>((K + 63) / 64, 1);
   Choice best{0, 1};
   int64_t least = INT64_MAX;
   for (int i = 0; i < kTiles; ++i) {
-    const int64_t tiles = tiles_of(i);
+    const int64_t tiles = tiles_of(i), room = cus * wide[i];
     // splits of at least 8 steps each, while they fit the chip at once
-    int64_t splits = std::min(std::max<int64_t>(cus * wide[i] / tiles, 1), std::max<int64_t>(steps / 8, 1));
-    splits = std::min<int64_t>(splits, 32);
-    const int64_t part = (steps + splits - 1) / splits;
-    splits = (steps + part - 1) / part;  // none of them empty
-    const int64_t rounds = (tiles * splits + cus * wide[i] - 1) / (cus * wide[i]);
-    const int64_t cost = rounds * (part + 8) * per[i] * wide[i] + (splits > 1 ? 800 : 0);
-    if (cost < least) least = cost, best = {i, (int)splits};
+    const int64_t most = std::min<int64_t>({std::max<int64_t>(room / tiles, 1), std::max<int64_t>(steps / 8, 1), 16});
+    for (int64_t want : {(int64_t)1, most / 2, most}) {
+      const int64_t part = (steps + std::max<int64_t>(want, 1) - 1) / std::max<int64_t>(want, 1);
+      const int64_t splits = (steps + part - 1) / part;  // none of them empty
+      int64_t cost = (tiles * splits + room - 1) / room * (part + 20) * per[i] * wide[i];
+      if (splits > 1) cost += 1260 + splits * rows * cols * (kind == kGemmGated ? 2 : 1) / 45000;
+      if (cost < least) least = cost, best = {i, (int)splits};
+    }
   }
   return best;
 }
