@@ -68,10 +68,40 @@ struct Row {
   __device__ __forceinline__ int64_t edge(int i) const { return i < head ? i : V - edges() + i; }  // the i-th of them
 };
 
+// The wave's sum, uniform: within rows of 16 lanes by DPP, the four rows' as scalars
+// (by six exchanges through LDS it took 0.25 us, and a row's way through a workgroup
+// has several).
+template <int CTRL>
+__device__ __forceinline__ double dpp_other(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
-  return v;
+  v += dpp_other<0xB1>(v);   // lane ^ 1
+  v += dpp_other<0x4E>(v);   // lane ^ 2
+  v += dpp_other<0x141>(v);  // half row mirrored
+  v += dpp_other<0x140>(v);  // row mirrored
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+// The wave's largest number, NaN only if all are.
+template <int CTRL>
+__device__ __forceinline__ float dpp_other(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp_other<0xB1>(v));
+  v = fmaxf(v, dpp_other<0x4E>(v));
+  v = fmaxf(v, dpp_other<0x141>(v));
+  v = fmaxf(v, dpp_other<0x140>(v));
+  auto at = [&](int lane) { return __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(v), lane)); };
+  return fmaxf(fmaxf(at(0), at(16)), fmaxf(at(32), at(48)));
 }
 
 // ----------------------------------------------------------------- sums of a row
@@ -110,10 +140,10 @@ __device__ __forceinline__ Total join(const Sums<MEAN>& a, float cl) {
   __shared__ float lm[W];
   __shared__ double ls[W], lt[W];
   const int wave = wave_id(), lane = threadIdx.x & 63;
-  float m = wave_max(a.m);
+  float m = row_max(a.m);
   if (lane == 0) lm[wave] = m;
   __syncthreads();
-  m = wave_max(lm[lane % W]);
+  m = row_max(lm[lane % W]);
   const float back = fmaxf((a.m - m) * cl, -1e4f);
   const double f = __builtin_amdgcn_exp2f(back);
   const double s = wave_sum(a.s * f);
@@ -141,6 +171,7 @@ struct Candidates {
   uint64_t top[kMaxTop];  // the k largest, in order
   uint64_t at_least;      // the threshold
   int n;                  // candidates met; those past kKeys are not held
+  int reached[2][16];     // by a wave's threshold: how many of the threads' best do
   int threads;            // threads whose best element reaches the threshold,
   uint16_t thread[1024];  // in no order
   uint32_t best[1024];    // the threads' best elements (order_key)
@@ -253,17 +284,38 @@ __device__ void select(Candidates& c, const Row<TYPE>& row, int64_t p0, int64_t 
   c.best[threadIdx.x] = mine;
   if (threadIdx.x == 0) c.n = 0, c.threads = 0;
   __syncthreads();
-  if (threadIdx.x < 64) {
-    uint32_t b[W], at = 0;
+  // The largest 16-bit threshold that k maxima reach. The waves try a digit's values, one
+  // each (two waves: a bit at a time by the first).
+  uint32_t b[W], at = 0;
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int w = 0; w < W; ++w) b[w] = c.best[64 * w + threadIdx.x] >> 16;
+  for (int w = 0; w < W; ++w) b[w] = c.best[64 * w + lane] >> 16;
+  auto reached = [&](uint32_t from) __attribute__((always_inline)) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) n += __popcll(__ballot(b[w] >= from));
+    return n;
+  };
+  if constexpr (W >= 8) {
+    constexpr int B = W == 16 ? 4 : 3;
+    const int wave = wave_id();
+    int round = 0;
 #pragma unroll 1
-    for (uint32_t bit = 1u << 15; bit > 0; bit >>= 1) {
-      int n = 0;
-#pragma unroll
-      for (int w = 0; w < W; ++w) n += __popcll(__ballot(b[w] >= (at | bit)));
-      if (n >= k) at |= bit;
+    for (int shift = 16; shift > 0; round ^= 1) {
+      shift = shift > B ? shift - B : 0;
+      const int n = reached(at | (uint32_t)wave << shift);
+      if (lane == 0) c.reached[round][wave] = n;
+      __syncthreads();
+      // the largest value that suffices (in a shorter last digit, a value that sets bits
+      // already decided changes nothing or does not suffice)
+      const uint64_t enough = __ballot(lane < W && c.reached[round][lane % W] >= k);
+      at |= (uint32_t)(63 - __clzll(enough)) << shift;
     }
+    if (threadIdx.x == 0) c.at_least = (uint64_t)at << 48;
+  } else if (threadIdx.x < 64) {
+#pragma unroll 1
+    for (uint32_t bit = 1u << 15; bit > 0; bit >>= 1)
+      if (reached(at | bit) >= k) at |= bit;
     if (threadIdx.x == 0) c.at_least = (uint64_t)at << 48;
   }
   __syncthreads();
@@ -335,10 +387,11 @@ __device__ __forceinline__ float given_logit(const ScoresArgs& a, const Row<TYPE
   return t >= 0 && t < a.V ? Logit<TYPE>::load(row.p, t) : 0.f;
 }
 
-// (at most 64 registers: four workgroups of 512 threads a CU)
-template <int TYPE, int THREADS, bool TOP>
+// (at most 64 registers for 512 threads: four workgroups a CU). N elements a thread and
+// tile, the next tile's under way meanwhile.
+template <int TYPE, int THREADS, int N, bool TOP>
 __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel(const ScoresArgs a, int parts) {
-  constexpr int E = Logit<TYPE>::kPiece, NP = 16 / E, N = NP * E;  // pieces, elements a thread and tile
+  constexpr int E = Logit<TYPE>::kPiece, NP = N / E;  // pieces
   __shared__ Candidates c;
   const int64_t m = blockIdx.x / parts;
   const int part = blockIdx.x % parts;
@@ -346,7 +399,6 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel
   const int64_t per = (row.pieces + parts - 1) / parts;
   const int64_t p0 = min(per * part, row.pieces), p1 = min(p0 + per, row.pieces);
   const bool edges = part == 0;
-  const float given = parts == 1 ? given_logit<TYPE>(a, row, m) : 0.f;
   Sums<true> sums;
 
   uint4 q[NP];
@@ -359,6 +411,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel
   };
   load(p0);
   float edge[1] = {edges && (int)threadIdx.x < row.edges() ? Logit<TYPE>::load(row.p, row.edge(threadIdx.x)) : -INFINITY};
+  const float given = parts == 1 ? given_logit<TYPE>(a, row, m) : 0.f;  // (two loads one behind the other, beside the tile's)
   sums.add(edge, kLog2e);
   for (int64_t base = p0; base < p1 || base == p0; base += NP * THREADS) {
     float v[N];
@@ -406,7 +459,7 @@ __global__ __launch_bounds__(256) void scores_join_kernel(const ScoresArgs a, in
   {  // every wave the same
     const int i = threadIdx.x & 63;
     const ScoresPart mine = i < parts ? p[i] : ScoresPart{-FLT_MAX, 0.f, 0, 0};
-    r.m = wave_max(mine.m);
+    r.m = row_max(mine.m);
     const double back = fmax((double)mine.m - r.m, -1e4), f = exp(back);
     r.s = wave_sum(mine.s * f);
     r.t = wave_sum((mine.t + mine.s * back) * f);
@@ -417,27 +470,32 @@ __global__ __launch_bounds__(256) void scores_join_kernel(const ScoresArgs a, in
 
 namespace {
 
-// Workgroups a row: the chip has room for four of 512 threads a CU; a part has at least
-// a tile's elements.
+// Workgroups a row of the sums: their join is a launch of its own, so a row is split only
+// where one workgroup takes longer. (A CU forms the sums of 131072 elements in 9 us: 16 x
+// 131072 fp32, 20.2 us by a workgroup a row, 14.0 by 16 and a join.)
 int parts_of(int64_t M, int64_t V, int cus) {
-  const int64_t room = 4 * (int64_t)cus / std::max<int64_t>(M, 1), tiles = V / 8192;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({room, tiles, (int64_t)kMaxParts}));
+  if (V <= 65536) return 1;
+  const int64_t room = 4 * (int64_t)cus / std::max<int64_t>(M, 1);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({room, V / 16384, (int64_t)kMaxParts}));
 }
+// Up to a row a CU, a workgroup has 1024 threads and twice the loads under way.
+bool few_rows(int64_t M, int parts, int cus) { return M <= cus && parts == 1; }
 
-template <int TYPE>
+template <int TYPE, bool TOP>
 hipError_t scores(const ScoresArgs& a, int cus, hipStream_t stream) {
   const int parts = parts_of(a.M, a.V, cus);
   const dim3 grid((unsigned)(a.M * parts));
   hipError_t e;
-  if (a.V <= 4096)
-    e = a.k ? launch_k(scores_kernel<TYPE, 128, true>, grid, dim3(128), 0, stream, Ev{}, a, parts)
-            : launch_k(scores_kernel<TYPE, 128, false>, grid, dim3(128), 0, stream, Ev{}, a, parts);
-  else
-    e = a.k ? launch_k(scores_kernel<TYPE, 512, true>, grid, dim3(512), 0, stream, Ev{}, a, parts)
-            : launch_k(scores_kernel<TYPE, 512, false>, grid, dim3(512), 0, stream, Ev{}, a, parts);
+  if (a.V <= 4096) e = launch_k(scores_kernel<TYPE, 128, 16, TOP>, grid, dim3(128), 0, stream, Ev{}, a, parts);
+  else if (few_rows(a.M, parts, cus)) e = launch_k(scores_kernel<TYPE, 1024, 32, TOP>, grid, dim3(1024), 0, stream, Ev{}, a, parts);
+  else e = launch_k(scores_kernel<TYPE, 512, 16, TOP>, grid, dim3(512), 0, stream, Ev{}, a, parts);
   if (e == hipSuccess && parts > 1)
     e = launch_k(scores_join_kernel<TYPE>, dim3((unsigned)a.M), dim3(256), 0, stream, Ev{}, a, parts);
   return e;
+}
+template <int TYPE>
+hipError_t scores(const ScoresArgs& a, int cus, hipStream_t stream) {
+  return a.k ? scores<TYPE, true>(a, cus, stream) : scores<TYPE, false>(a, cus, stream);
 }
 
 }  // namespace
@@ -467,7 +525,7 @@ __device__ void read_teacher(const DistillArgs& a, int64_t m, Teacher& w) {
     int32_t v = j < a.k ? a.ids[m * a.k + j] : -1;
     if (v < 0 || v >= a.V) v = -1;
     const float t = v >= 0 ? a.t[m * a.k + j] / a.temperature : -INFINITY;
-    const float mx = wave_max(t);
+    const float mx = row_max(t);
     const double e = t > -INFINITY || t != t ? exp((double)t - mx) : 0.0;
     const double s = wave_sum(e);
     w.id[j] = v;
@@ -594,9 +652,9 @@ __device__ void write_grad(const DistillArgs& a, int64_t m, const Row<TYPE>& row
   if (mine) Logit<GRAD>::store(out, w.id[threadIdx.x], slot);
 }
 
-template <int TYPE, int THREADS>
+template <int TYPE, int THREADS, int N>
 __device__ Sums<false> sum_pieces(const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, float cl) {
-  constexpr int E = Logit<TYPE>::kPiece, NP = 16 / E, N = NP * E;
+  constexpr int E = Logit<TYPE>::kPiece, NP = N / E;
   Sums<false> sums;
   uint4 q[NP];
   auto load = [&](int64_t base) __attribute__((always_inline)) {
@@ -620,7 +678,7 @@ __device__ Sums<false> sum_pieces(const Row<TYPE>& row, int64_t p0, int64_t p1, 
 }
 
 // Forward: a row's sums by `parts` workgroups; with one of them the loss too.
-template <int TYPE, int THREADS>
+template <int TYPE, int THREADS, int N>
 __global__ __launch_bounds__(THREADS) void distill_sums_kernel(const DistillArgs a, int parts) {
   __shared__ Teacher w;
   const int64_t m = blockIdx.x / parts;
@@ -629,7 +687,7 @@ __global__ __launch_bounds__(THREADS) void distill_sums_kernel(const DistillArgs
   const Row<TYPE> row(a.z, m, a.ldz, a.V);
   const int64_t per = (row.pieces + parts - 1) / parts;
   const int64_t p0 = min(per * part, row.pieces), p1 = min(p0 + per, row.pieces);
-  const Total r = join<THREADS>(sum_pieces<TYPE, THREADS>(row, p0, p1, part == 0, cl), cl);
+  const Total r = join<THREADS>(sum_pieces<TYPE, THREADS, N>(row, p0, p1, part == 0, cl), cl);
   if (parts == 1) {
     read_teacher(a, m, w);
     write_loss(a, m, w, r, slot_logit(row, w));
@@ -643,7 +701,7 @@ __device__ Total joined(const DistillArgs& a, int64_t row, int parts) {
   const double c = 1.f / a.temperature;
   const int i = threadIdx.x & 63;  // every wave the same
   const float m = i < parts ? p[i].m : -FLT_MAX;
-  const float top = wave_max(m);
+  const float top = row_max(m);
   return {top, wave_sum(i < parts ? p[i].s * exp(((double)m - top) * c) : 0.0), 0};
 }
 
@@ -688,7 +746,7 @@ __global__ __launch_bounds__(THREADS) void distill_both_kernel(const DistillArgs
   const int64_t m = blockIdx.x;
   const float c = 1.f / a.temperature, cl = c * kLog2e;
   const Row<TYPE> row(a.z, m, a.ldz, a.V);
-  const Total r = join<THREADS>(sum_pieces<TYPE, THREADS>(row, 0, row.pieces, true, cl), cl);
+  const Total r = join<THREADS>(sum_pieces<TYPE, THREADS, 16>(row, 0, row.pieces, true, cl), cl);
   read_teacher(a, m, w);
   write_loss(a, m, w, r, slot_logit(row, w));
   const float f = r.m < INFINITY && r.s > 0 ? (float)(a.weight[m] * c / r.s) : NAN;
@@ -756,10 +814,10 @@ __global__ __launch_bounds__(1024, TYPE == MOE_FP32 && H <= 8 ? 8 : 4) void dist
       __builtin_amdgcn_sched_barrier(0);
     }
     // the sums of the threads, in 64 bits
-    float top = wave_max(sums.m);
+    float top = row_max(sums.m);
     if (lane == 0) lm[wave] = top;
     __syncthreads();
-    top = wave_max(lm[lane % W]);
+    top = row_max(lm[lane % W]);
     const float part = sums.s * __builtin_amdgcn_exp2f(fmaxf((sums.m - top) * cl, -1e4f));
     const double ws = wave_sum((double)part);
     if (lane == 0) ls[wave] = ws;
@@ -806,51 +864,81 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(const DistillArgs a)
   if (mine) Logit<GRAD>::store(grad_row<GRAD>(a, m), w.id[j], v);
 }
 
-// Rows up to this are read again for the gradient, from the L2 (32000 of 16 bits: ).
-constexpr int64_t kHeldV = 16384;
+namespace {
 
-size_t distill_ws_bytes(int64_t M, int64_t V, int, int cus) {
-  const int parts = parts_of(M, V, cus);
-  // (one part: the held rows' sums and slots)
-  return (size_t)M * (parts * sizeof(ScoresPart) + (parts == 1 && V > kHeldV ? kMaxTop * sizeof(float) : 0));
+// Workgroups a row of the gradient, which needs no join: while the chip has room for
+// them (four of 512 threads a CU), a tile's elements each at least.
+int grad_parts(int64_t M, int64_t V, int cus) {
+  const int64_t room = 4 * (int64_t)cus / std::max<int64_t>(M, 1);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({room, V / 8192, (int64_t)kMaxParts}));
 }
 
-namespace {
+// How forward and backward at once go: kAlone, a row a workgroup, which reads it twice
+// (the second time from the L2 or the memory-side cache); kHeld, the row held between; kSplit, as the two calls
+// but with the sums in full.
+enum Both { kAlone, kHeld, kSplit };
+Both choose_both(int64_t M, int64_t V, int type, bool alike, int cus) {
+  const int64_t bytes = V * (type == MOE_FP32 ? 4 : 2), kb = 1024;
+  if (2 * M <= cus && V > 65536) return kSplit;
+  if (M <= cus || bytes <= 32 * kb) return kAlone;
+  return alike && bytes <= 256 * kb ? kHeld : kAlone;
+}
 
 template <int TYPE, int GRAD>
 hipError_t distill(DistillPass pass, const DistillArgs& a, int cus, hipStream_t stream) {
-  const int parts = parts_of(a.M, a.V, cus);
-  const dim3 grid((unsigned)(a.M * parts));
   const bool small = a.V <= 4096;
-  const dim3 block(small ? 128 : 512);
+  const int gparts = grad_parts(a.M, a.V, cus);
+  const dim3 rows((unsigned)a.M), grads((unsigned)(a.M * gparts));
   if (pass == kDistillBackward)
-    return small ? launch_k(distill_grad_kernel<TYPE, GRAD, 128, false>, grid, block, 0, stream, Ev{}, a, parts)
-                 : launch_k(distill_grad_kernel<TYPE, GRAD, 512, false>, grid, block, 0, stream, Ev{}, a, parts);
-  if (pass == kDistillBoth && parts == 1) {
-    if (small) return launch_k(distill_both_kernel<TYPE, GRAD, 128>, grid, block, 0, stream, Ev{}, a);
-    if constexpr (Logit<TYPE>::kBytes == Logit<GRAD>::kBytes) {
-      const int64_t held = (a.V / Logit<TYPE>::kPiece + 1023) / 1024;  // pieces a thread of 1024
-      const bool alike = (((uintptr_t)a.z - (uintptr_t)a.dz) & 15) == 0 && (a.ldz - a.lddz) * Logit<TYPE>::kBytes % 16 == 0;
-      if (a.V > kHeldV && alike && held <= 16) {
-        const dim3 rows((unsigned)std::min<int64_t>(a.M, a.type == MOE_FP32 && held <= 8 ? 2 * cus : cus));  // that fit at once
-        const hipError_t e = held <= 8 ? launch_k(distill_held_kernel<TYPE, GRAD, 8>, rows, dim3(1024), 0, stream, Ev{}, a)
-                                       : launch_k(distill_held_kernel<TYPE, GRAD, 16>, rows, dim3(1024), 0, stream, Ev{}, a);
-        return e != hipSuccess ? e : launch_k(distill_finish_kernel<TYPE, GRAD>, dim3((unsigned)a.M), dim3(64), 0, stream, Ev{}, a);
+    return small ? launch_k(distill_grad_kernel<TYPE, GRAD, 128, false>, grads, dim3(128), 0, stream, Ev{}, a, gparts)
+                 : launch_k(distill_grad_kernel<TYPE, GRAD, 512, false>, grads, dim3(512), 0, stream, Ev{}, a, gparts);
+  int parts = parts_of(a.M, a.V, cus);
+  const bool few = few_rows(a.M, parts, cus);
+  if (pass == kDistillBoth) {
+    constexpr bool same = Logit<TYPE>::kBytes == Logit<GRAD>::kBytes;
+    const bool alike = same && (((uintptr_t)a.z - (uintptr_t)a.dz) & 15) == 0 &&
+                       (a.ldz - a.lddz) * Logit<TYPE>::kBytes % 16 == 0;
+    const Both how = choose_both(a.M, a.V, a.type, alike, cus);
+    if constexpr (same) {
+      if (how == kHeld) {
+        const bool half = a.V * Logit<TYPE>::kBytes <= 128 * 1024;
+        // (as many workgroups as fit at once)
+        const dim3 grid((unsigned)std::min<int64_t>(a.M, TYPE == MOE_FP32 && half ? 2 * cus : cus));
+        const hipError_t e = half ? launch_k(distill_held_kernel<TYPE, GRAD, 8>, grid, dim3(1024), 0, stream, Ev{}, a)
+                                  : launch_k(distill_held_kernel<TYPE, GRAD, 16>, grid, dim3(1024), 0, stream, Ev{}, a);
+        return e != hipSuccess ? e : launch_k(distill_finish_kernel<TYPE, GRAD>, rows, dim3(64), 0, stream, Ev{}, a);
       }
     }
-    if (a.V <= 32768) return launch_k(distill_both_kernel<TYPE, GRAD, 512>, grid, block, 0, stream, Ev{}, a);
-    return launch_k(distill_both_kernel<TYPE, GRAD, 1024>, grid, dim3(1024), 0, stream, Ev{}, a);
+    if (how == kAlone)
+      return small ? launch_k(distill_both_kernel<TYPE, GRAD, 128>, rows, dim3(128), 0, stream, Ev{}, a)
+             : few || a.V > 32768 ? launch_k(distill_both_kernel<TYPE, GRAD, 1024>, rows, dim3(1024), 0, stream, Ev{}, a)
+                 : launch_k(distill_both_kernel<TYPE, GRAD, 512>, rows, dim3(512), 0, stream, Ev{}, a);
+    parts = std::max(gparts, 2);  // (more than 65536 elements, eight rooms a row: gparts is 8 at least)
   }
-  hipError_t e = small ? launch_k(distill_sums_kernel<TYPE, 128>, grid, block, 0, stream, Ev{}, a, parts)
-                       : launch_k(distill_sums_kernel<TYPE, 512>, grid, block, 0, stream, Ev{}, a, parts);
-  if (e == hipSuccess && parts > 1)
-    e = launch_k(distill_loss_kernel<TYPE>, dim3((unsigned)a.M), dim3(64), 0, stream, Ev{}, a, parts);
+  const dim3 grid((unsigned)(a.M * parts));
+  hipError_t e = small ? launch_k(distill_sums_kernel<TYPE, 128, 16>, grid, dim3(128), 0, stream, Ev{}, a, parts)
+                 : few && pass == kDistillForward
+                     ? launch_k(distill_sums_kernel<TYPE, 1024, 32>, grid, dim3(1024), 0, stream, Ev{}, a, parts)
+                     : launch_k(distill_sums_kernel<TYPE, 512, 16>, grid, dim3(512), 0, stream, Ev{}, a, parts);
+  if (e == hipSuccess && parts > 1) e = launch_k(distill_loss_kernel<TYPE>, rows, dim3(64), 0, stream, Ev{}, a, parts);
   if (e == hipSuccess && pass == kDistillBoth)
-    e = launch_k(distill_grad_kernel<TYPE, GRAD, 512, true>, grid, block, 0, stream, Ev{}, a, parts);
+    e = launch_k(distill_grad_kernel<TYPE, GRAD, 512, true>, grid, dim3(512), 0, stream, Ev{}, a, parts);
   return e;
 }
 
 }  // namespace
+
+size_t distill_ws_bytes(int64_t M, int64_t V, int type, int cus) {
+  if (M == 0) return 0;
+  size_t n = 0;  // bytes a row
+  auto need = [&](size_t bytes) { n = std::max(n, bytes); };
+  const int parts = parts_of(M, V, cus);
+  if (parts > 1) need(parts * sizeof(ScoresPart));
+  const Both how = choose_both(M, V, type, true, cus);
+  if (how == kSplit) need(std::max(grad_parts(M, V, cus), 2) * sizeof(ScoresPart));
+  if (how == kHeld) need(sizeof(ScoresPart) + kMaxTop * sizeof(float));
+  return (size_t)M * n;
+}
 
 hipError_t launch_distill(DistillPass pass, const DistillArgs& a, int cus, hipStream_t stream) {
   switch (a.type) {

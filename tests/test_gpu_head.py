@@ -86,7 +86,7 @@ def _check_scores(z, tokens, k, view=None):
 
 
 ROWS = [(1, 1), (1, 7), (3, 64), (2, 65), (5, 255), (1, 1000), (4, 4099), (17, 2048), (1, 131072), (2, 30011), (300, 515),
-        (33, 8193), (1, 262144)]
+        (33, 8193), (1, 262144), (2, 400003), (300, 20011)]
 
 
 @pytest.mark.parametrize("M,V", ROWS)
@@ -99,7 +99,7 @@ def test_scores(M, V, t):
 
 @pytest.mark.parametrize("kind", ["ties", "rising", "falling", "masked", "lowest", "one", "far"])
 @pytest.mark.parametrize("t", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("M,V", [(3, 100), (2, 5003), (40, 3001), (1, 70001)])
+@pytest.mark.parametrize("M,V", [(3, 100), (2, 5003), (40, 3001), (1, 70001), (2, 350001), (260, 5001)])
 def test_scores_distributions(kind, t, M, V):
     z, gen = _logits(V, M, V, t, kind)
     _check_scores(z, torch.randint(0, V, (M,), generator=gen).int(), 20)
@@ -200,7 +200,7 @@ def test_distill(M, V, t, gt):
 
 
 @pytest.mark.parametrize("kind", ["ties", "masked", "one", "far", "lowest"])
-@pytest.mark.parametrize("M,V", [(6, 900), (40, 5001)])
+@pytest.mark.parametrize("M,V", [(6, 900), (40, 5001), (270, 17001)])
 def test_distill_distributions(kind, M, V):
     for t in ("bf16", "fp32"):
         z, gen = _logits(V, M, V, t, kind)

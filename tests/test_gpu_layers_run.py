@@ -374,8 +374,8 @@ def test_refused_on_the_device():
     refused(B.MOE_ERR_WORKSPACE, lambda: op.backward(y, x, dx=x.clone(), pre=y.clone(), workspace=ws[:-256]))
     refused(B.MOE_ERR_WORKSPACE, lambda: op.backward(y, x, dx=x.clone(), pre=y.clone()))
     refused(B.MOE_ERR_WORKSPACE, lambda: op.backward(y, x, dx=x.clone(), pre=y.clone(), workspace=_ws(ws.numel() + 16)[16:]))
-    sc = B.TokenScores(70000, top_k=3, dtype=BF, max_M=4)
-    z = torch.zeros(4, 70000, dtype=BF, device="cuda")
+    sc = B.TokenScores(400000, top_k=3, dtype=BF, max_M=4)
+    z = torch.zeros(4, 400000, dtype=BF, device="cuda")
     top, ids = torch.zeros(4, 3, device="cuda"), torch.zeros(4, 3, dtype=I32, device="cuda")
     refused(B.MOE_ERR_WORKSPACE, lambda: sc.forward(z, None, None, top_logprobs=top, top_ids=ids))
     refused(B.MOE_ERR_INVALID_ARG, lambda: sc.forward(z, None, None, top_logprobs=top, top_ids=top.view(I32), workspace=_ws(sc.workspace_bytes(4))))
