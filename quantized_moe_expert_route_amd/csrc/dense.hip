@@ -15,7 +15,7 @@ namespace {
 
 // The kernels a product may run on: 16 TM rows by 16 TN columns a wave (gated: of both
 // products, so half of them columns of y).
-enum { k256x256, k256x192, k128x128, k64x64, kTiles, kWave16x16 = kTiles, kWave16x32, kWave32x16, kWave32x32, kChoices };
+enum { k256x256, k256x192, k128x128, k64x64, k64x64Pair, kTiles, kWave16x16 = kTiles, kWave16x32, kWave32x16, kWave32x32, kChoices };
 struct Choice {
   int kernel, splits;
 };
@@ -28,6 +28,7 @@ constexpr Size kSize[kChoices] = {
     {"256 x 192 tile", 256, 192},
     {"128 x 128 tile", 128, 128},
     {"64 x 64 tile", 64, 64},
+    {"64 x 64 tile, two groups of waves", 64, 64},
     {"16 x 16, K split over the waves", 16, 16},
     {"16 x 32, K split over the waves", 16, 32},
     {"32 x 16, K split over the waves", 32, 16},
@@ -54,26 +55,30 @@ Choice choose(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int cus) {
     }
   }
   // Tiles: rounds of workgroups over the CUs times a round's time, a K-step's per tile
-  // and 20 steps' for its start and end, in units of 10 ns; split sums are written, read
+  // and some steps' for its start and end, in units of 10 ns; split sums are written, read
   // and joined by a second launch besides. Fitted to 52 products of 8 .. 4096 rows, on which
-  // the kernels chosen take 1.2 % longer than the best of 4 tiles by 8 splits on average, 17 %
-  // at most (512 x 1024 x 1024: 64 x 64 whole 9.1 us, in 2 splits 11.0; 512 x 6144 x 6144: 256 x
-  // 192 in 4 splits 51, 128 x 128 in 2 58; 1024 x 6144 x 2048 39.5 by 128 x 128, 42 by 256 x 192;
-  // 4096 x 6144 x 2048 89, by 256 x 256 114).
-  constexpr int per[kTiles] = {167, 146, 63, 27};
-  constexpr int wide[kTiles] = {1, 1, 2, 2};  // workgroups a CU
+  // the kernels chosen take 0.8 % longer than the best tile and split on average, 10 % at
+  // most (512 x 1024 x 1024: 64 x 64 whole 9.0 us, in 2 splits 10.8; 512 x 6144 x 6144: 256 x
+  // 192 in 4 splits 51, 128 x 128 in 2 58; 1024 x 6144 x 2048 39 by 128 x 128, 42 by 256 x 192;
+  // 4096 x 6144 x 2048 89, by 256 x 256 114; with two groups of waves 64 x 64 tiles that are
+  // alone on their CUs take 12.5 us for 14.0, 333 x 2320 x 2056, and 16.4 for 18.8, 704 x 1000 x 3000).
+  constexpr int per[kTiles] = {160, 143, 59, 25, 63};
+  constexpr int start[kTiles] = {18, 18, 18, 18, 11};
+  constexpr int wide[kTiles] = {1, 1, 2, 2, 1};    // workgroups a CU
+  constexpr int groups[kTiles] = {1, 1, 1, 1, 2};  // of waves, which share the steps
   const int64_t steps = std::max<int64_t>((K + 63) / 64, 1);
   Choice best{0, 1};
   int64_t least = INT64_MAX;
   for (int i = 0; i < kTiles; ++i) {
     const int64_t tiles = tiles_of(i), room = cus * wide[i];
+    if (i == k64x64Pair && tiles > cus) continue;
     // splits of at least 8 steps each, while they fit the chip at once
     const int64_t most = std::min<int64_t>({std::max<int64_t>(room / tiles, 1), std::max<int64_t>(steps / 8, 1), 16});
     for (int64_t want : {(int64_t)1, most / 2, most}) {
       const int64_t part = (steps + std::max<int64_t>(want, 1) - 1) / std::max<int64_t>(want, 1);
       const int64_t splits = (steps + part - 1) / part;  // none of them empty
-      int64_t cost = (tiles * splits + room - 1) / room * (part + 20) * per[i] * wide[i];
-      if (splits > 1) cost += 1260 + splits * rows * cols * (kind == kGemmGated ? 2 : 1) / 45000;
+      int64_t cost = (tiles * splits + room - 1) / room * ((part + groups[i] - 1) / groups[i] + start[i]) * per[i] * wide[i];
+      if (splits > 1) cost += 960 + splits * rows * cols * (kind == kGemmGated ? 2 : 1) / 30000;
       if (cost < least) least = cost, best = {i, (int)splits};
     }
   }
@@ -96,6 +101,7 @@ hipError_t launch(GemmArgs a, const Choice& c, int cus, hipStream_t stream) {
     case k256x256: e = launch_tile<F16, KIND, 8, 4, 2, 4, 2>(a, stream); break;
     case k256x192: e = launch_tile<F16, KIND, 4, 6, 4, 2, 2>(a, stream); break;
     case k128x128: e = launch_tile<F16, KIND, 4, 4, 2, 2, 2>(a, stream); break;
+    case k64x64Pair: e = launch_tile<F16, KIND, 2, 2, 2, 2, 4, 2>(a, stream); break;
     default: e = launch_tile<F16, KIND, 2, 2, 2, 2, 4>(a, stream); break;
   }
   if (e == hipSuccess && c.splits > 1) {

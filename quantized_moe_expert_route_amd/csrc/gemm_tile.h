@@ -268,16 +268,19 @@ __device__ __forceinline__ float* split_sums(const GemmArgs& a, int split, int64
   return reinterpret_cast<float*>(a.ws) + (split * a.rows + m) * ld;
 }
 
-template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(const GemmArgs a, int tiles_m, int tiles_n) {
+// KG groups of WM x WN waves take the K-steps in turn, each through buffers of its own, and
+// join their sums at the end: small tiles leave most of a SIMD's time to the LDS's latency.
+template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN, int S, int KG>
+__global__ __launch_bounds__(64 * WM * WN * KG) void gemm_tile_kernel(const GemmArgs a, int tiles_m, int tiles_n) {
   constexpr int W = WM * WN, BM = 16 * TM * WM, BN = 16 * TN * WN;
   constexpr bool gated = KIND == kGemmGated;
   constexpr int cols = gated ? BN / 2 : BN;  // columns of y a tile
   typedef Operand<KIND == kGemmWeight, BM, W> OpA;
   typedef Operand<KIND == kGemmInput || KIND == kGemmWeight, BN, W> OpB;
   constexpr int kStage = OpA::kBytes + OpB::kBytes, kLoads = OpA::kLoads + OpB::kLoads;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kStage];
-  const int wave = wave_id(), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * S * kStage];
+  const int group = KG > 1 ? wave_id() / W : 0, wave = wave_id() - group * W;
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wm = wave / WN, wn = wave % WN;
   const int tiles = tiles_m * tiles_n, split = blockIdx.x / tiles;
   int tm, tn;
@@ -301,23 +304,25 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(const GemmArgs 
   // this split's part of K
   const int64_t part = ((a.K + 63) / 64 + a.splits - 1) / a.splits * 64, k0 = split * part;
   const int64_t K = min(part, a.K - k0);
-  const int steps = (int)((K + 63) / 64);
+  const int steps = (int)((K + 64 * KG - 1) / (64 * KG));  // of a group
   const int64_t step_a = KIND == kGemmWeight ? 64 * a.lda : 64, step_b = KIND >= kGemmInput ? 64 * a.ldb : 64;
   const uint16_t* pa = reinterpret_cast<const uint16_t*>(a.a) + (KIND == kGemmWeight ? m0 : m0 * a.lda) + k0 / 64 * step_a;
   const uint16_t* pb = reinterpret_cast<const uint16_t*>(a.b) + (KIND >= kGemmInput ? n0 : n0 * a.ldb) + k0 / 64 * step_b;
-  const uint32_t base = __builtin_amdgcn_readfirstlane(lds_address(lds));
+  uint8_t* const own = lds + group * (S * kStage);
+  const uint32_t base = __builtin_amdgcn_readfirstlane(lds_address(own));
 
-  // Loads of step t to buffer t % S, one at a time.
+  // Loads of the group's step t to buffer t % S, one at a time.
   v4i ba, bb, bc;
   uint32_t at;
   auto begin_loads = [&](int t, int buffer) __attribute__((always_inline)) {
-    if (t + 1 >= steps) {  // past the last step: zeros, not used
-      la.last((int)(K - (int64_t)t * 64));
-      lb.last((int)(K - (int64_t)t * 64));
+    const int64_t kt = (int64_t)t * KG + group;
+    if (t + 1 >= steps) {  // (past the last step: zeros, not used)
+      la.last((int)(K - kt * 64));
+      lb.last((int)(K - kt * 64));
     }
     at = base + (uint32_t)buffer * kStage;
-    ba = buffer_at(pa + t * step_a), bb = buffer_at(pb + t * step_b);
-    bc = gated ? buffer_at(pb + a.cols * a.ldb + t * step_b) : bb;
+    ba = buffer_at(pa + kt * step_a), bb = buffer_at(pb + kt * step_b);
+    bc = gated ? buffer_at(pb + a.cols * a.ldb + kt * step_b) : bb;
   };
   auto load = [&](int n) __attribute__((always_inline)) {
     if (n < OpA::kLoads) la.load(n, ba, ba, at, wave);
@@ -335,7 +340,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(const GemmArgs 
   // next are read from LDS, so that they are there when the step's one barrier ends.
   uint4 fa[2][TM], fb[2][TN];
   auto read = [&](int i, int j, int buffer) __attribute__((always_inline)) {  // operand i of half j of a step
-    const uint8_t* sa = lds + buffer * kStage;
+    const uint8_t* sa = own + buffer * kStage;
     if (i < TN) fb[j][i] = OpB::fragment(sa + OpA::kBytes, block_n(i), j, r, g);
     else fa[j][i - TN] = OpA::fragment(sa, wm * TM + i - TN, j, r, g);
   };
@@ -378,23 +383,34 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(const GemmArgs 
   // in the epilogue moves in 16-byte pieces along a row
   wait_and_barrier<0>();
   constexpr int C = 16 * TN, P = C + 4;
-  static_assert(S * kStage >= W * 16 * P * 4, "the sums fit the operands' buffers");
-  float* mine = reinterpret_cast<float*>(lds) + wave * 16 * P;
   constexpr int pieces = (gated ? C / 2 : C) / 8;
+  constexpr int rows = KG > 1 ? TM : 1;  // blocks of 16 rows at a time
+  float* mine = reinterpret_cast<float*>(lds) + wave * 16 * P * rows;
+  constexpr int other = W * 16 * P * rows;  // from a group's sums to the next one's
+  static_assert(S * kStage >= W * 16 * P * rows * 4, "the sums fit the operands' buffers");
 #pragma unroll
-  for (int u = 0; u < TM; ++u) {
+  for (int u0 = 0; u0 < TM; u0 += rows) {
 #pragma unroll
-    for (int t = 0; t < TN; ++t) *reinterpret_cast<v4f*>(&mine[r * P + 16 * t + 4 * g]) = acc[t][u];
-    wave_lds_order();
+    for (int u = 0; u < rows; ++u)
 #pragma unroll
-    for (int i = lane; i < 16 * pieces; i += 64) {
+      for (int t = 0; t < TN; ++t) *reinterpret_cast<v4f*>(&mine[group * other + (16 * u + r) * P + 16 * t + 4 * g]) = acc[t][u0 + u];
+    if constexpr (KG > 1) barrier_lds();
+    else wave_lds_order();
+#pragma unroll
+    for (int i = lane + 64 * group; i < 16 * rows * pieces; i += 64 * KG) {
       const int row = i / pieces, c = i % pieces * 8;
-      const int64_t m = m0 + 16 * (wm * TM + u) + row, n = n0 + (gated ? C / 2 : C) * wn + c;
+      const int64_t m = m0 + 16 * (wm * TM + u0) + row, n = n0 + (gated ? C / 2 : C) * wn + c;
       float v[8], up[8];
 #pragma unroll
       for (int q = 0; q < 8; q += 4) {
-        *reinterpret_cast<v4f*>(v + q) = *reinterpret_cast<const v4f*>(&mine[row * P + c + q]);
-        if constexpr (gated) *reinterpret_cast<v4f*>(up + q) = *reinterpret_cast<const v4f*>(&mine[row * P + C / 2 + c + q]);
+        auto sum = [&](int at) __attribute__((always_inline)) {
+          v4f s = *reinterpret_cast<const v4f*>(&mine[at]);
+#pragma unroll
+          for (int k = 1; k < KG; ++k) s += *reinterpret_cast<const v4f*>(&mine[k * other + at]);
+          return s;
+        };
+        *reinterpret_cast<v4f*>(v + q) = sum(row * P + c + q);
+        if constexpr (gated) *reinterpret_cast<v4f*>(up + q) = sum(row * P + C / 2 + c + q);
       }
       if (m < a.rows && n < a.cols) {
         if (a.splits > 1) {
@@ -406,7 +422,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(const GemmArgs 
         }
       }
     }
-    wave_lds_order();
+    if constexpr (KG == 1) wave_lds_order();
   }
 }
 
@@ -560,12 +576,12 @@ hipError_t launch_wave(const GemmArgs& a, int cus, hipStream_t stream) {
                   stream, Ev{}, a, (int)tm, (int)tn);
 }
 
-template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN, int S>
+template <bool F16, GemmKind KIND, int TM, int TN, int WM, int WN, int S, int KG = 1>
 hipError_t launch_tile(const GemmArgs& a, hipStream_t stream) {
   constexpr int BM = 16 * TM * WM, cols = 16 * TN * WN / (KIND == kGemmGated ? 2 : 1);
   const int64_t tm = (a.rows + BM - 1) / BM, tn = (a.cols + cols - 1) / cols;
-  return launch_k(gemm_tile_kernel<F16, KIND, TM, TN, WM, WN, S>, dim3((unsigned)(tm * tn * a.splits)),
-                  dim3(64 * WM * WN), 0, stream, Ev{}, a, (int)tm, (int)tn);
+  return launch_k(gemm_tile_kernel<F16, KIND, TM, TN, WM, WN, S, KG>, dim3((unsigned)(tm * tn * a.splits)),
+                  dim3(64 * WM * WN * KG), 0, stream, Ev{}, a, (int)tm, (int)tn);
 }
 
 }  // namespace qmoe

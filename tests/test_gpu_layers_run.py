@@ -41,7 +41,9 @@ PRODUCTS = [
     (2050, 6200, 72, "256 x 256 tile"), (700, 4104, 4104, "256 x 256 tile"),  # the second of each: K split
     (4100, 2056, 72, "256 x 192 tile"), (4100, 520, 4104, "256 x 192 tile"),
     (2050, 2056, 72, "128 x 128 tile"), (1030, 2056, 2056, "128 x 128 tile"),
-    (130, 40, 72, "64 x 64 tile"), (130, 40, 2056, "64 x 64 tile"),
+    (130, 6200, 72, "64 x 64 tile"), (130, 2056, 4104, "64 x 64 tile"),
+    (130, 40, 72, "64 x 64 tile, two groups of waves"), (130, 40, 4104, "64 x 64 tile, two groups of waves"),
+    (333, 2056, 2320, "64 x 64 tile, two groups of waves"),
 ]
 WAVES = [(5, 40, 72, "16 x 16, K split over the waves"), (5, 4104, 72, "16 x 32, K split over the waves"),
          (16, 16000, 1032, "16 x 32, K split over the waves"), (3, 300, 9000, "16 x 16, K split over the waves"),
@@ -85,8 +87,9 @@ def test_gradient_kernels(rows, cols, K, kernel, t):
 
 
 GATED = [(700, 8200, 72, "256 x 256 tile"), (130, 6200, 4104, "256 x 256 tile"), (2050, 2050, 72, "256 x 192 tile"),
-         (1030, 2050, 72, "128 x 128 tile"), (100, 8200, 2056, "128 x 128 tile"), (130, 40, 72, "64 x 64 tile"),
-         (130, 40, 2056, "64 x 64 tile"), (5, 40, 72, "16 x 16, K split over the waves"),
+         (1030, 2050, 72, "128 x 128 tile"), (100, 8200, 2056, "128 x 128 tile"), (130, 3100, 72, "64 x 64 tile"),
+         (130, 1030, 4104, "64 x 64 tile"), (130, 40, 72, "64 x 64 tile, two groups of waves"),
+         (130, 40, 4104, "64 x 64 tile, two groups of waves"), (333, 1159, 2056, "64 x 64 tile, two groups of waves"), (5, 40, 72, "16 x 16, K split over the waves"),
          (5, 2050, 72, "16 x 32, K split over the waves"), (20, 40, 72, "32 x 16, K split over the waves"),
          (20, 2050, 72, "32 x 32, K split over the waves"), (16, 5003, 1032, "16 x 16, K split over the waves")]
 
@@ -107,7 +110,7 @@ def test_gated_kernels(rows, cols, K, kernel, t):
 
 def test_every_kernel_is_here():
     names = {p[3] for p in PRODUCTS + WAVES}
-    assert names == {p[3] for p in GATED} and len(names) == 8
+    assert names == {p[3] for p in GATED} and len(names) == 9
 
 
 def test_kernel_refuses():
