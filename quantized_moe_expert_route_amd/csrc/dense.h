@@ -73,7 +73,7 @@ struct SlopeArgs {
   float* part;
   int type, act, pre_type;
 };
-constexpr int kBiasRows = 128;  // rows a partial sum of dbias takes
+constexpr int kBiasRows = 32;  // rows a partial sum of dbias takes (2^20 rows: 2^15 workgroups)
 inline int64_t dbias_parts(int64_t M) { return (M + kBiasRows - 1) / kBiasRows; }
 hipError_t launch_slope(const SlopeArgs& a, hipStream_t stream);
 

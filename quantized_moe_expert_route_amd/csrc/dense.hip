@@ -148,21 +148,22 @@ __device__ __forceinline__ void read_pre(const void* pre, int type, int64_t at, 
   else read8<F16, false>(reinterpret_cast<const uint16_t*>(pre) + at, vec, n, v);
 }
 
-// 64 columns a workgroup, eight a lane: a wave takes eight rows of them at a time, the
-// 16 waves 128. dbias's sums of a workgroup are joined in a fixed order, those of
-// several workgroups (kBiasRows rows each) by a second launch. Bound by memory.
-template <bool F16>
-__global__ __launch_bounds__(1024) void slope_kernel(const SlopeArgs a, int vec) {
-  __shared__ float sums[16][64];
+// Eight columns a lane; a wave takes RL rows of 512 / RL columns at a time, the W waves
+// of a workgroup `rows` rows together. dbias's sums of a workgroup are joined in a fixed
+// order, those of several workgroups by a second launch. Bound by memory.
+template <bool F16, int RL, int W>
+__global__ __launch_bounds__(64 * W) void slope_kernel(const SlopeArgs a, int vec, int rows) {
+  constexpr int L = 64 / RL, C = 8 * L;  // lanes of a row, columns
+  __shared__ float sums[W][C];
   const int wave = wave_id(), lane = threadIdx.x & 63;
-  const int64_t n = (int64_t)blockIdx.x * 64 + (lane & 7) * 8;
-  const int64_t m0 = (int64_t)blockIdx.y * kBiasRows, m1 = min(m0 + kBiasRows, a.M);
+  const int64_t n = (int64_t)blockIdx.x * C + (lane % L) * 8;
+  const int64_t m0 = (int64_t)blockIdx.y * rows, m1 = min(m0 + rows, a.M);
   const int left = (int)max((int64_t)0, min((int64_t)8, a.N - n));
   float sum[8] = {};
   if (left > 0) {
     with_act(a.act, [&](auto act) __attribute__((always_inline)) {
-#pragma unroll 2
-      for (int64_t m = m0 + 8 * wave + (lane >> 3); m < m1; m += 128) {
+#pragma unroll 4
+      for (int64_t m = m0 + RL * wave + lane / L; m < m1; m += RL * W) {
         float v[8], p[8];
         read8<F16, false>(reinterpret_cast<const uint16_t*>(a.dy) + m * a.lddy + n, vec & 1, left, v);
         if constexpr (act != MOE_ACT_NONE) {
@@ -184,17 +185,19 @@ __global__ __launch_bounds__(1024) void slope_kernel(const SlopeArgs a, int vec)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
 #pragma unroll
-    for (int o = 8; o < 64; o *= 2) sum[i] += __shfl_xor(sum[i], o, kWave);
-    if (lane < 8) sums[wave][lane * 8 + i] = sum[i];
+    for (int o = L; o < 64; o *= 2) sum[i] += __shfl_xor(sum[i], o, kWave);
+    if (lane < L) sums[wave][i * L + lane] = sum[i];
   }
   __syncthreads();
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  if (wave > 0 || c >= a.N) return;
-  float v = sums[0][lane];
+  for (int i = threadIdx.x; i < C; i += 64 * W) {
+    const int64_t c = (int64_t)blockIdx.x * C + (i % L) * 8 + i / L;
+    if (c >= a.N) continue;
+    float v = sums[0][i];
 #pragma unroll
-  for (int w = 1; w < 16; ++w) v += sums[w][lane];
-  if (gridDim.y == 1) reinterpret_cast<uint16_t*>(a.dbias)[c] = bits16<F16>(v);
-  else a.part[blockIdx.y * a.N + c] = v;
+    for (int w = 1; w < W; ++w) v += sums[w][i];
+    if (gridDim.y == 1) reinterpret_cast<uint16_t*>(a.dbias)[c] = bits16<F16>(v);
+    else a.part[blockIdx.y * a.N + c] = v;
+  }
 }
 
 // 64 columns a workgroup; its 16 waves take the partial sums in turn.
@@ -223,10 +226,16 @@ static bool on16(const void* p, int64_t ld, int64_t elem) { return ((uintptr_t)p
 hipError_t launch_slope(const SlopeArgs& a, hipStream_t stream) {
   const bool f16 = a.type == MOE_FP16;
   const int vec = (on16(a.dy, a.lddy, 2) ? 1 : 0) | (a.pre && on16(a.pre, a.ldp, a.pre_type == MOE_FP32 ? 4 : 2) ? 2 : 0);
-  const int64_t parts = std::max<int64_t>(dbias_parts(a.M), 1);  // (no rows: dbias is zero)
-  const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)parts);
-  hipError_t e = f16 ? launch_k(slope_kernel<true>, grid, dim3(1024), 0, stream, Ev{}, a, vec)
-                     : launch_k(slope_kernel<false>, grid, dim3(1024), 0, stream, Ev{}, a, vec);
+  // Up to 128 rows a workgroup takes all of 64 columns, and dbias needs no second launch (77 x
+  // 1543: 6 us, 9.4 + 3.4 by two); above, whole lines of a row a wave (4096 x 6144 33 us, by 64
+  // columns 40 to 59). No rows: dbias is zero.
+  const bool few = a.M <= 128;
+  const int64_t parts = few ? 1 : dbias_parts(a.M);
+  const dim3 grid((unsigned)(few ? (a.N + 63) / 64 : (a.N + 511) / 512), (unsigned)parts);
+  hipError_t e = few ? f16 ? launch_k(slope_kernel<true, 8, 16>, grid, dim3(1024), 0, stream, Ev{}, a, vec, 128)
+                           : launch_k(slope_kernel<false, 8, 16>, grid, dim3(1024), 0, stream, Ev{}, a, vec, 128)
+                     : f16 ? launch_k(slope_kernel<true, 1, 4>, grid, dim3(256), 0, stream, Ev{}, a, vec, kBiasRows)
+                           : launch_k(slope_kernel<false, 1, 4>, grid, dim3(256), 0, stream, Ev{}, a, vec, kBiasRows);
   if (e == hipSuccess && a.dbias && parts > 1) {
     const dim3 cols((unsigned)((a.N + 63) / 64));
     e = f16 ? launch_k(dbias_kernel<true>, cols, dim3(1024), 0, stream, Ev{}, (const float*)a.part, (uint16_t*)a.dbias, a.N, parts)
