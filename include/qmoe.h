@@ -525,16 +525,18 @@ moe_status moe_scores_forward(const moe_scores* scores, int64_t M, const void* z
 
 /* Distillation from a teacher's top logits. Of row m, the teacher gives k logits
  * (or log probabilities: only their differences count) t [M, k] fp32 at tokens ids
- * int32 [M, k]; a slot whose id is outside [0, V) is empty. With temperature T,
- * p the softmax of t/T over the row's filled slots and q that of z/T over all V:
+ * int32 [M, k]; a slot whose id is outside [0, V) or whose t is -inf is empty.
+ * With temperature T, p the softmax of t/T over the row's filled slots and q that
+ * of z/T over all V:
  *   loss = sum_j p_j (log p_j - log q_ids[j])                     fp32 [M]
  *   dz   = weight/T (q - sum_j p_j [v = ids_j])                    [M, V]
  * weight fp32 [M] is the gradient of the rows' losses. A token in two slots has
  * the sum of both. A row without a filled slot (padding) has loss 0 and gradient
  * 0, whatever its logits and weight; one whose logits hold a NaN or +inf, or nothing
- * but -inf, NaN. A slot of t = -inf has p 0 and takes no part in the loss.
+ * but -inf, NaN.
  * moe_distill_forward writes loss and lse (fp32 [M], log sum exp(z/T), for the
- * backward call; may be NULL); moe_distill_backward reads it;
+ * backward call; may be NULL); moe_distill_backward reads it (rows of |lse| above
+ * 128, whose rounding the gradient would show, it sums again);
  * moe_distill_forward_backward does both at once, for weights known beforehand
  * (1/rows, say). dz of type grad_type: z's own, MOE_BF16 or MOE_FP16, rows lddz
  * apart; it may be z itself (same pointer, stride and type). k 1 .. 64, T 1e-6

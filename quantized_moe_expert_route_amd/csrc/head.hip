@@ -363,13 +363,15 @@ struct ScoresPart {
   double s, t;
 };
 
+// (Log probabilities from the distance to m: lse has lost log s where all logits are the
+// type's lowest number.)
 __device__ void write_scores(const ScoresArgs& a, int64_t m, const Total& r, float given, const Candidates& c) {
   const bool ok = r.m < INFINITY && r.s > 0;  // not NaN either
   const double logs = log(r.s), lse = r.m + logs;
   if (threadIdx.x == 0) {
     if (a.tokens) {
       const int64_t t = a.tokens[m];
-      a.logprobs[m] = ok && t >= 0 && t < a.V ? (float)(given - lse) : NAN;
+      a.logprobs[m] = ok && t >= 0 && t < a.V ? (float)(((double)given - r.m) - logs) : NAN;
     }
     if (a.entropy) a.entropy[m] = ok ? (float)(logs - r.t / r.s) : NAN;
     if (a.lse) a.lse[m] = ok ? (float)lse : r.m == INFINITY ? INFINITY : r.s == 0 ? -INFINITY : NAN;
@@ -377,7 +379,7 @@ __device__ void write_scores(const ScoresArgs& a, int64_t m, const Total& r, flo
   for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
     const uint64_t key = c.top[j];
     a.top_ids[m * a.k + j] = (int32_t)~(uint32_t)key;
-    a.top_logprobs[m * a.k + j] = ok ? (float)(key_to_float((uint32_t)(key >> 32)) - lse) : NAN;
+    a.top_logprobs[m * a.k + j] = ok ? (float)(((double)key_to_float((uint32_t)(key >> 32)) - r.m) - logs) : NAN;
   }
 }
 
@@ -512,7 +514,7 @@ hipError_t launch_scores(const ScoresArgs& a, int cus, hipStream_t stream) {
 }
 
 // ----------------------------------------------------------------- distillation
-// The row's slots in LDS, from the first wave: token (-1 empty) and p, log p in 64
+// The row's slots in LDS, from the first wave: token (-1 empty, as is one of t = -inf) and p, log p in 64
 // bits (the loss of masked logits comes near binary32's largest number).
 struct Teacher {
   int32_t id[64];
@@ -524,13 +526,14 @@ __device__ void read_teacher(const DistillArgs& a, int64_t m, Teacher& w) {
     const int j = threadIdx.x;
     int32_t v = j < a.k ? a.ids[m * a.k + j] : -1;
     if (v < 0 || v >= a.V) v = -1;
-    const float t = v >= 0 ? a.t[m * a.k + j] / a.temperature : -INFINITY;
-    const float mx = row_max(t);
-    const double e = t > -INFINITY || t != t ? exp((double)t - mx) : 0.0;
+    const float t = v >= 0 ? a.t[m * a.k + j] : -INFINITY;
+    if (t == -INFINITY) v = -1;
+    const double d = ((double)t - row_max(t)) / a.temperature;
+    const double e = v >= 0 ? exp(d) : 0.0;
     const double s = wave_sum(e);
     w.id[j] = v;
     w.p[j] = v >= 0 ? e / s : 0.0;
-    w.logp[j] = (double)t - mx - log(s);
+    w.logp[j] = d - log(s);
     const bool any = __ballot(v >= 0) != 0;
     if (j == 0) w.some = any;
   }
@@ -544,9 +547,9 @@ __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t m, cons
   const int j = threadIdx.x;
   const double c = 1.f / a.temperature;
   const bool ok = r.m < INFINITY && r.s > 0;
-  const double lse = r.m * c + log(r.s);
+  const double logs = log(r.s), lse = r.m * c + logs;
   double l = 0;
-  if (w.p[j] != 0) l = w.p[j] * (w.logp[j] - (z * c - lse));
+  if (w.p[j] != 0) l = w.p[j] * (w.logp[j] - (((double)z - r.m) * c - logs));
   l = wave_sum(l);
   if (j == 0) {
     a.loss[m] = !w.some ? 0.f : ok ? (float)l : NAN;
@@ -714,6 +717,11 @@ __global__ __launch_bounds__(64) void distill_loss_kernel(const DistillArgs a, i
   write_loss(a, m, w, joined(a, m, parts), slot_logit(Row<TYPE>(a.z, m, a.ldz, a.V), w));
 }
 
+// Largest magnitude of an lse that the gradient is taken from: rounded to 32 bits it is off by
+// 2^-18 there, and so is the gradient. Rows past it (small temperatures; rows of nothing
+// but the type's lowest number) are summed again, by each of their workgroups.
+constexpr float kNearLse = 128.f;
+
 // The gradient from lse (backward), or from the parts' sums.
 template <int TYPE, int GRAD, int THREADS, bool SUMS>
 __global__ __launch_bounds__(THREADS) void distill_grad_kernel(const DistillArgs a, int parts) {
@@ -725,16 +733,18 @@ __global__ __launch_bounds__(THREADS) void distill_grad_kernel(const DistillArgs
   const int64_t per = (row.pieces + parts - 1) / parts;
   const int64_t p0 = min(per * part, row.pieces), p1 = min(p0 + per, row.pieces);
   read_teacher(a, m, w);
+  const float lse = SUMS ? 0.f : a.lse[m];
   float shift, f = a.weight[m] * c;
-  if constexpr (SUMS) {
-    const Total r = joined(a, m, parts);
+  if (!SUMS && fabsf(lse) <= kNearLse) {
+    // exp(c z - lse) = exp(c (z - shift)) r with shift = lse T rounded
+    shift = lse * a.temperature;
+    f *= expf(__builtin_fmaf(shift, c, -lse));
+  } else {
+    Total r{};
+    if constexpr (SUMS) r = joined(a, m, parts);
+    else if (w.some) r = join<THREADS>(sum_pieces<TYPE, THREADS, 16>(row, 0, row.pieces, true, c * kLog2e), c * kLog2e);
     shift = r.m;
     f = r.m < INFINITY && r.s > 0 ? (float)(f / r.s) : NAN;
-  } else {
-    // exp(c z - lse) = exp(c (z - shift)) r with shift = lse T rounded
-    const float lse = a.lse[m];
-    shift = lse * a.temperature;
-    f = fabsf(lse) < INFINITY ? f * expf(__builtin_fmaf(shift, c, -lse)) : NAN;
   }
   write_grad<TYPE, GRAD, THREADS>(a, m, row, p0, p1, part == 0, w, Slope{shift, f, c * kLog2e, w.some});
 }
@@ -789,7 +799,11 @@ __global__ __launch_bounds__(1024, TYPE == MOE_FP32 && H <= 8 ? 8 : 4) void dist
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     const Row<TYPE> row(a.z, m, a.ldz, a.V);
     if (threadIdx.x < 64) {
-      const int32_t id = lane < a.k ? a.ids[m * a.k + lane] : -1;
+      int32_t id = -1;
+      if (lane < a.k) {
+        const int64_t at = m * a.k + lane;
+        if (a.t[at] != -INFINITY) id = a.ids[at];
+      }
       const bool in = id >= 0 && id < a.V;
       if (in) slot_logits(a, m)[lane] = Logit<TYPE>::load(row.p, id);
       const bool any = __ballot(in) != 0;
@@ -887,7 +901,8 @@ Both choose_both(int64_t M, int64_t V, int type, bool alike, int cus) {
 template <int TYPE, int GRAD>
 hipError_t distill(DistillPass pass, const DistillArgs& a, int cus, hipStream_t stream) {
   const bool small = a.V <= 4096;
-  const int gparts = grad_parts(a.M, a.V, cus);
+  // (over z itself no workgroup may read what another one writes: rows are not split)
+  const int gparts = pass == kDistillBackward && a.dz == a.z ? 1 : grad_parts(a.M, a.V, cus);
   const dim3 rows((unsigned)a.M), grads((unsigned)(a.M * gparts));
   if (pass == kDistillBackward)
     return small ? launch_k(distill_grad_kernel<TYPE, GRAD, 128, false>, grads, dim3(128), 0, stream, Ev{}, a, gparts)

@@ -122,7 +122,7 @@ def gated_backward(dh, pre, x, w13, name, t):
 def lse_error(z, lse):
     """Of log sum exp of rows z: an exponent's argument off by 2 U of itself, exp by 4
     U, sums in chains of at most V/256 + 64, the result rounded once."""
-    q = torch.exp(z - lse[:, None])
+    q = torch.softmax(z, 1)
     far = (lse[:, None] - z).clamp(min=0)
     mean = torch.where(q > 0, q * far, 0.0).sum(1)
     return U * (2 * mean + 4 + z.shape[1] / 256 + 64)
@@ -131,7 +131,7 @@ def lse_error(z, lse):
 def scores(z, tokens, k):
     """lse, logprobs, entropy, top logprobs, top ids and the bounds of the first four."""
     lse = torch.logsumexp(z, 1)
-    lq = z - lse[:, None]
+    lq = torch.log_softmax(z, 1)
     ok = (tokens >= 0) & (tokens < z.shape[1])
     lp = torch.where(ok, lq.gather(1, tokens.clamp(0, z.shape[1] - 1).long()[:, None])[:, 0], math.nan)
     q = torch.exp(lq)
@@ -150,12 +150,12 @@ def scores(z, tokens, k):
 def distill(z, ids, t, weight, T):
     """loss and gradient with their bounds (of the gradient before its rounding)."""
     M, V = z.shape
-    held = (ids >= 0) & (ids < V)
+    held = (ids >= 0) & (ids < V) & (t != -math.inf)
     some = held.any(1)
     s = torch.where(held, t / T, -math.inf)
     p = torch.softmax(torch.where(some[:, None], s, 0.0), 1) * some[:, None]
     lse = torch.logsumexp(z / T, 1)
-    lq = z / T - lse[:, None]
+    lq = torch.log_softmax(z / T, 1)
     at = lq.gather(1, torch.where(held, ids, 0).long())
     lp = torch.where(p > 0, torch.log(p), 0.0)
     loss = torch.where(p > 0, p * (lp - at), 0.0).sum(1)
@@ -165,5 +165,6 @@ def distill(z, ids, t, weight, T):
     target = torch.zeros_like(z).scatter_add_(1, torch.where(held, ids, 0).long(), p)
     f = (weight / T)[:, None]
     grad = f * (q - target)
-    eg = f.abs() * (q * (el[:, None] + U * (8 + 4 * lq.abs().clamp(max=1e4) + 4 * lse.abs()[:, None])) + 16 * U * target) + 4 * U * grad.abs()
+    # (an exponential below the least normal number 2^-126 may come as 0, before f multiplies it)
+    eg = f.abs() * (2.0 ** -126 + q * (el[:, None] + U * (8 + 4 * lq.abs().clamp(max=1e4) + 4 * lse.abs()[:, None])) + 16 * U * target) + 4 * U * grad.abs()
     return loss, torch.where(some, el + 16 * U * (mag + 1), 0.0), grad, torch.where(some[:, None], eg, 0.0)
