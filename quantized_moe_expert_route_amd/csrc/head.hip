@@ -11,6 +11,7 @@
 #include <float.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "head.h"
 #include "mxfp4.h"
@@ -165,23 +166,24 @@ __device__ __forceinline__ uint64_t key_of(float v, int64_t id) {
   return ((uint64_t)order_key(v) << 32) | (uint32_t)~(uint32_t)id;
 }
 
-constexpr int kKeys = 2048;  // candidates held
+template <int THREADS>
 struct Candidates {
+  static constexpr int kKeys = THREADS == 128 ? 512 : 2048;  // candidates held
   uint64_t key[kKeys];
   uint64_t top[kMaxTop];  // the k largest, in order
   uint64_t at_least;      // the threshold
   int n;                  // candidates met; those past kKeys are not held
-  int reached[2][16];     // by a wave's threshold: how many of the threads' best do
+  int reached[2][THREADS / 64];  // by a wave's threshold: how many of the threads' best do
   int threads;            // threads whose best element reaches the threshold,
-  uint16_t thread[1024];  // in no order
-  uint32_t best[1024];    // the threads' best elements (order_key)
+  uint16_t thread[THREADS];  // in no order
+  uint32_t best[THREADS];    // the threads' best elements (order_key)
 };
 
 // The candidates held, largest first, c.n of them at most k; the threshold is the k-th.
 template <int THREADS>
-__device__ void sort_candidates(Candidates& c, int k) {
+__device__ void sort_candidates(Candidates<THREADS>& c, int k) {
   __syncthreads();
-  const int n = min(c.n, kKeys);
+  const int n = min(c.n, c.kKeys);
   int size = 2;
   while (size < n) size *= 2;
 #pragma unroll 1
@@ -209,7 +211,7 @@ __device__ void sort_candidates(Candidates& c, int k) {
 // c.top: the k largest of the candidates (zeros behind fewer). A few hundred are
 // ranked by counting the larger ones, more are sorted.
 template <int THREADS>
-__device__ void rank_candidates(Candidates& c, int k) {
+__device__ void rank_candidates(Candidates<THREADS>& c, int k) {
   __syncthreads();
   const int n = c.n;
   if (n > THREADS) {
@@ -230,16 +232,16 @@ __device__ void rank_candidates(Candidates& c, int k) {
 
 // A thread's N elements v with ids first .. as candidates; those of `left` that found
 // no room stay in it.
-template <int N>
-__device__ __forceinline__ void offer(Candidates& c, const float (&v)[N], int64_t first, uint32_t& left) {
+template <int THREADS, int N>
+__device__ __forceinline__ void offer(Candidates<THREADS>& c, const float (&v)[N], int64_t first, uint32_t& left) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (!(left >> i & 1)) continue;
     const uint64_t key = key_of(v[i], first + i);
     if (key >= c.at_least) {
-      if (c.n > kKeys) continue;
+      if (c.n > c.kKeys) continue;
       const int at = atomicAdd(&c.n, 1);
-      if (at >= kKeys) continue;
+      if (at >= c.kKeys) continue;
       c.key[at] = key;
     }
     left &= ~(1u << i);
@@ -250,7 +252,7 @@ __device__ __forceinline__ void offer(Candidates& c, const float (&v)[N], int64_
 // fit (or fewer than k: `from` is 0 then): whenever they are full, they are sorted, all
 // but k dropped and the threshold raised.
 template <int TYPE, int THREADS>
-__device__ __forceinline__ void reselect(Candidates& c, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, uint64_t from, int k) {
+__device__ __forceinline__ void reselect(Candidates<THREADS>& c, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, uint64_t from, int k) {
   if (threadIdx.x == 0) c.n = 0, c.at_least = from;
   __syncthreads();
   const int64_t inner = (p1 - p0) * Logit<TYPE>::kPiece, all = inner + (edges ? row.edges() : 0);
@@ -264,7 +266,7 @@ __device__ __forceinline__ void reselect(Candidates& c, const Row<TYPE>& row, in
     for (;;) {
       offer(c, v, first, left);
       __syncthreads();
-      const bool full = c.n >= kKeys;
+      const bool full = c.n >= c.kKeys;
       __syncthreads();
       if (!full) break;
       sort_candidates<THREADS>(c, k);
@@ -278,7 +280,7 @@ __device__ __forceinline__ void reselect(Candidates& c, const Row<TYPE>& row, in
 // reaches it. Those threads' pieces are read again. The threshold is taken from the
 // maxima's upper 16 bits.
 template <int TYPE, int THREADS>
-__device__ void select(Candidates& c, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, float edge, float best, int k) {
+__device__ void select(Candidates<THREADS>& c, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, float edge, float best, int k) {
   constexpr int E = Logit<TYPE>::kPiece, W = THREADS / 64;
   const uint32_t mine = order_key(best);
   c.best[threadIdx.x] = mine;
@@ -350,7 +352,7 @@ __device__ void select(Candidates& c, const Row<TYPE>& row, int64_t p0, int64_t 
   // equal ones
   const int met = c.n;
   __syncthreads();
-  if (met < k || met > kKeys) reselect<TYPE, THREADS>(c, row, p0, p1, edges, met < k ? 0 : at_least, k);
+  if (met < k || met > c.kKeys) reselect<TYPE, THREADS>(c, row, p0, p1, edges, met < k ? 0 : at_least, k);
   rank_candidates<THREADS>(c, k);
 }
 
@@ -365,7 +367,7 @@ struct ScoresPart {
 
 // (Log probabilities from the distance to m: lse has lost log s where all logits are the
 // type's lowest number.)
-__device__ void write_scores(const ScoresArgs& a, int64_t m, const Total& r, float given, const Candidates& c) {
+__device__ void write_scores(const ScoresArgs& a, int64_t m, const Total& r, float given, const uint64_t* top) {
   const bool ok = r.m < INFINITY && r.s > 0;  // not NaN either
   const double logs = log(r.s), lse = r.m + logs;
   if (threadIdx.x == 0) {
@@ -377,7 +379,7 @@ __device__ void write_scores(const ScoresArgs& a, int64_t m, const Total& r, flo
     if (a.lse) a.lse[m] = ok ? (float)lse : r.m == INFINITY ? INFINITY : r.s == 0 ? -INFINITY : NAN;
   }
   for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
-    const uint64_t key = c.top[j];
+    const uint64_t key = top[j];
     a.top_ids[m * a.k + j] = (int32_t)~(uint32_t)key;
     a.top_logprobs[m * a.k + j] = ok ? (float)(((double)key_to_float((uint32_t)(key >> 32)) - r.m) - logs) : NAN;
   }
@@ -394,7 +396,8 @@ __device__ __forceinline__ float given_logit(const ScoresArgs& a, const Row<TYPE
 template <int TYPE, int THREADS, int N, bool TOP>
 __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel(const ScoresArgs a, int parts) {
   constexpr int E = Logit<TYPE>::kPiece, NP = N / E;  // pieces
-  __shared__ Candidates c;
+  __shared__ std::conditional_t<TOP, Candidates<THREADS>, int> c;
+  const uint64_t* top = nullptr;
   const int64_t m = blockIdx.x / parts;
   const int part = blockIdx.x % parts;
   const Row<TYPE> row(a.z, m, a.ldz, a.V);
@@ -423,22 +426,25 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel
     sums.add(v, kLog2e);
   }
   const Total r = join<THREADS>(sums, kLog2e);
-  if constexpr (TOP) select<TYPE, THREADS>(c, row, p0, p1, edges, edge[0], sums.m, a.k);
+  if constexpr (TOP) {
+    select<TYPE, THREADS>(c, row, p0, p1, edges, edge[0], sums.m, a.k);
+    top = c.top;
+  }
   if (parts == 1) {
-    write_scores(a, m, r, given, c);
+    write_scores(a, m, r, given, top);
     return;
   }
   if (threadIdx.x == 0) reinterpret_cast<ScoresPart*>(a.ws)[blockIdx.x] = {r.m, 0.f, r.s, r.t};
   uint64_t* keys = reinterpret_cast<uint64_t*>(reinterpret_cast<ScoresPart*>(a.ws) + a.M * parts) + (int64_t)blockIdx.x * a.k;
-  for (int j = threadIdx.x; j < a.k; j += THREADS) keys[j] = c.top[j];
+  for (int j = threadIdx.x; j < a.k; j += THREADS) keys[j] = top[j];
 }
 
 constexpr int kMaxParts = 32;
-static_assert(kMaxParts * kMaxTop <= kKeys, "the parts' keys are sorted at once");
+static_assert(kMaxParts * kMaxTop <= Candidates<256>::kKeys, "the parts' keys are sorted at once");
 
 template <int TYPE>
 __global__ __launch_bounds__(256) void scores_join_kernel(const ScoresArgs a, int parts) {
-  __shared__ Candidates c;
+  __shared__ Candidates<256> c;
   const int64_t m = blockIdx.x;
   const Row<TYPE> row(a.z, m, a.ldz, a.V);
   const float given = given_logit<TYPE>(a, row, m);
@@ -467,7 +473,7 @@ __global__ __launch_bounds__(256) void scores_join_kernel(const ScoresArgs a, in
     r.t = wave_sum((mine.t + mine.s * back) * f);
   }
   if (a.k) rank_candidates<256>(c, a.k);
-  write_scores(a, m, r, given, c);
+  write_scores(a, m, r, given, c.top);
 }
 
 namespace {
@@ -574,7 +580,7 @@ __device__ __forceinline__ float slot_grad(const DistillArgs& a, int64_t m, cons
   const int j = threadIdx.x;
   double q = 0;
   mine = true;
-#pragma unroll 1
+#pragma unroll 4
   for (int i = 0; i < a.k; ++i)
     if (w.id[i] == w.id[j]) {
       if (i < j) mine = false;
@@ -583,12 +589,18 @@ __device__ __forceinline__ float slot_grad(const DistillArgs& a, int64_t m, cons
   return (float)(g.at(z) - a.weight[m] / a.temperature * q);
 }
 
+template <bool ONCE>
+__device__ __forceinline__ void store16(uint8_t* p, uint4 v) {
+  if constexpr (ONCE) __builtin_nontemporal_store(__builtin_bit_cast(v4i, v), reinterpret_cast<v4i*>(p));
+  else *reinterpret_cast<uint4*>(p) = v;
+}
+
 // A piece's gradients to elements o .. of a row of dz; `vec`: on 16 bytes for whole
-// pieces of dz's type.
-template <int GRAD, int E>
+// pieces of dz's type. ONCE: past the caches.
+template <int GRAD, int E, bool ONCE = false>
 __device__ __forceinline__ void store_grads(uint8_t* out, uint32_t o, bool vec, const float (&g)[E]) {
   if constexpr (GRAD == MOE_FP32) {
-    if (vec) *reinterpret_cast<float4*>(out + o * 4) = make_float4(g[0], g[1], g[2], g[3]);
+    if (vec) store16<ONCE>(out + o * 4, __builtin_bit_cast(uint4, make_float4(g[0], g[1], g[2], g[3])));
     else {
 #pragma unroll
       for (int i = 0; i < E; ++i) Logit<GRAD>::store(out, o + i, g[i]);
@@ -601,7 +613,7 @@ __device__ __forceinline__ void store_grads(uint8_t* out, uint32_t o, bool vec, 
     } s;
 #pragma unroll
     for (int i = 0; i < E; ++i) s.b[i] = GRAD == MOE_FP16 ? fp16_bits(g[i]) : bf16_bits(g[i]);
-    if (E == 8 && vec) *reinterpret_cast<uint4*>(out + o * 2) = s.q4;
+    if (E == 8 && vec) store16<ONCE>(out + o * 2, s.q4);
     else if (E == 4 && ((uintptr_t)(out + o * 2) & 7) == 0) *reinterpret_cast<uint2*>(out + o * 2) = s.q2;
     else {
 #pragma unroll
@@ -774,7 +786,7 @@ __device__ __forceinline__ float* slot_logits(const DistillArgs& a, int64_t m) {
 }
 
 template <int TYPE, int GRAD, int H>
-__global__ __launch_bounds__(1024, TYPE == MOE_FP32 && H <= 8 ? 8 : 4) void distill_held_kernel(const DistillArgs a) {
+__global__ __launch_bounds__(1024, H <= 8 ? 8 : 4) void distill_held_kernel(const DistillArgs a) {
   constexpr int E = Logit<TYPE>::kPiece, G = 16 / E, W = 16;  // pieces summed at a time, waves
   static_assert(H % G == 0, "whole groups");
   __shared__ float lm[W];
@@ -789,12 +801,38 @@ __global__ __launch_bounds__(1024, TYPE == MOE_FP32 && H <= 8 ? 8 : 4) void dist
   auto fresh = [](uint4& p) __attribute__((always_inline)) { asm volatile("" : "+v"(p.x), "+v"(p.y), "+v"(p.z), "+v"(p.w)); };
   auto load = [&](const Row<TYPE>& row, int h) __attribute__((always_inline)) {
     const uint32_t p = h * 1024 + tid;
-    q[h] = p < (uint32_t)row.pieces ? ld16(row.p + row.head * Logit<TYPE>::kBytes + p * 16u) : Logit<TYPE>::none();
+    const v4i* from = reinterpret_cast<const v4i*>(row.p + row.head * Logit<TYPE>::kBytes + p * 16u);
+    q[h] = p < (uint32_t)row.pieces ? __builtin_bit_cast(uint4, __builtin_nontemporal_load(from)) : Logit<TYPE>::none();
   };
+  Sums<false> sums;
+  float edge;
+  auto begin = [&](const Row<TYPE>& row) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(tid));
+    edge = (int)tid < row.edges() ? Logit<TYPE>::load(row.p, row.edge(tid)) : -INFINITY;
+    sums = Sums<false>{};
+  };
+  auto add = [&](const Row<TYPE>& row, int h) __attribute__((always_inline)) {  // pieces h .. h + G - 1
+    if (row.pieces <= h * 1024) return;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      // (after the last group's sums: else all groups' values come first)
+      asm volatile("" : "+v"(q[h + i].x), "+v"(q[h + i].y), "+v"(q[h + i].z), "+v"(q[h + i].w), "+v"(sums.s), "+v"(sums.m));
+    }
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = Logit<TYPE>::value(q[h + i / E], i % E);
+    sums.add(v, cl);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr int lag = 4;
+  static_assert(lag % G == 0, "whole groups");
   {
     const Row<TYPE> row(a.z, blockIdx.x, a.ldz, a.V);
 #pragma unroll
     for (int h = 0; h < H; ++h) load(row, h);
+    begin(row);
+#pragma unroll
+    for (int h = 0; h < H - lag; h += G) add(row, h);
   }
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     const Row<TYPE> row(a.z, m, a.ldz, a.V);
@@ -809,24 +847,10 @@ __global__ __launch_bounds__(1024, TYPE == MOE_FP32 && H <= 8 ? 8 : 4) void dist
       const bool any = __ballot(in) != 0;
       if (lane == 0) some = any;
     }
-    asm volatile("" : "+v"(tid));
-    const bool at_edge = (int)tid < row.edges();
-    const float edge[1] = {at_edge ? Logit<TYPE>::load(row.p, row.edge(tid)) : -INFINITY};
-    Sums<false> sums;
-    sums.add(edge, cl);
 #pragma unroll
-    for (int h = 0; h < H; h += G) {
-      float v[16];
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        // (after the last group's sums: else all groups' values come first)
-        asm volatile("" : "+v"(q[h + i].x), "+v"(q[h + i].y), "+v"(q[h + i].z), "+v"(q[h + i].w), "+v"(sums.s), "+v"(sums.m));
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = Logit<TYPE>::value(q[h + i / E], i % E);
-      sums.add(v, cl);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    for (int h = H - lag; h < H; h += G) add(row, h);
+    const float last[1] = {edge};
+    sums.add(last, cl);
     // the sums of the threads, in 64 bits
     float top = row_max(sums.m);
     if (lane == 0) lm[wave] = top;
@@ -840,9 +864,11 @@ __global__ __launch_bounds__(1024, TYPE == MOE_FP32 && H <= 8 ? 8 : 4) void dist
     if (threadIdx.x == 0) reinterpret_cast<ScoresPart*>(a.ws)[m] = {top, 0.f, s, 0};
     const Slope g{top, top < INFINITY && s > 0 ? (float)(a.weight[m] * c / s) : NAN, cl, some};
     uint8_t* out = grad_row<GRAD>(a, m);
-    if (at_edge) Logit<GRAD>::store(out, row.edge(tid), g.at(edge[0]));
+    asm volatile("" : "+v"(tid));
+    if ((int)tid < row.edges()) Logit<GRAD>::store(out, row.edge(tid), g.at(edge));
     const int64_t mn = m + gridDim.x;
     const Row<TYPE> next(a.z, mn < a.M ? mn : m, a.ldz, mn < a.M ? a.V : 0);
+    begin(next);
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       const uint32_t p = h * 1024 + tid;
@@ -851,10 +877,11 @@ __global__ __launch_bounds__(1024, TYPE == MOE_FP32 && H <= 8 ? 8 : 4) void dist
         float v[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) v[i] = g.at(Logit<TYPE>::value(q[h], i));
-        store_grads<GRAD>(out + row.head * Logit<GRAD>::kBytes, p * (uint32_t)E, true, v);
+        store_grads<GRAD, E, true>(out + row.head * Logit<GRAD>::kBytes, p * (uint32_t)E, true, v);
       }
       load(next, h);
       __builtin_amdgcn_sched_barrier(0);
+      if (h >= lag && (h + 1) % G == 0) add(next, h + 1 - G - lag);
     }
     __syncthreads();  // (all have read `some`)
   }
@@ -918,7 +945,7 @@ hipError_t distill(DistillPass pass, const DistillArgs& a, int cus, hipStream_t 
       if (how == kHeld) {
         const bool half = a.V * Logit<TYPE>::kBytes <= 128 * 1024;
         // (as many workgroups as fit at once)
-        const dim3 grid((unsigned)std::min<int64_t>(a.M, TYPE == MOE_FP32 && half ? 2 * cus : cus));
+        const dim3 grid((unsigned)std::min<int64_t>(a.M, half ? 2 * cus : cus));
         const hipError_t e = half ? launch_k(distill_held_kernel<TYPE, GRAD, 8>, grid, dim3(1024), 0, stream, Ev{}, a)
                                   : launch_k(distill_held_kernel<TYPE, GRAD, 16>, grid, dim3(1024), 0, stream, Ev{}, a);
         return e != hipSuccess ? e : launch_k(distill_finish_kernel<TYPE, GRAD>, rows, dim3(64), 0, stream, Ev{}, a);
