@@ -63,6 +63,9 @@ struct Row {
     pieces = (n - head) / e;
     tail = (int)(n - head - pieces * e);
   }
+  __device__ __forceinline__ uint4 piece_once(int64_t i) const {
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p + head * Logit<TYPE>::kBytes + i * 16)));
+  }
   __device__ __forceinline__ uint4 piece(int64_t i) const { return ld16(p + head * Logit<TYPE>::kBytes + i * 16); }
   __device__ __forceinline__ int64_t first(int64_t i) const { return head + i * Logit<TYPE>::kPiece; }  // its first element
   __device__ __forceinline__ int edges() const { return head + tail; }  // elements outside the pieces,
@@ -411,7 +414,8 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const int64_t p = base + u * THREADS + threadIdx.x;
-      q[u] = p < p1 ? row.piece(p) : Logit<TYPE>::none();
+      if constexpr (!TOP && THREADS == 512) q[u] = p < p1 ? row.piece_once(p) : Logit<TYPE>::none();
+      else q[u] = p < p1 ? row.piece(p) : Logit<TYPE>::none();
     }
   };
   load(p0);
@@ -597,7 +601,7 @@ __device__ __forceinline__ void store16(uint8_t* p, uint4 v) {
 
 // A piece's gradients to elements o .. of a row of dz; `vec`: on 16 bytes for whole
 // pieces of dz's type. ONCE: past the caches.
-template <int GRAD, int E, bool ONCE = false>
+template <int GRAD, bool ONCE, int E>
 __device__ __forceinline__ void store_grads(uint8_t* out, uint32_t o, bool vec, const float (&g)[E]) {
   if constexpr (GRAD == MOE_FP32) {
     if (vec) store16<ONCE>(out + o * 4, __builtin_bit_cast(uint4, make_float4(g[0], g[1], g[2], g[3])));
@@ -626,6 +630,10 @@ __device__ __forceinline__ uint8_t* grad_row(const DistillArgs& a, int64_t m) {
   return reinterpret_cast<uint8_t*>(a.dz) + m * a.lddz * Logit<GRAD>::kBytes;
 }
 
+// Gradients of more bytes are written past the caches, which would not hold them for
+// their reader, and the logits' second reading finds more of them there.
+constexpr int64_t kOnce = (int64_t)128 << 20;
+
 // The gradient of pieces [p0, p1) of a row (and of the elements outside the pieces).
 template <int TYPE, int GRAD, int THREADS>
 __device__ void write_grad(const DistillArgs& a, int64_t m, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges,
@@ -646,23 +654,27 @@ __device__ void write_grad(const DistillArgs& a, int64_t m, const Row<TYPE>& row
   __syncthreads();
   if (at_edge) Logit<GRAD>::store(out, row.edge(threadIdx.x), g.at(edge));
   const bool vec = ((uintptr_t)(out + (int64_t)row.head * Logit<GRAD>::kBytes) & 15) == 0;  // dz's pieces lie as z's
-  for (int64_t base = p0; base < p1; base += NP * THREADS) {
-    uint4 q[NP];
+  auto pieces = [&](auto once) __attribute__((always_inline)) {
+    for (int64_t base = p0; base < p1; base += NP * THREADS) {
+      uint4 q[NP];
 #pragma unroll
-    for (int u = 0; u < NP; ++u) {
-      const int64_t p = base + u * THREADS + threadIdx.x;
-      if (p < p1) q[u] = row.piece(p);
+      for (int u = 0; u < NP; ++u) {
+        const int64_t p = base + u * THREADS + threadIdx.x;
+        if (p < p1) q[u] = row.piece(p);
+      }
+#pragma unroll
+      for (int u = 0; u < NP; ++u) {
+        const int64_t p = base + u * THREADS + threadIdx.x;
+        if (p >= p1) continue;
+        float v[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = g.at(Logit<TYPE>::value(q[u], i));
+        store_grads<GRAD, decltype(once)::value>(out, (uint32_t)row.first(p), vec, v);
+      }
     }
-#pragma unroll
-    for (int u = 0; u < NP; ++u) {
-      const int64_t p = base + u * THREADS + threadIdx.x;
-      if (p >= p1) continue;
-      float v[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) v[i] = g.at(Logit<TYPE>::value(q[u], i));
-      store_grads<GRAD>(out, (uint32_t)row.first(p), vec, v);
-    }
-  }
+  };
+  if (a.M * a.lddz * Logit<GRAD>::kBytes > kOnce) pieces(std::true_type{});
+  else pieces(std::false_type{});
   __syncthreads();
   if (mine) Logit<GRAD>::store(out, w.id[threadIdx.x], slot);
 }
@@ -877,7 +889,7 @@ __global__ __launch_bounds__(1024, H <= 8 ? 8 : 4) void distill_held_kernel(cons
         float v[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) v[i] = g.at(Logit<TYPE>::value(q[h], i));
-        store_grads<GRAD, E, true>(out + row.head * Logit<GRAD>::kBytes, p * (uint32_t)E, true, v);
+        store_grads<GRAD, true>(out + row.head * Logit<GRAD>::kBytes, p * (uint32_t)E, true, v);
       }
       load(next, h);
       __builtin_amdgcn_sched_barrier(0);
