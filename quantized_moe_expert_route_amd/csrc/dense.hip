@@ -150,7 +150,8 @@ __device__ __forceinline__ void read_pre(const void* pre, int type, int64_t at, 
 
 // Eight columns a lane; a wave takes RL rows of 512 / RL columns at a time, the W waves
 // of a workgroup `rows` rows together. dbias's sums of a workgroup are joined in a fixed
-// order, those of several workgroups by a second launch. Bound by memory.
+// order, those of several workgroups by a second launch. Bound by memory: 4096 x 6144 33 us
+// (4.6 TB/s: dy and pre read, dz written), dbias's second launch 5 us.
 template <bool F16, int RL, int W>
 __global__ __launch_bounds__(64 * W) void slope_kernel(const SlopeArgs a, int vec, int rows) {
   constexpr int L = 64 / RL, C = 8 * L;  // lanes of a row, columns
@@ -244,7 +245,8 @@ hipError_t launch_slope(const SlopeArgs& a, hipStream_t stream) {
   return e;
 }
 
-// Eight columns of I of a row a lane, both halves of dz. vec: the rows and halves of dh
+// Eight columns of I of a row a lane, both halves of dz. Bound by memory: 4096 x 2 2048 25
+// us (4.7 TB/s, pre in 32 bits). vec: the rows and halves of dh
 // (1), pre (2) and dz (4) move in 16-byte pieces.
 template <bool F16>
 __global__ __launch_bounds__(256) void gated_slope_kernel(const GatedSlopeArgs a, int vec) {
