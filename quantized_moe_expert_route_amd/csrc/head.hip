@@ -169,22 +169,24 @@ __device__ __forceinline__ uint64_t key_of(float v, int64_t id) {
   return ((uint64_t)order_key(v) << 32) | (uint32_t)~(uint32_t)id;
 }
 
-template <int THREADS>
+template <int THREADS, int STRETCHES = 1>
 struct Candidates {
+  static constexpr int kStretches = STRETCHES;  // of a thread's pieces
   static constexpr int kKeys = THREADS == 128 ? 512 : 2048;  // candidates held
   uint64_t key[kKeys];
   uint64_t top[kMaxTop];  // the k largest, in order
   uint64_t at_least;      // the threshold
   int n;                  // candidates met; those past kKeys are not held
   int reached[2][THREADS / 64];  // by a wave's threshold: how many of the threads' best do
-  int threads;            // threads whose best element reaches the threshold,
-  uint16_t thread[THREADS];  // in no order
+  int stretches;  // of threads, whose best element reaches the threshold: thread + THREADS
+  uint16_t stretch[kStretches * THREADS];  // stretch, in no order
+  uint16_t high[kStretches * THREADS];     // of the stretches' best elements the upper 16 bits
   uint32_t best[THREADS];    // the threads' best elements (order_key)
 };
 
 // The candidates held, largest first, c.n of them at most k; the threshold is the k-th.
-template <int THREADS>
-__device__ void sort_candidates(Candidates<THREADS>& c, int k) {
+template <int THREADS, int S>
+__device__ void sort_candidates(Candidates<THREADS, S>& c, int k) {
   __syncthreads();
   const int n = min(c.n, c.kKeys);
   int size = 2;
@@ -213,12 +215,12 @@ __device__ void sort_candidates(Candidates<THREADS>& c, int k) {
 
 // c.top: the k largest of the candidates (zeros behind fewer). A few hundred are
 // ranked by counting the larger ones, more are sorted.
-template <int THREADS>
-__device__ void rank_candidates(Candidates<THREADS>& c, int k) {
+template <int THREADS, int S>
+__device__ void rank_candidates(Candidates<THREADS, S>& c, int k) {
   __syncthreads();
   const int n = c.n;
   if (n > THREADS) {
-    sort_candidates<THREADS>(c, k);
+    sort_candidates(c, k);
     for (int j = threadIdx.x; j < k; j += THREADS) c.top[j] = j < c.n ? c.key[j] : 0;
   } else {
     for (int j = n + threadIdx.x; j < k; j += THREADS) c.top[j] = 0;
@@ -235,8 +237,8 @@ __device__ void rank_candidates(Candidates<THREADS>& c, int k) {
 
 // A thread's N elements v with ids first .. as candidates; those of `left` that found
 // no room stay in it.
-template <int THREADS, int N>
-__device__ __forceinline__ void offer(Candidates<THREADS>& c, const float (&v)[N], int64_t first, uint32_t& left) {
+template <int THREADS, int S, int N>
+__device__ __forceinline__ void offer(Candidates<THREADS, S>& c, const float (&v)[N], int64_t first, uint32_t& left) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if (!(left >> i & 1)) continue;
@@ -254,8 +256,8 @@ __device__ __forceinline__ void offer(Candidates<THREADS>& c, const float (&v)[N
 // The k largest of a segment again, of which more candidates reach the threshold than
 // fit (or fewer than k: `from` is 0 then): whenever they are full, they are sorted, all
 // but k dropped and the threshold raised.
-template <int TYPE, int THREADS>
-__device__ __forceinline__ void reselect(Candidates<THREADS>& c, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, uint64_t from, int k) {
+template <int TYPE, int THREADS, int S>
+__device__ __forceinline__ void reselect(Candidates<THREADS, S>& c, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, uint64_t from, int k) {
   if (threadIdx.x == 0) c.n = 0, c.at_least = from;
   __syncthreads();
   const int64_t inner = (p1 - p0) * Logit<TYPE>::kPiece, all = inner + (edges ? row.edges() : 0);
@@ -272,7 +274,7 @@ __device__ __forceinline__ void reselect(Candidates<THREADS>& c, const Row<TYPE>
       const bool full = c.n >= c.kKeys;
       __syncthreads();
       if (!full) break;
-      sort_candidates<THREADS>(c, k);
+      sort_candidates(c, k);
     }
   }
 }
@@ -280,14 +282,16 @@ __device__ __forceinline__ void reselect(Candidates<THREADS>& c, const Row<TYPE>
 // The k largest of a segment whose threads hold their own elements' maxima: at least k
 // elements reach the k-th largest of these, and hardly more do (131072 elements of 512
 // threads, k 32: 33 where nothing ties), all of them elements of threads whose maximum
-// reaches it. Those threads' pieces are read again. The threshold is taken from the
-// maxima's upper 16 bits.
-template <int TYPE, int THREADS>
-__device__ void select(Candidates<THREADS>& c, const Row<TYPE>& row, int64_t p0, int64_t p1, bool edges, float edge, float best, int k) {
+// reaches it, in stretches of `span` of a thread's pieces whose maximum (c.high) does.
+// Those are read again (whole threads: 1.4 times the memory's traffic, a 16-byte piece
+// costs a line). The threshold is taken from the maxima's upper 16 bits.
+template <int TYPE, int THREADS, int S>
+__device__ void select(Candidates<THREADS, S>& c, const Row<TYPE>& row, int64_t p0, int64_t p1, int span, bool edges, float edge, float best,
+                       int k) {
   constexpr int E = Logit<TYPE>::kPiece, W = THREADS / 64;
   const uint32_t mine = order_key(best);
   c.best[threadIdx.x] = mine;
-  if (threadIdx.x == 0) c.n = 0, c.threads = 0;
+  if (threadIdx.x == 0) c.n = 0, c.stretches = 0;
   __syncthreads();
   // The largest 16-bit threshold that k maxima reach. The waves try a digit's values, one
   // each (two waves: a bit at a time by the first).
@@ -325,19 +329,24 @@ __device__ void select(Candidates<THREADS>& c, const Row<TYPE>& row, int64_t p0,
   }
   __syncthreads();
   const uint64_t at_least = c.at_least;
-  if (mine >= (uint32_t)(at_least >> 32)) c.thread[atomicAdd(&c.threads, 1)] = (uint16_t)threadIdx.x;
+  if (mine >= (uint32_t)(at_least >> 32)) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const int at = i * THREADS + threadIdx.x;
+      if (S == 1 || c.high[at] >= (uint32_t)(at_least >> 48)) c.stretch[atomicAdd(&c.stretches, 1)] = (uint16_t)at;
+    }
+  }
   if (edges && (int)threadIdx.x < row.edges()) {
     float v[1] = {edge};
     uint32_t left = 1;
     offer(c, v, row.edge(threadIdx.x), left);
   }
   __syncthreads();
-  const int n = c.threads;
-  const int rounds = (int)((p1 - p0 + THREADS - 1) / THREADS);  // pieces a thread
+  const int n = c.stretches;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < rounds * n; i += THREADS) {
-    const int r = i / n;
-    const int64_t p = p0 + r * THREADS + c.thread[i - r * n];
+  for (int i = threadIdx.x; i < span * n; i += THREADS) {
+    const int r = i / n, at = c.stretch[i - r * n];
+    const int64_t p = p0 + ((int64_t)(at / THREADS) * span + r) * THREADS + at % THREADS;
     if (p >= p1) continue;
     const uint4 q = row.piece(p);
     float v[E], top;
@@ -355,8 +364,8 @@ __device__ void select(Candidates<THREADS>& c, const Row<TYPE>& row, int64_t p0,
   // equal ones
   const int met = c.n;
   __syncthreads();
-  if (met < k || met > c.kKeys) reselect<TYPE, THREADS>(c, row, p0, p1, edges, met < k ? 0 : at_least, k);
-  rank_candidates<THREADS>(c, k);
+  if (met < k || met > c.kKeys) reselect<TYPE>(c, row, p0, p1, edges, met < k ? 0 : at_least, k);
+  rank_candidates(c, k);
 }
 
 // ----------------------------------------------------------------- scores
@@ -399,10 +408,10 @@ __device__ __forceinline__ float given_logit(const ScoresArgs& a, const Row<TYPE
 // TB/s) without alternatives, whose logits are read past the caches; 125 with 32 of them: the
 // search for the threshold and the second reading of some 33 threads' pieces are a
 // workgroup's own latency, and the logits pass through the caches for it.
-template <int TYPE, int THREADS, int N, bool TOP>
+template <int TYPE, int THREADS, int N, bool TOP, int S>
 __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel(const ScoresArgs a, int parts) {
   constexpr int E = Logit<TYPE>::kPiece, NP = N / E;  // pieces
-  __shared__ std::conditional_t<TOP, Candidates<THREADS>, int> c;
+  __shared__ std::conditional_t<TOP, Candidates<THREADS, S>, int> c;
   const uint64_t* top = nullptr;
   const int64_t m = blockIdx.x / parts;
   const int part = blockIdx.x % parts;
@@ -425,16 +434,29 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel
   float edge[1] = {edges && (int)threadIdx.x < row.edges() ? Logit<TYPE>::load(row.p, row.edge(threadIdx.x)) : -INFINITY};
   const float given = parts == 1 ? given_logit<TYPE>(a, row, m) : 0.f;  // (two loads one behind the other, beside the tile's)
   sums.add(edge, kLog2e);
-  for (int64_t base = p0; base < p1 || base == p0; base += NP * THREADS) {
+  const int tiles = (int)((p1 - p0 + NP * THREADS - 1) / (NP * THREADS)), span = (tiles + S - 1) / S;  // a stretch's tiles
+  int64_t base = p0;
+  auto sum_tile = [&]() __attribute__((always_inline)) {
     float v[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = Logit<TYPE>::value(q[i / E], i % E);
-    load(base + NP * THREADS);
-    sums.add(v, kLog2e);
+    load(base += NP * THREADS);
+    return sums.add(v, kLog2e);
+  };
+  if constexpr (S == 1) {
+    for (int t = 0; t < tiles; ++t) sum_tile();
+  } else {
+    int t = 0;
+#pragma unroll 1
+    for (int stretch = 0; stretch < S; ++stretch) {
+      float high = -INFINITY;
+      for (int end = min(t + span, tiles); t < end; ++t) high = fmaxf(high, sum_tile());
+      c.high[stretch * THREADS + threadIdx.x] = (uint16_t)(order_key(high) >> 16);
+    }
   }
   const Total r = join<THREADS>(sums, kLog2e);
   if constexpr (TOP) {
-    select<TYPE, THREADS>(c, row, p0, p1, edges, edge[0], sums.m, a.k);
+    select<TYPE>(c, row, p0, p1, span * NP, edges, edge[0], sums.m, a.k);
     top = c.top;
   }
   if (parts == 1) {
@@ -479,7 +501,7 @@ __global__ __launch_bounds__(256) void scores_join_kernel(const ScoresArgs a, in
     r.s = wave_sum(mine.s * f);
     r.t = wave_sum((mine.t + mine.s * back) * f);
   }
-  if (a.k) rank_candidates<256>(c, a.k);
+  if (a.k) rank_candidates(c, a.k);
   write_scores(a, m, r, given, c.top);
 }
 
@@ -496,14 +518,19 @@ int parts_of(int64_t M, int64_t V, int cus) {
 // Up to a row a CU, a workgroup has 1024 threads and twice the loads under way.
 bool few_rows(int64_t M, int parts, int cus) { return M <= cus && parts == 1; }
 
+// (Stretches pay where lines read twice do, many long rows: 2048 x 131072 bf16 125.5 us
+// without, 111 with them, fp32 1024 x 131072 119 and 102; 4096 x 8000 49 and 54, 16 x 131072
+// 13.2 and 14.7. Threads: 4096 x 1000 17 us by 128, 50 by 512; 77 x 30011 11.5 by 1024, 10.5 by
+// 512, 200 x 65000 15.5 and 16.1.)
 template <int TYPE, bool TOP>
 hipError_t scores(const ScoresArgs& a, int cus, hipStream_t stream) {
   const int parts = parts_of(a.M, a.V, cus);
   const dim3 grid((unsigned)(a.M * parts));
   hipError_t e;
-  if (a.V <= 4096) e = launch_k(scores_kernel<TYPE, 128, 16, TOP>, grid, dim3(128), 0, stream, Ev{}, a, parts);
-  else if (few_rows(a.M, parts, cus)) e = launch_k(scores_kernel<TYPE, 1024, 32, TOP>, grid, dim3(1024), 0, stream, Ev{}, a, parts);
-  else e = launch_k(scores_kernel<TYPE, 512, 16, TOP>, grid, dim3(512), 0, stream, Ev{}, a, parts);
+  if (a.V <= 4096) e = launch_k(scores_kernel<TYPE, 128, 16, TOP, 1>, grid, dim3(128), 0, stream, Ev{}, a, parts);
+  else if (few_rows(a.M, parts, cus)) e = launch_k(scores_kernel<TYPE, 1024, 32, TOP, 1>, grid, dim3(1024), 0, stream, Ev{}, a, parts);
+  else if (TOP && a.M > cus && a.V > 32768) e = launch_k(scores_kernel<TYPE, 512, 16, TOP, TOP ? 4 : 1>, grid, dim3(512), 0, stream, Ev{}, a, parts);
+  else e = launch_k(scores_kernel<TYPE, 512, 16, TOP, 1>, grid, dim3(512), 0, stream, Ev{}, a, parts);
   if (e == hipSuccess && parts > 1)
     e = launch_k(scores_join_kernel<TYPE>, dim3((unsigned)a.M), dim3(256), 0, stream, Ev{}, a, parts);
   return e;
@@ -934,13 +961,16 @@ int grad_parts(int64_t M, int64_t V, int cus) {
 
 // How forward and backward at once go: kAlone, a row a workgroup, which reads it twice
 // (the second time from the L2 or the memory-side cache); kHeld, the row held between; kSplit, as the two calls
-// but with the sums in full.
+// but with the sums in full. (bf16: 16 x 131072 14.2 us split, 24.3 alone, 100 rows 26.0 and 28.6;
+// 2048 x 131072 231 held, 264 alone; 2048 x 32768 67.7 and 68.1, 4096 x 18000 95 and 77; 300 x
+// 131072, which is two rounds, 61 and 46.)
 enum Both { kAlone, kHeld, kSplit };
 Both choose_both(int64_t M, int64_t V, int type, bool alike, int cus) {
   const int64_t bytes = V * (type == MOE_FP32 ? 4 : 2), kb = 1024;
   if (2 * M <= cus && V > 65536) return kSplit;
-  if (M <= cus || bytes <= 32 * kb) return kAlone;
-  return alike && bytes <= 256 * kb ? kHeld : kAlone;
+  // held: rounds of rows over the workgroups that are at most an eighth empty
+  const int64_t room = bytes <= 128 * kb ? 2 * cus : cus, rounds = (M + room - 1) / room;
+  return alike && bytes > 64 * kb && bytes <= 256 * kb && rounds * room * 7 <= M * 8 ? kHeld : kAlone;
 }
 
 template <int TYPE, int GRAD>

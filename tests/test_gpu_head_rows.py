@@ -15,10 +15,29 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("t,V", [("bf16", 40001), ("bf16", 70001), ("fp16", 131072), ("fp32", 20003), ("fp32", 40004), ("fp32", 65536)])
 @pytest.mark.parametrize("M,in_place", [(300, True), (530, False)])
 def test_held_rows(t, V, M, in_place):
-    """More rows than CUs, each held between the sums and the gradient."""
+    """More rows than CUs."""
     z, gen = _logits(V, M, V, t)
     ids, tl, weight = _teacher(gen, M, V, 33)
     _check_distill(z, ids, tl, weight, 2.0, _distill(z.cuda(), ids, tl, weight, 2.0, fused=True, in_place=in_place), t)
+
+
+@pytest.mark.parametrize("t,M,V", [("bf16", 500, 40001), ("bf16", 1000, 40001), ("bf16", 500, 70001), ("fp16", 512, 131072),
+                                   ("fp32", 1000, 20003), ("fp32", 500, 40004), ("fp32", 700, 65536)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rounds_of_rows(t, M, V, in_place):
+    """One to three rounds of rows over the workgroups."""
+    z, gen = _logits(V, M, V, t)
+    ids, tl, weight = _teacher(gen, M, V, 9)
+    _check_distill(z, ids, tl, weight, 2.0, _distill(z.cuda(), ids, tl, weight, 2.0, fused=True, in_place=in_place), t)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("kind", ["normal", "ties", "rising", "falling", "masked", "lowest", "one"])
+def test_alternatives_of_many_long_rows(t, kind):
+    M, V = 258, 33001
+    z, gen = _logits(7, M, V, t, kind)
+    for k in (1, 64):
+        _check_scores(z, torch.randint(0, V, (M,), generator=gen).int(), k)
 
 
 @pytest.mark.parametrize("t", ["bf16", "fp32"])
