@@ -405,9 +405,9 @@ __device__ __forceinline__ float given_logit(const ScoresArgs& a, const Row<TYPE
 
 // (at most 64 registers for 512 threads: four workgroups a CU). N elements a thread and
 // tile, the next tile's under way meanwhile. Bound by memory: 2048 x 131072 bf16 94 us (5.7
-// TB/s) without alternatives, whose logits are read past the caches; 125 with 32 of them: the
-// search for the threshold and the second reading of some 33 threads' pieces are a
-// workgroup's own latency, and the logits pass through the caches for it.
+// TB/s) without alternatives, whose logits are read past the caches; 112 with 32 of them: the
+// search for the threshold and the second reading of some 33 threads' pieces, S stretches a
+// thread, are a workgroup's own latency, and the logits pass through the caches for it.
 template <int TYPE, int THREADS, int N, bool TOP, int S>
 __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel(const ScoresArgs a, int parts) {
   constexpr int E = Logit<TYPE>::kPiece, NP = N / E;  // pieces
