@@ -182,7 +182,7 @@ def prepare(case, seed):
         d["out"] = empty((M, c["I"]), t)
         d["ws"] = scratch(d["op"].workspace_bytes(M, train=c["train"]))
         if c["train"]:
-            d["pre"] = empty((M, 2 * c["I"]), torch.float32)  # (in 16 bits it would cost the gradients precision)
+            d["pre"] = empty((M, 2 * c["I"]), t)
             d["dx"], d["dw"] = torch.empty_like(d["x"]), torch.empty_like(d["w"])
     elif c["op"] == "scores":
         d["op"] = B.TokenScores(c["V"], top_k=c["k"], dtype=d["z"].dtype, max_M=M)
