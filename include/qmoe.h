@@ -441,7 +441,8 @@ moe_status moe_layer_forward(moe_plan* plan, const moe_router* router, int64_t M
  *
  * Activations. gelu is z Phi(z), Phi the normal distribution function; gelu_tanh
  * is z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; silu is z / (1 + exp(-z));
- * relu's slope at 0 is 0. */
+ * relu's slope at 0 is 0. At -inf and +inf values and slopes are the limits (but for
+ * none, 0 and z, 0 and 1): sums past 65504 that are saved in fp16 stand there. */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4 } moe_activation;
 
 /* Matrix product with bias, activation and residual in its epilogue:
@@ -488,7 +489,9 @@ moe_status moe_dense_backward(const moe_dense* dense, int64_t M, const void* dy,
  * gradients' relative error 1.7 times the rounding of their own type, 32 bits 1.4
  * times), for moe_gated_backward:
  *   dg = dh u act'(g), du = dh act(g), dx = [dg du] w13, dw13 = [dg du]^T x
- * dg and du rounded to x's type before the products. dx [M, H], rows lddx apart,
+ * dg and du rounded to x's type before the products. A saved g or u past the type's
+ * range is an infinity (u's adds nothing where act' is 0; else the gradient overflows,
+ * where one of saved 32 bits need not). dx [M, H], rows lddx apart,
  * dw13 [2I, H] dense, of x's type; one of them may be NULL. Sizes, alignment,
  * M = 0, workspace and errors as moe_dense (H for K; I up to 2^21). */
 typedef struct moe_gated moe_gated;

@@ -1,6 +1,7 @@
 // The activations of the 16-bit layers and their slopes, in binary32.
 #pragma once
 
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <math.h>
 
@@ -15,6 +16,12 @@ namespace qmoe {
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
+
+// Arguments of -inf and +inf (saved in fp16, every sum past 65504 is one) take the limits:
+// z is bounded by the largest number where it multiplies what is 0 there. NaN stays NaN
+// through the other factor, for min and max drop it.
+__device__ __forceinline__ float above(float z) { return fmaxf(z, -FLT_MAX); }
+__device__ __forceinline__ float within(float z) { return fminf(above(z), FLT_MAX); }
 
 // u of gelu_tanh = z (1 + tanh u) / 2 = z sigmoid(2 u).
 __device__ __forceinline__ float gelu_tanh_2u(float z) { return z * (1.5957691216057308f + 0.0713548162726009f * z * z); }
@@ -36,11 +43,11 @@ __device__ __forceinline__ float normal_cdf(float z, float& density) {
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z < 0.f ? 0.f : z;
-  else if constexpr (ACT == MOE_ACT_SILU) return z * sigmoid(z);
+  else if constexpr (ACT == MOE_ACT_SILU) return above(z) * sigmoid(z);
   else if constexpr (ACT == MOE_ACT_GELU) {
     float density;
-    return z * normal_cdf(z, density);
-  } else if constexpr (ACT == MOE_ACT_GELU_TANH) return z * sigmoid(gelu_tanh_2u(z));
+    return above(z) * normal_cdf(z, density);
+  } else if constexpr (ACT == MOE_ACT_GELU_TANH) return above(z) * sigmoid(gelu_tanh_2u(z));
   else return z;
 }
 
@@ -52,19 +59,19 @@ __device__ __forceinline__ float act_slope(float z, float& value) {
     return z <= 0.f ? 0.f : z != z ? z : 1.f;
   } else if constexpr (ACT == MOE_ACT_SILU) {
     const float s = sigmoid(z);
-    value = z * s;
-    return s * (1.f + z * (1.f - s));
+    value = above(z) * s;
+    return s * (1.f + within(z) * (1.f - s));
   } else if constexpr (ACT == MOE_ACT_GELU) {
     float density;
     const float cdf = normal_cdf(z, density);
-    value = z * cdf;
-    return cdf + z * 0.3989422804014327f * density;
+    value = above(z) * cdf;
+    return cdf + within(z) * 0.3989422804014327f * density;
   } else if constexpr (ACT == MOE_ACT_GELU_TANH) {
     // past 16 in magnitude sigmoid(2u) is 0 or 1 in binary32 and the second term
     // is 0: bounded there, so that it is not infinity times zero
     const float c = z < -16.f ? -16.f : z > 16.f ? 16.f : z;
     const float s = sigmoid(gelu_tanh_2u(c));
-    value = z * sigmoid(gelu_tanh_2u(z));
+    value = above(z) * sigmoid(gelu_tanh_2u(z));
     return s + c * s * (1.f - s) * (1.5957691216057308f + 0.2140644488178027f * c * c);
   } else {
     value = z;
