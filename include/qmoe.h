@@ -442,7 +442,10 @@ moe_status moe_layer_forward(moe_plan* plan, const moe_router* router, int64_t M
  * Activations. gelu is z Phi(z), Phi the normal distribution function; gelu_tanh
  * is z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; silu is z / (1 + exp(-z));
  * relu's slope at 0 is 0. At -inf and +inf values and slopes are the limits (but for
- * none, 0 and z, 0 and 1): sums past 65504 that are saved in fp16 stand there. */
+ * none, 0 and z, 0 and 1): sums past 65504 that are saved in fp16 stand there. They
+ * are computed in binary32: values within (12 + 2 a) 2^-24 of themselves, a the
+ * exponent of the tail (z^2, |z| or gelu_tanh's 8 |z| + z^2 |z| / 3), below 2^-120 perhaps
+ * 0, slopes within 2^-20 (1 + |z|). */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4 } moe_activation;
 
 /* Matrix product with bias, activation and residual in its epilogue:

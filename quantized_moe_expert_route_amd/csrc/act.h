@@ -26,16 +26,21 @@ __device__ __forceinline__ float within(float z) { return fminf(above(z), FLT_MA
 // u of gelu_tanh = z (1 + tanh u) / 2 = z sigmoid(2 u).
 __device__ __forceinline__ float gelu_tanh_2u(float z) { return z * (1.5957691216057308f + 0.0713548162726009f * z * z); }
 
-// The normal distribution function Phi(z), and exp(-z^2 / 2) beside it, by Abramowitz and
-// Stegun 7.1.26: erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0,
-// off by at most 1.5e-7, so Phi by 0.75e-7, 1.3 half steps of 1. (erff, which branches
-// by ranges, cost 4096 x 6144 x 6144's epilogue 45 us more.)
+// The normal distribution function Phi(z), and exp(-z^2 / 2) beside it: Phi(-x) = exp(-x^2 / 2)
+// R(x), x >= 0, with R a polynomial in t = 1 / (1 + 0.3 x) without a constant (R falls as 1 / x),
+// fitted to erfcx(x / sqrt 2) / 2 over [0, 14.5], where Phi leaves binary32's range: least
+// largest relative error, 1.6e-7 = 2.7 U (U = 2^-24). With the arithmetic the lower tail, which
+// gelu multiplies by z, is off by (12 + 2 z^2) U of itself (z^2 / 2 as an exponent is rounded;
+// z's own rounding moves the tail by z^2 U). (A form that is exact in absolute terms only, Abramowitz and
+// Stegun 7.1.26, lost 0.16 % at z = -5 and took the same time; erff, which branches by ranges, cost
+// 4096 x 6144 x 6144 45 us of 250 more.)
 __device__ __forceinline__ float normal_cdf(float z, float& density) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
-  density = __builtin_amdgcn_exp2f(-1.4426950408889634f * x * x);
-  const float p = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-  const float tail = 0.5f * p * density;
+  const float x = fabsf(z);
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3f * x);
+  density = __builtin_amdgcn_exp2f(-0.72134752044448170f * (x * x));
+  const float p = t * (0.119632013f + t * (0.120712139f + t * (0.100175962f + t * (0.127691716f + t * (-0.0520339124f +
+                  t * (0.204556659f + t * (-0.156158388f + t * 0.0354237258f)))))));
+  const float tail = p * density;
   return z < 0.f ? tail : 1.0f - tail;
 }
 

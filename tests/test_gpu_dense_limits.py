@@ -78,3 +78,38 @@ def test_gated_past_the_range(act, pt):
     both = torch.tensor(keep + [I + i for i in keep])
     (want, bound), _ = R.gated_backward(_f64(dh[:, keep]), _f64(pre.cpu()[:, both]), _f64(x), _f64(w[both]), act, "fp16")
     _within(dx, want, bound, "dx")
+
+
+# Relative errors of the activations' lower tails in binary32, in U. silu and gelu_tanh: an
+# exponent's argument a off by 2 (z's product, the constant) or 6 (2u besides, of four more
+# roundings) of itself, the exponential, reciprocal, sum and product by 8. gelu: as beside
+# its code.
+TAILS = {
+    "silu": (-80.0, lambda z: 8 + 2 * z.abs()),
+    "gelu": (-12.5, lambda z: 12 + 2 * z * z),
+    "gelu_tanh": (-9.5, lambda z: 8 + 7 * (1.6 * z.abs() + 0.0714 * z.abs() ** 3)),
+}
+
+
+@pytest.mark.parametrize("act", list(TAILS))
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_lower_tail(t, act, wide):
+    """act(z) of negative z, which falls to the least numbers, to its own size."""
+    from quantized_moe_expert_route_amd.binding import Dense
+
+    low, units = TAILS[act]
+    M = 3001
+    x = torch.zeros(M, 8, dtype=DT[t])
+    x[:, 0] = torch.cat((torch.linspace(low, -1.0, 2000), -torch.logspace(-5, 0, 1001))).to(DT[t])
+    w = torch.zeros(1, 8, dtype=DT[t])
+    w[0, 0] = 1.0  # z = x
+    yt = "fp32" if wide else t
+    y = _nan((M, 1), DT[yt])
+    Dense(w.cuda(), activation=act).forward(x.cuda(), y)
+    z = x[:, :1].double()
+    want = R.act(act, z)  # (gelu by erfc; torch's ndtr is 1 + erf, which cancels here)
+    if act == "gelu_tanh":  # (1 + tanh u) / 2 would cancel
+        want = z * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))
+    bound = (units(z) * R.U * (1 + R.half_step(yt))) * want.abs() + R.rounding(yt, want)
+    _within(y, want, bound, act)
