@@ -51,13 +51,18 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 
 // 16 bytes a lane from `offset` to LDS at `lds` + 16 lane; zeros where the offset is
 // kOutside. In assembly, so that the compiler does not wait for it before every
-// read of LDS: wait_and_barrier does that. No register is written.
+// read of LDS: wait_and_barrier does that. No register is written but M0, which the
+// compiler sets anew where it needs it (it warns that it does not keep M0's value over
+// the block: it need not).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds16(v4i buffer, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(offset), "s"(buffer)
-               : "memory");
+               : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // All but the N newest of the wave's loads to LDS have arrived, its reads of LDS too; then the
 // workgroup's barrier.
