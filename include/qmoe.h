@@ -520,7 +520,8 @@ moe_status moe_gated_backward(const moe_gated* gated, int64_t M, const void* dh,
  * nothing but -inf, has NaN for all its scores (lse is NaN, +inf or -inf); its
  * top_ids are some ids in [0, V).
  * top_k 0 .. 64 and up to V, V up to 2^24, max_M up to 2^20. The handle belongs to
- * the current device. Sums in fp32 and float64. Errors as the router's. */
+ * the current device. Sums in fp32, whose error does not grow with V (some 2^-18 at
+ * most), and float64. Errors as the router's. */
 typedef struct moe_scores moe_scores;
 moe_status moe_scores_create(int64_t V, int64_t top_k, int type, int64_t max_M, moe_scores** out);
 void moe_scores_destroy(moe_scores* scores);

@@ -2,7 +2,7 @@
 // entropy, largest alternatives) and distillation from a teacher's top logits.
 //
 // One pass over a row forms, a thread over its elements and the threads at the end,
-//   m = max z, s = sum exp(c (z - m)), t = sum exp(c (z - m)) c (z - m)
+//   m near max z, s = sum exp(c (z - m)), t = sum exp(c (z - m)) c (z - m)
 // (c = 1 / temperature), the sums moved on by exp(c (m_old - m)) whenever m grows, so
 //   lse = c m + log s,  entropy = log s - t / s.
 // m starts at the type's lowest number, not at -inf: a row (or thread) of nothing but
@@ -109,25 +109,53 @@ __device__ __forceinline__ float row_max(float v) {
 }
 
 // ----------------------------------------------------------------- sums of a row
-template <bool MEAN>
+// A thread's sums, N elements at a time: each N by themselves, then added to the rest, from
+// kChain of them on (LONG) with the rounding errors carried along: a chain of plain additions of like
+// terms rounds them all the same way (it lost 3e-4 of a sum of 2^15). Carrying them costs 1 %
+// of 2048 x 131072. m stays while the elements pass it by no more than a factor 2^kOver of
+// the sums: of a row that rises slowly every N elements would scale the sums, by a
+// rounded factor each time. (SHORT: of some hundred elements at most, m is their largest.)
+constexpr float kOver = 6.f;
+constexpr int kChain = 32;
+template <bool MEAN, bool SHORT = false>
 struct Sums {
   float m = -FLT_MAX, s = 0.f, t = 0.f;
-  // N elements, in units of 1 / cl (cl = c log2 e: t is in log2 units)
-  template <int N>
+  float s_over = 0.f, t_over = 0.f;  // what the sums hold too much
+  static __device__ __forceinline__ void carry(float& sum, float& over, float v) {
+    const float y = v - over, n = sum + y;
+    over = (n - sum) - y;
+    sum = n;
+  }
+  // N elements, in units of 1 / cl (cl = c log2 e: t is in log2 units); returns the largest
+  template <bool LONG = false, int N>
   __device__ __forceinline__ float add(const float (&v)[N], float cl) {
+    const float bound = SHORT ? m : m + kOver / cl;
     float top = v[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]);
     // (a factor is 0 long before -1e4; no infinity, which zero sums would turn into NaN)
-    const float mn = fmaxf(m, top), back = fmaxf((m - mn) * cl, -1e4f), f = __builtin_amdgcn_exp2f(back);
+    const float mn = SHORT ? fmaxf(m, top) : top > bound ? top : m;
+    const float back = fmaxf((m - mn) * cl, -1e4f), f = __builtin_amdgcn_exp2f(back);
     if constexpr (MEAN) t = (t + s * back) * f;
     s *= f;
+    if constexpr (LONG) {
+      if constexpr (MEAN) t_over = (t_over + s_over * back) * f;
+      s_over *= f;
+    }
     m = mn;
+    float ps = 0.f, pt = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float d = (v[i] - m) * cl, e = __builtin_amdgcn_exp2f(d);
-      s += e;
-      if constexpr (MEAN) t += e * fmaxf(d, -1e4f);
+      ps += e;
+      if constexpr (MEAN) pt += e * fmaxf(d, -1e4f);
+    }
+    if constexpr (LONG) {
+      carry(s, s_over, ps);
+      if constexpr (MEAN) carry(t, t_over, pt);
+    } else {
+      s += ps;
+      if constexpr (MEAN) t += pt;
     }
     return top;
   }
@@ -150,10 +178,11 @@ __device__ __forceinline__ Total join(const Sums<MEAN>& a, float cl) {
   m = row_max(lm[lane % W]);
   const float back = fmaxf((a.m - m) * cl, -1e4f);
   const double f = __builtin_amdgcn_exp2f(back);
-  const double s = wave_sum(a.s * f);
+  const double mine = (double)a.s - a.s_over;
+  const double s = wave_sum(mine * f);
   if (lane == 0) ls[wave] = s;
   if constexpr (MEAN) {
-    const double t = wave_sum(((double)a.t + (double)a.s * back) * f);
+    const double t = wave_sum(((double)a.t - a.t_over + mine * back) * f);
     if (lane == 0) lt[wave] = t;
   }
   __syncthreads();
@@ -408,7 +437,7 @@ __device__ __forceinline__ float given_logit(const ScoresArgs& a, const Row<TYPE
 // TB/s) without alternatives, whose logits are read past the caches; 112 with 32 of them: the
 // search for the threshold and the second reading of some 33 threads' pieces, S stretches a
 // thread, are a workgroup's own latency, and the logits pass through the caches for it.
-template <int TYPE, int THREADS, int N, bool TOP, int S>
+template <int TYPE, int THREADS, int N, bool TOP, int S, bool LONG = false>
 __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel(const ScoresArgs a, int parts) {
   constexpr int E = Logit<TYPE>::kPiece, NP = N / E;  // pieces
   __shared__ std::conditional_t<TOP, Candidates<THREADS, S>, int> c;
@@ -433,7 +462,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel
   load(p0);
   float edge[1] = {edges && (int)threadIdx.x < row.edges() ? Logit<TYPE>::load(row.p, row.edge(threadIdx.x)) : -INFINITY};
   const float given = parts == 1 ? given_logit<TYPE>(a, row, m) : 0.f;  // (two loads one behind the other, beside the tile's)
-  sums.add(edge, kLog2e);
+  float best = fmaxf(sums.add(edge, kLog2e), -FLT_MAX);
   const int tiles = (int)((p1 - p0 + NP * THREADS - 1) / (NP * THREADS)), span = (tiles + S - 1) / S;  // a stretch's tiles
   int64_t base = p0;
   auto sum_tile = [&]() __attribute__((always_inline)) {
@@ -441,22 +470,23 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 8 : 4) void scores_kernel
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = Logit<TYPE>::value(q[i / E], i % E);
     load(base += NP * THREADS);
-    return sums.add(v, kLog2e);
+    return sums.template add<LONG>(v, kLog2e);
   };
   if constexpr (S == 1) {
-    for (int t = 0; t < tiles; ++t) sum_tile();
+    for (int t = 0; t < tiles; ++t) best = fmaxf(best, sum_tile());
   } else {
     int t = 0;
 #pragma unroll 1
     for (int stretch = 0; stretch < S; ++stretch) {
       float high = -INFINITY;
       for (int end = min(t + span, tiles); t < end; ++t) high = fmaxf(high, sum_tile());
+      best = fmaxf(best, high);
       c.high[stretch * THREADS + threadIdx.x] = (uint16_t)(order_key(high) >> 16);
     }
   }
   const Total r = join<THREADS>(sums, kLog2e);
   if constexpr (TOP) {
-    select<TYPE>(c, row, p0, p1, span * NP, edges, edge[0], sums.m, a.k);
+    select<TYPE>(c, row, p0, p1, span * NP, edges, edge[0], best, a.k);
     top = c.top;
   }
   if (parts == 1) {
@@ -529,6 +559,8 @@ hipError_t scores(const ScoresArgs& a, int cus, hipStream_t stream) {
   hipError_t e;
   if (a.V <= 4096) e = launch_k(scores_kernel<TYPE, 128, 16, TOP, 1>, grid, dim3(128), 0, stream, Ev{}, a, parts);
   else if (few_rows(a.M, parts, cus)) e = launch_k(scores_kernel<TYPE, 1024, 32, TOP, 1>, grid, dim3(1024), 0, stream, Ev{}, a, parts);
+  else if (a.V / parts > kChain * 512 * 16)  // (both sums in one kernel: fp32's would not fit 64 registers)
+    e = launch_k(scores_kernel<TYPE, 512, 16, TOP, TOP ? 4 : 1, true>, grid, dim3(512), 0, stream, Ev{}, a, parts);
   else if (TOP && a.M > cus && a.V > 32768) e = launch_k(scores_kernel<TYPE, 512, 16, TOP, TOP ? 4 : 1>, grid, dim3(512), 0, stream, Ev{}, a, parts);
   else e = launch_k(scores_kernel<TYPE, 512, 16, TOP, 1>, grid, dim3(512), 0, stream, Ev{}, a, parts);
   if (e == hipSuccess && parts > 1)
@@ -724,13 +756,17 @@ __device__ Sums<false> sum_pieces(const Row<TYPE>& row, int64_t p0, int64_t p1, 
   load(p0);
   float edge[1] = {edges && (int)threadIdx.x < row.edges() ? Logit<TYPE>::load(row.p, row.edge(threadIdx.x)) : -INFINITY};
   sums.add(edge, cl);
-  for (int64_t base = p0; base < p1; base += NP * THREADS) {
-    float v[N];
+  auto sum_tiles = [&](auto chain) __attribute__((always_inline)) {
+    for (int64_t base = p0; base < p1; base += NP * THREADS) {
+      float v[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = Logit<TYPE>::value(q[i / E], i % E);
-    load(base + NP * THREADS);
-    sums.add(v, cl);
-  }
+      for (int i = 0; i < N; ++i) v[i] = Logit<TYPE>::value(q[i / E], i % E);
+      load(base + NP * THREADS);
+      sums.template add<decltype(chain)::value>(v, cl);
+    }
+  };
+  if (THREADS == 128 || p1 - p0 <= kChain * NP * THREADS) sum_tiles(std::false_type{});
+  else sum_tiles(std::true_type{});
   return sums;
 }
 
@@ -849,12 +885,12 @@ __global__ __launch_bounds__(1024, H <= 8 ? 8 : 4) void distill_held_kernel(cons
     const v4i* from = reinterpret_cast<const v4i*>(row.p + row.head * Logit<TYPE>::kBytes + p * 16u);
     q[h] = p < (uint32_t)row.pieces ? __builtin_bit_cast(uint4, __builtin_nontemporal_load(from)) : Logit<TYPE>::none();
   };
-  Sums<false> sums;
+  Sums<false, true> sums;
   float edge;
   auto begin = [&](const Row<TYPE>& row) __attribute__((always_inline)) {
     asm volatile("" : "+v"(tid));
     edge = (int)tid < row.edges() ? Logit<TYPE>::load(row.p, row.edge(tid)) : -INFINITY;
-    sums = Sums<false>{};
+    sums = Sums<false, true>{};
   };
   auto add = [&](const Row<TYPE>& row, int h) __attribute__((always_inline)) {  // pieces h .. h + G - 1
     if (row.pieces <= h * 1024) return;
