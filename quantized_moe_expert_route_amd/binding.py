@@ -527,10 +527,10 @@ class Dense(_Product):
     def backward(self, dy, x, dx=None, dw=None, dbias=None, pre=None, workspace=None, M: Optional[int] = None, stream=None):
         """The gradients of x into dx[:M], of w into dw and of the bias into dbias
         (each may be None), for dy[:M] = the gradient of forward's out (in w's type);
-        `pre` is what forward saved, needed with an activation."""
+        x may be None without dw, `pre` is what forward saved, needed with an activation."""
         M = self._rows(dy, M)
         lddy = self._check("dy", dy, self.dtype, M, self.N)
-        ldx = self._check("x", x, self.dtype, M, self.K)
+        ldx = 0 if x is None and dw is None else self._check("x", x, self.dtype, M, self.K)
         ldp, lddx, p_code = 0, 0, self._code
         if self.activation != "none":
             if pre is None:
@@ -544,9 +544,9 @@ class Dense(_Product):
             self._check("dw", dw, self.dtype, self.N, self.K, dense=True)
         ws, nws = self._workspace(workspace)
         self._call("moe_dense_backward", M, dy.data_ptr(), lddy, None if pre is None else pre.data_ptr(), ldp, p_code,
-                   x.data_ptr(), ldx, None if dx is None else dx.data_ptr(), lddx, None if dw is None else dw.data_ptr(),
-                   None if dbias is None else self._vector("dbias", dbias, self.dtype, self.N), ws, nws,
-                   self._stream(stream))
+                   None if x is None else x.data_ptr(), ldx, None if dx is None else dx.data_ptr(), lddx,
+                   None if dw is None else dw.data_ptr(),
+                   None if dbias is None else self._vector("dbias", dbias, self.dtype, self.N), ws, nws, self._stream(stream))
 
 
 class Gated(_Product):
@@ -581,18 +581,18 @@ class Gated(_Product):
 
     def backward(self, dh, x, pre, dx=None, dw=None, workspace=None, M: Optional[int] = None, stream=None):
         """The gradients of x into dx[:M] and of w13 into dw (one may be None), for
-        dh[:M] = the gradient of forward's out, `pre` what forward saved."""
+        dh[:M] = the gradient of forward's out, `pre` what forward saved; x may be None without dw."""
         M = self._rows(dh, M)
         lddh = self._check("dh", dh, self.dtype, M, self.I)
-        ldx = self._check("x", x, self.dtype, M, self.H)
+        ldx = 0 if x is None and dw is None else self._check("x", x, self.dtype, M, self.H)
         p_code = self._pre(pre, M, 2 * self.I, dense=True)[1]
         lddx = 0 if dx is None else self._check("dx", dx, self.dtype, M, self.H)
         if dw is not None:
             self._check("dw", dw, self.dtype, 2 * self.I, self.H, dense=True)
         ws, nws = self._workspace(workspace)
-        self._call("moe_gated_backward", M, dh.data_ptr(), lddh, pre.data_ptr(), p_code, x.data_ptr(), ldx,
-                   None if dx is None else dx.data_ptr(), lddx, None if dw is None else dw.data_ptr(), ws, nws,
-                   self._stream(stream))
+        self._call("moe_gated_backward", M, dh.data_ptr(), lddh, pre.data_ptr(), p_code,
+                   None if x is None else x.data_ptr(), ldx, None if dx is None else dx.data_ptr(), lddx,
+                   None if dw is None else dw.data_ptr(), ws, nws, self._stream(stream))
 
 
 class _Head(_Sized):
