@@ -434,7 +434,8 @@ moe_status moe_layer_forward(moe_plan* plan, const moe_router* router, int64_t M
  *
  * `workspace` of these calls is caller-owned device memory, 256-byte aligned, of
  * at least the handle's workspace bytes for the call's M (its contents need not
- * be kept between calls; NULL where none are needed). Handles hold no mutable
+ * be kept between calls; NULL where none are needed). A smaller M may need more: few
+ * rows and tiles are split over workgroups, whose parts go there. Handles hold no mutable
  * state; calls that may overlap (other streams, captured graphs replayed side by
  * side) need workspaces of their own. MOE_ERR_WORKSPACE for a workspace that is
  * missing, short or misaligned.
@@ -469,7 +470,9 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GEL
  * Rows of 16-bit matrices that products read (x; w) start on 16 bytes: K and ldx
  * multiples of 8, K up to 65536, ldx up to 2^22 elements; N any up to 2^22; dy,
  * pre, residual, y and dx aligned to their elements, rows up to 2^40 apart.
- * moe_dense_workspace_bytes: for moe_dense_forward (train = 0) or for both (1).
+ * moe_dense_workspace_bytes: for moe_dense_forward (train = 0), for both (1), or for both
+ * without dz (2, no more than 1 gives): backward calls without dbias whose dy is the
+ * products' operand itself (no activation, N and lddy multiples of 8, lddy up to 2^22, dy on 16 bytes).
  * Errors as the linear layer's. */
 typedef struct moe_dense moe_dense;
 moe_status moe_dense_create(int64_t N, int64_t K, int type, const void* w, const void* bias, int activation,

@@ -407,7 +407,8 @@ class Linear(_Handle):
 
 class _Sized(_Handle):
     """A handle whose calls may take a workspace: a uint8 tensor of at least
-    workspace_bytes(M), the caller's; calls that may overlap need one each."""
+    workspace_bytes(M) for the call's M (a smaller M may need more), the caller's; calls that
+    may overlap need one each."""
 
     def _create(self, name, *args):
         h = ctypes.c_void_p()
@@ -501,9 +502,11 @@ class Dense(_Product):
         self._create("moe_dense_create", self.N, self.K, self._code, _ptr(w), None if bias is None else _ptr(bias), act,
                      self.max_M)
 
-    def workspace_bytes(self, M: int, train: bool = False) -> int:
-        """Workspace of forward, with `train` of backward too, for M rows."""
-        return self._bytes("moe_dense_workspace_bytes", int(M), int(bool(train)))
+    def workspace_bytes(self, M: int, train: bool = False, plain: bool = False) -> int:
+        """Workspace of forward, with `train` of backward too, for M rows (fewer rows may
+        need more); `plain`: of backward calls without dbias that read dy as it is, for
+        which no activation, N and dy's row distance multiples of 8 and dy on 16 bytes are needed."""
+        return self._bytes("moe_dense_workspace_bytes", int(M), 2 if train and plain else int(bool(train)))
 
     def forward(self, x, out, residual=None, pre=None, workspace=None, M: Optional[int] = None, stream=None):
         """out[:M] = act(x[:M] w^T + bias) (+ residual[:M]); out is of x's type or

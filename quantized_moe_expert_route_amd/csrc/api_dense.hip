@@ -44,11 +44,11 @@ int64_t up8(int64_t n) { return (n + 7) & ~(int64_t)7; }
 struct Backward {
   size_t dz, part, split, bytes;
 };
-Backward backward_layout(int64_t M, int64_t N, int64_t K, bool bias, int type, int cus) {
+Backward backward_layout(int64_t M, int64_t N, int64_t K, bool dz, bool bias, int type, int cus) {
   Backward l;
   size_t at = 0;
   l.dz = at;
-  at += align256((size_t)M * up8(N) * 2);
+  at += dz ? align256((size_t)M * up8(N) * 2) : 0;
   l.part = at;
   at += bias ? align256((size_t)dbias_parts(M) * N * 4) : 0;
   l.split = at;
@@ -112,9 +112,10 @@ const char* moe_dense_kernel(const moe_dense* d, int64_t M, int product) {
 }
 
 moe_status moe_dense_workspace_bytes(const moe_dense* d, int64_t M, int train, size_t* bytes) {
-  if (!d || !bytes || M < 0 || M > d->max_M || (train != 0 && train != 1)) return MOE_ERR_INVALID_ARG;
+  if (!d || !bytes || M < 0 || M > d->max_M || train < 0 || train > 2) return MOE_ERR_INVALID_ARG;
+  if (train == 2 && (d->act != MOE_ACT_NONE || d->N % 8 != 0)) train = 1;
   const size_t f = gemm_ws_bytes(kGemmForward, M, d->N, d->K, d->type, d->num_cus);
-  const size_t b = train ? backward_layout(M, d->N, d->K, true, d->type, d->num_cus).bytes : 0;
+  const size_t b = train ? backward_layout(M, d->N, d->K, train == 1, train == 1, d->type, d->num_cus).bytes : 0;
   *bytes = f > b ? f : b;
   return MOE_OK;
 }
@@ -166,7 +167,9 @@ moe_status moe_dense_backward(const moe_dense* d, int64_t M, const void* dy, int
     if (dx && !matrix_ok(dx, lddx, K, 2)) return MOE_ERR_INVALID_ARG;
   }
   if ((dw && !aligned16(dw)) || ((uintptr_t)dbias & 1)) return MOE_ERR_INVALID_ARG;
-  const Backward l = backward_layout(M, N, K, true, d->type, d->num_cus);
+  // dy is dz itself where it needs no slope and its rows are an operand's
+  const bool direct = d->act == MOE_ACT_NONE && N % 8 == 0 && (M == 0 || operand_ok(dy, lddy, N));
+  const Backward l = backward_layout(M, N, K, !direct, !direct || dbias, d->type, d->num_cus);
   moe_status st = check_ws(workspace, workspace_bytes, l.bytes);
   if (st != MOE_OK) return st;
   const Buf b[] = {{dx, span(M, lddx, K, 2), true},
@@ -184,8 +187,6 @@ moe_status moe_dense_backward(const moe_dense* d, int64_t M, const void* dy, int
   if (!guard.ok) return MOE_ERR_DEVICE;
   hipStream_t s = (hipStream_t)stream;
   uint8_t* ws = (uint8_t*)workspace;
-  // dy is dz itself where it needs no slope and its rows are an operand's
-  const bool direct = d->act == MOE_ACT_NONE && N % 8 == 0 && (M == 0 || operand_ok(dy, lddy, N));
   const bool need_dz = !direct && (dx || dw);
   hipError_t e = hipSuccess;
   if (need_dz || dbias) {
@@ -227,7 +228,7 @@ const char* moe_gated_kernel(const moe_gated* d, int64_t M, int product) {
 moe_status moe_gated_workspace_bytes(const moe_gated* d, int64_t M, int train, size_t* bytes) {
   if (!d || !bytes || M < 0 || M > d->max_M || (train != 0 && train != 1)) return MOE_ERR_INVALID_ARG;
   const size_t f = gemm_ws_bytes(kGemmGated, M, d->I, d->H, d->type, d->num_cus);
-  const size_t b = train ? backward_layout(M, 2 * d->I, d->H, false, d->type, d->num_cus).bytes : 0;
+  const size_t b = train ? backward_layout(M, 2 * d->I, d->H, true, false, d->type, d->num_cus).bytes : 0;
   *bytes = f > b ? f : b;
   return MOE_OK;
 }
@@ -269,7 +270,7 @@ moe_status moe_gated_backward(const moe_gated* d, int64_t M, const void* dh, int
     if (dx && !matrix_ok(dx, lddx, H, 2)) return MOE_ERR_INVALID_ARG;
   }
   if (dw13 && !aligned16(dw13)) return MOE_ERR_INVALID_ARG;
-  const Backward l = backward_layout(M, N, H, false, d->type, d->num_cus);
+  const Backward l = backward_layout(M, N, H, true, false, d->type, d->num_cus);
   moe_status st = check_ws(workspace, workspace_bytes, l.bytes);
   if (st != MOE_OK) return st;
   const Buf b[] = {{dx, span(M, lddx, H, 2), true},
