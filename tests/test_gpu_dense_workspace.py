@@ -69,7 +69,7 @@ def test_head_step_on_one_workspace():
     logits = torch.empty(M, V, device="cuda")
     scores = B.TokenScores(V, top_k=k, dtype=logits.dtype)
     distill = B.Distill(V, k=k, dtype=logits.dtype, grad_dtype=x.dtype, temperature=2.0)
-    ws = _ws(max(head.workspace_bytes(M, train=True), scores.workspace_bytes(M), distill.workspace_bytes(M)))
+    ws = _ws(max(head.workspace_bytes(M, train=True, plain=True), scores.workspace_bytes(M), distill.workspace_bytes(M)))
     head.forward(x, logits, workspace=ws)
     tokens = torch.randint(0, V, (M,), generator=gen).int().cuda()
     logprobs, entropy, loss = (torch.empty(M, device="cuda") for _ in range(3))
