@@ -543,7 +543,8 @@ moe_status moe_scores_forward(const moe_scores* scores, int64_t M, const void* z
  * weight fp32 [M] is the gradient of the rows' losses. A token in two slots has
  * the sum of both. A row without a filled slot (padding) has loss 0 and gradient
  * 0, whatever its logits and weight; one whose logits hold a NaN or +inf, or nothing
- * but -inf, NaN.
+ * but -inf, NaN. A filled slot of t = NaN or +inf makes the loss and the gradient at the
+ * row's slots' tokens NaN.
  * moe_distill_forward writes loss and lse (fp32 [M], log sum exp(z/T), for the
  * backward call; may be NULL); moe_distill_backward reads it (rows of |lse| above
  * 128, whose rounding the gradient would show, it sums again);
@@ -603,6 +604,10 @@ const char* moe_linear_kernel(const moe_linear* linear, int64_t M);
  * (NULL for another number). */
 const char* moe_dense_kernel(const moe_dense* dense, int64_t M, int product);
 const char* moe_gated_kernel(const moe_gated* gated, int64_t M, int product);
+/* Of the head's operators; distillation by pass: 0 forward, 1 backward, 2 both at once, whose
+ * gradient lies beside the logits and as they do (the same distance from 16 bytes in every row). */
+const char* moe_scores_kernel(const moe_scores* scores, int64_t M);
+const char* moe_distill_kernel(const moe_distill* distill, int64_t M, int pass);
 
 /* Static text for a status code. */
 const char* moe_status_str(moe_status status);

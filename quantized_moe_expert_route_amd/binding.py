@@ -153,8 +153,9 @@ def lib() -> ctypes.CDLL:
     }.items():
         f = getattr(L, name)
         f.restype, f.argtypes = st, args
-    for f in (L.moe_dense_kernel, L.moe_gated_kernel):
+    for f in (L.moe_dense_kernel, L.moe_gated_kernel, L.moe_distill_kernel):
         f.restype, f.argtypes = ctypes.c_char_p, [vp, i64, ci]
+    L.moe_scores_kernel.restype, L.moe_scores_kernel.argtypes = ctypes.c_char_p, [vp, i64]
     for f in (L.moe_dense_destroy, L.moe_gated_destroy, L.moe_scores_destroy, L.moe_distill_destroy):
         f.restype, f.argtypes = None, [vp]
     L.moe_plan_set_tp_exchange.restype = st
@@ -674,6 +675,14 @@ class Distill(_Head):
 
     def workspace_bytes(self, M: int) -> int:
         return self._bytes("moe_distill_workspace_bytes", int(M))
+
+    def kernel(self, M: int, step: int = 2) -> str:
+        """Which of its kernels a call of M rows launches forward (0), backward (1) or for both
+        at once (2), there with the gradient's rows as the logits' (profiling aid)."""
+        name = lib().moe_distill_kernel(self._h, int(M), int(step))
+        if name is None:
+            raise ValueError(f"M = {M} outside [1, {self.max_M}], step {step} not 0, 1 or 2, or no handle")
+        return name.decode()
 
     def _inputs(self, logits, ids, t, M):
         M = self._rows(logits, M)

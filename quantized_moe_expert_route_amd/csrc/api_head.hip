@@ -44,6 +44,10 @@ moe_status moe_scores_create(int64_t V, int64_t top_k, int type, int64_t max_M, 
 
 void moe_scores_destroy(moe_scores* s) { delete s; }
 
+const char* moe_scores_kernel(const moe_scores* s, int64_t M) {
+  return s && M > 0 && M <= s->max_M ? scores_kernel_name(M, s->V, s->k, s->num_cus) : nullptr;
+}
+
 moe_status moe_scores_workspace_bytes(const moe_scores* s, int64_t M, size_t* bytes) {
   if (!s || !bytes || M < 0 || M > s->max_M) return MOE_ERR_INVALID_ARG;
   *bytes = scores_ws_bytes(M, s->V, s->k, s->type, s->num_cus);
@@ -95,6 +99,11 @@ moe_status moe_distill_create(int64_t V, int64_t k, int type, int grad_type, flo
 }
 
 void moe_distill_destroy(moe_distill* d) { delete d; }
+
+const char* moe_distill_kernel(const moe_distill* d, int64_t M, int pass) {
+  if (!d || M <= 0 || M > d->max_M || pass < kDistillForward || pass > kDistillBoth) return nullptr;
+  return distill_kernel_name((DistillPass)pass, M, d->V, d->type, d->grad_type, d->num_cus);
+}
 
 moe_status moe_distill_workspace_bytes(const moe_distill* d, int64_t M, size_t* bytes) {
   if (!d || !bytes || M < 0 || M > d->max_M) return MOE_ERR_INVALID_ARG;

@@ -39,6 +39,7 @@ struct ScoresArgs {
 };
 hipError_t launch_scores(const ScoresArgs& a, int cus, hipStream_t stream);
 size_t scores_ws_bytes(int64_t M, int64_t V, int64_t k, int type, int cus);
+const char* scores_kernel_name(int64_t M, int64_t V, int64_t k, int cus);  // M > 0
 
 struct DistillArgs {
   int64_t M, V, ldz, lddz;
@@ -56,5 +57,6 @@ struct DistillArgs {
 enum DistillPass { kDistillForward = 0, kDistillBackward = 1, kDistillBoth = 2 };
 hipError_t launch_distill(DistillPass pass, const DistillArgs& a, int cus, hipStream_t stream);
 size_t distill_ws_bytes(int64_t M, int64_t V, int type, int cus);
+const char* distill_kernel_name(DistillPass pass, int64_t M, int64_t V, int type, int grad_type, int cus);  // M > 0
 
 }  // namespace qmoe

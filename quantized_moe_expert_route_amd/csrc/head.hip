@@ -548,21 +548,34 @@ int parts_of(int64_t M, int64_t V, int cus) {
 // Up to a row a CU, a workgroup has 1024 threads and twice the loads under way.
 bool few_rows(int64_t M, int parts, int cus) { return M <= cus && parts == 1; }
 
+// Threads of a workgroup, and how it goes through its row or part of one.
+enum Threads { kRow128, kRow1024, kRowLong, kRowStretches, kRow512 };
+constexpr const char* kRowName[] = {"128 threads", "1024 threads", "512 threads, long sums", "512 threads, in stretches", "512 threads"};
+constexpr const char* kPartName = "parts of a row, 512 threads";
 // (Stretches pay where lines read twice do, many long rows: 2048 x 131072 bf16 125.5 us
 // without, 111 with them, fp32 1024 x 131072 119 and 102; 4096 x 8000 49 and 54, 16 x 131072
 // 13.2 and 14.7. Threads: 4096 x 1000 17 us by 128, 50 by 512; 77 x 30011 11.5 by 1024, 10.5 by
-// 512, 200 x 65000 15.5 and 16.1.)
+// 512, 200 x 65000 15.5 and 16.1. Both sums in one kernel: fp32's would not fit 64 registers.)
+Threads row_of(int64_t M, int64_t V, int64_t k, int parts, int cus) {
+  if (V <= 4096) return kRow128;
+  if (few_rows(M, parts, cus)) return kRow1024;
+  if (V / parts > kChain * 512 * 16) return kRowLong;
+  return k > 0 && M > cus && V > 32768 ? kRowStretches : kRow512;
+}
+
 template <int TYPE, bool TOP>
 hipError_t scores(const ScoresArgs& a, int cus, hipStream_t stream) {
   const int parts = parts_of(a.M, a.V, cus);
+  constexpr int S = TOP ? 4 : 1;
   const dim3 grid((unsigned)(a.M * parts));
   hipError_t e;
-  if (a.V <= 4096) e = launch_k(scores_kernel<TYPE, 128, 16, TOP, 1>, grid, dim3(128), 0, stream, Ev{}, a, parts);
-  else if (few_rows(a.M, parts, cus)) e = launch_k(scores_kernel<TYPE, 1024, 32, TOP, 1>, grid, dim3(1024), 0, stream, Ev{}, a, parts);
-  else if (a.V / parts > kChain * 512 * 16)  // (both sums in one kernel: fp32's would not fit 64 registers)
-    e = launch_k(scores_kernel<TYPE, 512, 16, TOP, TOP ? 4 : 1, true>, grid, dim3(512), 0, stream, Ev{}, a, parts);
-  else if (TOP && a.M > cus && a.V > 32768) e = launch_k(scores_kernel<TYPE, 512, 16, TOP, TOP ? 4 : 1>, grid, dim3(512), 0, stream, Ev{}, a, parts);
-  else e = launch_k(scores_kernel<TYPE, 512, 16, TOP, 1>, grid, dim3(512), 0, stream, Ev{}, a, parts);
+  switch (row_of(a.M, a.V, a.k, parts, cus)) {
+    case kRow128: e = launch_k(scores_kernel<TYPE, 128, 16, TOP, 1>, grid, dim3(128), 0, stream, Ev{}, a, parts); break;
+    case kRow1024: e = launch_k(scores_kernel<TYPE, 1024, 32, TOP, 1>, grid, dim3(1024), 0, stream, Ev{}, a, parts); break;
+    case kRowLong: e = launch_k(scores_kernel<TYPE, 512, 16, TOP, S, true>, grid, dim3(512), 0, stream, Ev{}, a, parts); break;
+    case kRowStretches: e = launch_k(scores_kernel<TYPE, 512, 16, TOP, S>, grid, dim3(512), 0, stream, Ev{}, a, parts); break;
+    default: e = launch_k(scores_kernel<TYPE, 512, 16, TOP, 1>, grid, dim3(512), 0, stream, Ev{}, a, parts); break;
+  }
   if (e == hipSuccess && parts > 1)
     e = launch_k(scores_join_kernel<TYPE>, dim3((unsigned)a.M), dim3(256), 0, stream, Ev{}, a, parts);
   return e;
@@ -577,6 +590,11 @@ hipError_t scores(const ScoresArgs& a, int cus, hipStream_t stream) {
 size_t scores_ws_bytes(int64_t M, int64_t V, int64_t k, int, int cus) {
   const int parts = parts_of(M, V, cus);
   return parts > 1 ? (size_t)M * parts * (sizeof(ScoresPart) + 8 * (size_t)k) : 0;
+}
+
+const char* scores_kernel_name(int64_t M, int64_t V, int64_t k, int cus) {
+  const int parts = parts_of(M, V, cus);
+  return parts > 1 ? kPartName : kRowName[row_of(M, V, k, parts, cus)];
 }
 
 hipError_t launch_scores(const ScoresArgs& a, int cus, hipStream_t stream) {
@@ -798,7 +816,7 @@ __device__ Total joined(const DistillArgs& a, int64_t row, int parts) {
   return {top, wave_sum(i < parts ? p[i].s * exp(((double)m - top) * c) : 0.0), 0};
 }
 
-// Forward, the parts' sums joined: the loss. (PARTS workgroups with the gradient.)
+// Forward, the parts' sums joined: the loss.
 template <int TYPE>
 __global__ __launch_bounds__(64) void distill_loss_kernel(const DistillArgs a, int parts) {
   __shared__ Teacher w;
@@ -1064,6 +1082,20 @@ size_t distill_ws_bytes(int64_t M, int64_t V, int type, int cus) {
   if (how == kSplit) need(std::max(grad_parts(M, V, cus), 2) * sizeof(ScoresPart));
   if (how == kHeld) need(sizeof(ScoresPart) + kMaxTop * sizeof(float));
   return (size_t)M * n;
+}
+
+const char* distill_kernel_name(DistillPass pass, int64_t M, int64_t V, int type, int grad_type, int cus) {
+  const int parts = pass == kDistillBackward ? grad_parts(M, V, cus) : parts_of(M, V, cus);
+  const bool few = few_rows(M, parts, cus);
+  if (pass == kDistillBoth) {
+    const bool same = (type == MOE_FP32) == (grad_type == MOE_FP32);
+    const Both how = choose_both(M, V, type, same, cus);
+    if (how == kHeld) return "rows held in registers";
+    if (how == kSplit) return kPartName;
+    return kRowName[V <= 4096 ? kRow128 : few || V > 32768 ? kRow1024 : kRow512];
+  }
+  if (parts > 1) return kPartName;
+  return kRowName[V <= 4096 ? kRow128 : few && pass == kDistillForward ? kRow1024 : kRow512];
 }
 
 hipError_t launch_distill(DistillPass pass, const DistillArgs& a, int cus, hipStream_t stream) {

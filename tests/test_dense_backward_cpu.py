@@ -28,3 +28,11 @@ def test_x_is_read_for_dw_alone(cls):
 
 class _Stream:
     cuda_stream = 0
+
+
+def test_kernel_names_refuse_a_missing_handle():
+    L = B.lib()
+    assert L.moe_scores_kernel(None, 1) is None and L.moe_distill_kernel(None, 1, 0) is None
+    for cls in (B.TokenScores, B.Distill):
+        with pytest.raises(ValueError):
+            _bare(cls, device=CPU, max_M=4).kernel(1)
