@@ -44,7 +44,7 @@ int64_t up8(int64_t n) { return (n + 7) & ~(int64_t)7; }
 struct Backward {
   size_t dz, part, split, bytes;
 };
-Backward backward_layout(int64_t M, int64_t N, int64_t K, bool dz, bool bias, int type, int cus) {
+Backward backward_layout(int64_t M, int64_t N, int64_t K, bool dz, bool bias, int cus) {
   Backward l;
   size_t at = 0;
   l.dz = at;
@@ -52,7 +52,7 @@ Backward backward_layout(int64_t M, int64_t N, int64_t K, bool dz, bool bias, in
   l.part = at;
   at += bias ? align256((size_t)dbias_parts(M) * N * 4) : 0;
   l.split = at;
-  const size_t a = gemm_ws_bytes(kGemmInput, M, K, N, type, cus), b = gemm_ws_bytes(kGemmWeight, N, K, M, type, cus);
+  const size_t a = gemm_ws_bytes(kGemmInput, M, K, N, cus), b = gemm_ws_bytes(kGemmWeight, N, K, M, cus);
   l.bytes = at + (a > b ? a : b);
   return l;
 }
@@ -65,7 +65,6 @@ hipError_t products(int64_t M, int64_t N, int64_t K, int type, int cus, const vo
   GemmArgs g{};
   g.type = g.y_type = type;
   g.ws = ws ? ws + l.split : nullptr;
-  g.ws_bytes = l.bytes - l.split;
   if (dx && M > 0) {
     g.rows = M, g.cols = K, g.K = N;
     g.a = dz, g.lda = ldz, g.b = w, g.ldb = K;
@@ -114,8 +113,8 @@ const char* moe_dense_kernel(const moe_dense* d, int64_t M, int product) {
 moe_status moe_dense_workspace_bytes(const moe_dense* d, int64_t M, int train, size_t* bytes) {
   if (!d || !bytes || M < 0 || M > d->max_M || train < 0 || train > 2) return MOE_ERR_INVALID_ARG;
   if (train == 2 && (d->act != MOE_ACT_NONE || d->N % 8 != 0)) train = 1;
-  const size_t f = gemm_ws_bytes(kGemmForward, M, d->N, d->K, d->type, d->num_cus);
-  const size_t b = train ? backward_layout(M, d->N, d->K, train == 1, train == 1, d->type, d->num_cus).bytes : 0;
+  const size_t f = gemm_ws_bytes(kGemmForward, M, d->N, d->K, d->num_cus);
+  const size_t b = train ? backward_layout(M, d->N, d->K, train == 1, train == 1, d->num_cus).bytes : 0;
   *bytes = f > b ? f : b;
   return MOE_OK;
 }
@@ -132,7 +131,7 @@ moe_status moe_dense_forward(const moe_dense* d, int64_t M, const void* x, int64
   if (residual && !matrix_ok(residual, ldr, d->N, es)) return MOE_ERR_INVALID_ARG;
   const size_t ps = type_bytes(pre_type);
   if (pre && !matrix_ok(pre, ldp, d->N, ps)) return MOE_ERR_INVALID_ARG;
-  const size_t need = gemm_ws_bytes(kGemmForward, M, d->N, d->K, d->type, d->num_cus);
+  const size_t need = gemm_ws_bytes(kGemmForward, M, d->N, d->K, d->num_cus);
   moe_status st = check_ws(workspace, workspace_bytes, need);
   if (st != MOE_OK) return st;
   // in place (y is the residual itself) every element is read before it is written
@@ -149,7 +148,7 @@ moe_status moe_dense_forward(const moe_dense* d, int64_t M, const void* x, int64
   DeviceGuard guard(d->device);
   if (!guard.ok) return MOE_ERR_DEVICE;
   GemmArgs g{M, d->N, d->K, x, d->w, ldx, d->K, d->type, d->bias, residual, y, pre, ldr, ldy, ldp, d->act, y_type, pre_type, 0, 1,
-             workspace, need};
+             workspace};
   return launch_gemm(kGemmForward, g, d->num_cus, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
@@ -169,7 +168,7 @@ moe_status moe_dense_backward(const moe_dense* d, int64_t M, const void* dy, int
   if ((dw && !aligned16(dw)) || ((uintptr_t)dbias & 1)) return MOE_ERR_INVALID_ARG;
   // dy is dz itself where it needs no slope and its rows are an operand's
   const bool direct = d->act == MOE_ACT_NONE && N % 8 == 0 && (M == 0 || operand_ok(dy, lddy, N));
-  const Backward l = backward_layout(M, N, K, !direct, !direct || dbias, d->type, d->num_cus);
+  const Backward l = backward_layout(M, N, K, !direct, !direct || dbias, d->num_cus);
   moe_status st = check_ws(workspace, workspace_bytes, l.bytes);
   if (st != MOE_OK) return st;
   const Buf b[] = {{dx, span(M, lddx, K, 2), true},
@@ -227,8 +226,8 @@ const char* moe_gated_kernel(const moe_gated* d, int64_t M, int product) {
 
 moe_status moe_gated_workspace_bytes(const moe_gated* d, int64_t M, int train, size_t* bytes) {
   if (!d || !bytes || M < 0 || M > d->max_M || (train != 0 && train != 1)) return MOE_ERR_INVALID_ARG;
-  const size_t f = gemm_ws_bytes(kGemmGated, M, d->I, d->H, d->type, d->num_cus);
-  const size_t b = train ? backward_layout(M, 2 * d->I, d->H, true, false, d->type, d->num_cus).bytes : 0;
+  const size_t f = gemm_ws_bytes(kGemmGated, M, d->I, d->H, d->num_cus);
+  const size_t b = train ? backward_layout(M, 2 * d->I, d->H, true, false, d->num_cus).bytes : 0;
   *bytes = f > b ? f : b;
   return MOE_OK;
 }
@@ -240,7 +239,7 @@ moe_status moe_gated_forward(const moe_gated* d, int64_t M, const void* x, int64
   if (M == 0) return MOE_OK;
   const size_t ps = type_bytes(pre_type);
   if (!operand_ok(x, ldx, d->H) || !matrix_ok(h, ldh, d->I, 2) || ((uintptr_t)pre & (ps - 1))) return MOE_ERR_INVALID_ARG;
-  const size_t need = gemm_ws_bytes(kGemmGated, M, d->I, d->H, d->type, d->num_cus);
+  const size_t need = gemm_ws_bytes(kGemmGated, M, d->I, d->H, d->num_cus);
   moe_status st = check_ws(workspace, workspace_bytes, need);
   if (st != MOE_OK) return st;
   const Buf b[] = {{h, span(M, ldh, d->I, 2), true},
@@ -253,7 +252,7 @@ moe_status moe_gated_forward(const moe_gated* d, int64_t M, const void* x, int64
   DeviceGuard guard(d->device);
   if (!guard.ok) return MOE_ERR_DEVICE;
   GemmArgs g{M, d->I, d->H, x, d->w13, ldx, d->H, d->type, nullptr, nullptr, h, pre, 0, ldh, 2 * d->I, d->act, d->type, pre_type, 0, 1,
-             workspace, need};
+             workspace};
   return launch_gemm(kGemmGated, g, d->num_cus, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
@@ -270,7 +269,7 @@ moe_status moe_gated_backward(const moe_gated* d, int64_t M, const void* dh, int
     if (dx && !matrix_ok(dx, lddx, H, 2)) return MOE_ERR_INVALID_ARG;
   }
   if (dw13 && !aligned16(dw13)) return MOE_ERR_INVALID_ARG;
-  const Backward l = backward_layout(M, N, H, true, false, d->type, d->num_cus);
+  const Backward l = backward_layout(M, N, H, true, false, d->num_cus);
   moe_status st = check_ws(workspace, workspace_bytes, l.bytes);
   if (st != MOE_OK) return st;
   const Buf b[] = {{dx, span(M, lddx, H, 2), true},

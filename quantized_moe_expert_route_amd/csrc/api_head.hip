@@ -50,7 +50,7 @@ const char* moe_scores_kernel(const moe_scores* s, int64_t M) {
 
 moe_status moe_scores_workspace_bytes(const moe_scores* s, int64_t M, size_t* bytes) {
   if (!s || !bytes || M < 0 || M > s->max_M) return MOE_ERR_INVALID_ARG;
-  *bytes = scores_ws_bytes(M, s->V, s->k, s->type, s->num_cus);
+  *bytes = scores_ws_bytes(M, s->V, s->k, s->num_cus);
   return MOE_OK;
 }
 
@@ -63,7 +63,7 @@ moe_status moe_scores_forward(const moe_scores* s, int64_t M, const void* z, int
   if (!rows_ok(z, ldz, s->V, es)) return MOE_ERR_INVALID_ARG;
   if ((tokens != nullptr) != (logprobs != nullptr)) return MOE_ERR_INVALID_ARG;
   if (s->k > 0 ? !top_logprobs || !top_ids : top_logprobs || top_ids) return MOE_ERR_INVALID_ARG;
-  const size_t need = scores_ws_bytes(M, s->V, s->k, s->type, s->num_cus);
+  const size_t need = scores_ws_bytes(M, s->V, s->k, s->num_cus);
   moe_status st = check_ws(workspace, workspace_bytes, need);
   if (st != MOE_OK) return st;
   const size_t col = 4 * (size_t)M, top = col * (size_t)s->k;

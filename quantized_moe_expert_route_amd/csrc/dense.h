@@ -43,9 +43,7 @@ struct GemmArgs {
   int act, y_type, pre_type;
   int vec;  // set by launch_gemm: which of the matrices move in 16-byte pieces
   int splits;  // parts of K, set by launch_gemm
-  // workspace of the splits' sums
-  void* ws;
-  size_t ws_bytes;
+  void* ws;  // gemm_ws_bytes of the splits' sums
 };
 
 enum GemmKind {
@@ -57,7 +55,7 @@ enum GemmKind {
 
 hipError_t launch_gemm(GemmKind kind, const GemmArgs& a, int cus, hipStream_t stream);
 // bytes of GemmArgs::ws that the launch wants for these sizes
-size_t gemm_ws_bytes(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int type, int cus);
+size_t gemm_ws_bytes(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int cus);
 
 const char* gemm_kernel_name(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int cus);  // rows, cols > 0
 

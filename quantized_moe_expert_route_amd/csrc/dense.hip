@@ -114,7 +114,7 @@ hipError_t launch(GemmArgs a, const Choice& c, int cus, hipStream_t stream) {
 
 }  // namespace
 
-size_t gemm_ws_bytes(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int, int cus) {
+size_t gemm_ws_bytes(GemmKind kind, int64_t rows, int64_t cols, int64_t K, int cus) {
   if (rows == 0 || cols == 0) return 0;
   const Choice c = choose(kind, rows, cols, K, cus);
   return c.splits > 1 ? (size_t)c.splits * rows * ((cols + 7) / 8 * 8) * (kind == kGemmGated ? 8 : 4) : 0;

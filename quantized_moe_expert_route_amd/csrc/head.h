@@ -38,7 +38,7 @@ struct ScoresArgs {
   void* ws;
 };
 hipError_t launch_scores(const ScoresArgs& a, int cus, hipStream_t stream);
-size_t scores_ws_bytes(int64_t M, int64_t V, int64_t k, int type, int cus);
+size_t scores_ws_bytes(int64_t M, int64_t V, int64_t k, int cus);
 const char* scores_kernel_name(int64_t M, int64_t V, int64_t k, int cus);  // M > 0
 
 struct DistillArgs {

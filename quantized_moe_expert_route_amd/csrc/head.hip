@@ -587,7 +587,7 @@ hipError_t scores(const ScoresArgs& a, int cus, hipStream_t stream) {
 
 }  // namespace
 
-size_t scores_ws_bytes(int64_t M, int64_t V, int64_t k, int, int cus) {
+size_t scores_ws_bytes(int64_t M, int64_t V, int64_t k, int cus) {
   const int parts = parts_of(M, V, cus);
   return parts > 1 ? (size_t)M * parts * (sizeof(ScoresPart) + 8 * (size_t)k) : 0;
 }
