@@ -492,7 +492,7 @@ moe_status moe_dense_backward(const moe_dense* dense, int64_t M, const void* dy,
  * handle, not copied; act any but MOE_ACT_NONE. x [M, H], rows ldx apart; h [M, I],
  * rows ldh >= I apart, of x's type, rounded once from fp32 g and u. `pre`, or
  * NULL: [M, 2I] dense, g and u in x's type or MOE_FP32 (pre_type: 16 bits make the
- * gradients' relative error 1.7 times the rounding of their own type, 32 bits 1.4
+ * gradients' relative error 1.8 times the rounding of their own type, 32 bits 1.4
  * times), for moe_gated_backward:
  *   dg = dh u act'(g), du = dh act(g), dx = [dg du] w13, dw13 = [dg du]^T x
  * dg and du rounded to x's type before the products. A saved g or u past the type's

@@ -245,8 +245,8 @@ hipError_t launch_slope(const SlopeArgs& a, hipStream_t stream) {
   return e;
 }
 
-// Eight columns of I of a row a lane, both halves of dz. Bound by memory: 4096 x 2 2048 25
-// us (4.7 TB/s, pre in 32 bits). vec: the rows and halves of dh
+// Eight columns of I of a row a lane, both halves of dz. Bound by memory: 4096 x 2 2048 23
+// us (3.6 TB/s; pre in 32 bits 25, 4.7 TB/s). vec: the rows and halves of dh
 // (1), pre (2) and dz (4) move in 16-byte pieces.
 template <bool F16>
 __global__ __launch_bounds__(256) void gated_slope_kernel(const GatedSlopeArgs a, int vec) {

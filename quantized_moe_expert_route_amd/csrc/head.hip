@@ -109,8 +109,8 @@ __device__ __forceinline__ float row_max(float v) {
 }
 
 // ----------------------------------------------------------------- sums of a row
-// A thread's sums, N elements at a time: each N by themselves, then added to the rest, from
-// kChain of them on (LONG) with the rounding errors carried along: a chain of plain additions of like
+// A thread's sums, N elements at a time: each N by themselves, then added to the rest, with
+// more than kChain of them (LONG) with the rounding errors carried along: a chain of plain additions of like
 // terms rounds them all the same way (it lost 3e-4 of a sum of 2^15). Carrying them costs 1 %
 // of 2048 x 131072. m stays while the elements pass it by no more than a factor 2^kOver of
 // the sums: of a row that rises slowly every N elements would scale the sums, by a
@@ -434,7 +434,7 @@ __device__ __forceinline__ float given_logit(const ScoresArgs& a, const Row<TYPE
 
 // (at most 64 registers for 512 threads: four workgroups a CU). N elements a thread and
 // tile, the next tile's under way meanwhile. Bound by memory: 2048 x 131072 bf16 94 us (5.7
-// TB/s) without alternatives, whose logits are read past the caches; 112 with 32 of them: the
+// TB/s) without alternatives, whose logits are read past the caches; 114 with 32 of them: the
 // search for the threshold and the second reading of some 33 threads' pieces, S stretches a
 // thread, are a workgroup's own latency, and the logits pass through the caches for it.
 template <int TYPE, int THREADS, int N, bool TOP, int S, bool LONG = false>
@@ -875,7 +875,7 @@ __global__ __launch_bounds__(THREADS) void distill_both_kernel(const DistillArgs
 // and the gradient: every logit is read once. A workgroup takes rows one after another
 // and loads a piece of the next as soon as that piece's gradient is on its way, and sums
 // it `lag` pieces later, so that memory is not left idle for a row's sums. Bound by memory:
-// 2048 x 131072 bf16 228 us, 2048 x 32000 fp32 103 with its second launch (4.7 and 5.1
+// 2048 x 131072 bf16 228 us, 2048 x 32000 fp32 107 with its second launch (4.7 and 4.9
 // TB/s; with accesses through the caches 251 and 118). dz's elements have z's size and
 // its rows z's alignment. The rows' sums and their logits at the slots go to the
 // workspace for distill_finish_kernel, which writes the loss and the gradient at the
