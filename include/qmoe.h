@@ -605,7 +605,8 @@ const char* moe_linear_kernel(const moe_linear* linear, int64_t M);
 const char* moe_dense_kernel(const moe_dense* dense, int64_t M, int product);
 const char* moe_gated_kernel(const moe_gated* gated, int64_t M, int product);
 /* Of the head's operators; distillation by pass: 0 forward, 1 backward, 2 both at once, whose
- * gradient lies beside the logits and as they do (the same distance from 16 bytes in every row). */
+ * gradient lies beside the logits (1 too) and as they do (the same distance from 16 bytes in
+ * every row). */
 const char* moe_scores_kernel(const moe_scores* scores, int64_t M);
 const char* moe_distill_kernel(const moe_distill* distill, int64_t M, int pass);
 

@@ -267,7 +267,7 @@ __global__ __launch_bounds__(256) void gated_slope_kernel(const GatedSlopeArgs a
           float value;
           const float s = act_slope<act>(g[q], value);
           // (an infinite u beside a gate that passes nothing: 0, as h has it)
-          g[q] = s == 0.f && fabsf(u[q]) == INFINITY ? 0.f : d[q] * u[q] * s;
+          g[q] = s == 0.f && fabsf(u[q]) == INFINITY ? d[q] * s : d[q] * u[q] * s;
           u[q] = d[q] * value;
         }
         write8<F16, false>(dz, vec & 4, left, g);

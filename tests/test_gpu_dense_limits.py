@@ -78,6 +78,9 @@ def test_gated_past_the_range(act, pt):
     both = torch.tensor(keep + [I + i for i in keep])
     (want, bound), _ = R.gated_backward(_f64(dh[:, keep]), _f64(pre.cpu()[:, both]), _f64(x), _f64(w[both]), act, "fp16")
     _within(dx, want, bound, "dx")
+    dh[5, 1], dh[6, 3] = math.nan, math.inf  # a gradient that is none stays none
+    op.backward(dh.cuda(), x.cuda(), pre, dx=dx, dw=dw, workspace=ws)
+    assert dx[5:7].isnan().all() and not dx[:5].isnan().any() and dw[[1, 3, I + 1, I + 3]].isnan().all()
 
 
 # Relative errors of the activations' lower tails in binary32, in U. silu and gelu_tanh: an
