@@ -573,7 +573,8 @@ class Gated(_Product):
 
     def forward(self, x, out, pre=None, workspace=None, M: Optional[int] = None, stream=None):
         """out[:M] [M, I]; `pre` [M, 2I] (contiguous, of x's type or float32) takes [g u],
-        for backward."""
+        for backward (float32 where the gradients' precision counts: 1.4 roundings of their type
+        for 1.8)."""
         M = self._rows(x, M)
         ldx = self._check("x", x, self.dtype, M, self.H)
         ldh = self._check("out", out, self.dtype, M, self.I)
